@@ -17,6 +17,15 @@ Functions carry the C names:
 * ``mxq_export_mxfp8_grouped`` export of many storages (per expert) in one launch
 * ``mxq_quantize_export_mxfp8`` quantize a bf16/fp32 weight and export it in one call
 
+The FP8 linear layer on the 128x128 blockwise weights, and the mixture of experts around it:
+
+* ``mxq_fp8_quant_1x128`` / ``_128x1``  activations -> E4M3, one power-of-two scale per 128 elements of a row / column
+* ``mxq_fp8_matmul``, ``_dgrad``, ``_wgrad``  y = x W^T, its input gradient g W and weight gradient g^T x
+* ``mxq_fp8_grouped_matmul``, ``_dgrad``, ``_wgrad``  the same for rows sorted by expert
+* ``mxq_moe_sort``             a router's choices in the experts' order
+* ``mxq_moe_dispatch``, ``_dispatch_grad``  token rows to that order, and the gradient
+* ``mxq_moe_combine``, ``_combine_grad``    weighted sums of the experts' rows per token, and the gradients
+
 The ``skip=`` argument of the converters selects the ``*_update`` entry
 points: a device int32 tensor, read when the kernel runs; nonzero means the
 call writes nothing (for cached weights inside captured CUDA graphs).
@@ -39,6 +48,9 @@ __all__ = [
     "mxq_dequantize", "mxq_export_mxfp8", "mxq_mxfp4_pack", "mxq_mxfp8_col_direct", "mxq_scale_bytes",
     "mxq_tile_scale_count", "mxq_export_mxfp8_grouped", "mxq_quantize_export_mxfp8",
     "COMPACT", "PADDED", "SWIZZLED", "scale_cols",
+    "MoeOrder", "mxq_fp8_quant_1x128", "mxq_fp8_quant_128x1", "mxq_fp8_matmul", "mxq_fp8_matmul_dgrad",
+    "mxq_fp8_matmul_wgrad", "mxq_fp8_grouped_matmul", "mxq_fp8_grouped_matmul_dgrad", "mxq_fp8_grouped_matmul_wgrad",
+    "mxq_moe_sort", "mxq_moe_dispatch", "mxq_moe_dispatch_grad", "mxq_moe_combine", "mxq_moe_combine_grad",
 ]
 
 COMPACT, PADDED, SWIZZLED = 0, 1, 2
@@ -47,6 +59,7 @@ _LAYOUTS = {"compact": COMPACT, "padded": PADDED, "swizzled": SWIZZLED, COMPACT:
 _BF16, _FP32, _FP16 = 0, 1, 2
 _E4M3, _E5M2 = 0, 1
 _MXFP8_ROW, _BLOCK128, _MXFP4, _MXFP8_COL = 0, 1, 2, 3
+_FWD, _DGRAD, _WGRAD = 0, 1, 2
 
 
 class MXQError(RuntimeError):
@@ -77,6 +90,21 @@ class _Components(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("fp8", ctypes.c_int), ("scales", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("scale_cols", ctypes.c_int64),
                 ("is_view", ctypes.c_int)]
+
+
+class MoeOrder(NamedTuple):
+    """A router's choices sorted by expert (choice c = token * topk + place)."""
+    offsets: torch.Tensor  # int32 [experts + 1], where each expert's rows begin
+    source: torch.Tensor   # int32 [capacity], the choice at each row, -1 for none
+    slots: torch.Tensor    # int32 [tokens, topk], the row of each choice, -1 if dropped
+
+
+class _Product(ctypes.Structure):
+    _fields_ = [("dir", ctypes.c_int), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("a_scales", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("b_scales", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_dt", ctypes.c_int), ("ldo", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("E", ctypes.c_int64)]
 
 
 def scale_cols(K: int) -> int:
@@ -156,6 +184,34 @@ def _check_storage(lib, data, scales, rows: int, K: int, layout):
         raise ValueError("data must be the contiguous rows*K payload bytes of the storage")
 
 
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _check_fp8(t: torch.Tensor, name: str):
+    if t.dtype != torch.uint8 and t.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"{name} must hold E4M3 bytes (uint8 or float8_e4m3fn)")
+
+
+def _check_int32(t: torch.Tensor, numel: int, name: str):
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {numel} values")
+
+
+def _check_scales(t: torch.Tensor, dtype, numel: int, name: str, what: str):
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {what} = {numel} values")
+
+
+def _one_device(x: torch.Tensor, *ts):
+    if not x.is_cuda:
+        raise ValueError("libmxq works on CUDA tensors only")
+    dev = x.device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("every tensor of a call must sit on one CUDA device")
+
+
 class Library:
     """One loaded libmxq variant (``fastmath=True`` loads the --use_fast_math build)."""
 
@@ -190,11 +246,26 @@ class Library:
         L.mxq_tile_scale_count.restype = ctypes.c_size_t
         L.mxq_status_string.argtypes = [ci]
         L.mxq_status_string.restype = ctypes.c_char_p
+        i32, sz = ctypes.c_int32, ctypes.c_size_t
+        for fn in (L.mxq_fp8_quant_1x128, L.mxq_fp8_quant_128x1):
+            fn.argtypes = [vp, ci, i64, i64, i64, vp, i32, i64, vp, vp, vp]
+        L.mxq_fp8_matmul.argtypes = [ctypes.POINTER(_Product), vp, sz, vp]
+        L.mxq_fp8_matmul_workspace.argtypes = [ctypes.POINTER(_Product)]
+        L.mxq_fp8_matmul_workspace.restype = sz
+        L.mxq_moe_sort.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+        L.mxq_moe_capacity.argtypes = [i64, i64, i64, i64]
+        L.mxq_moe_capacity.restype = i64
+        L.mxq_moe_sort_workspace.argtypes = [i64, i64, i64]
+        L.mxq_moe_sort_workspace.restype = sz
+        L.mxq_moe_dispatch.argtypes = [vp, ci, i64, i64, i64, vp, i64, i64, vp, vp]
+        L.mxq_moe_combine.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, i64, vp, vp]
+        L.mxq_moe_combine_grad.argtypes = [vp, vp, ci, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp]
         for fn in ("mxq_fake_quant_mxfp4", "mxq_mxfp8_row_direct", "mxq_fp8_block128_direct", "mxq_dequantize",
                    "mxq_export_mxfp8", "mxq_fake_quant_mxfp4_update", "mxq_mxfp8_row_direct_update",
                    "mxq_fp8_block128_direct_update", "mxq_mxfp4_pack", "mxq_mxfp8_col_direct",
                    "mxq_mxfp4_pack_update", "mxq_mxfp8_col_direct_update", "mxq_export_mxfp8_grouped",
-                   "mxq_quantize_export_mxfp8"):
+                   "mxq_quantize_export_mxfp8", "mxq_fp8_quant_1x128", "mxq_fp8_quant_128x1", "mxq_fp8_matmul",
+                   "mxq_moe_sort", "mxq_moe_dispatch", "mxq_moe_combine", "mxq_moe_combine_grad"):
             getattr(L, fn).restype = ci
         self.L = L
 
@@ -567,6 +638,250 @@ class Library:
         call()
         return comp
 
+    # -- the FP8 linear layer -------------------------------------------
+
+    def _plan_quant128(self, name, columns, x, data, scales, index, index_div):
+        _one_device(x, data, scales, index)
+        dt = _dt_code(x)
+        rows, K, ldx = _rows_view(x)
+        n = rows
+        if index is not None:
+            n = index.numel()
+            _check_int32(index, n, "index")
+        if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != n * K:
+            raise ValueError("data must be a contiguous uint8 tensor of one byte per output element")
+        if columns:
+            _check_scales(scales, torch.uint8, _blocks(n) * K, "scales", "ceil(rows/128) * K")
+        else:
+            _check_scales(scales, torch.uint8, n * _blocks(K), "scales", "rows * ceil(K/128)")
+        args = (x.data_ptr(), dt, rows, K, ldx, index.data_ptr() if index is not None else None, index_div, n,
+                data.data_ptr(), scales.data_ptr(), _stream(x))
+        return Call(self, getattr(self.L, name), args, name, (x, data, scales, index), x.device)
+
+    def plan_fp8_quant_1x128(self, x: torch.Tensor, data: torch.Tensor, scales: torch.Tensor,
+                             index: Optional[torch.Tensor] = None, index_div: int = 1) -> "Call":
+        return self._plan_quant128("mxq_fp8_quant_1x128", False, x, data, scales, index, index_div)
+
+    def plan_fp8_quant_128x1(self, x: torch.Tensor, data: torch.Tensor, scales: torch.Tensor,
+                             index: Optional[torch.Tensor] = None, index_div: int = 1) -> "Call":
+        return self._plan_quant128("mxq_fp8_quant_128x1", True, x, data, scales, index, index_div)
+
+    def fp8_quant_1x128(self, x: torch.Tensor, index: Optional[torch.Tensor] = None, index_div: int = 1,
+                        data: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+        """Returns (E4M3 bytes of x's shape, UE8M0 codes (*shape[:-1],
+        ceil(K/128))).  With ``index`` (int32, one entry per output row) row i
+        is row index[i] // index_div of x, zeros for a negative index; the
+        results are then two-dimensional."""
+        lead = tuple(x.shape[:-1]) if index is None else (index.numel(),)
+        K = x.shape[-1]
+        if data is None:
+            data = torch.empty(lead + (K,), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty(lead + (_blocks(K),), dtype=torch.uint8, device=x.device)
+        self.plan_fp8_quant_1x128(x, data, scales, index, index_div)()
+        return data, scales
+
+    def fp8_quant_128x1(self, x: torch.Tensor, index: Optional[torch.Tensor] = None, index_div: int = 1,
+                        data: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+        """Returns (E4M3 bytes [rows, K], UE8M0 codes [ceil(rows/128), K]);
+        ``index`` as in fp8_quant_1x128."""
+        rows, K, _ = _rows_view(x)
+        n = rows if index is None else index.numel()
+        if data is None:
+            data = torch.empty((n, K), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty((_blocks(n), K), dtype=torch.uint8, device=x.device)
+        self.plan_fp8_quant_128x1(x, data, scales, index, index_div)()
+        return data, scales
+
+    def plan_fp8_matmul(self, direction: str, a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
+                        b_scales: torch.Tensor, out: torch.Tensor, offsets: Optional[torch.Tensor] = None) -> "Call":
+        """``direction`` "fwd": out = a b^T with a = x, b = w; "dgrad": out = a
+        b with a = g, b = w; "wgrad": out = a^T b with a = g, b = x.  w is [N, K]
+        with fp32 tile scales, or a stack [E, N, K] with ``offsets`` (int32
+        [E + 1], the experts' rows); the gradient of a stack is [E, N, K]."""
+        _one_device(a, a_scales, b, b_scales, out, offsets)
+        if direction not in ("fwd", "dgrad", "wgrad"):
+            raise ValueError('direction must be "fwd", "dgrad" or "wgrad"')
+        _check_fp8(a, "the left operand")
+        _check_fp8(b, "the right operand")
+        p = _Product()
+        M, an, p.lda = _rows_view(a)
+        rb, K, p.ldb = _rows_view(b)
+        E = 1 if offsets is None else offsets.numel() - 1
+        if offsets is not None:
+            _check_int32(offsets, max(E, 0) + 1, "offsets")
+        if direction == "wgrad":
+            p.dir, N = _WGRAD, an
+            if rb != M:
+                raise ValueError("g and x must have the same number of rows")
+            _check_scales(a_scales, torch.uint8, _blocks(M) * N, "g's scales", "ceil(rows/128) * N")
+            _check_scales(b_scales, torch.uint8, _blocks(M) * K, "x's scales", "ceil(rows/128) * K")
+            rows, n = N * E, K
+        else:
+            if b.dim() != (2 if offsets is None else 3) or (offsets is not None and b.shape[0] != E):
+                raise ValueError("w must be [N, K], or [E, N, K] with offsets of E + 1 values")
+            N = b.shape[-2]
+            p.dir = _FWD if direction == "fwd" else _DGRAD
+            if an != (K if direction == "fwd" else N):
+                raise ValueError("the operands' inner sizes differ")
+            _check_scales(a_scales, torch.uint8, M * _blocks(an), "the left operand's scales", "rows * ceil(n/128)")
+            _check_scales(b_scales, torch.float32, E * _blocks(N) * _blocks(K), "w's tile scales",
+                          "ceil(N/128) * ceil(K/128) per weight")
+            rows, n = M, N if direction == "fwd" else K
+        orows, on, p.ldo = _rows_view(out)
+        if orows != rows or on != n:
+            raise ValueError(f"out must have {rows} rows of {n}")
+        p.M, p.N, p.K = M, N, K
+        pa, pb = a.data_ptr(), b.data_ptr()
+        p.a, p.a_scales, p.b, p.b_scales = pa, a_scales.data_ptr(), pb, b_scales.data_ptr()
+        p.out, p.out_dt = out.data_ptr(), _dt_code(out)
+        if offsets is not None:
+            p.offsets, p.E = offsets.data_ptr(), E
+        ref = ctypes.byref(p)
+        ws, need = None, 0
+        if (pa | p.lda | pb | p.ldb) & 15:  # rows that TMA cannot address
+            need = self.L.mxq_fp8_matmul_workspace(ref)
+            ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+        args = (ref, ws.data_ptr() if ws is not None else None, need, _stream(a))
+        return Call(self, self.L.mxq_fp8_matmul, args, "mxq_fp8_matmul",
+                    (a, a_scales, b, b_scales, out, offsets, ws, p), a.device)
+
+    def fp8_matmul(self, x, x_scales, w, w_tile_scale_inv, offsets=None, out_dtype=torch.bfloat16, out=None):
+        """y = x W^T: x [..., K] with 1x128 scales, w [N, K] with the tile
+        scales of fp8_block128_direct (a stack [E, N, K] with ``offsets``)."""
+        if out is None:
+            out = torch.empty(tuple(x.shape[:-1]) + (w.shape[-2],), dtype=out_dtype, device=x.device)
+        self.plan_fp8_matmul("fwd", x, x_scales, w, w_tile_scale_inv, out, offsets)()
+        return out
+
+    def fp8_matmul_dgrad(self, g, g_scales, w, w_tile_scale_inv, offsets=None, out_dtype=torch.bfloat16, out=None):
+        """dx = g W: g [..., N] with 1x128 scales, w as in fp8_matmul."""
+        if out is None:
+            out = torch.empty(tuple(g.shape[:-1]) + (w.shape[-1],), dtype=out_dtype, device=g.device)
+        self.plan_fp8_matmul("dgrad", g, g_scales, w, w_tile_scale_inv, out, offsets)()
+        return out
+
+    def fp8_matmul_wgrad(self, g, g_scales, x, x_scales, offsets=None, out_dtype=torch.float32, out=None):
+        """dW = g^T x: g [M, N] and x [M, K] with 128x1 scales."""
+        if out is None:
+            lead = () if offsets is None else (offsets.numel() - 1,)
+            out = torch.empty(lead + (g.shape[-1], x.shape[-1]), dtype=out_dtype, device=g.device)
+        self.plan_fp8_matmul("wgrad", g, g_scales, x, x_scales, out, offsets)()
+        return out
+
+    # -- mixture of experts ---------------------------------------------
+
+    def plan_moe_sort(self, ids: torch.Tensor, num_experts: int, offsets: torch.Tensor, source: torch.Tensor,
+                      slots: torch.Tensor, align: int = 1) -> "Call":
+        _one_device(ids, offsets, source, slots)
+        if ids.dim() != 2:
+            raise ValueError("ids must be [tokens, topk]")
+        T, topk = ids.shape
+        _check_int32(ids, T * topk, "ids")
+        _check_int32(offsets, num_experts + 1, "offsets")
+        _check_int32(source, self.L.mxq_moe_capacity(T, topk, num_experts, align), "source")
+        _check_int32(slots, T * topk, "slots")
+        need = self.L.mxq_moe_sort_workspace(T, topk, num_experts)
+        ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+        args = (ids.data_ptr(), T, topk, num_experts, align, offsets.data_ptr(), source.data_ptr(), slots.data_ptr(),
+                ws.data_ptr() if ws is not None else None, need, _stream(ids))
+        return Call(self, self.L.mxq_moe_sort, args, "mxq_moe_sort", (ids, offsets, source, slots, ws), ids.device)
+
+    def moe_sort(self, ids: torch.Tensor, num_experts: int, align: int = 1) -> MoeOrder:
+        """Sorts a router's choices ids [tokens, topk] (int32) by expert,
+        each expert's rows rounded up to a multiple of ``align`` (128 for the
+        weight gradient).  Ids outside 0..num_experts-1 are dropped."""
+        if ids.dim() != 2:
+            raise ValueError("ids must be [tokens, topk]")
+        if num_experts < 1 or align < 1:
+            raise ValueError("num_experts and align must be positive")
+        dev = ids.device
+        order = MoeOrder(torch.empty(num_experts + 1, dtype=torch.int32, device=dev),
+                         torch.empty(self.L.mxq_moe_capacity(ids.shape[0], ids.shape[1], num_experts, align),
+                                     dtype=torch.int32, device=dev),
+                         torch.empty(ids.shape, dtype=torch.int32, device=dev))
+        self.plan_moe_sort(ids, num_experts, *order, align=align)()
+        return order
+
+    def _row_major(self, t: torch.Tensor, name: str):
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be a matrix of contiguous rows")
+        return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+    def plan_moe_dispatch(self, x: torch.Tensor, source: torch.Tensor, topk: int, out: torch.Tensor) -> "Call":
+        _one_device(x, source, out)
+        ldx = self._row_major(x, "x")
+        R, H = source.numel(), x.shape[1]
+        _check_int32(source, R, "source")
+        if tuple(out.shape) != (R, H) or out.dtype != x.dtype or not out.is_contiguous():
+            raise ValueError("out must be a contiguous [rows, H] tensor of x's dtype")
+        args = (x.data_ptr(), _dt_code(x), x.shape[0], H, ldx, source.data_ptr(), topk, R, out.data_ptr(), _stream(x))
+        return Call(self, self.L.mxq_moe_dispatch, args, "mxq_moe_dispatch", (x, source, out), x.device)
+
+    def moe_dispatch(self, x: torch.Tensor, source: torch.Tensor, topk: int, out: Optional[torch.Tensor] = None):
+        """Token rows x [tokens, H] in the experts' order: row r is token
+        source[r] // topk, zeros where source is -1."""
+        if out is None:
+            out = torch.empty((source.numel(), x.shape[-1]), dtype=x.dtype, device=x.device)
+        self.plan_moe_dispatch(x, source, topk, out)()
+        return out
+
+    def plan_moe_combine(self, y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor],
+                         out: torch.Tensor) -> "Call":
+        _one_device(y, slots, weights, out)
+        ldy = self._row_major(y, "y")
+        if slots.dim() != 2:
+            raise ValueError("slots must be [tokens, topk]")
+        T, topk = slots.shape
+        _check_int32(slots, T * topk, "slots")
+        if weights is not None:
+            _check_scales(weights, torch.float32, T * topk, "weights", "tokens * topk")
+        if tuple(out.shape) != (T, y.shape[1]) or out.dtype != y.dtype or not out.is_contiguous():
+            raise ValueError("out must be a contiguous [tokens, H] tensor of y's dtype")
+        args = (y.data_ptr(), _dt_code(y), y.shape[0], y.shape[1], ldy, slots.data_ptr(),
+                weights.data_ptr() if weights is not None else None, T, topk, out.data_ptr(), _stream(y))
+        return Call(self, self.L.mxq_moe_combine, args, "mxq_moe_combine", (y, slots, weights, out), y.device)
+
+    def moe_combine(self, y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None):
+        """out[t] = sum_j weights[t, j] * y[slots[t, j]], dropped choices left
+        out; weights of one when None."""
+        if out is None:
+            out = torch.empty((slots.shape[0], y.shape[-1]), dtype=y.dtype, device=y.device)
+        self.plan_moe_combine(y, slots, weights, out)()
+        return out
+
+    def plan_moe_combine_grad(self, g: torch.Tensor, y: torch.Tensor, source: torch.Tensor, slots: torch.Tensor,
+                              weights: torch.Tensor, d_rows: torch.Tensor, d_weights: torch.Tensor) -> "Call":
+        _one_device(g, y, source, slots, weights, d_rows, d_weights)
+        ldg, ldy = self._row_major(g, "g"), self._row_major(y, "y")
+        if slots.dim() != 2:
+            raise ValueError("slots must be [tokens, topk]")
+        T, topk = slots.shape
+        R, H = y.shape
+        _check_int32(slots, T * topk, "slots")
+        _check_int32(source, R, "source")
+        _check_scales(weights, torch.float32, T * topk, "weights", "tokens * topk")
+        _check_scales(d_weights, torch.float32, T * topk, "d_weights", "tokens * topk")
+        if tuple(g.shape) != (T, H) or g.dtype != y.dtype:
+            raise ValueError("g must be [tokens, H] of y's dtype")
+        if tuple(d_rows.shape) != (R, H) or d_rows.dtype != y.dtype or not d_rows.is_contiguous():
+            raise ValueError("d_rows must be a contiguous [rows, H] tensor of y's dtype")
+        args = (g.data_ptr(), y.data_ptr(), _dt_code(g), T, topk, R, H, ldg, ldy, source.data_ptr(), slots.data_ptr(),
+                weights.data_ptr(), d_rows.data_ptr(), d_weights.data_ptr(), _stream(g))
+        return Call(self, self.L.mxq_moe_combine_grad, args, "mxq_moe_combine_grad",
+                    (g, y, source, slots, weights, d_rows, d_weights), g.device)
+
+    def moe_combine_grad(self, g: torch.Tensor, y: torch.Tensor, source: torch.Tensor, slots: torch.Tensor,
+                         weights: torch.Tensor):
+        """Returns (d_rows [rows, H], d_weights [tokens, topk] fp32), the
+        gradients of moe_combine for the gradient g of its output."""
+        d_rows = torch.empty((y.shape[0], y.shape[-1]), dtype=y.dtype, device=y.device)
+        d_weights = torch.empty(slots.shape, dtype=torch.float32, device=y.device)
+        self.plan_moe_combine_grad(g, y, source, slots, weights, d_rows, d_weights)()
+        return d_rows, d_weights
+
 
 class Call:
     """A prepared libmxq call (see Library.plan_*)."""
@@ -635,6 +950,58 @@ def mxq_export_mxfp8_grouped(storages, scale_out=None):
 
 def mxq_quantize_export_mxfp8(x, data=None, scales=None):
     return library().quantize_export_mxfp8(x, data, scales)
+
+
+def mxq_fp8_quant_1x128(x, index=None, index_div=1, data=None, scales=None):
+    return library().fp8_quant_1x128(x, index, index_div, data, scales)
+
+
+def mxq_fp8_quant_128x1(x, index=None, index_div=1, data=None, scales=None):
+    return library().fp8_quant_128x1(x, index, index_div, data, scales)
+
+
+def mxq_fp8_matmul(x, x_scales, w, w_tile_scale_inv, out_dtype=torch.bfloat16, out=None):
+    return library().fp8_matmul(x, x_scales, w, w_tile_scale_inv, None, out_dtype, out)
+
+
+def mxq_fp8_matmul_dgrad(g, g_scales, w, w_tile_scale_inv, out_dtype=torch.bfloat16, out=None):
+    return library().fp8_matmul_dgrad(g, g_scales, w, w_tile_scale_inv, None, out_dtype, out)
+
+
+def mxq_fp8_matmul_wgrad(g, g_scales, x, x_scales, out_dtype=torch.float32, out=None):
+    return library().fp8_matmul_wgrad(g, g_scales, x, x_scales, None, out_dtype, out)
+
+
+def mxq_fp8_grouped_matmul(x, x_scales, w, w_tile_scale_inv, offsets, out_dtype=torch.bfloat16, out=None):
+    return library().fp8_matmul(x, x_scales, w, w_tile_scale_inv, offsets, out_dtype, out)
+
+
+def mxq_fp8_grouped_matmul_dgrad(g, g_scales, w, w_tile_scale_inv, offsets, out_dtype=torch.bfloat16, out=None):
+    return library().fp8_matmul_dgrad(g, g_scales, w, w_tile_scale_inv, offsets, out_dtype, out)
+
+
+def mxq_fp8_grouped_matmul_wgrad(g, g_scales, x, x_scales, offsets, out_dtype=torch.float32, out=None):
+    return library().fp8_matmul_wgrad(g, g_scales, x, x_scales, offsets, out_dtype, out)
+
+
+def mxq_moe_sort(ids, num_experts, align=1):
+    return library().moe_sort(ids, num_experts, align)
+
+
+def mxq_moe_dispatch(x, source, topk, out=None):
+    return library().moe_dispatch(x, source, topk, out)
+
+
+def mxq_moe_dispatch_grad(g, slots, out=None):
+    return library().moe_combine(g, slots, None, out)
+
+
+def mxq_moe_combine(y, slots, weights, out=None):
+    return library().moe_combine(y, slots, weights, out)
+
+
+def mxq_moe_combine_grad(g, y, source, slots, weights):
+    return library().moe_combine_grad(g, y, source, slots, weights)
 
 
 def mxq_scale_bytes(rows, K, layout="compact"):

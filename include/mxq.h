@@ -300,6 +300,129 @@ MXQ_API mxq_status mxq_quantize_export_mxfp8(const void* x, mxq_dtype dt, int64_
                                              uint8_t* data, uint8_t* scales, mxq_mxfp8_components* out,
                                              cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The FP8 linear layer on 128x128 blockwise weights, and the mixture-of-
+ * experts layer around it (TE PR #3264, "Test results (B200)" and "Known
+ * limitations": the blockwise weights feed FP8 matrix products; its grouped
+ * linear layers hold one such weight per expert).
+ * ------------------------------------------------------------------------ */
+
+/* Activations and gradients to FP8, one power-of-two scale per 128 elements.
+ * Blocks run along the rows (1x128: elements [128j, min(128j+128, K)) of a
+ * row) or down the columns (128x1: rows [128i, min(128i+128, out_rows)) of a
+ * column).  For a block with largest magnitude amax, s = ceil(log2(amax/448))
+ * clamped to [-127, 127] (-127 for a zero block), code s + 127, payloads
+ * RTNE_E4M3(x / 2^s), subnormals included (never saturating).  A block that
+ * holds a NaN or an Inf has code 0xFF and payloads 0x7F.
+ *   x:      [rows, ldx] bf16 or fp32.
+ *   index:  NULL (out_rows == rows), or device int32 [out_rows]: output row i
+ *           is row index[i] / index_div of x; a negative index, or one that
+ *           leaves x, gives a row of zeros.  With index = the `source` of
+ *           mxq_moe_sort and index_div = topk this takes tokens to the
+ *           experts' order and quantizes them in one pass.
+ *   data:   [out_rows, K] E4M3 bytes, contiguous.
+ *   scales: uint8 [out_rows, ceil(K/128)] (1x128), or
+ *           [ceil(out_rows/128), K] (128x1).
+ * Errors: INVALID_ARG, UNSUPPORTED_DTYPE. */
+MXQ_API mxq_status mxq_fp8_quant_1x128(const void* x, mxq_dtype dt, int64_t rows, int64_t K, int64_t ldx,
+                                       const int32_t* index, int32_t index_div, int64_t out_rows, uint8_t* data,
+                                       uint8_t* scales, cudaStream_t stream);
+MXQ_API mxq_status mxq_fp8_quant_128x1(const void* x, mxq_dtype dt, int64_t rows, int64_t K, int64_t ldx,
+                                       const int32_t* index, int32_t index_div, int64_t out_rows, uint8_t* data,
+                                       uint8_t* scales, cudaStream_t stream);
+
+/* The three matrix products of a linear layer y = x W^T with x [M, K] and W
+ * [N, K]; g is the gradient of y.
+ *   FWD:   out [M, N] = x W^T    a = x [M, K], 1x128 scales; b = W, tile scales
+ *   DGRAD: out [M, K] = g W      a = g [M, N], 1x128 scales; b = W, tile scales
+ *   WGRAD: out [N, K] = g^T x    a = g [M, N], 128x1 scales; b = x [M, K], 128x1 scales */
+typedef enum { MXQ_MATMUL_FWD = 0, MXQ_MATMUL_DGRAD = 1, MXQ_MATMUL_WGRAD = 2 } mxq_matmul_dir;
+
+typedef struct {
+    mxq_matmul_dir dir;
+    int64_t M, N, K;       /* each 0 .. 2^31 - 1 */
+    const uint8_t* a;      /* E4M3 bytes, row r at a + r*lda */
+    int64_t lda;
+    const uint8_t* a_scales; /* UE8M0 codes, contiguous: [M, ceil(K/128)] (FWD), [M, ceil(N/128)] (DGRAD),
+                                [ceil(M/128), N] (WGRAD) */
+    const uint8_t* b;      /* E4M3 bytes, row r at b + r*ldb; a stack of weights is E*N such rows */
+    int64_t ldb;
+    const void* b_scales;  /* FWD, DGRAD: fp32 [ceil(N/128), ceil(K/128)] tile scales, powers of two as
+                              mxq_fp8_block128_direct writes them (any other value makes its tile NaN);
+                              WGRAD: UE8M0 codes [ceil(M/128), K] */
+    void* out;             /* bf16 or fp32 (out_dt), row r at out + r*ldo elements */
+    mxq_dtype out_dt;
+    int64_t ldo;
+    /* Experts (offsets != NULL): rows [offsets[e], offsets[e+1]) of a (and, for WGRAD, of b) belong to
+     * expert e, which has the weight W[e] of a stack [E, N, K] and tile scales [E, ceil(N/128),
+     * ceil(K/128)].  FWD and DGRAD: every row is multiplied by its own expert's weight, rows outside
+     * every expert's come out as zero.  WGRAD: out is a stack of E gradients [E, N, K] (row stride
+     * ldo), expert e's from its own rows alone; the offsets must be multiples of 128 (align = 128 of
+     * mxq_moe_sort), so that no 128x1 block is shared, and a lower offset is rounded up to one.
+     * offsets is device int32 [E + 1]; values are clamped into 0..M and to be non-decreasing. */
+    const int32_t* offsets;
+    int64_t E;             /* 1 .. 1024 with offsets, ignored without */
+} mxq_fp8_product;
+
+/* out = the product described by p, accumulated in fp32 and rounded once
+ * (round to nearest even) to out_dt.  The scales are applied as exact powers
+ * of two to the products of each 128-block.  A block whose code is 0xFF, and
+ * a payload NaN, make the sums that they enter NaN.  Results do not depend
+ * on the order in which blocks of the grid run.
+ * Rows whose starts are not 16-byte aligned (lda, ldb or the pointers) are
+ * first copied into `workspace`, mxq_fp8_matmul_workspace(p) bytes of device
+ * memory (0 for aligned operands; NULL is then allowed), 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED_DTYPE, BUFFER_TOO_SMALL (workspace). */
+MXQ_API mxq_status mxq_fp8_matmul(const mxq_fp8_product* p, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+MXQ_API size_t mxq_fp8_matmul_workspace(const mxq_fp8_product* p);
+
+/* Tokens sorted by expert.  ids [tokens, topk] are the experts that a router
+ * chose; choice c = t*topk + j has a row in the sorted order.  Experts'
+ * rows are consecutive, in the order of c within an expert, and each expert's
+ * part is rounded up to a multiple of `align` rows.  An id outside
+ * 0..experts-1 is a dropped choice without a row.
+ *   offsets: int32 [experts + 1], where each part begins; the last is the end.
+ *   source:  int32 [mxq_moe_capacity(...)]: the choice at each row, -1 where
+ *            there is none (the rounding, and behind the last part).
+ *   slots:   int32 [tokens, topk]: the row of each choice, -1 if dropped.
+ *   workspace: mxq_moe_sort_workspace(...) bytes, 4-byte aligned.
+ * tokens*topk and the capacity fit in int32; experts 1..2048; align >= 1.
+ * Errors: INVALID_ARG, BUFFER_TOO_SMALL (workspace). */
+MXQ_API mxq_status mxq_moe_sort(const int32_t* ids, int64_t tokens, int64_t topk, int64_t experts, int64_t align,
+                                int32_t* offsets, int32_t* source, int32_t* slots, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+/* tokens*topk + min(experts, tokens*topk)*(align - 1). */
+MXQ_API int64_t mxq_moe_capacity(int64_t tokens, int64_t topk, int64_t experts, int64_t align);
+MXQ_API size_t mxq_moe_sort_workspace(int64_t tokens, int64_t topk, int64_t experts);
+
+/* Tokens to the sorted order: out[r] = x[source[r] / topk], zeros where
+ * source[r] is negative or leaves x.  x [tokens, ldx], out [rows, H]
+ * contiguous, both dt. */
+MXQ_API mxq_status mxq_moe_dispatch(const void* x, mxq_dtype dt, int64_t tokens, int64_t H, int64_t ldx,
+                                    const int32_t* source, int64_t topk, int64_t rows, void* out,
+                                    cudaStream_t stream);
+
+/* Rows back to their tokens: out[t] = sum_j weights[t, j] * y[slots[t, j]],
+ * summed in fp32 in the order of j and rounded once; slots outside 0..rows-1
+ * add nothing (their rows are not read: 0 * NaN does not arise).  weights
+ * fp32 [tokens, topk], or NULL for weights of one, which is the gradient of
+ * mxq_moe_dispatch.  y [rows, ldy], out [tokens, H] contiguous, both dt. */
+MXQ_API mxq_status mxq_moe_combine(const void* y, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldy,
+                                   const int32_t* slots, const float* weights, int64_t tokens, int64_t topk, void* out,
+                                   cudaStream_t stream);
+
+/* Gradient of mxq_moe_combine for the gradient g of its output:
+ *   d_rows[slots[t, j]] = weights[t, j] * g[t], zeros where source is -1;
+ *   d_weights[t, j] = <g[t], y[slots[t, j]]> in fp32, 0 for a dropped choice.
+ * source and slots are those of one mxq_moe_sort.  g [tokens, ldg], y [rows,
+ * ldy], d_rows [rows, H] contiguous, all dt; d_weights fp32 [tokens, topk].
+ * Errors of the three: INVALID_ARG, UNSUPPORTED_DTYPE. */
+MXQ_API mxq_status mxq_moe_combine_grad(const void* g, const void* y, mxq_dtype dt, int64_t tokens, int64_t topk,
+                                        int64_t rows, int64_t H, int64_t ldg, int64_t ldy, const int32_t* source,
+                                        const int32_t* slots, const float* weights, void* d_rows, float* d_weights,
+                                        cudaStream_t stream);
+
 /* Static description of a status code. */
 MXQ_API const char* mxq_status_string(mxq_status s);
 
