@@ -1,125 +1,571 @@
-// mxq_matmul.cu -- products of block-scaled FP8 operands:
+// mxq_matmul.cu -- products of block-scaled FP8 operands on the tensor cores:
 //   out[i, j] = sum_b 2^(sa(i, b) + sb(j, b)) sum_{k in block b} A[i, k] B[j, k]
 // with blocks of 128 along the depth, accumulated in fp32.
+//
+// Every scale of this library is a power of two, so tcgen05.mma's block
+// scaling (kind::mxf8f6f4, one UE8M0 byte per 32 elements of depth) applies
+// it inside the instruction: the four 32-deep instructions of a 128-block name
+// the same byte.  Tile scales (one per 128x128 weights) become that byte for
+// 128 rows.  Nothing is rescaled in registers and the accumulator stays in
+// tensor memory from the first block to the last.
+//
+// An operand's depth runs either along the rows in memory or across them
+// (gradients); both are what one TMA box of 128 bytes x 128 and one matrix
+// descriptor describe, so all three products of a linear layer are one kernel.
+//
+// One thread block (or a pair of them, on two SMs) is a pipeline of warps:
+//   warp 0     TMA: boxes of both operands, 128 deep, into a ring of stages
+//   warp 1     one thread issues scale copies and MMAs
+//   warp 2, 3  gather the scale bytes of four blocks (512 of depth) of each operand
+//   warps 4-7  take finished sums out of tensor memory, round and store them
+// Blocks walk over their tiles, so that loads and MMAs of the next tile run
+// while the last one is being stored.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
+#include "mxq_tcgen05.cuh"
 
 namespace mxq {
 namespace {
 
-constexpr int kNaNScale = 1 << 20;
+constexpr int kThreads = 256;
+constexpr int kRing = 4;  // scale buffers
 
-// Exponent of the scale of row i and depth block kb.
-__device__ __forceinline__ int operand_scale(const MatOperand& o, int64_t e, int64_t i, int64_t kb) {
-    if (o.tiles) {
-        const uint32_t t = static_cast<const uint32_t*>(o.scales)[e * o.s_expert + (i >> 7) * o.s_row + kb * o.s_kb];
-        if (t == 0x00400000u) return -127;
-        const bool power = (t & 0x7FFFFFu) == 0u && t - 1u < 0x7F7FFFFFu;
-        return power ? (int)(t >> 23) - 127 : kNaNScale;
+// The operand whose rows are the accumulator's lanes is called P, the one
+// whose rows are its columns Q.
+struct ScaleSource {
+    const void* base;
+    int64_t s_row, s_kb, s_expert;
+    int rows;
+    bool tiles;
+    bool words;  // four consecutive bytes of a row can be read as one aligned word
+};
+
+enum RaggedBy { kNone, kRowsOfP, kRowsOfQ, kDepth };
+
+struct Problem {
+    ScaleSource sp, sq;
+    const int32_t* offsets;
+    void* out;
+    int64_t ldo, out_expert;
+    int E, depth;
+    int p_rows, q_rows, p_tiles, q_tiles;
+    int ragged;
+    bool p_mn, q_mn, p_expert, q_expert;  // the operand's major; whether it is a stack of experts'
+    bool out_bf16;
+    bool wide;  // 32-byte stores of the output's rows are aligned
+};
+
+struct Tile {
+    int e, p0, p_end, q0, q_end;
+    int kb0, kb1;
+};
+
+// Rows (or depth) of the experts: bound[e] .. bound[e + 1], and the tiles in front of expert e.
+struct Ragged {
+    int *bound, *tiles;
+};
+
+// Warp-wide: clamps the offsets into 0..limit and to be non-decreasing, and counts tiles of `step`.
+__device__ void read_offsets(const Problem& g, int limit, int step, Ragged r) {
+    const int lane = threadIdx.x & 31;
+    int top = 0, sum = 0;
+    for (int i0 = 0; i0 <= g.E; i0 += 32) {
+        const int i = i0 + lane;
+        int v = i <= g.E ? min(max(g.offsets[i], 0), limit) : 0;
+        if (g.ragged == kDepth) v = min((v + 127) / 128 * 128, limit);
+        v = max(v, top);
+        for (int d = 1; d < 32; d *= 2) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, v, d);
+            if (lane >= d) v = max(v, up);
+        }
+        const int prev_lane = __shfl_up_sync(0xFFFFFFFFu, v, 1);
+        const int prev = lane ? prev_lane : top;
+        int n = i > 0 && i <= g.E ? (v - prev + step - 1) / step : 0;
+        for (int d = 1; d < 32; d *= 2) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, n, d);
+            if (lane >= d) n += up;
+        }
+        if (i <= g.E) {
+            r.bound[i] = v;
+            r.tiles[i] = sum + n;
+        }
+        top = __shfl_sync(0xFFFFFFFFu, v, 31);
+        sum += __shfl_sync(0xFFFFFFFFu, n, 31);
     }
-    const int c = static_cast<const uint8_t*>(o.scales)[i * o.s_row + kb * o.s_kb];
-    return c == 255 ? kNaNScale : c - 127;
 }
 
-__device__ __forceinline__ float operand_value(const MatOperand& o, int64_t e, int64_t i, int64_t k) {
-    const uint8_t* at = o.data + e * o.expert + (o.mn ? k * o.ld + i : i * o.ld + k);
-    return __uint_as_float(decode_scaled<false>(*at, 0x3F800000u));
+// Tiles are numbered so that those in flight together share operands: groups
+// of eight tiles of P are walked along Q; within an expert the few tiles of
+// its rows come first.
+template <int PT, int QT>
+__device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t) {
+    Tile c;
+    c.e = 0;
+    c.kb0 = 0;
+    c.kb1 = (g.depth + 127) >> 7;
+    if (g.ragged == kRowsOfP || g.ragged == kRowsOfQ) {
+        const int others = g.ragged == kRowsOfP ? g.q_tiles : g.p_tiles;
+        int lo = 0, hi = g.E - 1;  // the last expert whose tiles begin at or before t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (r.tiles[mid] * others <= t)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        c.e = lo;
+        t -= r.tiles[lo] * others;
+        const int n = r.tiles[lo + 1] - r.tiles[lo];
+        const int x = t % n, y = t / n;
+        if (g.ragged == kRowsOfP) {
+            c.p0 = r.bound[lo] + x * PT;
+            c.p_end = r.bound[lo + 1];
+            c.q0 = y * QT;
+            c.q_end = g.q_rows;
+        } else {
+            c.q0 = r.bound[lo] + x * QT;
+            c.q_end = r.bound[lo + 1];
+            c.p0 = y * PT;
+            c.p_end = g.p_rows;
+        }
+        return c;
+    }
+    if (g.ragged == kDepth) {
+        const int per = g.p_tiles * g.q_tiles;
+        c.e = t / per;
+        t -= c.e * per;
+        c.kb0 = (r.bound[c.e] + 127) >> 7;  // only `depth` itself is no multiple of 128: nothing begins there
+        c.kb1 = (r.bound[c.e + 1] + 127) >> 7;
+    }
+    constexpr int G = 8;
+    const int group = t / (G * g.q_tiles), first = group * G, n = min(G, g.p_tiles - first);
+    t -= group * G * g.q_tiles;
+    c.p0 = (first + t % n) * PT;
+    c.q0 = t / n * QT;
+    c.p_end = g.p_rows;
+    c.q_end = g.q_rows;
+    return c;
 }
 
-// v * 2^e
-__device__ __forceinline__ float times_power(float v, int e) {
-    if (e >= kNaNScale / 2) return __uint_as_float(0x7FC00000u);
-    const int h = e / 2;  // two powers, each a normal number: |e| <= 254
-    return v * __uint_as_float((uint32_t)(h + 127) << 23) * __uint_as_float((uint32_t)(e - h + 127) << 23);
+// Scale bytes of blocks kb .. kb + 3 of one row; 0 where there is none.
+__device__ __forceinline__ uint32_t scale_bytes4(const ScaleSource& s, int e, int row, int kb, int kb_end) {
+    if (row >= s.rows) return 0;
+    uint32_t w = 0;
+    if (s.tiles) {
+        const uint32_t* p = static_cast<const uint32_t*>(s.base) + e * s.s_expert + (row >> 7) * s.s_row;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (kb + j < kb_end) {
+                const uint32_t t = p[(kb + j) * s.s_kb];
+                // 2^c has the byte c + 127: the exponent field, and 0 for the subnormal 2^-127; all else is NaN
+                const uint32_t c = (t & 0x7FFFFFu) == 0u && t - 1u < 0x7F7FFFFFu ? t >> 23 : t == 0x00400000u ? 0u : 255u;
+                w |= c << (8 * j);
+            }
+        return w;
+    }
+    const uint8_t* p = static_cast<const uint8_t*>(s.base) + (int64_t)row * s.s_row;
+    if (s.words) return *reinterpret_cast<const uint32_t*>(p + kb);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (kb + j < kb_end) w |= (uint32_t)p[(kb + j) * s.s_kb] << (8 * j);
+    return w;
 }
 
-__device__ __forceinline__ void store_out(const MatmulArgs& g, int64_t at, float v) {
-    uint32_t u = __float_as_uint(v);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0x7FC00000u;
+__device__ __forceinline__ uint32_t canonical(uint32_t u) { return (u & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FC00000u : u; }
+
+__device__ __forceinline__ void store_one(const Problem& g, int64_t at, uint32_t u) {
+    u = canonical(u);
     if (g.out_bf16)
         static_cast<uint16_t*>(g.out)[at] = (uint16_t)bf16_rne(u);
     else
         static_cast<uint32_t*>(g.out)[at] = u;
 }
 
-// 64x64 outputs per block of 256 threads, 4x4 each, depth in steps of 16 through shared memory.
-__global__ void __launch_bounds__(256) matmul_kernel(MatmulArgs g) {
-    __shared__ float As[16][65], Bs[16][65];
-    int64_t e = 0, i0 = (int64_t)blockIdx.y * 64, i_end = g.a.rows, k0 = 0, k_end = g.depth, out0 = 0;
-    bool zero = false;
-    if (g.grouping == Grouping::ROWS) {
-        // blocks of 64 rows of the experts in turn; the rows behind the last expert form one more part, of zeros
-        int64_t tile = blockIdx.y, lo = 0;
-        for (e = 0; e <= g.E; ++e) {
-            int64_t hi = e < g.E ? max(lo, min((int64_t)g.offsets[e + 1], g.a.rows)) : g.a.rows;
-            if (e == 0) lo = max((int64_t)0, min((int64_t)g.offsets[0], g.a.rows)), hi = max(lo, hi);
-            const int64_t n = (hi - lo + 63) / 64;
-            if (tile < n) {
-                i0 = lo + tile * 64;
-                i_end = hi;
-                break;
-            }
-            tile -= n;
-            lo = hi;
-        }
-        if (e > g.E) {  // rows in front of the first expert
-            if (tile > 0) return;
-            i0 = 0;
-            i_end = max((int64_t)0, min((int64_t)g.offsets[0], g.a.rows));
-        }
-        zero = e >= g.E;
-    } else if (g.grouping == Grouping::DEPTH) {
-        e = blockIdx.z;
-        int64_t lo = 0;
-        for (int64_t x = 0; x <= e + 1; ++x) {
-            const int64_t v = max(lo, min((int64_t)g.offsets[x], g.depth));
-            if (x <= e) k0 = v;
-            if (x == e + 1) k_end = v;
-            lo = v;
-        }
-        k0 = (k0 + 127) / 128 * 128;
-        out0 = e * g.out_expert;
+// QT: columns of the accumulator.  CG 2: a pair of blocks, 256 lanes, each
+// holding half of Q's rows; the output's rows are P's.  CG 1: 128 lanes; the
+// output's rows are Q's (few tokens, many features).  SPLIT: the blocks of a
+// cluster share a tile, each with a part of the depth, and add their sums
+// through shared memory.
+template <int QT, int CG, bool SPLIT>
+struct Shape {
+    static constexpr int kQRows = QT / CG;                           // rows of Q that a block loads
+    static constexpr int kPBytes = 128 * 128, kQBytes = kQRows * 128;
+    static constexpr int kStageBytes = kPBytes + kQBytes;
+    static constexpr int kStages = CG == 2 ? 6 : QT == 128 ? 6 : QT == 64 ? 4 : 5;
+    static constexpr int kQAtoms = QT <= 128 ? 1 : QT / 128;         // 128 scales each
+    static constexpr int kScaleBytes = 512 * (1 + kQAtoms);
+    static constexpr int kScaleColumns = 4 * (1 + kQAtoms);
+    // Two accumulators.  Two of 256 columns and the scales exceed the 512 columns, so
+    // there the second begins 64 columns before the first one's end and the
+    // shared ones are taken out first.
+    static constexpr int kAcc1 = QT == 256 ? 192 : QT;
+    static constexpr int kScaleAt = QT == 256 ? 448 : 2 * QT;
+    static constexpr int kUsed = kScaleAt + kRing * kScaleColumns;
+    static constexpr int kColumns = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static constexpr int kTranspose = CG == 2 ? 4 * 32 * 33 * 4 : 0;
+    static constexpr int kBarriers = 2 * kStages + 2 * kRing + 4 + 1;
+    static size_t smem(int E) {
+        return 1024 + (size_t)kStages * kStageBytes + (size_t)kRing * kScaleBytes + kTranspose + 8 * kBarriers + 16 +
+               (E ? 8 * (size_t)(E + 1) : 0);
     }
-    const int64_t eb = g.grouping == Grouping::ROWS ? min(e, g.E - 1) : 0;
-    for (; i0 < i_end; i0 += zero ? 64 : i_end) {  // zeros: every block of rows in turn, else one
-        const int64_t j0 = (int64_t)blockIdx.x * 64;
-        const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-        float acc[4][4] = {};
-        for (int64_t kb = k0; !zero && kb < k_end; kb = (kb / 128 + 1) * 128) {
-            float sum[4][4] = {};
-            const int64_t kb_end = min(k_end, (kb / 128 + 1) * 128);
-            for (int64_t k = kb; k < kb_end; k += 16) {
-                for (int q = threadIdx.x; q < 1024; q += 256) {
-                    const int r = q / 16, c = q % 16;
-                    As[c][r] = i0 + r < i_end && k + c < kb_end ? operand_value(g.a, 0, i0 + r, k + c) : 0.0f;
-                    Bs[c][r] = j0 + r < g.b.rows && k + c < kb_end ? operand_value(g.b, eb, j0 + r, k + c) : 0.0f;
-                }
-                __syncthreads();
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) sum[y][x] = fmaf(As[c][ty + 16 * y], Bs[c][tx + 16 * x], sum[y][x]);
-                __syncthreads();
+};
+
+template <int QT, int CG, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    matmul_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                  const __grid_constant__ Problem g, const uint32_t idesc, const int tile_count) {
+    using S = Shape<QT, CG, SPLIT>;
+    constexpr int PT = 128 * CG;
+    extern __shared__ uint8_t raw[];
+    uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* scales = stages + S::kStages * S::kStageBytes;
+    float* transpose = reinterpret_cast<float*>(scales + kRing * S::kScaleBytes);
+    uint8_t* bars = reinterpret_cast<uint8_t*>(transpose) + S::kTranspose;
+    volatile int* gave_up = reinterpret_cast<volatile int*>(bars + 8 * S::kBarriers);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 8 * S::kBarriers + 4);
+    Ragged rag;
+    rag.bound = reinterpret_cast<int*>(bars + 8 * S::kBarriers + 16);
+    rag.tiles = rag.bound + g.E + 1;
+
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, sc_full = empty + 8 * S::kStages,
+                   sc_empty = sc_full + 8 * kRing, acc_full = sc_empty + 8 * kRing, acc_empty = acc_full + 16,
+                   drained = acc_empty + 16;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 || SPLIT ? cluster_rank() : 0;
+    const uint32_t pair_rank = CG == 2 ? rank : 0;
+    const bool leader = pair_rank == 0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_map(&p_map);
+            prefetch_map(&q_map);
+            for (int i = 0; i < S::kStages; ++i) {
+                mbar_init(full + 8 * i, 1);
+                mbar_init(empty + 8 * i, 1);
             }
-            for (int y = 0; y < 4; ++y)
-                for (int x = 0; x < 4; ++x) {
-                    const int64_t i = i0 + ty + 16 * y, j = j0 + tx + 16 * x;
-                    if (i < i_end && j < g.b.rows)
-                        acc[y][x] += times_power(sum[y][x], operand_scale(g.a, 0, i, kb >> 7) +
-                                                                operand_scale(g.b, eb, j, kb >> 7));
-                }
+            for (int i = 0; i < kRing; ++i) {
+                mbar_init(sc_full + 8 * i, 2 * CG);
+                mbar_init(sc_empty + 8 * i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(acc_full + 8 * i, 1);
+                mbar_init(acc_empty + 8 * i, 4 * CG);
+            }
+            mbar_init(drained, 1);
+            *gave_up = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-        for (int y = 0; y < 4; ++y)
-            for (int x = 0; x < 4; ++x) {
-                const int64_t i = i0 + ty + 16 * y, j = j0 + tx + 16 * x;
-                if (i < i_end && j < g.b.rows) store_out(g, out0 + i * g.ldo + j, acc[y][x]);
+    } else if (warp == 1) {
+        tmem_alloc<CG>(smem_u32(tmem_at), S::kColumns);
+    } else if (warp == 2 && g.ragged != kNone) {
+        read_offsets(g, g.ragged == kDepth ? g.depth : g.ragged == kRowsOfP ? g.p_rows : g.q_rows,
+                     g.ragged == kRowsOfP ? PT : QT, rag);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2 || SPLIT) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    int tiles = tile_count;
+    if (g.ragged == kRowsOfP) tiles = rag.tiles[g.E] * g.q_tiles;
+    if (g.ragged == kRowsOfQ) tiles = rag.tiles[g.E] * g.p_tiles;
+    const int span = SPLIT ? (int)(gridDim.x) : (int)gridDim.x / CG;  // SPLIT: one tile per cluster
+    int split = 1, first_tile = (int)blockIdx.x / CG;
+    if constexpr (SPLIT) {
+        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+        first_tile = (int)blockIdx.x / split;
+    }
+    // Blocks of depth of a tile that this block takes: all, or its share of the groups of four.
+    auto depth_of = [&](const Tile& c, int& kb0, int& kb1) {
+        kb0 = c.kb0;
+        kb1 = c.kb1;
+        if constexpr (SPLIT) {
+            const int quads = (kb1 - kb0 + 3) / 4;
+            const int q0 = (int)((int64_t)quads * (int)rank / split), q1 = (int)((int64_t)quads * ((int)rank + 1) / split);
+            kb1 = min(kb1, kb0 + 4 * q1);
+            kb0 = kb0 + 4 * q0;
+        }
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- loads
+        if (lane == 0) {
+            int n = 0;  // boxes' ring position
+            bool ok = true;
+            for (int t = first_tile; ok && t < tiles; t += span) {
+                const Tile c = tile_at<PT, QT>(g, rag, t);
+                int kb0, kb1;
+                depth_of(c, kb0, kb1);
+                const int p_row = c.p0 + 128 * (int)pair_rank, q_row = c.q0 + S::kQRows * (int)pair_rank;
+                const int pe = g.p_expert ? c.e : 0, qe = g.q_expert ? c.e : 0;
+                for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                    const int s = n % S::kStages, round = n / S::kStages;
+                    if (round > 0 && !mbar_wait(empty + 8 * s, (round - 1) & 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_expect_tx(full + 8 * s, CG * S::kStageBytes);
+                    const uint32_t at = smem_u32(stages + s * S::kStageBytes);
+                    if (g.p_mn)
+                        tma_load<CG == 2>(at, &p_map, full + 8 * s, p_row, kb * 128, pe);
+                    else
+                        tma_load<CG == 2>(at, &p_map, full + 8 * s, kb * 128, p_row, pe);
+                    if (g.q_mn)
+                        tma_load<CG == 2>(at + S::kPBytes, &q_map, full + 8 * s, q_row, kb * 128, qe);
+                    else
+                        tma_load<CG == 2>(at + S::kPBytes, &q_map, full + 8 * s, kb * 128, q_row, qe);
+                }
             }
+            if (!ok && leader) {  // copies in flight land before the block ends
+                volatile int again = 0;
+                for (int i = n < S::kStages ? 0 : n - S::kStages; i < n; ++i)
+                    mbar_wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1, &again);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ----------------------------------------------------------- MMAs
+        if (leader && lane == 0) {
+            int n = 0, quad = 0, it = 0;
+            bool ok = true;
+            for (int t = first_tile; ok && t < tiles; t += span) {
+                const Tile c = tile_at<PT, QT>(g, rag, t);
+                int kb0, kb1;
+                depth_of(c, kb0, kb1);
+                if (kb0 >= kb1) continue;
+                // the accumulator that this tile writes has been taken out
+                if constexpr (QT == 256) {
+                    ok = it < 1 || mbar_wait(acc_empty, (it - 1) & 1, gave_up);
+                } else {
+                    ok = it < 2 || mbar_wait(acc_empty + 8 * (it & 1), ((it >> 1) - 1) & 1, gave_up);
+                }
+                tc_fence_after();
+                const uint32_t acc = tmem + (it & 1) * S::kAcc1;
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++n) {
+                    const int s = n % S::kStages, j = (kb - kb0) & 3;
+                    const int r = quad % kRing;
+                    const uint32_t sfp = tmem + S::kScaleAt + r * S::kScaleColumns, sfq = sfp + 4;
+                    if (j == 0) {
+                        ok = mbar_wait(sc_full + 8 * r, (quad / kRing) & 1, gave_up);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t from = smem_u32(scales + r * S::kScaleBytes);
+#pragma unroll
+                        for (int a = 0; a <= S::kQAtoms; ++a) copy_scales<CG>(sfp + 4 * a, desc_scales(from + 512 * a));
+                    }
+                    ok = mbar_wait(full + 8 * s, (n / S::kStages) & 1, gave_up);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = smem_u32(stages + s * S::kStageBytes);
+                    const uint64_t dp = desc_swizzle128(at, g.p_mn), dq = desc_swizzle128(at + S::kPBytes, g.q_mn);
+                    // 32 of depth: 32 bytes along a row, or 32 rows of 128 bytes
+                    const uint64_t step_p = g.p_mn ? 4096 >> 4 : 32 >> 4, step_q = g.q_mn ? 4096 >> 4 : 32 >> 4;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_block_scaled<CG>(acc, dp + k * step_p, dq + k * step_q, idesc | scale_byte(j), sfp, sfq,
+                                             kb > kb0 || k > 0);
+                    mma_commit<CG>(empty + 8 * s);
+                    if (j == 3 || kb + 1 == kb1) {
+                        mma_commit<CG>(sc_empty + 8 * r);
+                        ++quad;
+                    }
+                }
+                if (!ok) break;
+                mma_commit<CG>(acc_full + 8 * (it & 1));
+                ++it;
+            }
+            if (!ok) {  // what has been issued ends before the block does
+                volatile int again = 0;
+                mma_commit<CG>(drained);
+                mbar_wait(drained, 0, &again);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // --------------------------------------------------------- scales
+        const bool is_p = warp == 2;
+        const ScaleSource& src = is_p ? g.sp : g.sq;
+        constexpr int kWords = QT >= 128 ? QT / 32 : 4;
+        const int words = is_p ? 4 : kWords, rows = is_p ? 128 : QT;
+        int quad = 0;
+        bool ok = true;
+        const uint32_t arrive_at = CG == 2 ? map_rank(sc_full, 0) : 0;
+        for (int t = first_tile; ok && t < tiles; t += span) {
+            const Tile c = tile_at<PT, QT>(g, rag, t);
+            int kb0, kb1;
+            depth_of(c, kb0, kb1);
+            const int row0 = is_p ? c.p0 + 128 * (int)pair_rank : c.q0;
+            uint32_t w[kWords];
+            auto read = [&](int kb) {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i)
+                    w[i] = i < words && 32 * i + lane < rows && kb < kb1
+                               ? scale_bytes4(src, c.e, row0 + 32 * i + lane, kb, c.kb1)
+                               : 0u;
+            };
+            read(kb0);
+            for (int kb = kb0; kb < kb1; kb += 4, ++quad) {
+                const int r = quad % kRing, round = quad / kRing;
+                if (round > 0 && !mbar_wait(sc_empty + 8 * r, (round - 1) & 1, gave_up)) {
+                    ok = false;
+                    break;
+                }
+                // row i of 128 has its four bytes at 16 (i % 32) + 4 (i / 32)
+                uint8_t* to = scales + r * S::kScaleBytes + (is_p ? 0 : 512);
+#pragma unroll
+                for (int a = 0; a < kWords / 4; ++a)
+                    if (4 * a < words)
+                        *reinterpret_cast<uint4*>(to + 512 * a + 16 * lane) =
+                            make_uint4(w[4 * a], w[4 * a + 1], w[4 * a + 2], w[4 * a + 3]);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_cluster(arrive_at + 8 * r);
+                    else
+                        mbar_arrive(sc_full + 8 * r);
+                }
+                read(kb + 4);  // on its way while the ring drains
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+    } else {
+        // --------------------------------------------------------- results
+        const int band = warp & 3;  // lanes 32 band .. of tensor memory are this warp's
+        const uint32_t lanes = (uint32_t)(32 * band) << 16;
+        const uint32_t release_at = CG == 2 ? map_rank(acc_empty, 0) : 0;
+        constexpr int W = QT < 32 ? QT : 32;  // columns at a time
+        constexpr int kChunks = QT / W;
+        int it = 0;
+        bool ok = true;
+        for (int t = first_tile; t < tiles; t += span) {
+            const Tile c = tile_at<PT, QT>(g, rag, t);
+            int kb0, kb1;
+            depth_of(c, kb0, kb1);
+            const bool none = kb0 >= kb1;  // a sum of nothing
+            const int a = it & 1;
+            if (!none) {
+                ok = ok && mbar_wait(acc_full + 8 * a, (it >> 1) & 1, gave_up);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                tc_fence_after();
+                ++it;
+            }
+            const int64_t base = g.ragged == kDepth ? c.e * g.out_expert : 0;
+            const int lane_row = c.p0 + 128 * (int)pair_rank + 32 * band + lane;
+#pragma unroll 1
+            for (int x = 0; x < kChunks; ++x) {
+                // the columns that the two accumulators share come first (the second one's first, the first
+                // one's last): only they hold up the next tile
+                const int chunk = QT == 256 && a == 0 ? (x + kChunks - 2) % kChunks : x;
+                uint32_t v[W];
+                if (!none && ok) {
+                    tmem_ld(v, tmem + lanes + a * S::kAcc1 + chunk * W);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) v[i] = none ? 0u : 0x7FC00000u;
+                }
+                if (!none && x == (QT == 256 ? 1 : kChunks - 1)) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int bar = QT == 256 ? 0 : a;
+                        if constexpr (CG == 2)
+                            mbar_arrive_cluster(release_at + 8 * bar);
+                        else
+                            mbar_arrive(acc_empty + 8 * bar);
+                    }
+                }
+                if constexpr (SPLIT) {
+                    float* part = reinterpret_cast<float*>(stages);  // [QT][128]: every load and MMA is done
+#pragma unroll
+                    for (int i = 0; i < W; ++i) part[(chunk * W + i) * 128 + 32 * band + lane] = __uint_as_float(v[i]);
+                } else if constexpr (CG == 1) {
+                    // rows of the output are columns here: 32 lanes store neighbours
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const int row = c.q0 + chunk * W + i;
+                        if (row < c.q_end && lane_row < c.p_end) store_one(g, base + row * g.ldo + lane_row, v[i]);
+                    }
+                } else {
+                    const int col = c.q0 + chunk * W;
+                    if (g.wide && col + W <= c.q_end) {
+                        if (lane_row < c.p_end) {
+                            if (g.out_bf16) {
+                                uint16_t* to = static_cast<uint16_t*>(g.out) + base + lane_row * g.ldo + col;
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    uint32_t p[8];
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        p[i] = bf16_rne(canonical(v[16 * h + 2 * i])) |
+                                               (bf16_rne(canonical(v[16 * h + 2 * i + 1])) << 16);
+                                    st32(to + 16 * h, p);
+                                }
+                            } else {
+                                uint32_t* to = static_cast<uint32_t*>(g.out) + base + lane_row * g.ldo + col;
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    uint32_t p[8];
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) p[i] = canonical(v[8 * h + i]);
+                                    st32(to + 8 * h, p);
+                                }
+                            }
+                        }
+                    } else {
+                        // through shared memory, so that neighbouring lanes store neighbouring columns
+                        uint32_t* buf = reinterpret_cast<uint32_t*>(transpose) + band * (32 * 33);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) buf[lane * 33 + i] = v[i];
+                        __syncwarp();
+                        const int row0 = lane_row - lane, rows = min(32, c.p_end - row0);
+                        for (int i = 0; i < rows; ++i)
+                            if (col + lane < c.q_end) store_one(g, base + (row0 + i) * g.ldo + col + lane, buf[i * 33 + lane]);
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        // rows that belong to no expert
+        if (g.ragged == kRowsOfP || g.ragged == kRowsOfQ) {
+            const int rows = g.ragged == kRowsOfP ? g.p_rows : g.q_rows, n = g.ragged == kRowsOfP ? g.q_rows : g.p_rows;
+            const int front = rag.bound[0], behind = rag.bound[g.E];
+            for (int64_t i = blockIdx.x; i < front + (rows - behind); i += gridDim.x) {
+                const int64_t row = i < front ? i : behind + (i - front);
+                for (int j = threadIdx.x - 128; j < n; j += 128) store_one(g, row * g.ldo + j, 0u);
+            }
+        }
+    }
+
+    if constexpr (SPLIT) {
+        // every block adds a share of the columns, in the order of the ranks
+        cluster_sync();
+        if (first_tile < tiles) {
+            const Tile c = tile_at<PT, QT>(g, rag, first_tile);
+            const uint32_t part = smem_u32(stages);
+            const int row = c.p0 + (threadIdx.x & 127);
+            const int j1 = min(QT * ((int)rank + 1) / split, c.q_end - c.q0);
+            for (int j = QT * (int)rank / split + (threadIdx.x >> 7); j < j1; j += kThreads / 128) {
+                float sum = 0.0f;
+                for (int s = 0; s < split; ++s) sum += ld_cluster_f32(map_rank(part + (j * 128 + (threadIdx.x & 127)) * 4, s));
+                const int64_t base = g.ragged == kDepth ? c.e * g.out_expert : 0;
+                if (row < c.p_end) store_one(g, base + (int64_t)(c.q0 + j) * g.ldo + row, __float_as_uint(sum));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2 || SPLIT) cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<CG>(tmem, S::kColumns);
     }
 }
 
@@ -131,15 +577,138 @@ __global__ void __launch_bounds__(256) repack_kernel(const uint8_t* src, int64_t
     }
 }
 
+// ------------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Boxes of 128 bytes of a row by `box` rows of one operand, of each expert where it is a stack.
+bool make_map(CUtensorMap* map, const MatOperand& o, int64_t depth, int64_t E, int box) {
+    const int64_t inner = o.mn ? o.rows : depth, outer = o.mn ? depth : o.rows;
+    const int64_t ld = outer > 1 || o.expert ? o.ld : (inner + 15) / 16 * 16;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)(o.expert ? E : 1)};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)(o.expert ? o.expert : ld)};
+    const cuuint32_t boxes[3] = {128, (cuuint32_t)box, 1}, steps[3] = {1, 1, 1};
+    const EncodeTiled encode = encode_tiled();
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(o.data), dims, strides, boxes,
+                            steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+ScaleSource scale_source(const MatOperand& o, int64_t depth) {
+    ScaleSource s{};
+    s.base = o.scales;
+    s.s_row = o.s_row;
+    s.s_kb = o.s_kb;
+    s.s_expert = o.s_expert;
+    s.rows = (int)o.rows;
+    s.tiles = o.tiles;
+    s.words = !o.tiles && o.s_kb == 1 && o.s_row % 4 == 0 && reinterpret_cast<uintptr_t>(o.scales) % 4 == 0 &&
+              ceil_div(depth, 128) % 4 == 0;
+    return s;
+}
+
+template <int QT, int CG, bool SPLIT>
+cudaError_t launch(const MatmulArgs& m, const MatOperand& p, const MatOperand& q, int ragged, int split, cudaStream_t stream) {
+    using S = Shape<QT, CG, SPLIT>;
+    constexpr int PT = 128 * CG;
+    Problem g{};
+    g.sp = scale_source(p, m.depth);
+    g.sq = scale_source(q, m.depth);
+    g.offsets = m.offsets;
+    g.out = m.out;
+    g.ldo = m.ldo;
+    g.out_expert = m.out_expert;
+    g.E = (int)m.E;
+    g.depth = (int)m.depth;
+    g.p_rows = (int)p.rows;
+    g.q_rows = (int)q.rows;
+    g.p_tiles = (int)ceil_div(p.rows, PT);
+    g.q_tiles = (int)ceil_div(q.rows, QT);
+    g.ragged = ragged;
+    g.p_mn = p.mn;
+    g.q_mn = q.mn;
+    g.p_expert = p.expert != 0;
+    g.q_expert = q.expert != 0;
+    g.out_bf16 = m.out_bf16;
+    const int64_t es = m.out_bf16 ? 2 : 4;
+    g.wide = reinterpret_cast<uintptr_t>(m.out) % 32 == 0 && m.ldo * es % 32 == 0;
+    CUtensorMap pm, qm;
+    if (!make_map(&pm, p, m.depth, m.E, 128) || !make_map(&qm, q, m.depth, m.E, q.mn ? 128 : S::kQRows))
+        return cudaErrorInvalidValue;
+
+    int64_t tiles = (int64_t)g.p_tiles * g.q_tiles * (ragged == kDepth ? m.E : 1);
+    if (ragged == kRowsOfP || ragged == kRowsOfQ) {  // at most: every expert has a last, partial tile
+        const int64_t rows = ragged == kRowsOfP ? p.rows : q.rows, step = ragged == kRowsOfP ? PT : QT;
+        tiles = (rows / step + (m.E < rows ? m.E : rows)) * (ragged == kRowsOfP ? g.q_tiles : g.p_tiles);
+    }
+    if (tiles > INT64_C(0x3FFFFFFF)) return cudaErrorInvalidValue;
+    auto kernel = matmul_kernel<QT, CG, SPLIT>;
+    const size_t smem = S::smem((int)m.E);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = (unsigned)(CG == 2 ? 2 : split);
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    const int per_sm = CG == 2 || QT == 128 ? 1 : 2;  // what shared memory and tensor memory leave room for
+    const int64_t room = (int64_t)sm_count() * per_sm / CG;
+    const int64_t blocks = SPLIT ? tiles * split : (tiles < room ? tiles : room) * CG;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = CG == 2 || SPLIT ? 1 : 0;
+    const uint32_t idesc = instruction_desc(PT, QT, p.mn, q.mn);
+    return cudaLaunchKernelEx(&cfg, kernel, pm, qm, g, idesc, (int)tiles);
+}
+
 }  // namespace
 
-cudaError_t launch_matmul(const MatmulArgs& g, cudaStream_t s) {
-    dim3 grid((unsigned)ceil_div(g.b.rows, 64), (unsigned)ceil_div(g.a.rows, 64));
-    if (g.grouping == Grouping::ROWS) grid.y = (unsigned)(ceil_div(g.a.rows, 64) + g.E + 2);
-    if (g.grouping == Grouping::DEPTH) grid.z = (unsigned)g.E;
-    if (grid.y > 65535u) return cudaErrorInvalidValue;
-    matmul_kernel<<<grid, 256, 0, s>>>(g);
-    return cudaGetLastError();
+cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
+    const bool grouped = m.grouping == Grouping::ROWS;
+    const int ragged = m.grouping == Grouping::DEPTH ? kDepth : kNone;
+    cudaError_t e;
+    if (m.a.rows > 256 && m.b.rows > 128 && !(grouped && m.a.rows / m.E < 128)) {
+        e = launch<256, 2, false>(m, m.a, m.b, grouped ? kRowsOfP : ragged, 1, s);
+    } else {
+        // A's rows as columns
+        const int r = grouped ? kRowsOfQ : ragged;
+        const int64_t rows = grouped ? ceil_div(m.a.rows, m.E) : m.a.rows;
+        const int64_t qt = m.a.mn || rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
+        const int64_t tiles = ceil_div(m.b.rows, 128) * ceil_div(m.a.rows, qt), quads = ceil_div(m.depth, 512);
+        int split = 1;
+        if (r == kNone)
+            while (split < 8 && split * 2 <= quads && tiles * split * 2 <= 2 * sm_count()) split *= 2;
+        if (split > 1)
+            e = qt == 16   ? launch<16, 1, true>(m, m.b, m.a, r, split, s)
+                : qt == 32 ? launch<32, 1, true>(m, m.b, m.a, r, split, s)
+                : qt == 64 ? launch<64, 1, true>(m, m.b, m.a, r, split, s)
+                           : launch<128, 1, true>(m, m.b, m.a, r, split, s);
+        else
+            e = qt == 16   ? launch<16, 1, false>(m, m.b, m.a, r, 1, s)
+                : qt == 32 ? launch<32, 1, false>(m, m.b, m.a, r, 1, s)
+                : qt == 64 ? launch<64, 1, false>(m, m.b, m.a, r, 1, s)
+                           : launch<128, 1, false>(m, m.b, m.a, r, 1, s);
+    }
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_repack(const uint8_t* src, int64_t ld, int64_t rows, int64_t n, uint8_t* dst, int64_t ldd,

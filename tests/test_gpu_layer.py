@@ -380,6 +380,20 @@ def test_grouped_weight_gradient(mx, counts, N, K):
         close(out.t, want, S, max(room), dtype)
 
 
+@pytest.mark.parametrize("off", [[0, 200, 200], [0, 128, 200], [0, 0, 999], [-4, 100, 150]])
+def test_grouped_weight_gradient_clamps_and_rounds_offsets(mx, off):
+    rng = np.random.default_rng(23)
+    M, N, K = 200, 136, 140
+    g, gs = make_columns(rng, M, N)
+    x, xs = make_columns(rng, M, K)
+    gd, xd = ref.decode_columns(g, gs), ref.decode_columns(x, xs)
+    o = np.minimum(-(-ref.clamp_offsets(np.array(off), M) // 128) * 128, M)
+    want, S = np.zeros((2, N, K)), np.zeros((2, N, K))
+    for e in range(2):
+        want[e], S[e] = ref.product(gd[o[e]:o[e + 1]].T, xd[o[e]:o[e + 1]].T)
+    close(mx.fp8_matmul_wgrad(*map(bytes_dev, (g, gs, x, xs)), offsets=bytes_dev(np.int32(off))), want, S, M, F32)
+
+
 # -------------------------------------------------------------------- sort
 
 
