@@ -34,7 +34,9 @@ call writes nothing (for cached weights inside captured CUDA graphs).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 import threading
 from typing import NamedTuple, Optional
 
@@ -99,12 +101,12 @@ class MoeOrder(NamedTuple):
     slots: torch.Tensor    # int32 [tokens, topk], the row of each choice, -1 if dropped
 
 
-class _Product(ctypes.Structure):
-    _fields_ = [("dir", ctypes.c_int), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
-                ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("a_scales", ctypes.c_void_p),
-                ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("b_scales", ctypes.c_void_p),
-                ("out", ctypes.c_void_p), ("out_dt", ctypes.c_int), ("ldo", ctypes.c_int64),
-                ("offsets", ctypes.c_void_p), ("E", ctypes.c_int64)]
+# The C struct mxq_fp8_product: packing its bytes costs a fraction of filling a ctypes.Structure.
+_PRODUCT = struct.Struct("@i3qPqPPqPPiqPq").pack
+_DIRECTIONS = {"fwd": _FWD, "dgrad": _DGRAD, "wgrad": _WGRAD}
+# PyTorch's own C entry points behind torch.cuda.current_stream() and current_device()
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_this_device = torch._C._cuda_getDevice
 
 
 def scale_cols(K: int) -> int:
@@ -198,18 +200,53 @@ def _check_int32(t: torch.Tensor, numel: int, name: str):
         raise ValueError(f"{name} must be a contiguous int32 tensor of {numel} values")
 
 
-def _check_scales(t: torch.Tensor, dtype, numel: int, name: str, what: str):
+def _check_values(t: torch.Tensor, dtype, numel: int, name: str, what: str):
     if t.dtype != dtype or not t.is_contiguous() or t.numel() != numel:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {what} = {numel} values")
 
 
-def _one_device(x: torch.Tensor, *ts):
-    if not x.is_cuda:
+def _cuda_index(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("libmxq works on CUDA tensors only")
-    dev = x.device
+    return dev
+
+
+def _same_device(dev: int, *ts):
     for t in ts:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("every tensor of a call must sit on one CUDA device")
+
+
+def _matrix(t: torch.Tensor, name: str, rank: int = 0):
+    """(rows, n, ld) of t seen as rows of its last dimension, without a copy.
+    Rows that overlap, as those of an expanded tensor do, are refused."""
+    if t.dim() != 2:
+        if rank:
+            raise ValueError(f"{name} must be a matrix")
+        if t.dim() == 0:
+            raise ValueError(f"{name} needs at least one dimension")
+        n = t.shape[-1]
+        try:
+            t = t.view(t.numel() // n if n else math.prod(t.shape[:-1]), n)
+        except RuntimeError as exc:
+            raise ValueError(f"{name}'s leading dimensions must flatten to one row stride (no copy is made)") from exc
+    rows, n = t.shape
+    ld, step = t.stride()
+    if rows <= 1 or n == 0:
+        ld = n
+    if (step != 1 and n > 1 and rows > 0) or ld < n:
+        raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
+    return rows, n, ld
+
+
+def _row_output(out, rows: int, H: int, like: torch.Tensor, name: str, dev: int):
+    if out is None:
+        return torch.empty((rows, H), dtype=like.dtype, device=like.device)
+    _same_device(dev, out)
+    if tuple(out.shape) != (rows, H) or out.dtype != like.dtype or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{rows}, {H}] tensor of dtype {like.dtype}")
+    return out
 
 
 class Library:
@@ -249,8 +286,8 @@ class Library:
         i32, sz = ctypes.c_int32, ctypes.c_size_t
         for fn in (L.mxq_fp8_quant_1x128, L.mxq_fp8_quant_128x1):
             fn.argtypes = [vp, ci, i64, i64, i64, vp, i32, i64, vp, vp, vp]
-        L.mxq_fp8_matmul.argtypes = [ctypes.POINTER(_Product), vp, sz, vp]
-        L.mxq_fp8_matmul_workspace.argtypes = [ctypes.POINTER(_Product)]
+        L.mxq_fp8_matmul.argtypes = [ctypes.c_char_p, vp, sz, vp]
+        L.mxq_fp8_matmul_workspace.argtypes = [ctypes.c_char_p]
         L.mxq_fp8_matmul_workspace.restype = sz
         L.mxq_moe_sort.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, vp, sz, vp]
         L.mxq_moe_capacity.argtypes = [i64, i64, i64, i64]
@@ -639,32 +676,60 @@ class Library:
         return comp
 
     # -- the FP8 linear layer -------------------------------------------
+    # The smallest of these kernels run for a few microseconds, so the eager
+    # methods marshal once and call, without a Call in between; each plan_*
+    # keeps the same arguments in one.
 
-    def _plan_quant128(self, name, columns, x, data, scales, index, index_div):
-        _one_device(x, data, scales, index)
-        dt = _dt_code(x)
-        rows, K, ldx = _rows_view(x)
-        n = rows
+    def _call(self, fn, args, where: str, dev: int):
+        if _this_device() != dev:
+            with torch.cuda.device(dev):
+                status = fn(*args)
+        else:
+            status = fn(*args)
+        if status != 0:
+            self._check(status, where)
+
+    def _quant128(self, columns, x, index, index_div, data, scales):
+        """(fn, args, name, data, scales), outputs allocated where None."""
+        dev = _cuda_index(x)
+        rows, K, ldx = _matrix(x, "x")
+        n, at = rows, None
         if index is not None:
             n = index.numel()
             _check_int32(index, n, "index")
-        if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != n * K:
-            raise ValueError("data must be a contiguous uint8 tensor of one byte per output element")
-        if columns:
-            _check_scales(scales, torch.uint8, _blocks(n) * K, "scales", "ceil(rows/128) * K")
+            at = index.data_ptr()
+            _same_device(dev, index)
+        ns = _blocks(n) * K if columns else n * _blocks(K)
+        if data is None:
+            flat = columns or index is not None or x.dim() == 2
+            data = torch.empty((n, K) if flat else x.shape, dtype=torch.uint8, device=x.device)
         else:
-            _check_scales(scales, torch.uint8, n * _blocks(K), "scales", "rows * ceil(K/128)")
-        args = (x.data_ptr(), dt, rows, K, ldx, index.data_ptr() if index is not None else None, index_div, n,
-                data.data_ptr(), scales.data_ptr(), _stream(x))
-        return Call(self, getattr(self.L, name), args, name, (x, data, scales, index), x.device)
+            _same_device(dev, data)
+            if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != n * K:
+                raise ValueError("data must be a contiguous uint8 tensor of one byte per output element")
+        if scales is None:
+            if columns:
+                shape = (_blocks(n), K)
+            else:
+                shape = (n, _blocks(K)) if index is not None else tuple(x.shape[:-1]) + (_blocks(K),)
+            scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        else:
+            _same_device(dev, scales)
+            _check_values(scales, torch.uint8, ns, "scales", "ceil(rows/128) * K" if columns else "rows * ceil(K/128)")
+        name = "mxq_fp8_quant_128x1" if columns else "mxq_fp8_quant_1x128"
+        args = (x.data_ptr(), _dt_code(x), rows, K, ldx, at, index_div, n, data.data_ptr(), scales.data_ptr(),
+                _raw_stream(dev))
+        return (self.L.mxq_fp8_quant_128x1 if columns else self.L.mxq_fp8_quant_1x128), args, name, data, scales
 
     def plan_fp8_quant_1x128(self, x: torch.Tensor, data: torch.Tensor, scales: torch.Tensor,
                              index: Optional[torch.Tensor] = None, index_div: int = 1) -> "Call":
-        return self._plan_quant128("mxq_fp8_quant_1x128", False, x, data, scales, index, index_div)
+        fn, args, name, *_ = self._quant128(False, x, index, index_div, data, scales)
+        return Call(self, fn, args, name, (x, data, scales, index), x.device)
 
     def plan_fp8_quant_128x1(self, x: torch.Tensor, data: torch.Tensor, scales: torch.Tensor,
                              index: Optional[torch.Tensor] = None, index_div: int = 1) -> "Call":
-        return self._plan_quant128("mxq_fp8_quant_128x1", True, x, data, scales, index, index_div)
+        fn, args, name, *_ = self._quant128(True, x, index, index_div, data, scales)
+        return Call(self, fn, args, name, (x, data, scales, index), x.device)
 
     def fp8_quant_1x128(self, x: torch.Tensor, index: Optional[torch.Tensor] = None, index_div: int = 1,
                         data: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
@@ -672,27 +737,71 @@ class Library:
         ceil(K/128))).  With ``index`` (int32, one entry per output row) row i
         is row index[i] // index_div of x, zeros for a negative index; the
         results are then two-dimensional."""
-        lead = tuple(x.shape[:-1]) if index is None else (index.numel(),)
-        K = x.shape[-1]
-        if data is None:
-            data = torch.empty(lead + (K,), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty(lead + (_blocks(K),), dtype=torch.uint8, device=x.device)
-        self.plan_fp8_quant_1x128(x, data, scales, index, index_div)()
+        fn, args, name, data, scales = self._quant128(False, x, index, index_div, data, scales)
+        self._call(fn, args, name, x.get_device())
         return data, scales
 
     def fp8_quant_128x1(self, x: torch.Tensor, index: Optional[torch.Tensor] = None, index_div: int = 1,
                         data: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
         """Returns (E4M3 bytes [rows, K], UE8M0 codes [ceil(rows/128), K]);
         ``index`` as in fp8_quant_1x128."""
-        rows, K, _ = _rows_view(x)
-        n = rows if index is None else index.numel()
-        if data is None:
-            data = torch.empty((n, K), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty((_blocks(n), K), dtype=torch.uint8, device=x.device)
-        self.plan_fp8_quant_128x1(x, data, scales, index, index_div)()
+        fn, args, name, data, scales = self._quant128(True, x, index, index_div, data, scales)
+        self._call(fn, args, name, x.get_device())
         return data, scales
+
+    def _product(self, direction, a, a_scales, b, b_scales, offsets, out, out_dtype):
+        """(args, out, workspace) of mxq_fp8_matmul."""
+        dev = _cuda_index(a)
+        _same_device(dev, a_scales, b, b_scales)
+        _check_fp8(a, "the left operand")
+        _check_fp8(b, "the right operand")
+        M, an, lda = _matrix(a, "the left operand")
+        rb, K, ldb = _matrix(b, "the right operand")
+        E, po = 1, None
+        if offsets is not None:
+            E = offsets.numel() - 1
+            if E < 1:
+                raise ValueError("offsets must hold E + 1 values")
+            _check_int32(offsets, E + 1, "offsets")
+            _same_device(dev, offsets)
+            po = offsets.data_ptr()
+        if direction == _WGRAD:
+            N = an
+            if rb != M:
+                raise ValueError("g and x must have the same number of rows")
+            _check_values(a_scales, torch.uint8, _blocks(M) * N, "g's scales", "ceil(rows/128) * N")
+            _check_values(b_scales, torch.uint8, _blocks(M) * K, "x's scales", "ceil(rows/128) * K")
+            rows, n = N * E, K
+        else:
+            if b.dim() != (2 if po is None else 3) or (po is not None and b.shape[0] != E):
+                raise ValueError("w must be [N, K], or [E, N, K] with offsets of E + 1 values")
+            N = b.shape[-2]
+            if an != (K if direction == _FWD else N):
+                raise ValueError("the operands' inner sizes differ")
+            _check_values(a_scales, torch.uint8, M * _blocks(an), "the left operand's scales", "rows * ceil(n/128)")
+            _check_values(b_scales, torch.float32, E * _blocks(N) * _blocks(K), "w's tile scales",
+                          "ceil(N/128) * ceil(K/128) per weight")
+            rows, n = M, N if direction == _FWD else K
+        if out is None:
+            if direction == _WGRAD:
+                shape = (N, K) if po is None else (E, N, K)
+            else:
+                shape = (M, n) if a.dim() == 2 else tuple(a.shape[:-1]) + (n,)
+            out = torch.empty(shape, dtype=out_dtype, device=a.device)
+            ldo = n
+        else:
+            _same_device(dev, out)
+            orows, on, ldo = _matrix(out, "out")
+            if orows != rows or on != n:
+                raise ValueError(f"out must have {rows} rows of {n}")
+        pa, pb = a.data_ptr(), b.data_ptr()
+        p = _PRODUCT(direction, M, N, K, pa, lda, a_scales.data_ptr(), pb, ldb, b_scales.data_ptr(), out.data_ptr(),
+                     _dt_code(out), ldo, po or 0, E)
+        ws, need = None, 0
+        if (pa | lda | pb | ldb) & 15:  # rows that TMA cannot address
+            need = self.L.mxq_fp8_matmul_workspace(p)
+            ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+        return (p, ws.data_ptr() if ws is not None else None, need, _raw_stream(dev)), out, ws
 
     def plan_fp8_matmul(self, direction: str, a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
                         b_scales: torch.Tensor, out: torch.Tensor, offsets: Optional[torch.Tensor] = None) -> "Call":
@@ -700,176 +809,144 @@ class Library:
         b with a = g, b = w; "wgrad": out = a^T b with a = g, b = x.  w is [N, K]
         with fp32 tile scales, or a stack [E, N, K] with ``offsets`` (int32
         [E + 1], the experts' rows); the gradient of a stack is [E, N, K]."""
-        _one_device(a, a_scales, b, b_scales, out, offsets)
-        if direction not in ("fwd", "dgrad", "wgrad"):
+        if direction not in _DIRECTIONS:
             raise ValueError('direction must be "fwd", "dgrad" or "wgrad"')
-        _check_fp8(a, "the left operand")
-        _check_fp8(b, "the right operand")
-        p = _Product()
-        M, an, p.lda = _rows_view(a)
-        rb, K, p.ldb = _rows_view(b)
-        E = 1 if offsets is None else offsets.numel() - 1
-        if offsets is not None:
-            _check_int32(offsets, max(E, 0) + 1, "offsets")
-        if direction == "wgrad":
-            p.dir, N = _WGRAD, an
-            if rb != M:
-                raise ValueError("g and x must have the same number of rows")
-            _check_scales(a_scales, torch.uint8, _blocks(M) * N, "g's scales", "ceil(rows/128) * N")
-            _check_scales(b_scales, torch.uint8, _blocks(M) * K, "x's scales", "ceil(rows/128) * K")
-            rows, n = N * E, K
-        else:
-            if b.dim() != (2 if offsets is None else 3) or (offsets is not None and b.shape[0] != E):
-                raise ValueError("w must be [N, K], or [E, N, K] with offsets of E + 1 values")
-            N = b.shape[-2]
-            p.dir = _FWD if direction == "fwd" else _DGRAD
-            if an != (K if direction == "fwd" else N):
-                raise ValueError("the operands' inner sizes differ")
-            _check_scales(a_scales, torch.uint8, M * _blocks(an), "the left operand's scales", "rows * ceil(n/128)")
-            _check_scales(b_scales, torch.float32, E * _blocks(N) * _blocks(K), "w's tile scales",
-                          "ceil(N/128) * ceil(K/128) per weight")
-            rows, n = M, N if direction == "fwd" else K
-        orows, on, p.ldo = _rows_view(out)
-        if orows != rows or on != n:
-            raise ValueError(f"out must have {rows} rows of {n}")
-        p.M, p.N, p.K = M, N, K
-        pa, pb = a.data_ptr(), b.data_ptr()
-        p.a, p.a_scales, p.b, p.b_scales = pa, a_scales.data_ptr(), pb, b_scales.data_ptr()
-        p.out, p.out_dt = out.data_ptr(), _dt_code(out)
-        if offsets is not None:
-            p.offsets, p.E = offsets.data_ptr(), E
-        ref = ctypes.byref(p)
-        ws, need = None, 0
-        if (pa | p.lda | pb | p.ldb) & 15:  # rows that TMA cannot address
-            need = self.L.mxq_fp8_matmul_workspace(ref)
-            ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
-        args = (ref, ws.data_ptr() if ws is not None else None, need, _stream(a))
+        args, out, ws = self._product(_DIRECTIONS[direction], a, a_scales, b, b_scales, offsets, out, None)
         return Call(self, self.L.mxq_fp8_matmul, args, "mxq_fp8_matmul",
-                    (a, a_scales, b, b_scales, out, offsets, ws, p), a.device)
+                    (a, a_scales, b, b_scales, out, offsets, ws), a.device)
 
     def fp8_matmul(self, x, x_scales, w, w_tile_scale_inv, offsets=None, out_dtype=torch.bfloat16, out=None):
         """y = x W^T: x [..., K] with 1x128 scales, w [N, K] with the tile
         scales of fp8_block128_direct (a stack [E, N, K] with ``offsets``)."""
-        if out is None:
-            out = torch.empty(tuple(x.shape[:-1]) + (w.shape[-2],), dtype=out_dtype, device=x.device)
-        self.plan_fp8_matmul("fwd", x, x_scales, w, w_tile_scale_inv, out, offsets)()
+        args, out, _ = self._product(_FWD, x, x_scales, w, w_tile_scale_inv, offsets, out, out_dtype)
+        self._call(self.L.mxq_fp8_matmul, args, "mxq_fp8_matmul", x.get_device())
         return out
 
     def fp8_matmul_dgrad(self, g, g_scales, w, w_tile_scale_inv, offsets=None, out_dtype=torch.bfloat16, out=None):
         """dx = g W: g [..., N] with 1x128 scales, w as in fp8_matmul."""
-        if out is None:
-            out = torch.empty(tuple(g.shape[:-1]) + (w.shape[-1],), dtype=out_dtype, device=g.device)
-        self.plan_fp8_matmul("dgrad", g, g_scales, w, w_tile_scale_inv, out, offsets)()
+        args, out, _ = self._product(_DGRAD, g, g_scales, w, w_tile_scale_inv, offsets, out, out_dtype)
+        self._call(self.L.mxq_fp8_matmul, args, "mxq_fp8_matmul", g.get_device())
         return out
 
     def fp8_matmul_wgrad(self, g, g_scales, x, x_scales, offsets=None, out_dtype=torch.float32, out=None):
         """dW = g^T x: g [M, N] and x [M, K] with 128x1 scales."""
-        if out is None:
-            lead = () if offsets is None else (offsets.numel() - 1,)
-            out = torch.empty(lead + (g.shape[-1], x.shape[-1]), dtype=out_dtype, device=g.device)
-        self.plan_fp8_matmul("wgrad", g, g_scales, x, x_scales, out, offsets)()
+        args, out, _ = self._product(_WGRAD, g, g_scales, x, x_scales, offsets, out, out_dtype)
+        self._call(self.L.mxq_fp8_matmul, args, "mxq_fp8_matmul", g.get_device())
         return out
 
     # -- mixture of experts ---------------------------------------------
 
-    def plan_moe_sort(self, ids: torch.Tensor, num_experts: int, offsets: torch.Tensor, source: torch.Tensor,
-                      slots: torch.Tensor, align: int = 1) -> "Call":
-        _one_device(ids, offsets, source, slots)
+    def _sort_args(self, ids, num_experts, align, order):
         if ids.dim() != 2:
             raise ValueError("ids must be [tokens, topk]")
+        if num_experts < 1 or align < 1:
+            raise ValueError("num_experts and align must be positive")
+        dev = _cuda_index(ids)
         T, topk = ids.shape
-        _check_int32(ids, T * topk, "ids")
-        _check_int32(offsets, num_experts + 1, "offsets")
-        _check_int32(source, self.L.mxq_moe_capacity(T, topk, num_experts, align), "source")
-        _check_int32(slots, T * topk, "slots")
+        n = T * topk
+        _check_int32(ids, n, "ids")
+        cap = n + min(num_experts, n) * (align - 1)  # mxq_moe_capacity
+        if order is None:
+            buf = torch.empty(num_experts + 1 + cap + n, dtype=torch.int32, device=ids.device)  # one allocation
+            offsets, source, slots = buf.split_with_sizes((num_experts + 1, cap, n))
+            order = MoeOrder(offsets, source, slots.view(T, topk))
+        else:
+            _same_device(dev, *order)
+            _check_int32(order.offsets, num_experts + 1, "offsets")
+            _check_int32(order.source, cap, "source")
+            _check_int32(order.slots, n, "slots")
         need = self.L.mxq_moe_sort_workspace(T, topk, num_experts)
         ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
-        args = (ids.data_ptr(), T, topk, num_experts, align, offsets.data_ptr(), source.data_ptr(), slots.data_ptr(),
-                ws.data_ptr() if ws is not None else None, need, _stream(ids))
-        return Call(self, self.L.mxq_moe_sort, args, "mxq_moe_sort", (ids, offsets, source, slots, ws), ids.device)
+        args = (ids.data_ptr(), T, topk, num_experts, align, order.offsets.data_ptr(), order.source.data_ptr(),
+                order.slots.data_ptr(), ws.data_ptr() if ws is not None else None, need, _raw_stream(dev))
+        return args, order, ws
+
+    def plan_moe_sort(self, ids: torch.Tensor, num_experts: int, order: MoeOrder, align: int = 1) -> "Call":
+        args, order, ws = self._sort_args(ids, num_experts, align, order)
+        return Call(self, self.L.mxq_moe_sort, args, "mxq_moe_sort", (ids, order, ws), ids.device)
 
     def moe_sort(self, ids: torch.Tensor, num_experts: int, align: int = 1) -> MoeOrder:
         """Sorts a router's choices ids [tokens, topk] (int32) by expert,
         each expert's rows rounded up to a multiple of ``align`` (128 for the
         weight gradient).  Ids outside 0..num_experts-1 are dropped."""
-        if ids.dim() != 2:
-            raise ValueError("ids must be [tokens, topk]")
-        if num_experts < 1 or align < 1:
-            raise ValueError("num_experts and align must be positive")
-        dev = ids.device
-        order = MoeOrder(torch.empty(num_experts + 1, dtype=torch.int32, device=dev),
-                         torch.empty(self.L.mxq_moe_capacity(ids.shape[0], ids.shape[1], num_experts, align),
-                                     dtype=torch.int32, device=dev),
-                         torch.empty(ids.shape, dtype=torch.int32, device=dev))
-        self.plan_moe_sort(ids, num_experts, *order, align=align)()
+        args, order, _ = self._sort_args(ids, num_experts, align, None)
+        self._call(self.L.mxq_moe_sort, args, "mxq_moe_sort", ids.get_device())
         return order
 
-    def _row_major(self, t: torch.Tensor, name: str):
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be a matrix of contiguous rows")
-        return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    def _dispatch_args(self, x, source, topk, out):
+        dev = _cuda_index(x)
+        T, H, ldx = _matrix(x, "x", 2)
+        R = source.numel()
+        _check_int32(source, R, "source")
+        _same_device(dev, source)
+        out = _row_output(out, R, H, x, "out", dev)
+        return (x.data_ptr(), _dt_code(x), T, H, ldx, source.data_ptr(), topk, R, out.data_ptr(), _raw_stream(dev)), out
 
     def plan_moe_dispatch(self, x: torch.Tensor, source: torch.Tensor, topk: int, out: torch.Tensor) -> "Call":
-        _one_device(x, source, out)
-        ldx = self._row_major(x, "x")
-        R, H = source.numel(), x.shape[1]
-        _check_int32(source, R, "source")
-        if tuple(out.shape) != (R, H) or out.dtype != x.dtype or not out.is_contiguous():
-            raise ValueError("out must be a contiguous [rows, H] tensor of x's dtype")
-        args = (x.data_ptr(), _dt_code(x), x.shape[0], H, ldx, source.data_ptr(), topk, R, out.data_ptr(), _stream(x))
+        args, out = self._dispatch_args(x, source, topk, out)
         return Call(self, self.L.mxq_moe_dispatch, args, "mxq_moe_dispatch", (x, source, out), x.device)
 
     def moe_dispatch(self, x: torch.Tensor, source: torch.Tensor, topk: int, out: Optional[torch.Tensor] = None):
         """Token rows x [tokens, H] in the experts' order: row r is token
         source[r] // topk, zeros where source is -1."""
-        if out is None:
-            out = torch.empty((source.numel(), x.shape[-1]), dtype=x.dtype, device=x.device)
-        self.plan_moe_dispatch(x, source, topk, out)()
+        args, out = self._dispatch_args(x, source, topk, out)
+        self._call(self.L.mxq_moe_dispatch, args, "mxq_moe_dispatch", x.get_device())
         return out
 
-    def plan_moe_combine(self, y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor],
-                         out: torch.Tensor) -> "Call":
-        _one_device(y, slots, weights, out)
-        ldy = self._row_major(y, "y")
+    def _combine_args(self, y, slots, weights, out):
+        dev = _cuda_index(y)
+        R, H, ldy = _matrix(y, "y", 2)
         if slots.dim() != 2:
             raise ValueError("slots must be [tokens, topk]")
         T, topk = slots.shape
         _check_int32(slots, T * topk, "slots")
+        _same_device(dev, slots, weights)
+        pw = None
         if weights is not None:
-            _check_scales(weights, torch.float32, T * topk, "weights", "tokens * topk")
-        if tuple(out.shape) != (T, y.shape[1]) or out.dtype != y.dtype or not out.is_contiguous():
-            raise ValueError("out must be a contiguous [tokens, H] tensor of y's dtype")
-        args = (y.data_ptr(), _dt_code(y), y.shape[0], y.shape[1], ldy, slots.data_ptr(),
-                weights.data_ptr() if weights is not None else None, T, topk, out.data_ptr(), _stream(y))
+            _check_values(weights, torch.float32, T * topk, "weights", "tokens * topk")
+            pw = weights.data_ptr()
+        out = _row_output(out, T, H, y, "out", dev)
+        return (y.data_ptr(), _dt_code(y), R, H, ldy, slots.data_ptr(), pw, T, topk, out.data_ptr(),
+                _raw_stream(dev)), out
+
+    def plan_moe_combine(self, y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor],
+                         out: torch.Tensor) -> "Call":
+        args, out = self._combine_args(y, slots, weights, out)
         return Call(self, self.L.mxq_moe_combine, args, "mxq_moe_combine", (y, slots, weights, out), y.device)
 
     def moe_combine(self, y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None,
                     out: Optional[torch.Tensor] = None):
         """out[t] = sum_j weights[t, j] * y[slots[t, j]], dropped choices left
         out; weights of one when None."""
-        if out is None:
-            out = torch.empty((slots.shape[0], y.shape[-1]), dtype=y.dtype, device=y.device)
-        self.plan_moe_combine(y, slots, weights, out)()
+        args, out = self._combine_args(y, slots, weights, out)
+        self._call(self.L.mxq_moe_combine, args, "mxq_moe_combine", y.get_device())
         return out
 
-    def plan_moe_combine_grad(self, g: torch.Tensor, y: torch.Tensor, source: torch.Tensor, slots: torch.Tensor,
-                              weights: torch.Tensor, d_rows: torch.Tensor, d_weights: torch.Tensor) -> "Call":
-        _one_device(g, y, source, slots, weights, d_rows, d_weights)
-        ldg, ldy = self._row_major(g, "g"), self._row_major(y, "y")
+    def _combine_grad_args(self, g, y, source, slots, weights, d_rows, d_weights):
+        dev = _cuda_index(g)
+        gT, gH, ldg = _matrix(g, "g", 2)
+        R, H, ldy = _matrix(y, "y", 2)
         if slots.dim() != 2:
             raise ValueError("slots must be [tokens, topk]")
         T, topk = slots.shape
-        R, H = y.shape
         _check_int32(slots, T * topk, "slots")
         _check_int32(source, R, "source")
-        _check_scales(weights, torch.float32, T * topk, "weights", "tokens * topk")
-        _check_scales(d_weights, torch.float32, T * topk, "d_weights", "tokens * topk")
-        if tuple(g.shape) != (T, H) or g.dtype != y.dtype:
+        _check_values(weights, torch.float32, T * topk, "weights", "tokens * topk")
+        _same_device(dev, y, source, slots, weights)
+        if gT != T or gH != H or g.dtype != y.dtype:
             raise ValueError("g must be [tokens, H] of y's dtype")
-        if tuple(d_rows.shape) != (R, H) or d_rows.dtype != y.dtype or not d_rows.is_contiguous():
-            raise ValueError("d_rows must be a contiguous [rows, H] tensor of y's dtype")
-        args = (g.data_ptr(), y.data_ptr(), _dt_code(g), T, topk, R, H, ldg, ldy, source.data_ptr(), slots.data_ptr(),
-                weights.data_ptr(), d_rows.data_ptr(), d_weights.data_ptr(), _stream(g))
+        d_rows = _row_output(d_rows, R, H, y, "d_rows", dev)
+        if d_weights is None:
+            d_weights = torch.empty((T, topk), dtype=torch.float32, device=y.device)
+        else:
+            _same_device(dev, d_weights)
+            _check_values(d_weights, torch.float32, T * topk, "d_weights", "tokens * topk")
+        return (g.data_ptr(), y.data_ptr(), _dt_code(g), T, topk, R, H, ldg, ldy, source.data_ptr(), slots.data_ptr(),
+                weights.data_ptr(), d_rows.data_ptr(), d_weights.data_ptr(), _raw_stream(dev)), d_rows, d_weights
+
+    def plan_moe_combine_grad(self, g: torch.Tensor, y: torch.Tensor, source: torch.Tensor, slots: torch.Tensor,
+                              weights: torch.Tensor, d_rows: torch.Tensor, d_weights: torch.Tensor) -> "Call":
+        args, *_ = self._combine_grad_args(g, y, source, slots, weights, d_rows, d_weights)
         return Call(self, self.L.mxq_moe_combine_grad, args, "mxq_moe_combine_grad",
                     (g, y, source, slots, weights, d_rows, d_weights), g.device)
 
@@ -877,9 +954,8 @@ class Library:
                          weights: torch.Tensor):
         """Returns (d_rows [rows, H], d_weights [tokens, topk] fp32), the
         gradients of moe_combine for the gradient g of its output."""
-        d_rows = torch.empty((y.shape[0], y.shape[-1]), dtype=y.dtype, device=y.device)
-        d_weights = torch.empty(slots.shape, dtype=torch.float32, device=y.device)
-        self.plan_moe_combine_grad(g, y, source, slots, weights, d_rows, d_weights)()
+        args, d_rows, d_weights = self._combine_grad_args(g, y, source, slots, weights, None, None)
+        self._call(self.L.mxq_moe_combine_grad, args, "mxq_moe_combine_grad", g.get_device())
         return d_rows, d_weights
 
 
@@ -910,6 +986,8 @@ _lock = threading.Lock()
 def library() -> Library:
     """The default libmxq, built in-tree on first use."""
     global _default
+    if _default is not None:
+        return _default
     with _lock:
         if _default is None:
             _default = Library()

@@ -152,29 +152,57 @@ __device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t
     return c;
 }
 
-// Scale bytes of blocks kb .. kb + 3 of one row; 0 where there is none.
-__device__ __forceinline__ uint32_t scale_bytes4(const ScaleSource& s, int e, int row, int kb, int kb_end) {
-    if (row >= s.rows) return 0;
-    uint32_t w = 0;
-    if (s.tiles) {
-        const uint32_t* p = static_cast<const uint32_t*>(s.base) + e * s.s_expert + (row >> 7) * s.s_row;
+// The scales of W * 32 rows from row0 on and four blocks from kb on, read by
+// one warp.  Loads are unconditional, at indexes clamped into the operand: a
+// row behind its end has no output and a block behind kb_end no product.
+// They are raw until pack(), so that a warp's loads are all in flight at once
+// and those of the next four blocks while the ring is full.
+template <int W>
+struct ScaleReader {
+    uint32_t raw[W][4];
+
+    __device__ __forceinline__ void load(const ScaleSource& s, int e, int row0, int kb, int kb_end) {
+        const int lane = threadIdx.x & 31;
+        if (s.tiles) {  // one of 4 blocks x W/4 tiles a lane
+            const int tile = min((row0 >> 7) + min(lane >> 2, W / 4 - 1), (s.rows - 1) >> 7);
+            raw[0][0] = static_cast<const uint32_t*>(
+                s.base)[e * s.s_expert + tile * s.s_row + min(kb + (lane & 3), kb_end - 1) * s.s_kb];
+            return;
+        }
+        const uint8_t* p = static_cast<const uint8_t*>(s.base);
+        if (s.words) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (kb + j < kb_end) {
-                const uint32_t t = p[(kb + j) * s.s_kb];
-                // 2^c has the byte c + 127: the exponent field, and 0 for the subnormal 2^-127; all else is NaN
-                const uint32_t c = (t & 0x7FFFFFu) == 0u && t - 1u < 0x7F7FFFFFu ? t >> 23 : t == 0x00400000u ? 0u : 255u;
-                w |= c << (8 * j);
-            }
-        return w;
+            for (int i = 0; i < W; ++i)
+                raw[i][0] = *reinterpret_cast<const uint32_t*>(p + min(row0 + 32 * i + lane, s.rows - 1) * s.s_row + kb);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                raw[i][j] = p[min(row0 + 32 * i + lane, s.rows - 1) * s.s_row + min(kb + j, kb_end - 1) * s.s_kb];
     }
-    const uint8_t* p = static_cast<const uint8_t*>(s.base) + (int64_t)row * s.s_row;
-    if (s.words) return *reinterpret_cast<const uint32_t*>(p + kb);
+
+    // UE8M0 bytes of the four blocks of row row0 + 32 i + lane.
+    __device__ __forceinline__ void pack(const ScaleSource& s, uint32_t (&w)[W]) const {
+        if (s.tiles) {
+            // 2^c has the byte c + 127: the exponent field, and 0 for the subnormal 2^-127; all else is NaN
+            const uint32_t t = raw[0][0];
+            const uint32_t c = (t & 0x7FFFFFu) == 0u && t - 1u < 0x7F7FFFFFu ? t >> 23 : t == 0x00400000u ? 0u : 255u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (kb + j < kb_end) w |= (uint32_t)p[(kb + j) * s.s_kb] << (8 * j);
-    return w;
-}
+            for (int a = 0; a < W / 4; ++a) {
+                uint32_t v = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v |= __shfl_sync(0xFFFFFFFFu, c, 4 * a + j) << (8 * j);
+                w[4 * a] = w[4 * a + 1] = w[4 * a + 2] = w[4 * a + 3] = v;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                w[i] = s.words ? raw[i][0] : raw[i][0] | raw[i][1] << 8 | raw[i][2] << 16 | raw[i][3] << 24;
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t canonical(uint32_t u) { return (u & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FC00000u : u; }
 
@@ -389,52 +417,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp < 4) {
         // --------------------------------------------------------- scales
-        const bool is_p = warp == 2;
-        const ScaleSource& src = is_p ? g.sp : g.sq;
-        constexpr int kWords = QT >= 128 ? QT / 32 : 4;
-        const int words = is_p ? 4 : kWords, rows = is_p ? 128 : QT;
-        int quad = 0;
-        bool ok = true;
-        const uint32_t arrive_at = CG == 2 ? map_rank(sc_full, 0) : 0;
-        for (int t = first_tile; ok && t < tiles; t += span) {
-            const Tile c = tile_at<PT, QT>(g, rag, t);
-            int kb0, kb1;
-            depth_of(c, kb0, kb1);
-            const int row0 = is_p ? c.p0 + 128 * (int)pair_rank : c.q0;
-            uint32_t w[kWords];
-            auto read = [&](int kb) {
+        // row i of 128 has its four bytes at 16 (i % 32) + 4 (i / 32)
+        auto gather = [&](auto reader, const ScaleSource& src, bool is_p) {
+            constexpr int W = sizeof(reader) / 16;
+            const uint32_t arrive_at = CG == 2 ? map_rank(sc_full, 0) : 0;
+            int quad = 0;
+            bool ok = true;
+            for (int t = first_tile; ok && t < tiles; t += span) {
+                const Tile c = tile_at<PT, QT>(g, rag, t);
+                int kb0, kb1;
+                depth_of(c, kb0, kb1);
+                const int row0 = is_p ? c.p0 + 128 * (int)pair_rank : c.q0;
+                if (kb0 < kb1) reader.load(src, c.e, row0, kb0, kb1);
+                for (int kb = kb0; kb < kb1; kb += 4, ++quad) {
+                    const int r = quad % kRing, round = quad / kRing;
+                    uint32_t w[W];
+                    reader.pack(src, w);
+                    if (kb + 4 < kb1) reader.load(src, c.e, row0, kb + 4, kb1);
+                    if (round > 0 && !mbar_wait(sc_empty + 8 * r, (round - 1) & 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* to = scales + r * S::kScaleBytes + (is_p ? 0 : 512);
 #pragma unroll
-                for (int i = 0; i < kWords; ++i)
-                    w[i] = i < words && 32 * i + lane < rows && kb < kb1
-                               ? scale_bytes4(src, c.e, row0 + 32 * i + lane, kb, c.kb1)
-                               : 0u;
-            };
-            read(kb0);
-            for (int kb = kb0; kb < kb1; kb += 4, ++quad) {
-                const int r = quad % kRing, round = quad / kRing;
-                if (round > 0 && !mbar_wait(sc_empty + 8 * r, (round - 1) & 1, gave_up)) {
-                    ok = false;
-                    break;
-                }
-                // row i of 128 has its four bytes at 16 (i % 32) + 4 (i / 32)
-                uint8_t* to = scales + r * S::kScaleBytes + (is_p ? 0 : 512);
-#pragma unroll
-                for (int a = 0; a < kWords / 4; ++a)
-                    if (4 * a < words)
+                    for (int a = 0; a < W / 4; ++a)
                         *reinterpret_cast<uint4*>(to + 512 * a + 16 * lane) =
                             make_uint4(w[4 * a], w[4 * a + 1], w[4 * a + 2], w[4 * a + 3]);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2)
-                        mbar_arrive_cluster(arrive_at + 8 * r);
-                    else
-                        mbar_arrive(sc_full + 8 * r);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2)
+                            mbar_arrive_cluster(arrive_at + 8 * r);
+                        else
+                            mbar_arrive(sc_full + 8 * r);
+                    }
                 }
-                read(kb + 4);  // on its way while the ring drains
+                ok = __all_sync(0xFFFFFFFFu, ok);
             }
-            ok = __all_sync(0xFFFFFFFFu, ok);
-        }
+        };
+        if (warp == 2)
+            gather(ScaleReader<4>{}, g.sp, true);
+        else
+            gather(ScaleReader<4 * S::kQAtoms>{}, g.sq, false);
     } else {
         // --------------------------------------------------------- results
         const int band = warp & 3;  // lanes 32 band .. of tensor memory are this warp's

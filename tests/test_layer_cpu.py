@@ -19,13 +19,27 @@ def lib():
     return mxq.Library()
 
 
+class _Product(ctypes.Structure):
+    """mxq_fp8_product as include/mxq.h declares it."""
+    _fields_ = [("dir", ctypes.c_int), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("a_scales", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("b_scales", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_dt", ctypes.c_int), ("ldo", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("E", ctypes.c_int64)]
+
+
 def product(**kw):
-    p = mxq._Product()
     base = dict(dir=0, M=4, N=256, K=128, a=FAKE, lda=128, a_scales=FAKE, b=FAKE, ldb=128, b_scales=FAKE, out=FAKE,
                 out_dt=0, ldo=256, offsets=None, E=0)
-    for k, v in (base | kw).items():
-        setattr(p, k, v)
-    return p
+    return bytes(_Product(**(base | kw)))
+
+
+def test_the_binding_packs_the_struct():
+    values = (2, 3, 5, 7, 11, 13, 17, 19, 23, 29, 31, 1, 37, 41, 43)
+    p = _Product(*values)
+    packed = mxq._PRODUCT(*values)
+    assert len(packed) == ctypes.sizeof(p)
+    assert tuple(getattr(_Product.from_buffer_copy(packed), f) for f, _ in _Product._fields_) == values
 
 
 @pytest.mark.parametrize("change,status", [
@@ -38,7 +52,7 @@ def product(**kw):
     (dict(M=0), OK), (dict(N=0), OK), (dict(dir=1, lda=255), INVALID), (dict(dir=2, lda=256, ldo=127), INVALID),
 ])
 def test_product_refusals(lib, change, status):
-    assert lib.L.mxq_fp8_matmul(ctypes.byref(product(**change)), None, 0, None) == status
+    assert lib.L.mxq_fp8_matmul(product(**change), None, 0, None) == status
 
 
 def test_product_refuses_no_description(lib):
@@ -47,15 +61,15 @@ def test_product_refuses_no_description(lib):
 
 
 def test_workspace_of_rows_that_are_not_aligned(lib):
-    need = lambda **kw: lib.L.mxq_fp8_matmul_workspace(ctypes.byref(product(**kw)))  # noqa: E731
+    need = lambda **kw: lib.L.mxq_fp8_matmul_workspace(product(**kw))  # noqa: E731
     assert need() == 0
     assert need(K=100, lda=100, ldb=100) == 4 * 112 + 256 * 112
     assert need(K=100, lda=112, ldb=112) == 0
     assert need(M=1, K=100, lda=100, ldb=112) == 0  # one row has no stride
     assert need(a=FAKE + 8) == 4 * 128
     assert need(K=100, lda=112, ldb=100, offsets=FAKE, E=3) == 3 * 256 * 112
-    assert lib.L.mxq_fp8_matmul(ctypes.byref(product(a=FAKE + 8)), FAKE, 511, None) == TOO_SMALL
-    assert lib.L.mxq_fp8_matmul(ctypes.byref(product(a=FAKE + 8)), FAKE + 4, 512, None) == INVALID
+    assert lib.L.mxq_fp8_matmul(product(a=FAKE + 8), FAKE, 511, None) == TOO_SMALL
+    assert lib.L.mxq_fp8_matmul(product(a=FAKE + 8), FAKE + 4, 512, None) == INVALID
 
 
 def test_quant_refusals(lib):
@@ -114,6 +128,22 @@ def test_the_binding_refuses_cpu_tensors(lib):
               lambda: lib.moe_combine(x, torch.zeros(4, 1, dtype=torch.int32))):
         with pytest.raises(ValueError):
             f()
+
+
+def test_the_binding_sees_rows():
+    t = torch.zeros(6, 8, 32, dtype=torch.uint8)
+    assert mxq._matrix(t, "t") == (48, 32, 32)
+    assert mxq._matrix(t[:, :, :20], "t") == (48, 20, 32)
+    assert mxq._matrix(t[0, 0], "t") == (1, 32, 32)
+    assert mxq._matrix(t[0, :1, 3:9], "t") == (1, 6, 6)
+    assert mxq._matrix(t[0, :, :1], "t") == (8, 1, 32)
+    assert mxq._matrix(t[:0], "t") == (0, 32, 32)
+    assert mxq._matrix(t[0, :, :0], "t") == (8, 0, 0)
+    for bad in (t[0, :1].expand(8, 32), t[0].t(), t[:, :4], t[0, :, ::2], torch.zeros(())):
+        with pytest.raises(ValueError):
+            mxq._matrix(bad, "t")
+    with pytest.raises(ValueError):
+        mxq._matrix(t, "t", 2)
 
 
 def test_the_reference_rounds_to_nearest_even():
