@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, sc_full = empty + 8 * S::kStages,
                    sc_empty = sc_full + 8 * kRing, acc_full = sc_empty + 8 * kRing, acc_empty = acc_full + 16,
                    drained = acc_empty + 16;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 || SPLIT ? cluster_rank() : 0;
     const uint32_t pair_rank = CG == 2 ? rank : 0;
     const bool leader = pair_rank == 0;
@@ -323,94 +323,98 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------- loads
-        if (lane == 0) {
-            int n = 0;  // boxes' ring position
-            bool ok = true;
-            for (int t = first_tile; ok && t < tiles; t += span) {
-                const Tile c = tile_at<PT, QT>(g, rag, t);
-                int kb0, kb1;
-                depth_of(c, kb0, kb1);
-                const int p_row = c.p0 + 128 * (int)pair_rank, q_row = c.q0 + S::kQRows * (int)pair_rank;
-                const int pe = g.p_expert ? c.e : 0, qe = g.q_expert ? c.e : 0;
-                for (int kb = kb0; kb < kb1; ++kb, ++n) {
-                    const int s = n % S::kStages, round = n / S::kStages;
-                    if (round > 0 && !mbar_wait(empty + 8 * s, (round - 1) & 1, gave_up)) {
-                        ok = false;
-                        break;
-                    }
-                    if (leader) mbar_expect_tx(full + 8 * s, CG * S::kStageBytes);
-                    const uint32_t at = smem_u32(stages + s * S::kStageBytes);
+        int n = 0, s = 0;  // boxes so far, and their place in the ring
+        uint32_t parity = 1;  // of the round before: a ring that was never filled is empty
+        bool ok = true;
+        for (int t = first_tile; ok && t < tiles; t += span) {
+            const Tile c = tile_at<PT, QT>(g, rag, t);
+            int kb0, kb1;
+            depth_of(c, kb0, kb1);
+            const int p_row = c.p0 + 128 * (int)pair_rank, q_row = c.q0 + S::kQRows * (int)pair_rank;
+            const int pe = g.p_expert ? c.e : 0, qe = g.q_expert ? c.e : 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = mbar_wait(empty + 8 * s, parity, gave_up);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t at = smem_u32(stages) + s * S::kStageBytes, bar = full + 8 * s;
+                    if (leader) mbar_expect_tx(bar, CG * S::kStageBytes);
                     if (g.p_mn)
-                        tma_load<CG == 2>(at, &p_map, full + 8 * s, p_row, kb * 128, pe);
+                        tma_load<CG == 2>(at, &p_map, bar, p_row, kb * 128, pe);
                     else
-                        tma_load<CG == 2>(at, &p_map, full + 8 * s, kb * 128, p_row, pe);
+                        tma_load<CG == 2>(at, &p_map, bar, kb * 128, p_row, pe);
                     if (g.q_mn)
-                        tma_load<CG == 2>(at + S::kPBytes, &q_map, full + 8 * s, q_row, kb * 128, qe);
+                        tma_load<CG == 2>(at + S::kPBytes, &q_map, bar, q_row, kb * 128, qe);
                     else
-                        tma_load<CG == 2>(at + S::kPBytes, &q_map, full + 8 * s, kb * 128, q_row, qe);
+                        tma_load<CG == 2>(at + S::kPBytes, &q_map, bar, kb * 128, q_row, qe);
                 }
+                __syncwarp();
+                ++n;
+                if (++s == S::kStages) s = 0, parity ^= 1;
             }
-            if (!ok && leader) {  // copies in flight land before the block ends
-                volatile int again = 0;
-                for (int i = n < S::kStages ? 0 : n - S::kStages; i < n; ++i)
-                    mbar_wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1, &again);
-            }
+        }
+        if (!ok && leader) {  // copies in flight land before the block ends
+            volatile int again = 0;
+            for (int i = n < S::kStages ? 0 : n - S::kStages; i < n; ++i)
+                mbar_wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1, &again);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------------- MMAs
-        if (leader && lane == 0) {
-            int n = 0, quad = 0, it = 0;
+        if (leader) {
+            int s = 0, r = 0, it = 0;
+            uint32_t parity = 0, sc_parity = 0;
             bool ok = true;
+            // 32 of depth: 32 bytes along a row, or 32 rows of 128 bytes
+            const uint64_t step_p = g.p_mn ? 4096 >> 4 : 32 >> 4, step_q = g.q_mn ? 4096 >> 4 : 32 >> 4;
+            const uint64_t desc_p = desc_swizzle128(smem_u32(stages), g.p_mn),
+                           desc_q = desc_swizzle128(smem_u32(stages) + S::kPBytes, g.q_mn),
+                           desc_s = desc_scales(smem_u32(scales));
             for (int t = first_tile; ok && t < tiles; t += span) {
                 const Tile c = tile_at<PT, QT>(g, rag, t);
                 int kb0, kb1;
                 depth_of(c, kb0, kb1);
                 if (kb0 >= kb1) continue;
                 // the accumulator that this tile writes has been taken out
-                if constexpr (QT == 256) {
+                if constexpr (QT == 256)
                     ok = it < 1 || mbar_wait(acc_empty, (it - 1) & 1, gave_up);
-                } else {
+                else
                     ok = it < 2 || mbar_wait(acc_empty + 8 * (it & 1), ((it >> 1) - 1) & 1, gave_up);
-                }
-                tc_fence_after();
                 const uint32_t acc = tmem + (it & 1) * S::kAcc1;
-                for (int kb = kb0; ok && kb < kb1; ++kb, ++n) {
-                    const int s = n % S::kStages, j = (kb - kb0) & 3;
-                    const int r = quad % kRing;
+                for (int kb = kb0; ok && kb < kb1; ++kb) {
+                    const uint32_t j = (kb - kb0) & 3;
                     const uint32_t sfp = tmem + S::kScaleAt + r * S::kScaleColumns, sfq = sfp + 4;
-                    if (j == 0) {
-                        ok = mbar_wait(sc_full + 8 * r, (quad / kRing) & 1, gave_up);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t from = smem_u32(scales + r * S::kScaleBytes);
-#pragma unroll
-                        for (int a = 0; a <= S::kQAtoms; ++a) copy_scales<CG>(sfp + 4 * a, desc_scales(from + 512 * a));
-                    }
-                    ok = mbar_wait(full + 8 * s, (n / S::kStages) & 1, gave_up);
+                    if (j == 0) ok = mbar_wait(sc_full + 8 * r, sc_parity, gave_up);
+                    ok = ok && mbar_wait(full + 8 * s, parity, gave_up);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t at = smem_u32(stages + s * S::kStageBytes);
-                    const uint64_t dp = desc_swizzle128(at, g.p_mn), dq = desc_swizzle128(at + S::kPBytes, g.q_mn);
-                    // 32 of depth: 32 bytes along a row, or 32 rows of 128 bytes
-                    const uint64_t step_p = g.p_mn ? 4096 >> 4 : 32 >> 4, step_q = g.q_mn ? 4096 >> 4 : 32 >> 4;
+                    const bool last = kb + 1 == kb1;
+                    if (elect_one()) {
+                        if (j == 0) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_block_scaled<CG>(acc, dp + k * step_p, dq + k * step_q, idesc | scale_byte(j), sfp, sfq,
-                                             kb > kb0 || k > 0);
-                    mma_commit<CG>(empty + 8 * s);
-                    if (j == 3 || kb + 1 == kb1) {
-                        mma_commit<CG>(sc_empty + 8 * r);
-                        ++quad;
+                            for (int a = 0; a <= S::kQAtoms; ++a)
+                                copy_scales<CG>(sfp + 4 * a, desc_s + ((r * S::kScaleBytes + 512 * a) >> 4));
+                        }
+                        const uint64_t dp = desc_p + ((s * S::kStageBytes) >> 4), dq = desc_q + ((s * S::kStageBytes) >> 4);
+                        const uint32_t id = idesc | scale_byte(j);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_block_scaled<CG>(acc, dp + k * step_p, dq + k * step_q, id, sfp, sfq, kb > kb0 || k > 0);
+                        mma_commit<CG>(empty + 8 * s);
+                        if (j == 3 || last) mma_commit<CG>(sc_empty + 8 * r);
+                        if (last) mma_commit<CG>(acc_full + 8 * (it & 1));
                     }
+                    __syncwarp();
+                    if (++s == S::kStages) s = 0, parity ^= 1;
+                    if ((j == 3 || last) && ++r == kRing) r = 0, sc_parity ^= 1;
                 }
-                if (!ok) break;
-                mma_commit<CG>(acc_full + 8 * (it & 1));
                 ++it;
             }
             if (!ok) {  // what has been issued ends before the block does
                 volatile int again = 0;
-                mma_commit<CG>(drained);
+                if (elect_one()) mma_commit<CG>(drained);
+                __syncwarp();
                 mbar_wait(drained, 0, &again);
             }
         }
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // row i of 128 has its four bytes at 16 (i % 32) + 4 (i / 32)
         auto gather = [&](auto reader, const ScaleSource& src, bool is_p) {
             constexpr int W = sizeof(reader) / 16;
-            const uint32_t arrive_at = CG == 2 ? map_rank(sc_full, 0) : 0;
+            [[maybe_unused]] const uint32_t arrive_at = CG == 2 ? map_rank(sc_full, 0) : 0;
             int quad = 0;
             bool ok = true;
             for (int t = first_tile; ok && t < tiles; t += span) {
