@@ -33,7 +33,10 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRing = 4;  // scale buffers
+// Scales move in groups of two words a row, eight blocks of depth: what a warp spends on a group (its loads, which the
+// proxy fence waits for, and the fence) is about 2000 clocks, as long as the products of four blocks.
+constexpr int kGroup = 8;
+constexpr int kRing = 2;  // groups, both in shared and in tensor memory
 
 // The operand whose rows are the accumulator's lanes is called P, the one
 // whose rows are its columns Q.
@@ -226,19 +229,20 @@ struct Shape {
     static constexpr int kStageBytes = kPBytes + kQBytes;
     static constexpr int kStages = CG == 2 ? 6 : QT == 128 ? 6 : QT == 64 ? 4 : 5;
     static constexpr int kQAtoms = QT <= 128 ? 1 : QT / 128;         // 128 scales each
-    static constexpr int kScaleBytes = 512 * (1 + kQAtoms);
+    static constexpr int kScaleBytes = 512 * (1 + kQAtoms);           // of four blocks
     static constexpr int kScaleColumns = 4 * (1 + kQAtoms);
+    static constexpr int kScaleParts = kRing * (kGroup / 4);
     // Two accumulators.  Two of 256 columns and the scales exceed the 512 columns, so
     // there the second begins 64 columns before the first one's end and the
     // shared ones are taken out first.
     static constexpr int kAcc1 = QT == 256 ? 192 : QT;
     static constexpr int kScaleAt = QT == 256 ? 448 : 2 * QT;
-    static constexpr int kUsed = kScaleAt + kRing * kScaleColumns;
+    static constexpr int kUsed = kScaleAt + kScaleParts * kScaleColumns;
     static constexpr int kColumns = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr int kTranspose = CG == 2 ? 4 * 32 * 33 * 4 : 0;
     static constexpr int kBarriers = 2 * kStages + 2 * kRing + 4 + 1;
     static size_t smem(int E) {
-        return 1024 + (size_t)kStages * kStageBytes + (size_t)kRing * kScaleBytes + kTranspose + 8 * kBarriers + 16 +
+        return 1024 + (size_t)kStages * kStageBytes + (size_t)kScaleParts * kScaleBytes + kTranspose + 8 * kBarriers + 16 +
                (E ? 8 * (size_t)(E + 1) : 0);
     }
 };
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* scales = stages + S::kStages * S::kStageBytes;
-    float* transpose = reinterpret_cast<float*>(scales + kRing * S::kScaleBytes);
+    float* transpose = reinterpret_cast<float*>(scales + S::kScaleParts * S::kScaleBytes);
     uint8_t* bars = reinterpret_cast<uint8_t*>(transpose) + S::kTranspose;
     volatile int* gave_up = reinterpret_cast<volatile int*>(bars + 8 * S::kBarriers);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 8 * S::kBarriers + 4);
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (CG == 2 || SPLIT) cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_at, 0);  // known to be the same in a warp: see elect_one()
 
     int tiles = tile_count;
     if (g.ragged == kRowsOfP) tiles = rag.tiles[g.E] * g.q_tiles;
@@ -362,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ----------------------------------------------------------- MMAs
         if (leader) {
-            int s = 0, r = 0, it = 0;
-            uint32_t parity = 0, sc_parity = 0;
+            int s = 0, it = 0, group = 0;
+            uint32_t parity = 0;
             bool ok = true;
             // 32 of depth: 32 bytes along a row, or 32 rows of 128 bytes
             const uint64_t step_p = g.p_mn ? 4096 >> 4 : 32 >> 4, step_q = g.q_mn ? 4096 >> 4 : 32 >> 4;
@@ -374,41 +378,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Tile c = tile_at<PT, QT>(g, rag, t);
                 int kb0, kb1;
                 depth_of(c, kb0, kb1);
-                if (kb0 >= kb1) continue;
+                const int blocks = __shfl_sync(0xFFFFFFFFu, kb1 - kb0, 0);
+                if (blocks <= 0) continue;
                 // the accumulator that this tile writes has been taken out
                 if constexpr (QT == 256)
                     ok = it < 1 || mbar_wait(acc_empty, (it - 1) & 1, gave_up);
                 else
                     ok = it < 2 || mbar_wait(acc_empty + 8 * (it & 1), ((it >> 1) - 1) & 1, gave_up);
                 const uint32_t acc = tmem + (it & 1) * S::kAcc1;
-                for (int kb = kb0; ok && kb < kb1; ++kb) {
-                    const uint32_t j = (kb - kb0) & 3;
-                    const uint32_t sfp = tmem + S::kScaleAt + r * S::kScaleColumns, sfq = sfp + 4;
-                    if (j == 0) ok = mbar_wait(sc_full + 8 * r, sc_parity, gave_up);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                // Copies the scales of group x of this block's.  That they have arrived says, too, that the
+                // products which used the same bytes and columns before are done.
+                auto scales_of = [&](int x) {
+                    const int slot = x % kRing;
+                    const bool there = __all_sync(0xFFFFFFFFu, mbar_wait<CG == 2>(sc_full + 8 * slot, (x / kRing) & 1, gave_up));
+                    tc_fence_after();
+                    if (there && elect_one()) {
+#pragma unroll
+                        for (int h = slot * (kGroup / 4), a = 0; a < (kGroup / 4) * (1 + S::kQAtoms); ++a)
+                            copy_scales<CG>(tmem + S::kScaleAt + h * S::kScaleColumns + 4 * a,
+                                            desc_s + ((h * S::kScaleBytes + 512 * a) >> 4));
+                    }
+                    __syncwarp();
+                    return there;
+                };
+                ok = ok && scales_of(group);
+                for (int i = 0; ok && i < blocks; ++i) {
+                    const uint32_t j = i % kGroup;
+                    const uint32_t sfp = tmem + S::kScaleAt + ((group % kRing) * (kGroup / 4) + j / 4) * S::kScaleColumns,
+                                   sfq = sfp + 4;
                     ok = ok && mbar_wait(full + 8 * s, parity, gave_up);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const bool last = kb + 1 == kb1;
+                    const bool last = i + 1 == blocks;
                     if (elect_one()) {
-                        if (j == 0) {
-#pragma unroll
-                            for (int a = 0; a <= S::kQAtoms; ++a)
-                                copy_scales<CG>(sfp + 4 * a, desc_s + ((r * S::kScaleBytes + 512 * a) >> 4));
-                        }
                         const uint64_t dp = desc_p + ((s * S::kStageBytes) >> 4), dq = desc_q + ((s * S::kStageBytes) >> 4);
-                        const uint32_t id = idesc | scale_byte(j);
+                        const uint32_t id = idesc | scale_byte(j & 3);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_block_scaled<CG>(acc, dp + k * step_p, dq + k * step_q, id, sfp, sfq, kb > kb0 || k > 0);
+                            mma_block_scaled<CG>(acc, dp + k * step_p, dq + k * step_q, id, sfp, sfq, i > 0 || k > 0);
                         mma_commit<CG>(empty + 8 * s);
-                        if (j == 3 || last) mma_commit<CG>(sc_empty + 8 * r);
+                        if (j == kGroup - 1 || last) mma_commit<CG>(sc_empty + 8 * (group % kRing));
                         if (last) mma_commit<CG>(acc_full + 8 * (it & 1));
                     }
                     __syncwarp();
                     if (++s == S::kStages) s = 0, parity ^= 1;
-                    if ((j == 3 || last) && ++r == kRing) r = 0, sc_parity ^= 1;
+                    // copied well in front of the products that need them
+                    if (j == kGroup - 3 && i + 3 < blocks) ok = scales_of(group + 1);
+                    if (j == kGroup - 1) ++group;
                 }
+                if (!ok) break;
+                if (blocks % kGroup) ++group;
                 ++it;
             }
             if (!ok) {  // what has been issued ends before the block does
@@ -422,31 +443,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 4) {
         // --------------------------------------------------------- scales
         // row i of 128 has its four bytes at 16 (i % 32) + 4 (i / 32)
-        auto gather = [&](auto reader, const ScaleSource& src, bool is_p) {
-            constexpr int W = sizeof(reader) / 16;
+        auto gather = [&](auto proto, const ScaleSource& src, bool is_p) {
+            using Reader = decltype(proto);
+            constexpr int W = sizeof(Reader) / 16, H = kGroup / 4;
+            Reader reader[H];
             [[maybe_unused]] const uint32_t arrive_at = CG == 2 ? map_rank(sc_full, 0) : 0;
-            int quad = 0;
+            int group = 0;
             bool ok = true;
             for (int t = first_tile; ok && t < tiles; t += span) {
                 const Tile c = tile_at<PT, QT>(g, rag, t);
                 int kb0, kb1;
                 depth_of(c, kb0, kb1);
                 const int row0 = is_p ? c.p0 + 128 * (int)pair_rank : c.q0;
-                if (kb0 < kb1) reader.load(src, c.e, row0, kb0, kb1);
-                for (int kb = kb0; kb < kb1; kb += 4, ++quad) {
-                    const int r = quad % kRing, round = quad / kRing;
-                    uint32_t w[W];
-                    reader.pack(src, w);
-                    if (kb + 4 < kb1) reader.load(src, c.e, row0, kb + 4, kb1);
-                    if (round > 0 && !mbar_wait(sc_empty + 8 * r, (round - 1) & 1, gave_up)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* to = scales + r * S::kScaleBytes + (is_p ? 0 : 512);
+                auto load = [&](int kb) {
 #pragma unroll
-                    for (int a = 0; a < W / 4; ++a)
-                        *reinterpret_cast<uint4*>(to + 512 * a + 16 * lane) =
-                            make_uint4(w[4 * a], w[4 * a + 1], w[4 * a + 2], w[4 * a + 3]);
+                    for (int h = 0; h < H; ++h)
+                        if (kb + 4 * h < kb1) reader[h].load(src, c.e, row0, kb + 4 * h, kb1);
+                };
+                load(kb0);
+                for (int kb = kb0; kb < kb1; kb += kGroup, ++group) {
+                    const int r = group % kRing, round = group / kRing;
+                    uint32_t w[H][W];
+#pragma unroll
+                    for (int h = 0; h < H; ++h) reader[h].pack(src, w[h]);
+                    ok = round == 0 || mbar_wait(sc_empty + 8 * r, (round - 1) & 1, gave_up);
+                    if (!ok) break;
+                    uint8_t* to = scales + r * H * S::kScaleBytes + (is_p ? 0 : 512);
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+#pragma unroll
+                        for (int a = 0; a < W / 4; ++a)
+                            *reinterpret_cast<uint4*>(to + h * S::kScaleBytes + 512 * a + 16 * lane) =
+                                make_uint4(w[h][4 * a], w[h][4 * a + 1], w[h][4 * a + 2], w[h][4 * a + 3]);
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -455,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             mbar_arrive(sc_full + 8 * r);
                     }
+                    load(kb + kGroup);
                 }
                 ok = __all_sync(0xFFFFFFFFu, ok);
             }
@@ -468,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int band = warp & 3;  // lanes 32 band .. of tensor memory are this warp's
         const uint32_t lanes = (uint32_t)(32 * band) << 16;
         const uint32_t release_at = CG == 2 ? map_rank(acc_empty, 0) : 0;
-        constexpr int W = QT < 32 ? QT : 32;  // columns at a time
+        constexpr int W = QT < 64 ? QT : 64;  // columns at a time
         constexpr int kChunks = QT / W;
         int it = 0;
         bool ok = true;
@@ -490,16 +519,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < kChunks; ++x) {
                 // the columns that the two accumulators share come first (the second one's first, the first
                 // one's last): only they hold up the next tile
-                const int chunk = QT == 256 && a == 0 ? (x + kChunks - 2) % kChunks : x;
+                const int chunk = QT == 256 && a == 0 ? (x + kChunks - 1) % kChunks : x;
                 uint32_t v[W];
                 if (!none && ok) {
-                    tmem_ld(v, tmem + lanes + a * S::kAcc1 + chunk * W);
+                    const uint32_t from = tmem + lanes + a * S::kAcc1 + chunk * W;
+                    if constexpr (W == 16) {
+                        tmem_ld(v, from);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < W / 32; ++h) tmem_ld(reinterpret_cast<uint32_t(&)[32]>(v[32 * h]), from + 32 * h);
+                    }
                     tmem_ld_wait();
                 } else {
 #pragma unroll
                     for (int i = 0; i < W; ++i) v[i] = none ? 0u : 0x7FC00000u;
                 }
-                if (!none && x == (QT == 256 ? 1 : kChunks - 1)) {
+                if (!none && x == (QT == 256 ? 0 : kChunks - 1)) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -528,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (g.out_bf16) {
                                 uint16_t* to = static_cast<uint16_t*>(g.out) + base + lane_row * g.ldo + col;
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
+                                for (int h = 0; h < W / 16; ++h) {
                                     uint32_t p[8];
 #pragma unroll
                                     for (int i = 0; i < 8; ++i)
@@ -539,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             } else {
                                 uint32_t* to = static_cast<uint32_t*>(g.out) + base + lane_row * g.ldo + col;
 #pragma unroll
-                                for (int h = 0; h < 4; ++h) {
+                                for (int h = 0; h < W / 8; ++h) {
                                     uint32_t p[8];
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) p[i] = canonical(v[8 * h + i]);
@@ -550,13 +585,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         // through shared memory, so that neighbouring lanes store neighbouring columns
                         uint32_t* buf = reinterpret_cast<uint32_t*>(transpose) + band * (32 * 33);
-#pragma unroll
-                        for (int i = 0; i < W; ++i) buf[lane * 33 + i] = v[i];
-                        __syncwarp();
                         const int row0 = lane_row - lane, rows = min(32, c.p_end - row0);
-                        for (int i = 0; i < rows; ++i)
-                            if (col + lane < c.q_end) store_one(g, base + (row0 + i) * g.ldo + col + lane, buf[i * 33 + lane]);
-                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < W / 32; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = v[32 * h + i];
+                            __syncwarp();
+                            const int at = col + 32 * h + lane;
+                            for (int i = 0; i < rows; ++i)
+                                if (at < c.q_end) store_one(g, base + (row0 + i) * g.ldo + at, buf[i * 33 + lane]);
+                            __syncwarp();
+                        }
                     }
                 }
             }
