@@ -13,204 +13,369 @@ namespace {
 
 // ------------------------------------------------------------------- sort
 
-constexpr int kSortThreads = 256;
-constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kChunk = 4096;  // choices per block
-constexpr int kPerWarp = kChunk / kSortWarps;
 
-// Adds each warp's choices to its own histogram hist[warp][expert].  A warp's
-// choices are consecutive and taken 32 at a time, so that a choice's rank
-// among those of its expert is the count before its step plus the lanes below
-// it with the same expert: the order is that of the choices.
-template <typename F>
-__device__ __forceinline__ void walk_choices(const MoeSortArgs& a, int64_t chunk, int* hist, F&& f) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    int* mine = hist + warp * a.experts;
-    const int64_t first = chunk * kChunk + warp * kPerWarp;
-    for (int i = 0; i < kPerWarp; i += 32) {
-        const int64_t c = first + i + lane;
-        if (first + i >= a.choices) break;
-        const int id = c < a.choices ? a.ids[c] : -1;
-        const bool valid = id >= 0 && id < a.experts;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, valid ? id : -1);
-        const int before = valid ? mine[id] : 0;
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (valid && rank == 0) mine[id] = before + __popc(same);
-        __syncwarp();
-        if (c < a.choices) f(c, valid, id, before + rank);
+// Choices of the block that a walking warp takes: consecutive ones.
+__device__ __forceinline__ void warp_range(const MoeSortArgs& a, int walkers, int64_t& first, int64_t& end) {
+    const int warp = threadIdx.x / 32, per_warp = (kChunk / 32 + walkers - 1) / walkers * 32;
+    const int64_t begin = (int64_t)blockIdx.x * kChunk;
+    end = min(begin + kChunk, a.choices);
+    first = min(begin + (int64_t)warp * per_warp, end);
+    end = warp < walkers ? min(first + per_warp, end) : first;
+}
+
+// Histogram of the block's choices, one for each walking warp ([walkers][E])
+// or one for all.
+template <bool PER_WARP>
+__device__ __forceinline__ void count_chunk(const MoeSortArgs& a, int walkers, int* hist) {
+    const int E = (int)a.experts;
+    for (int i = threadIdx.x; i < (PER_WARP ? walkers : 1) * E; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    int64_t first, end;
+    warp_range(a, walkers, first, end);
+    int* mine = hist + (PER_WARP ? threadIdx.x / 32 * E : 0);
+    for (int64_t c = first + (threadIdx.x & 31); c < end; c += 32) {
+        const int id = a.ids[c];
+        if (id >= 0 && id < E) atomicAdd(&mine[id], 1);
     }
-}
-
-__device__ __forceinline__ void count_chunk(const MoeSortArgs& a, int64_t chunk, int* hist) {
-    for (int i = threadIdx.x; i < kSortWarps * a.experts; i += kSortThreads) hist[i] = 0;
-    __syncthreads();
-    walk_choices(a, chunk, hist, [](int64_t, bool, int, int) {});
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(kSortThreads) count_kernel(MoeSortArgs a) {
+__global__ void __launch_bounds__(1024) count_kernel(MoeSortArgs a, int walkers) {
     extern __shared__ int hist[];
-    count_chunk(a, blockIdx.x, hist);
-    for (int e = threadIdx.x; e < a.experts; e += kSortThreads) {
-        int n = 0;
-        for (int w = 0; w < kSortWarps; ++w) n += hist[w * a.experts + e];
-        a.counts[blockIdx.x * a.experts + e] = n;
-    }
+    count_chunk<false>(a, walkers, hist);
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) a.counts[blockIdx.x * a.experts + e] = hist[e];
 }
 
 // Every block finds all experts' totals and where each part begins, then the
 // rows of its own choices.  With one chunk the counts come from the block's
-// own histogram, else from count_kernel's.
-__global__ void __launch_bounds__(kSortThreads) place_kernel(MoeSortArgs a, int chunks) {
+// own histogram, else from count_kernel's, summed by as many threads an
+// expert as the block has.
+__global__ void __launch_bounds__(1024) place_kernel(MoeSortArgs a, int chunks, int walkers) {
     extern __shared__ int smem[];
     const int E = (int)a.experts;
-    int* hist = smem;                    // [warps][E]
-    int* begin = smem + kSortWarps * E;  // [E + 1]
-    int* total = begin + E + 1;          // [E]
-    int* mine = total + E;               // [E]: this chunk's first rank
-    count_chunk(a, blockIdx.x, hist);
-    for (int e = threadIdx.x; e < E; e += kSortThreads) {
-        int sum = 0, before = 0;
-        if (chunks == 1) {
-            for (int w = 0; w < kSortWarps; ++w) sum += hist[w * E + e];
-        } else {
-            for (int c = 0; c < chunks; ++c) {
-                if (c == (int)blockIdx.x) before = sum;
-                sum += a.counts[(int64_t)c * E + e];
-            }
+    int* hist = smem;                 // [walkers][E]
+    int* begin = smem + walkers * E;  // [E + 1]
+    int* total = begin + E + 1;       // [E]
+    int* mine = total + E;            // [E]: this chunk's first rank
+    for (int e = threadIdx.x; e < E; e += blockDim.x) total[e] = mine[e] = 0;
+    count_chunk<true>(a, walkers, hist);
+    if (chunks == 1) {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            int sum = 0;
+            for (int w = 0; w < walkers; ++w) sum += hist[w * E + e];
+            total[e] = sum;
         }
-        total[e] = sum;
-        mine[e] = before;
+    } else {
+        const int parts = max(1, (int)blockDim.x / E), step = (chunks + parts - 1) / parts;
+        for (int i = threadIdx.x; i < parts * E; i += blockDim.x) {
+            const int e = i % E, c0 = i / E * step, c1 = min(chunks, c0 + step);
+            int sum = 0, before = 0;
+#pragma unroll 16
+            for (int c = c0; c < c1; ++c) {
+                const int n = a.counts[(int64_t)c * E + e];
+                sum += n;
+                before += c < (int)blockIdx.x ? n : 0;
+            }
+            if (sum) atomicAdd(&total[e], sum);
+            if (before) atomicAdd(&mine[e], before);
+        }
     }
     __syncthreads();
-    if (threadIdx.x < 32) {  // exclusive scan of the rounded-up totals
-        int64_t run = 0;
+    if (threadIdx.x < 32) {  // exclusive scan of the rounded-up totals; their sum is the capacity at most, which is an int
+        const int align = (int)a.align;
+        int run = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + threadIdx.x;
-            const int64_t room = e < E ? (total[e] + a.align - 1) / a.align * a.align : 0;
-            int64_t incl = room;
+            const int n = e < E ? total[e] : 0, room = align == 1 ? n : (n + align - 1) / align * align;
+            int incl = room;
             for (int d = 1; d < 32; d *= 2) {
-                const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                const int up = __shfl_up_sync(0xFFFFFFFFu, incl, d);
                 if ((int)threadIdx.x >= d) incl += up;
             }
-            if (e < E) begin[e] = (int)(run + incl - room);
+            if (e < E) begin[e] = run + incl - room;
             run += __shfl_sync(0xFFFFFFFFu, incl, 31);
         }
-        if (threadIdx.x == 0) begin[E] = (int)run;
+        if (threadIdx.x == 0) begin[E] = run;
     }
     __syncthreads();
     // hist[w][e] becomes the row of the warp's first choice of e
-    for (int e = threadIdx.x; e < E; e += kSortThreads) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int row = begin[e] + mine[e];
-        for (int w = 0; w < kSortWarps; ++w) {
+        for (int w = 0; w < walkers; ++w) {
             const int n = hist[w * E + e];
             hist[w * E + e] = row;
             row += n;
         }
     }
     __syncthreads();
-    walk_choices(a, blockIdx.x, hist, [&](int64_t c, bool valid, int, int row) {
-        a.slots[c] = valid ? row : -1;
+    // A warp takes its choices 32 at a time, so that a choice's rank among those of its expert is the count before its step
+    // plus the lanes below it with the same expert: the order is that of the choices.  Lanes with the same expert are
+    // found bit by bit (__match_any_sync took about five times as long here).
+    int64_t first, end;
+    warp_range(a, walkers, first, end);
+    int* mine_w = hist + threadIdx.x / 32 * E;
+    const int lane = threadIdx.x & 31, bits = 32 - __clz(E);
+    for (int64_t c0 = first; c0 < end; c0 += 32) {
+        const int64_t c = c0 + lane;
+        int id = c < end ? a.ids[c] : -1;
+        const bool valid = id >= 0 && id < E;
+        id = valid ? id : E;
+        unsigned same = 0xFFFFFFFFu;
+        for (int b = 0; b < bits; ++b) {
+            const unsigned set = __ballot_sync(0xFFFFFFFFu, id >> b & 1);
+            same &= id >> b & 1 ? set : ~set;
+        }
+        const int row = valid ? mine_w[id] + __popc(same & ((1u << lane) - 1u)) : -1;
+        __syncwarp();
+        if (valid && (same >> lane) == 1u) mine_w[id] = row + 1;  // the last lane of the expert
+        __syncwarp();
+        if (c < end) a.slots[c] = row;
         if (valid) a.source[row] = (int)c;
-    });
+    }
     if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= E; e += kSortThreads) a.offsets[e] = begin[e];
-    // rows without a choice: behind each part, and behind the last
-    for (int e = blockIdx.x; e < E; e += gridDim.x)
-        for (int r = begin[e] + total[e] + threadIdx.x; r < begin[e + 1]; r += kSortThreads) a.source[r] = -1;
-    for (int64_t r = begin[E] + (int64_t)blockIdx.x * kSortThreads + threadIdx.x; r < a.capacity;
-         r += (int64_t)gridDim.x * kSortThreads)
+        for (int e = threadIdx.x; e <= E; e += blockDim.x) a.offsets[e] = begin[e];
+    // rows without a choice: behind each part (a warp each), and behind the last
+    if (a.align > 1)
+        for (int e = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; e < E; e += gridDim.x * (blockDim.x / 32))
+            for (int r = begin[e] + total[e] + (threadIdx.x & 31); r < begin[e + 1]; r += 32) a.source[r] = -1;
+    for (int64_t r = begin[E] + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.capacity;
+         r += (int64_t)gridDim.x * blockDim.x)
         a.source[r] = -1;
 }
 
 // ------------------------------------------------------------------- rows
 
-template <Elt ELT>
-__device__ __forceinline__ float load(const void* p, int64_t i) {
-    if constexpr (ELT == Elt::BF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-    return static_cast<const float*>(p)[i];
-}
-
-template <Elt ELT>
-__device__ __forceinline__ void store(void* p, int64_t i, float v) {
-    uint32_t u = __float_as_uint(v);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0x7FC00000u;
-    if constexpr (ELT == Elt::BF16)
-        static_cast<uint16_t*>(p)[i] = (uint16_t)bf16_rne(u);
-    else
-        static_cast<uint32_t*>(p)[i] = u;
-}
-
 constexpr int kRowThreads = 256;
+constexpr int kGradThreads = 128;
+constexpr int kTogether = 4;  // choices of a token taken at a time
 
-template <Elt ELT>
+// VEC consecutive elements: 32 bytes (bf16: 16, fp32: 8), or one where rows
+// do not begin on 32 bytes.
+template <Elt ELT, int VEC>
+struct Piece {
+    static constexpr int kWords = VEC == 1 ? 1 : VEC * (ELT == Elt::BF16 ? 2 : 4) / 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void read(const void* p, int64_t i) {
+        if constexpr (VEC == 1) {
+            if constexpr (ELT == Elt::BF16)
+                w[0] = static_cast<const uint16_t*>(p)[i];
+            else
+                w[0] = static_cast<const uint32_t*>(p)[i];
+        } else if constexpr (kWords == 4) {
+            asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "l"(static_cast<const char*>(p) + i * (ELT == Elt::BF16 ? 2 : 4)));
+        } else {
+            ld32(w, static_cast<const char*>(p) + i * (ELT == Elt::BF16 ? 2 : 4));
+        }
+    }
+    __device__ __forceinline__ void write(void* p, int64_t i) const {
+        if constexpr (VEC == 1) {
+            if constexpr (ELT == Elt::BF16)
+                static_cast<uint16_t*>(p)[i] = (uint16_t)w[0];
+            else
+                static_cast<uint32_t*>(p)[i] = w[0];
+        } else if constexpr (kWords == 4) {
+            st16(static_cast<char*>(p) + i * (ELT == Elt::BF16 ? 2 : 4), w[0], w[1], w[2], w[3]);
+        } else {
+            st32(static_cast<char*>(p) + i * (ELT == Elt::BF16 ? 2 : 4), w);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (uint32_t& v : w) v = 0;
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (ELT == Elt::FP32) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+    // Rounds element i to nearest even; every i in ascending order.
+    __device__ __forceinline__ void set(int i, float v) {
+        uint32_t u = __float_as_uint(v);
+        if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0x7FC00000u;
+        if constexpr (ELT == Elt::FP32) w[i] = u;
+        else if (i & 1) w[i / 2] |= bf16_rne(u) << 16;
+        else w[i / 2] = bf16_rne(u);
+    }
+};
+
+// One row of the order to blockIdx.x, a slice of its pieces to blockIdx.y.
+template <Elt ELT, int VEC>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
+    const int64_t pieces = a.H / VEC;
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
         const int c = a.source[r];
         const int64_t t = c < 0 ? -1 : c / a.topk;
         const bool there = t >= 0 && t < a.T;
-        for (int64_t h = threadIdx.x; h < a.H; h += kRowThreads)
-            if constexpr (ELT == Elt::BF16)
-                static_cast<uint16_t*>(a.out)[r * a.H + h] =
-                    there ? static_cast<const uint16_t*>(a.tokens)[t * a.ld_tokens + h] : (uint16_t)0;
+        for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.y * kRowThreads) {
+            Piece<ELT, VEC> p;
+            if (there)
+                p.read(a.tokens, t * a.ld_tokens + i * VEC);
             else
-                static_cast<uint32_t*>(a.out)[r * a.H + h] =
-                    there ? static_cast<const uint32_t*>(a.tokens)[t * a.ld_tokens + h] : 0u;
+                p.clear();
+            p.write(a.out, r * a.H + i * VEC);
+        }
     }
 }
 
-template <Elt ELT>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(MoeRowsArgs a) {
+// out[t] = sum_j w_j y[slot_j]: one token to blockIdx.x, a slice of its pieces
+// to blockIdx.y; the rows of four choices are loaded before they are added.
+template <Elt ELT, int VEC>
+__global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(MoeRowsArgs a) {
+    const int64_t pieces = a.H / VEC;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x)
-        for (int64_t h = threadIdx.x; h < a.H; h += kRowThreads) {
-            float sum = 0.0f;
-            for (int64_t j = 0; j < a.topk; ++j) {
-                const int64_t r = a.slots[t * a.topk + j];
-                if (r < 0 || r >= a.R) continue;
-                const float y = load<ELT>(a.rows, r * a.ld_rows + h);
-                sum = a.weights ? fmaf(a.weights[t * a.topk + j], y, sum) : sum + y;
+        for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.y * kRowThreads) {
+            float sum[VEC] = {};
+            for (int64_t j0 = 0; j0 < a.topk; j0 += kTogether) {
+                Piece<ELT, VEC> p[kTogether];
+                bool there[kTogether];
+                float w[kTogether];
+#pragma unroll
+                for (int j = 0; j < kTogether; ++j) {
+                    const int64_t c = t * a.topk + j0 + j;
+                    const int64_t r = j0 + j < a.topk ? a.slots[c] : -1;
+                    there[j] = r >= 0 && r < a.R;
+                    w[j] = there[j] && a.weights ? a.weights[c] : 1.0f;
+                    if (there[j]) p[j].read(a.rows, r * a.ld_rows + i * VEC);
+                }
+#pragma unroll
+                for (int j = 0; j < kTogether; ++j)
+                    if (there[j])
+#pragma unroll
+                        for (int q = 0; q < VEC; ++q) sum[q] = fmaf(w[j], p[j].at(q), sum[q]);
             }
-            store<ELT>(a.out, t * a.H + h, sum);
+            Piece<ELT, VEC> o;
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) o.set(q, sum[q]);
+            o.write(a.out, t * a.H + i * VEC);
         }
 }
 
-template <Elt ELT>
-__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(MoeRowsArgs a) {
-    __shared__ float part[kRowThreads / 32];
+// TG choices of one token to a block.  The dot products are summed in a fixed
+// order: a thread's pieces, the warp's lanes, the warps.  The blocks behind
+// the tokens' clear the rows of no choice.
+template <Elt ELT, int VEC, int TG>
+__global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsArgs a, int64_t work, int64_t work_blocks) {
+    const int64_t pieces = a.H / VEC, n = a.T * a.topk;
+    if (blockIdx.x >= work_blocks) {
+        // each thread looks at one of the block's next rows; those of no choice are cleared by the whole block
+        __shared__ int empty[kGradThreads];
+        __shared__ int found;
+        for (int64_t r0 = (blockIdx.x - work_blocks) * kGradThreads; r0 < a.R; r0 += (gridDim.x - work_blocks) * kGradThreads) {
+            if (threadIdx.x == 0) found = 0;
+            __syncthreads();
+            const int64_t r = r0 + threadIdx.x;
+            const int c = r < a.R ? a.source[r] : 0;
+            if (c < 0 || c >= n) empty[atomicAdd(&found, 1)] = (int)threadIdx.x;
+            __syncthreads();
+            Piece<ELT, VEC> zero;
+            zero.clear();
+            for (int x = 0; x < found; ++x)
+                for (int64_t i = threadIdx.x; i < pieces; i += kGradThreads) zero.write(a.out, (r0 + empty[x]) * a.H + i * VEC);
+            __syncthreads();
+        }
+        return;
+    }
+    __shared__ float part[kGradThreads / 32][TG];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int64_t n = a.T * a.topk;
-    for (int64_t c = blockIdx.x; c < n; c += gridDim.x) {
-        const int64_t t = c / a.topk, r = a.slots[c];
-        const bool there = r >= 0 && r < a.R;
-        float dot = 0.0f;
-        if (there) {
-            const float w = a.weights[c];
-            for (int64_t h = threadIdx.x; h < a.H; h += kRowThreads) {
-                const float g = load<ELT>(a.tokens, t * a.ld_tokens + h);
-                dot = fmaf(g, load<ELT>(a.rows, r * a.ld_rows + h), dot);
-                store<ELT>(a.out, r * a.H + h, w * g);
-            }
+    const int64_t groups = (a.topk + TG - 1) / TG;
+    for (int64_t x = blockIdx.x; x < work; x += work_blocks) {
+        int64_t t, j0;
+        split_index(x, groups, t, j0);
+        j0 *= TG;
+        float dot[TG] = {}, w[TG];
+        int64_t row[TG];
+#pragma unroll
+        for (int j = 0; j < TG; ++j) {
+            const int64_t c = t * a.topk + j0 + j;
+            row[j] = j0 + j < a.topk ? a.slots[c] : -1;
+            if (row[j] >= a.R) row[j] = -1;
+            w[j] = row[j] >= 0 ? a.weights[c] : 0.0f;
         }
-        for (int d = 16; d; d /= 2) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
-        if (lane == 0) part[warp] = dot;
+#pragma unroll 1
+        for (int64_t i = threadIdx.x; i < pieces; i += kGradThreads) {
+            Piece<ELT, VEC> g, y[TG];
+            g.read(a.tokens, t * a.ld_tokens + i * VEC);
+#pragma unroll
+            for (int j = 0; j < TG; ++j)
+                if (row[j] >= 0) y[j].read(a.rows, row[j] * a.ld_rows + i * VEC);
+#pragma unroll
+            for (int j = 0; j < TG; ++j)
+                if (row[j] >= 0) {
+                    Piece<ELT, VEC> o;
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) {
+                        dot[j] = fmaf(g.at(q), y[j].at(q), dot[j]);
+                        o.set(q, w[j] * g.at(q));
+                    }
+                    o.write(a.out, row[j] * a.H + i * VEC);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < TG; ++j) {
+#pragma unroll
+            for (int d = 16; d; d /= 2) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+            if (lane == 0) part[warp][j] = dot[j];
+        }
         __syncthreads();
-        if (threadIdx.x == 0) {
+        if (threadIdx.x < TG && j0 + threadIdx.x < a.topk) {
             float sum = 0.0f;
-            for (int w = 0; w < kRowThreads / 32; ++w) sum += part[w];
-            a.d_weights[c] = there ? sum : 0.0f;
+#pragma unroll
+            for (int v = 0; v < kGradThreads / 32; ++v) sum += part[v][threadIdx.x];
+            a.d_weights[t * a.topk + j0 + threadIdx.x] = sum;
         }
         __syncthreads();
-    }
-    for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-        if (a.source[r] >= 0 && a.source[r] < n) continue;
-        for (int64_t h = threadIdx.x; h < a.H; h += kRowThreads) store<ELT>(a.out, r * a.H + h, 0.0f);
     }
 }
 
-unsigned row_grid(int64_t rows) {
-    const int64_t most = (int64_t)sm_count() * 64;
-    return (unsigned)(rows < 1 ? 1 : rows < most ? rows : most);
+// Rows that begin on 32 bytes and hold whole pieces.
+template <Elt ELT>
+bool whole_pieces(const MoeRowsArgs& a) {
+    constexpr int64_t es = ELT == Elt::BF16 ? 2 : 4;
+    const auto on32 = [](const void* p, int64_t rows, int64_t bytes) {
+        return reinterpret_cast<uintptr_t>(p) % 32 == 0 && (rows <= 1 || bytes % 32 == 0);
+    };
+    return a.H * es % 32 == 0 && on32(a.tokens, a.T, a.ld_tokens * es) && on32(a.rows, a.R, a.ld_rows * es) &&
+           on32(a.out, 2, a.H * es);
+}
+
+constexpr int64_t kMostBlocks = INT64_C(0x7FFFFFFF);
+
+// One row to a block; few rows are cut into slices so that the device is full.
+dim3 row_grid(int64_t rows, int64_t pieces) {
+    const int64_t slices = ceil_div(pieces, kRowThreads), wanted = ceil_div((int64_t)sm_count() * 8, rows);
+    return dim3((unsigned)(rows < kMostBlocks ? rows : kMostBlocks),
+                (unsigned)(wanted < 1 ? 1 : wanted < slices ? wanted : slices < 65535 ? slices : 65535));
+}
+
+template <Elt ELT, int VEC>
+cudaError_t rows_launch(int what, const MoeRowsArgs& a, cudaStream_t s) {
+    if (what == 0) {
+        dispatch_kernel<ELT, VEC><<<row_grid(a.R, a.H / VEC), kRowThreads, 0, s>>>(a);
+    } else if (what == 1) {
+        combine_kernel<ELT, VEC><<<row_grid(a.T, a.H / VEC), kRowThreads, 0, s>>>(a);
+    } else {
+        // four choices to a block, or one where that leaves the device empty (64 tokens of 7184, topk 4, bf16: 10.3 us with
+        // four, GRADSMALL with one; 8191 tokens: 214 and 282)
+        const int together = a.T * ceil_div(a.topk, kTogether) < 8 * (int64_t)sm_count() ? 1 : kTogether;
+        const int64_t work = a.T * ceil_div(a.topk, together), work_blocks = work < (1 << 30) ? work : 1 << 30;
+        const int64_t room = ceil_div(a.R, kGradThreads), clear = room < sm_count() ? room : sm_count();
+        const unsigned grid = (unsigned)(work_blocks + clear);
+        constexpr int V = VEC == 1 ? 1 : VEC / 2;
+        if (together == 1)
+            combine_grad_kernel<ELT, V, 1><<<grid, kGradThreads, 0, s>>>(a, work, work_blocks);
+        else
+            combine_grad_kernel<ELT, V, kTogether><<<grid, kGradThreads, 0, s>>>(a, work, work_blocks);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t rows_launch(int what, Elt elt, const MoeRowsArgs& a, cudaStream_t s) {
+    if (elt == Elt::BF16)
+        return whole_pieces<Elt::BF16>(a) ? rows_launch<Elt::BF16, 16>(what, a, s) : rows_launch<Elt::BF16, 1>(what, a, s);
+    return whole_pieces<Elt::FP32>(a) ? rows_launch<Elt::FP32, 8>(what, a, s) : rows_launch<Elt::FP32, 1>(what, a, s);
 }
 
 }  // namespace
@@ -219,47 +384,29 @@ int64_t moe_sort_chunks(int64_t choices) { return ceil_div(choices, kChunk); }
 
 cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
     const int chunks = (int)moe_sort_chunks(a.choices);
-    const int hist = (int)(kSortWarps * a.experts * 4), place = hist + (int)(3 * a.experts + 1) * 4;
+    // as many warps as have choices and as shared memory has room for histograms of
+    const int threads = a.choices <= 1024 ? 256 : 1024;
+    int walkers = (int)(INT64_C(128) * 1024 / (a.experts * 4));
+    walkers = walkers < threads / 32 ? walkers : threads / 32;
+    const int one = (int)a.experts * 4, hist = walkers * one, place = hist + (int)(3 * a.experts + 1) * 4;
     if (place > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, hist);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, place);
+        const cudaError_t e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, place);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return e;
         }
     }
     if (chunks > 1) {
-        count_kernel<<<chunks, kSortThreads, hist, s>>>(a);
+        count_kernel<<<chunks, threads, one, s>>>(a, walkers);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    place_kernel<<<chunks, kSortThreads, place, s>>>(a, chunks);
+    place_kernel<<<chunks, threads, place, s>>>(a, chunks, walkers);
     return cudaGetLastError();
 }
 
-cudaError_t launch_moe_dispatch(Elt elt, const MoeRowsArgs& a, cudaStream_t s) {
-    if (elt == Elt::BF16)
-        dispatch_kernel<Elt::BF16><<<row_grid(a.R), kRowThreads, 0, s>>>(a);
-    else
-        dispatch_kernel<Elt::FP32><<<row_grid(a.R), kRowThreads, 0, s>>>(a);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_moe_combine(Elt elt, const MoeRowsArgs& a, cudaStream_t s) {
-    if (elt == Elt::BF16)
-        combine_kernel<Elt::BF16><<<row_grid(a.T), kRowThreads, 0, s>>>(a);
-    else
-        combine_kernel<Elt::FP32><<<row_grid(a.T), kRowThreads, 0, s>>>(a);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_moe_combine_grad(Elt elt, const MoeRowsArgs& a, cudaStream_t s) {
-    const int64_t work = a.T * a.topk > a.R ? a.T * a.topk : a.R;
-    if (elt == Elt::BF16)
-        combine_grad_kernel<Elt::BF16><<<row_grid(work), kRowThreads, 0, s>>>(a);
-    else
-        combine_grad_kernel<Elt::FP32><<<row_grid(work), kRowThreads, 0, s>>>(a);
-    return cudaGetLastError();
-}
+cudaError_t launch_moe_dispatch(Elt elt, const MoeRowsArgs& a, cudaStream_t s) { return rows_launch(0, elt, a, s); }
+cudaError_t launch_moe_combine(Elt elt, const MoeRowsArgs& a, cudaStream_t s) { return rows_launch(1, elt, a, s); }
+cudaError_t launch_moe_combine_grad(Elt elt, const MoeRowsArgs& a, cudaStream_t s) { return rows_launch(2, elt, a, s); }
 
 }  // namespace mxq

@@ -37,20 +37,88 @@ __device__ __forceinline__ int64_t source_row(const Quant128Args& a, int64_t r) 
     return t < a.rows ? t : -1;
 }
 
-// One warp per 1x128 block.
+// 16 consecutive elements as fp32 patterns, 32-byte loads.
+template <Elt ELT>
+struct Unit {
+    uint32_t w[ELT == Elt::BF16 ? 8 : 16];
+
+    __device__ __forceinline__ void load(const void* x, int64_t i) {
+        if constexpr (ELT == Elt::BF16) {
+            ld32(w, static_cast<const uint16_t*>(x) + i);
+        } else {
+            ld32(reinterpret_cast<uint32_t(&)[8]>(w[0]), static_cast<const uint32_t*>(x) + i);
+            ld32(reinterpret_cast<uint32_t(&)[8]>(w[8]), static_cast<const uint32_t*>(x) + i + 8);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (uint32_t& v : w) v = 0;
+    }
+    __device__ __forceinline__ uint32_t at(int i) const {
+        if constexpr (ELT == Elt::BF16) return i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16;
+        return w[i];
+    }
+};
+
+// Rows of 16-element units, eight lanes to a 1x128 block: 32 bytes (bf16) or
+// 64 (fp32) of loads and one 16-byte store a lane, the block's maximum by
+// three shuffles.  Memory-bound; UNITS units of a lane are loaded before the
+// first is used (4 of bf16, 2 of fp32: 128 bytes in flight a thread).
+// 8192 x 7184 bf16: see the table of figures in the launcher's comment.
+template <Elt ELT, int UNITS>
+__global__ void __launch_bounds__(256) quant_rows_unit_kernel(Quant128Args a, int64_t nb) {
+    const int64_t first = (int64_t)blockIdx.x * (256 * UNITS) + threadIdx.x, total = a.out_rows * nb * 8;
+    Unit<ELT> u[UNITS];
+    int64_t row[UNITS], b[UNITS];
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+        split_index((first + 256 * i) >> 3, nb, row[i], b[i]);
+        const int64_t k = b[i] * 128 + (threadIdx.x & 7) * 16;
+        const bool inside = first + 256 * i < total && k < a.K;
+        const int64_t src = inside ? source_row(a, row[i]) : -1;
+        if (src >= 0)
+            u[i].load(a.x, src * a.ldx + k);
+        else
+            u[i].clear();
+    }
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) amax = max(amax, u[i].at(j) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        const uint32_t code = scale_code128(amax), inv = inv_scale128(code);
+        if (first + 256 * i >= total) continue;
+        const int64_t k = b[i] * 128 + (threadIdx.x & 7) * 16;
+        if ((threadIdx.x & 7) == 0) a.scales[row[i] * nb + b[i]] = (uint8_t)code;
+        if (k >= a.K) continue;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            o[j] = e4m3x2_from_f32(f32_mul(u[i].at(4 * j + 1), inv), f32_mul(u[i].at(4 * j), inv)) |
+                   e4m3x2_from_f32(f32_mul(u[i].at(4 * j + 3), inv), f32_mul(u[i].at(4 * j + 2), inv)) << 16;
+            if (code == 255u) o[j] = 0x7F7F7F7Fu;
+        }
+        st16(a.data + row[i] * a.K + k, o[0], o[1], o[2], o[3]);
+    }
+}
+
+// Any alignment and any K: one warp per 1x128 block, an element at a time.
 template <Elt ELT>
 __global__ void __launch_bounds__(256) quant_rows_kernel(Quant128Args a, int64_t nb) {
     const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32;
     if (unit >= a.out_rows * nb) return;
-    const int64_t r = unit / nb, b = unit - r * nb;
+    int64_t r, b;
+    split_index(unit, nb, r, b);
     const int lane = threadIdx.x & 31;
     const int64_t src = source_row(a, r);
-    const int64_t k0 = b * 128 + lane * 4;
+    const int64_t k0 = b * 128 + lane;
     uint32_t v[4];
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[i] = src >= 0 && k0 + i < a.K ? load_f32<ELT>(a.x, src * a.ldx + k0 + i) : 0u;
+        v[i] = src >= 0 && k0 + 32 * i < a.K ? load_f32<ELT>(a.x, src * a.ldx + k0 + 32 * i) : 0u;
         amax = max(amax, v[i] & 0x7FFFFFFFu);
     }
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
@@ -58,12 +126,88 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(Quant128Args a, int64_t
     if (lane == 0) a.scales[r * nb + b] = (uint8_t)code;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (k0 + i < a.K)
-            a.data[r * a.K + k0 + i] =
+        if (k0 + 32 * i < a.K)
+            a.data[r * a.K + k0 + 32 * i] =
                 code == 255u ? 0x7F : (uint8_t)e4m3x2_from_f32(0u, f32_mul(v[i], inv_scale128(code)));
 }
 
-// One thread per 128x1 block.
+// 128 rows x 64 columns a block, 8 columns x 4 rows a thread, all in registers
+// between the maximum and the rounding: each element is read once.  The
+// maximum of a column goes through two shuffles (four threads of a warp share
+// it) and shared memory.
+template <Elt ELT>
+__global__ void __launch_bounds__(256) quant_columns_tile_kernel(Quant128Args a) {
+    constexpr int R = 4;
+    __shared__ uint4 top[8][16];  // [warp][64 columns]
+    __shared__ uint2 codes[8];    // 64 bytes
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+    const int64_t c = (int64_t)blockIdx.x * 64 + tx * 8, r0 = (int64_t)blockIdx.y * 128 + ty;
+    uint32_t v[R][ELT == Elt::BF16 ? 4 : 8];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = r0 + 32 * i;
+        const int64_t src = r < a.out_rows && c < a.K ? source_row(a, r) : -1;
+#pragma unroll
+        for (uint32_t& x : v[i]) x = 0;
+        if (src >= 0) {
+            if constexpr (ELT == Elt::BF16) {
+                const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + src * a.ldx + c);
+                v[i][0] = q.x, v[i][1] = q.y, v[i][2] = q.z, v[i][3] = q.w;
+            } else {
+                ld32(v[i], static_cast<const uint32_t*>(a.x) + src * a.ldx + c);
+            }
+        }
+    }
+    const auto at = [&](int i, int j) {
+        if constexpr (ELT == Elt::BF16) return j & 1 ? v[i][j / 2] & 0xFFFF0000u : v[i][j / 2] << 16;
+        else return v[i][j];
+    };
+    uint32_t m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        m[j] = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) m[j] = max(m[j], at(i, j) & 0x7FFFFFFFu);
+        m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 8));
+        m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+    }
+    if ((threadIdx.x & 31) < 8) {
+        top[threadIdx.x / 32][2 * tx] = make_uint4(m[0], m[1], m[2], m[3]);
+        top[threadIdx.x / 32][2 * tx + 1] = make_uint4(m[4], m[5], m[6], m[7]);
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) amax = max(amax, reinterpret_cast<const uint32_t*>(top[w])[threadIdx.x]);
+        const uint8_t own = (uint8_t)scale_code128(amax);
+        reinterpret_cast<uint8_t*>(codes)[threadIdx.x] = own;
+        const int64_t column = (int64_t)blockIdx.x * 64 + threadIdx.x;
+        if (column < a.K) a.scales[(int64_t)blockIdx.y * a.K + column] = own;
+    }
+    __syncthreads();
+    if (c >= a.K) return;
+    uint32_t code[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) code[j] = ((j < 4 ? codes[tx].x : codes[tx].y) >> (8 * (j & 3))) & 0xFFu;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (r0 + 32 * i >= a.out_rows) break;
+        uint32_t o[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = 4 * h;
+            o[h] = e4m3x2_from_f32(f32_mul(at(i, j + 1), inv_scale128(code[j + 1])), f32_mul(at(i, j), inv_scale128(code[j]))) |
+                   e4m3x2_from_f32(f32_mul(at(i, j + 3), inv_scale128(code[j + 3])), f32_mul(at(i, j + 2), inv_scale128(code[j + 2]))) << 16;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (code[j + q] == 255u) o[h] = (o[h] & ~(0xFFu << (8 * q))) | 0x7Fu << (8 * q);
+        }
+        *reinterpret_cast<uint2*>(a.data + (r0 + 32 * i) * a.K + c) = make_uint2(o[0], o[1]);
+    }
+}
+
+// Any alignment and any K: one thread per 128x1 block.
 template <Elt ELT>
 __global__ void __launch_bounds__(128) quant_columns_kernel(Quant128Args a) {
     const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
@@ -83,9 +227,16 @@ __global__ void __launch_bounds__(128) quant_columns_kernel(Quant128Args a) {
     }
 }
 
+bool on(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 template <Elt ELT>
 cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
+    constexpr int64_t es = ELT == Elt::BF16 ? 2 : 4;
+    const bool one_row = a.rows <= 1;  // then the stride is not used
     if (columns) {
+        // 8 columns: 16 bytes of bf16, 32 of fp32, 8 of payload and scales
+        const bool tiled = a.K % 8 == 0 && on(a.x, 8 * es) && (one_row || a.ldx * es % (8 * es) == 0) && on(a.data, 8) &&
+                           on(a.scales, 8);
         // blockIdx.y reaches 65535: 2^23 rows at a time
         for (int64_t r0 = 0; r0 < a.out_rows; r0 += INT64_C(128) * 65535) {
             Quant128Args p = a;
@@ -98,8 +249,11 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
             }
             p.data = a.data + r0 * a.K;
             p.scales = a.scales + r0 / 128 * a.K;
-            quant_columns_kernel<ELT>
-                <<<dim3((unsigned)ceil_div(a.K, 128), (unsigned)ceil_div(p.out_rows, 128)), 128, 0, s>>>(p);
+            const unsigned y = (unsigned)ceil_div(p.out_rows, 128);
+            if (tiled)
+                quant_columns_tile_kernel<ELT><<<dim3((unsigned)ceil_div(a.K, 64), y), 256, 0, s>>>(p);
+            else
+                quant_columns_kernel<ELT><<<dim3((unsigned)ceil_div(a.K, 128), y), 128, 0, s>>>(p);
             const cudaError_t e = cudaGetLastError();
             if (e != cudaSuccess) return e;
         }
@@ -107,6 +261,13 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
     }
     const int64_t nb = ceil_div(a.K, 128);
     if (ceil_div(a.out_rows * nb, 8) > INT64_C(0x7FFFFFFF)) return cudaErrorInvalidValue;
+    // units of 16 elements: 32-byte loads and 16-byte stores
+    if (a.K % 16 == 0 && on(a.x, 32) && (one_row || a.ldx * es % 32 == 0) && on(a.data, 16)) {
+        constexpr int units = 1;
+        quant_rows_unit_kernel<ELT, units>
+            <<<(unsigned)ceil_div(a.out_rows * nb * 8, 256 * units), 256, 0, s>>>(a, nb);
+        return cudaGetLastError();
+    }
     quant_rows_kernel<ELT><<<(unsigned)ceil_div(a.out_rows * nb, 8), 256, 0, s>>>(a, nb);
     return cudaGetLastError();
 }
