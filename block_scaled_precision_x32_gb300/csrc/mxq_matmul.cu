@@ -23,6 +23,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "mxq_device.cuh"
@@ -33,6 +34,7 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMostExperts = 1024;
 // Scales move in groups of two words a row, eight blocks of depth: what a warp spends on a group (its loads, which the
 // proxy fence waits for, and the fence) is about 2000 clocks, as long as the products of four blocks.
 constexpr int kGroup = 8;
@@ -217,6 +219,23 @@ __device__ __forceinline__ void store_one(const Problem& g, int64_t at, uint32_t
         static_cast<uint32_t*>(g.out)[at] = u;
 }
 
+// Four neighbours of one output row, the first `n` of them inside.
+__device__ __forceinline__ void store_four(const Problem& g, int64_t at, int n, float4 v) {
+    const uint32_t u[4] = {canonical(__float_as_uint(v.x)), canonical(__float_as_uint(v.y)), canonical(__float_as_uint(v.z)),
+                           canonical(__float_as_uint(v.w))};
+    if (g.wide && n >= 4) {  // at is a multiple of four then
+        if (g.out_bf16)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + at) =
+                make_uint2(bf16_rne(u[0]) | bf16_rne(u[1]) << 16, bf16_rne(u[2]) | bf16_rne(u[3]) << 16);
+        else
+            *reinterpret_cast<uint4*>(static_cast<uint32_t*>(g.out) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) store_one(g, at + i, u[i]);
+}
+
 // QT: columns of the accumulator.  CG 2: a pair of blocks, 256 lanes, each
 // holding half of Q's rows; the output's rows are P's.  CG 1: 128 lanes; the
 // output's rows are Q's (few tokens, many features).  SPLIT: the blocks of a
@@ -227,16 +246,16 @@ struct Shape {
     static constexpr int kQRows = QT / CG;                           // rows of Q that a block loads
     static constexpr int kPBytes = 128 * 128, kQBytes = kQRows * 128;
     static constexpr int kStageBytes = kPBytes + kQBytes;
-    static constexpr int kStages = CG == 2 ? 6 : QT == 128 ? 6 : QT == 64 ? 4 : 5;
+    static constexpr int kStages = CG == 2 ? 6 : QT == 128 ? (SPLIT ? 3 : 6) : QT == 64 ? 4 : 5;
     static constexpr int kQAtoms = QT <= 128 ? 1 : QT / 128;         // 128 scales each
     static constexpr int kScaleBytes = 512 * (1 + kQAtoms);           // of four blocks
     static constexpr int kScaleColumns = 4 * (1 + kQAtoms);
     static constexpr int kScaleParts = kRing * (kGroup / 4);
-    // Two accumulators.  Two of 256 columns and the scales exceed the 512 columns, so
+    // Two accumulators (one where a block has one tile).  Two of 256 columns and the scales exceed the 512 columns, so
     // there the second begins 64 columns before the first one's end and the
     // shared ones are taken out first.
     static constexpr int kAcc1 = QT == 256 ? 192 : QT;
-    static constexpr int kScaleAt = QT == 256 ? 448 : 2 * QT;
+    static constexpr int kScaleAt = QT == 256 ? 448 : SPLIT ? QT : 2 * QT;
     static constexpr int kUsed = kScaleAt + kScaleParts * kScaleColumns;
     static constexpr int kColumns = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr int kTranspose = CG == 2 ? 4 * 32 * 33 * 4 : 0;
@@ -300,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (CG == 2 || SPLIT) cluster_sync();
+    if constexpr (CG == 2) cluster_sync();  // its barriers take the other block's arrivals from here on
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_at, 0);  // known to be the same in a warp: see elect_one()
 
@@ -616,14 +635,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();
         if (first_tile < tiles) {
             const Tile c = tile_at<PT, QT>(g, rag, first_tile);
+            const int64_t base = g.ragged == kDepth ? c.e * g.out_expert : 0;
             const uint32_t part = smem_u32(stages);
-            const int row = c.p0 + (threadIdx.x & 127);
-            const int j1 = min(QT * ((int)rank + 1) / split, c.q_end - c.q0);
-            for (int j = QT * (int)rank / split + (threadIdx.x >> 7); j < j1; j += kThreads / 128) {
-                float sum = 0.0f;
-                for (int s = 0; s < split; ++s) sum += ld_cluster_f32(map_rank(part + (j * 128 + (threadIdx.x & 127)) * 4, s));
-                const int64_t base = g.ragged == kDepth ? c.e * g.out_expert : 0;
-                if (row < c.p_end) store_one(g, base + (int64_t)(c.q0 + j) * g.ldo + row, __float_as_uint(sum));
+            const int j0 = QT * (int)rank / split, j1 = min(QT * ((int)rank + 1) / split, c.q_end - c.q0);
+            // four neighbouring rows of P a thread, the sums of all blocks on their way together
+            for (int x = threadIdx.x; x < (j1 - j0) * 32; x += kThreads) {
+                const int j = j0 + (x >> 5), r = (x & 31) * 4;
+                float4 v[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < split) v[s] = ld_cluster_f32x4(map_rank(part + (j * 128 + r) * 4, s));
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < split) sum.x += v[s].x, sum.y += v[s].y, sum.z += v[s].z, sum.w += v[s].w;
+                store_four(g, base + (int64_t)(c.q0 + j) * g.ldo + c.p0 + r, c.p_end - (c.p0 + r), sum);
             }
         }
     }
@@ -725,8 +751,16 @@ cudaError_t launch(const MatmulArgs& m, const MatOperand& p, const MatOperand& q
     if (tiles > INT64_C(0x3FFFFFFF)) return cudaErrorInvalidValue;
     auto kernel = matmul_kernel<QT, CG, SPLIT>;
     const size_t smem = S::smem((int)m.E);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // once a device: the most that any number of experts asks for
+    static std::atomic<bool> allowed[64];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
+    if (device >= 64 || !allowed[device].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem(kMostExperts));
+        if (e != cudaSuccess) return e;
+        if (device < 64) allowed[device].store(true, std::memory_order_relaxed);
+    }
 
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute cluster{};
@@ -760,9 +794,12 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
         const int64_t rows = grouped ? ceil_div(m.a.rows, m.E) : m.a.rows;
         const int64_t qt = m.a.mn || rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
         const int64_t tiles = ceil_div(m.b.rows, 128) * ceil_div(m.a.rows, qt), quads = ceil_div(m.depth, 512);
+        // as many blocks to a tile's depth as the device has room for at once (two a multiprocessor), and no more than
+        // shorten the longest share
         int split = 1;
         if (r == kNone)
-            while (split < 8 && split * 2 <= quads && tiles * split * 2 <= 2 * sm_count()) split *= 2;
+            for (int x = 2; x <= 8 && x <= quads && tiles * x <= 2 * sm_count(); ++x)
+                if (ceil_div(quads, x) < ceil_div(quads, split)) split = x;
         if (split > 1)
             e = qt == 16   ? launch<16, 1, true>(m, m.b, m.a, r, split, s)
                 : qt == 32 ? launch<32, 1, true>(m, m.b, m.a, r, split, s)
