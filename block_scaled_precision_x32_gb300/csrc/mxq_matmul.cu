@@ -42,12 +42,19 @@ constexpr int kRing = 2;  // groups, both in shared and in tensor memory
 
 // The operand whose rows are the accumulator's lanes is called P, the one
 // whose rows are its columns Q.
+enum ScaleForm {
+    kTiles,          // an fp32 power of two per 128x128 tile
+    kAlongDepth,     // a byte per row and block, a row's bytes together
+    kAcrossDepth,    // a byte per row and block, a block's bytes together
+    kAcrossAligned,  // and those of four neighbouring rows in an aligned word
+};
+
 struct ScaleSource {
     const void* base;
     int64_t s_row, s_kb, s_expert;
+    int64_t bytes;  // kAlongDepth: of the whole matrix
     int rows;
-    bool tiles;
-    bool words;  // four consecutive bytes of a row can be read as one aligned word
+    int form;
 };
 
 enum RaggedBy { kNone, kRowsOfP, kRowsOfQ, kDepth };
@@ -157,54 +164,112 @@ __device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t
     return c;
 }
 
-// The scales of W * 32 rows from row0 on and four blocks from kb on, read by
-// one warp.  Loads are unconditional, at indexes clamped into the operand: a
-// row behind its end has no output and a block behind kb_end no product.
-// They are raw until pack(), so that a warp's loads are all in flight at once
-// and those of the next four blocks while the ring is full.
+// The scales of W * 32 rows from row0 on and kGroup = 8 blocks from kb on, read
+// by one warp.  Loads are unconditional, at indexes clamped into the operand:
+// a row behind its end has no output and a block behind kb_end no product.
+// They stay raw until pack(), so that all of a warp's loads are in flight at
+// once, and those of the next group while the ring is full.
 template <int W>
 struct ScaleReader {
-    uint32_t raw[W][4];
+    uint32_t raw[8 * W];
 
     __device__ __forceinline__ void load(const ScaleSource& s, int e, int row0, int kb, int kb_end) {
         const int lane = threadIdx.x & 31;
-        if (s.tiles) {  // one of 4 blocks x W/4 tiles a lane
-            const int tile = min((row0 >> 7) + min(lane >> 2, W / 4 - 1), (s.rows - 1) >> 7);
-            raw[0][0] = static_cast<const uint32_t*>(
-                s.base)[e * s.s_expert + tile * s.s_row + min(kb + (lane & 3), kb_end - 1) * s.s_kb];
+        if (s.form == kTiles) {  // one of 8 blocks x W/4 tiles a lane
+            const int tile = min((row0 >> 7) + min(lane >> 3, W / 4 - 1), (s.rows - 1) >> 7);
+            raw[0] = static_cast<const uint32_t*>(
+                s.base)[e * s.s_expert + tile * s.s_row + min(kb + (lane & 7), kb_end - 1) * s.s_kb];
             return;
         }
         const uint8_t* p = static_cast<const uint8_t*>(s.base);
-        if (s.words) {
+        if (s.form == kAlongDepth) {  // eight bytes at any address: three words, shifted by pack()
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                raw[i][0] = *reinterpret_cast<const uint32_t*>(p + min(row0 + 32 * i + lane, s.rows - 1) * s.s_row + kb);
-            return;
-        }
+            for (int i = 0; i < W; ++i) {
+                const int64_t at = min(row0 + 32 * i + lane, s.rows - 1) * s.s_row + kb;
+                const uint8_t* word = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p + at) & ~uintptr_t(3));
+                if (word >= p && word + 12 <= p + s.bytes) {
 #pragma unroll
-        for (int i = 0; i < W; ++i)
+                    for (int j = 0; j < 3; ++j) raw[3 * i + j] = reinterpret_cast<const uint32_t*>(word)[j];
+                } else {  // at the matrix's ends, byte by byte into the same places
+                    const int shift = (int)(p + at - word);
+                    raw[3 * i] = raw[3 * i + 1] = raw[3 * i + 2] = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                raw[i][j] = p[min(row0 + 32 * i + lane, s.rows - 1) * s.s_row + min(kb + j, kb_end - 1) * s.s_kb];
-    }
-
-    // UE8M0 bytes of the four blocks of row row0 + 32 i + lane.
-    __device__ __forceinline__ void pack(const ScaleSource& s, uint32_t (&w)[W]) const {
-        if (s.tiles) {
-            // 2^c has the byte c + 127: the exponent field, and 0 for the subnormal 2^-127; all else is NaN
-            const uint32_t t = raw[0][0];
-            const uint32_t c = (t & 0x7FFFFFu) == 0u && t - 1u < 0x7F7FFFFFu ? t >> 23 : t == 0x00400000u ? 0u : 255u;
-#pragma unroll
-            for (int a = 0; a < W / 4; ++a) {
-                uint32_t v = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v |= __shfl_sync(0xFFFFFFFFu, c, 4 * a + j) << (8 * j);
-                w[4 * a] = w[4 * a + 1] = w[4 * a + 2] = w[4 * a + 3] = v;
+                    for (int j = 0; j < 11; ++j)
+                        if (j >= shift && j < shift + 8 && kb + j - shift < kb_end)
+                            raw[3 * i + j / 4] |= (uint32_t)word[j] << (8 * (j & 3));
+                }
             }
+        } else if (s.form == kAcrossAligned) {  // four rows, 4 lane .. 4 lane + 3 of each 128, a word
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    raw[8 * i + j] = *reinterpret_cast<const uint32_t*>(p + min(row0 + 128 * i + 4 * lane, s.rows - 4) +
+                                                                        min(kb + j, kb_end - 1) * s.s_kb);
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i)
-                w[i] = s.words ? raw[i][0] : raw[i][0] | raw[i][1] << 8 | raw[i][2] << 16 | raw[i][3] << 24;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    raw[8 * i + j] = p[min(row0 + 32 * i + lane, s.rows - 1) + min(kb + j, kb_end - 1) * s.s_kb];
+        }
+    }
+
+    // Writes the UE8M0 bytes where tcgen05.cp takes them: of four blocks and 128
+    // rows 512 bytes, row r's four at 16 (r % 32) + 4 (r / 32); the second four
+    // blocks `next` bytes on.
+    __device__ __forceinline__ void pack(const ScaleSource& s, int row0, int kb, uint8_t* to, int next) const {
+        const int lane = threadIdx.x & 31;
+        if (s.form == kTiles) {
+            // 2^c has the byte c + 127: the exponent field, and 0 for the subnormal 2^-127; all else is NaN
+            const uint32_t t = raw[0];
+            const uint32_t c = (t & 0x7FFFFFu) == 0u && t - 1u < 0x7F7FFFFFu ? t >> 23 : t == 0x00400000u ? 0u : 255u;
+#pragma unroll
+            for (int a = 0; a < W / 4; ++a)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v |= __shfl_sync(0xFFFFFFFFu, c, 8 * a + 4 * h + j) << (8 * j);
+                    *reinterpret_cast<uint4*>(to + h * next + 512 * a + 16 * lane) = make_uint4(v, v, v, v);
+                }
+        } else if (s.form == kAcrossAligned) {
+#pragma unroll
+            for (int a = 0; a < W / 4; ++a)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t* w = raw + 8 * a + 4 * h;  // block j's bytes of four rows -> row i's of four blocks
+                    const uint32_t lo01 = prmt(w[0], w[1], 0x5140), hi01 = prmt(w[0], w[1], 0x7362),
+                                   lo23 = prmt(w[2], w[3], 0x5140), hi23 = prmt(w[2], w[3], 0x7362);
+                    const uint32_t row[4] = {prmt(lo01, lo23, 0x5410), prmt(lo01, lo23, 0x7632), prmt(hi01, hi23, 0x5410),
+                                             prmt(hi01, hi23, 0x7632)};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint32_t*>(to + h * next + 512 * a + 16 * (4 * (lane & 7) + i) + 4 * (lane >> 3)) =
+                            row[i];
+                }
+        } else {
+            uint32_t w[2][W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                if (s.form == kAlongDepth) {
+                    const int64_t at = min(row0 + 32 * i + lane, s.rows - 1) * s.s_row + kb;
+                    const uint32_t shift = 8 * ((uint32_t)(reinterpret_cast<uintptr_t>(s.base) + at) & 3u);
+                    w[0][i] = __funnelshift_r(raw[3 * i], raw[3 * i + 1], shift);
+                    w[1][i] = __funnelshift_r(raw[3 * i + 1], raw[3 * i + 2], shift);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        w[h][i] = raw[8 * i + 4 * h] | raw[8 * i + 4 * h + 1] << 8 | raw[8 * i + 4 * h + 2] << 16 |
+                                  raw[8 * i + 4 * h + 3] << 24;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int a = 0; a < W / 4; ++a)
+                    *reinterpret_cast<uint4*>(to + h * next + 512 * a + 16 * lane) =
+                        make_uint4(w[h][4 * a], w[h][4 * a + 1], w[h][4 * a + 2], w[h][4 * a + 3]);
         }
     }
 };
@@ -258,6 +323,7 @@ struct Shape {
     static constexpr int kScaleAt = QT == 256 ? 448 : SPLIT ? QT : 2 * QT;
     static constexpr int kUsed = kScaleAt + kScaleParts * kScaleColumns;
     static constexpr int kColumns = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static constexpr int kPerSm = CG == 2 || (QT == 128 && !SPLIT) ? 1 : 2;  // shared and tensor memory have room for
     static constexpr int kTranspose = CG == 2 ? 4 * 32 * 33 * 4 : 0;
     static constexpr int kBarriers = 2 * kStages + 2 * kRing + 4 + 1;
     static size_t smem(int E) {
@@ -267,7 +333,7 @@ struct Shape {
 };
 
 template <int QT, int CG, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
     matmul_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ Problem g, const uint32_t idesc, const int tile_count) {
     using S = Shape<QT, CG, SPLIT>;
@@ -410,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // products which used the same bytes and columns before are done.
                 auto scales_of = [&](int x) {
                     const int slot = x % kRing;
-                    const bool there = __all_sync(0xFFFFFFFFu, mbar_wait<CG == 2>(sc_full + 8 * slot, (x / kRing) & 1, gave_up));
+                    const bool there = __all_sync(0xFFFFFFFFu, mbar_wait(sc_full + 8 * slot, (x / kRing) & 1, gave_up));
                     tc_fence_after();
                     if (there && elect_one()) {
 #pragma unroll
@@ -461,11 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp < 4) {
         // --------------------------------------------------------- scales
-        // row i of 128 has its four bytes at 16 (i % 32) + 4 (i / 32)
-        auto gather = [&](auto proto, const ScaleSource& src, bool is_p) {
-            using Reader = decltype(proto);
-            constexpr int W = sizeof(Reader) / 16, H = kGroup / 4;
-            Reader reader[H];
+        auto gather = [&](auto reader, const ScaleSource& src, bool is_p) {
             [[maybe_unused]] const uint32_t arrive_at = CG == 2 ? map_rank(sc_full, 0) : 0;
             int group = 0;
             bool ok = true;
@@ -474,26 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int kb0, kb1;
                 depth_of(c, kb0, kb1);
                 const int row0 = is_p ? c.p0 + 128 * (int)pair_rank : c.q0;
-                auto load = [&](int kb) {
-#pragma unroll
-                    for (int h = 0; h < H; ++h)
-                        if (kb + 4 * h < kb1) reader[h].load(src, c.e, row0, kb + 4 * h, kb1);
-                };
-                load(kb0);
+                if (kb0 < kb1) reader.load(src, c.e, row0, kb0, kb1);
                 for (int kb = kb0; kb < kb1; kb += kGroup, ++group) {
                     const int r = group % kRing, round = group / kRing;
-                    uint32_t w[H][W];
-#pragma unroll
-                    for (int h = 0; h < H; ++h) reader[h].pack(src, w[h]);
                     ok = round == 0 || mbar_wait(sc_empty + 8 * r, (round - 1) & 1, gave_up);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    uint8_t* to = scales + r * H * S::kScaleBytes + (is_p ? 0 : 512);
-#pragma unroll
-                    for (int h = 0; h < H; ++h)
-#pragma unroll
-                        for (int a = 0; a < W / 4; ++a)
-                            *reinterpret_cast<uint4*>(to + h * S::kScaleBytes + 512 * a + 16 * lane) =
-                                make_uint4(w[h][4 * a], w[h][4 * a + 1], w[h][4 * a + 2], w[h][4 * a + 3]);
+                    reader.pack(src, row0, kb, scales + r * (kGroup / 4) * S::kScaleBytes + (is_p ? 0 : 512), S::kScaleBytes);
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -502,9 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             mbar_arrive(sc_full + 8 * r);
                     }
-                    load(kb + kGroup);
+                    if (kb + kGroup < kb1) reader.load(src, c.e, row0, kb + kGroup, kb1);
                 }
-                ok = __all_sync(0xFFFFFFFFu, ok);
             }
         };
         if (warp == 2)
@@ -708,9 +756,13 @@ ScaleSource scale_source(const MatOperand& o, int64_t depth) {
     s.s_kb = o.s_kb;
     s.s_expert = o.s_expert;
     s.rows = (int)o.rows;
-    s.tiles = o.tiles;
-    s.words = !o.tiles && o.s_kb == 1 && o.s_row % 4 == 0 && reinterpret_cast<uintptr_t>(o.scales) % 4 == 0 &&
-              ceil_div(depth, 128) % 4 == 0;
+    s.bytes = o.rows * ceil_div(depth, 128);
+    if (o.tiles)
+        s.form = kTiles;
+    else if (!o.mn)
+        s.form = kAlongDepth;
+    else
+        s.form = o.rows % 4 == 0 && reinterpret_cast<uintptr_t>(o.scales) % 4 == 0 ? kAcrossAligned : kAcrossDepth;
     return s;
 }
 
@@ -767,8 +819,7 @@ cudaError_t launch(const MatmulArgs& m, const MatOperand& p, const MatOperand& q
     cluster.id = cudaLaunchAttributeClusterDimension;
     cluster.val.clusterDim.x = (unsigned)(CG == 2 ? 2 : split);
     cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    const int per_sm = CG == 2 || QT == 128 ? 1 : 2;  // what shared memory and tensor memory leave room for
-    const int64_t room = (int64_t)sm_count() * per_sm / CG;
+    const int64_t room = (int64_t)sm_count() * S::kPerSm / CG;
     const int64_t blocks = SPLIT ? tiles * split : (tiles < room ? tiles : room) * CG;
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kThreads);

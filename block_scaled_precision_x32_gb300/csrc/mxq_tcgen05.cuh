@@ -53,35 +53,29 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// `bar` is an address of map_rank().
+// `bar` is an address of map_rank().  The arrival orders what this thread did
+// before it within its own block, which is what the barrier's waiter relies
+// on: it starts tensor core instructions that read this block's shared memory
+// on this block's multiprocessor, and reads nothing itself.  With .release.cluster
+// an arrival took about 2000 clocks, as long as four 128-deep products.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// REMOTE: threads of the cluster's other CTAs arrive on it too, so what they wrote is acquired in the cluster's scope.
-template <bool REMOTE>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    if constexpr (REMOTE)
-        asm volatile(
-            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    else
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                     : "=r"(ok)
-                     : "r"(bar), "r"(parity)
-                     : "memory");
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
     return ok != 0;
 }
 // Waits until the phase `parity` of `bar` has completed: false when another
 // wait of the block has given up (*gave_up), or after about 2^32 SM clocks (two
 // seconds; never expected), which sets *gave_up.
-template <bool REMOTE = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-    if (mbar_try<REMOTE>(bar, parity)) return true;
+    if (mbar_try(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try<REMOTE>(bar, parity)) {
+    while (!mbar_try(bar, parity)) {
         if (*gave_up) return false;
         if (clock64() - t0 > (1ll << 32)) {
             *gave_up = 1;
