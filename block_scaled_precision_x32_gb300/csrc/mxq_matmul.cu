@@ -17,7 +17,7 @@
 //   warp 0     TMA: boxes of both operands, 128 deep, into a ring of stages
 //   warp 1     one thread issues scale copies and MMAs
 //   warp 2, 3  gather the scale bytes of four blocks (512 of depth) of each operand
-//   warps 4-7  take finished sums out of tensor memory, round and store them
+//   warps 4..  take finished sums out of tensor memory, round and store them
 // Blocks walk over their tiles, so that loads and MMAs of the next tile run
 // while the last one is being stored.
 #include <cuda.h>
@@ -33,7 +33,6 @@
 namespace mxq {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMostExperts = 1024;
 // Scales move in groups of two words a row, eight blocks of depth: what a warp spends on a group (its loads, which the
 // proxy fence waits for, and the fence) is about 2000 clocks, as long as the products of four blocks.
@@ -41,7 +40,11 @@ constexpr int kGroup = 8;
 constexpr int kRing = 2;  // groups, both in shared and in tensor memory
 
 // The operand whose rows are the accumulator's lanes is called P, the one
-// whose rows are its columns Q.
+// whose rows are its columns Q.  Lanes come 128 at a time, columns in any
+// multiple of 16.  Where tokens are few or an expert's, they are the columns:
+// odd numbers of them then cost little more than their own products.  Where
+// they are many they are the lanes, whose thread holds neighbours of one row
+// of the output.
 enum ScaleForm {
     kTiles,          // an fp32 power of two per 128x128 tile
     kAlongDepth,     // a byte per row and block, a row's bytes together
@@ -57,7 +60,7 @@ struct ScaleSource {
     int form;
 };
 
-enum RaggedBy { kNone, kRowsOfP, kRowsOfQ, kDepth };
+enum RaggedBy { kNone, kRowsOfQ, kDepth };
 
 struct Problem {
     ScaleSource sp, sq;
@@ -66,14 +69,17 @@ struct Problem {
     int64_t ldo, out_expert;
     int E, depth;
     int p_rows, q_rows, p_tiles, q_tiles;
+    int columns;  // of the accumulator a tile takes, where experts' rows do not decide it
     int ragged;
-    bool p_mn, q_mn, p_expert, q_expert;  // the operand's major; whether it is a stack of experts'
+    bool p_mn, q_mn;   // the operand's depth runs across its rows in memory
+    bool p_expert;     // P is a stack of experts' weights
     bool out_bf16;
-    bool wide;  // 32-byte stores of the output's rows are aligned
+    bool wide;  // four neighbours of the output can be stored at once
 };
 
 struct Tile {
-    int e, p0, p_end, q0, q_end;
+    int e, p0, q0, q_end;
+    int columns;  // of the accumulator: q_end - q0, rounded up
     int kb0, kb1;
 };
 
@@ -120,31 +126,22 @@ __device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t
     c.e = 0;
     c.kb0 = 0;
     c.kb1 = (g.depth + 127) >> 7;
-    if (g.ragged == kRowsOfP || g.ragged == kRowsOfQ) {
-        const int others = g.ragged == kRowsOfP ? g.q_tiles : g.p_tiles;
+    if (g.ragged == kRowsOfQ) {
         int lo = 0, hi = g.E - 1;  // the last expert whose tiles begin at or before t
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            if (r.tiles[mid] * others <= t)
+            if (r.tiles[mid] * g.p_tiles <= t)
                 lo = mid;
             else
                 hi = mid - 1;
         }
         c.e = lo;
-        t -= r.tiles[lo] * others;
-        const int n = r.tiles[lo + 1] - r.tiles[lo];
-        const int x = t % n, y = t / n;
-        if (g.ragged == kRowsOfP) {
-            c.p0 = r.bound[lo] + x * PT;
-            c.p_end = r.bound[lo + 1];
-            c.q0 = y * QT;
-            c.q_end = g.q_rows;
-        } else {
-            c.q0 = r.bound[lo] + x * QT;
-            c.q_end = r.bound[lo + 1];
-            c.p0 = y * PT;
-            c.p_end = g.p_rows;
-        }
+        t -= r.tiles[lo] * g.p_tiles;
+        const int n = r.tiles[lo + 1] - r.tiles[lo], rows = r.bound[lo + 1] - r.bound[lo];
+        c.columns = QT < 256 ? QT : ((rows + n - 1) / n + 15) & ~15;  // as even as they can be; none is left empty
+        c.q0 = r.bound[lo] + t % n * c.columns;
+        c.q_end = min(r.bound[lo + 1], c.q0 + c.columns);
+        c.p0 = t / n * PT;
         return c;
     }
     if (g.ragged == kDepth) {
@@ -158,9 +155,9 @@ __device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t
     const int group = t / (G * g.q_tiles), first = group * G, n = min(G, g.p_tiles - first);
     t -= group * G * g.q_tiles;
     c.p0 = (first + t % n) * PT;
-    c.q0 = t / n * QT;
-    c.p_end = g.p_rows;
-    c.q_end = g.q_rows;
+    c.q0 = t / n * g.columns;
+    c.q_end = min(g.q_rows, c.q0 + g.columns);
+    c.columns = QT < 256 ? QT : min(g.columns, (c.q_end - c.q0 + 31) & ~31);
     return c;
 }
 
@@ -301,17 +298,19 @@ __device__ __forceinline__ void store_four(const Problem& g, int64_t at, int n, 
         if (i < n) store_one(g, at + i, u[i]);
 }
 
-// QT: columns of the accumulator.  CG 2: a pair of blocks, 256 lanes, each
-// holding half of Q's rows; the output's rows are P's.  CG 1: 128 lanes; the
-// output's rows are Q's (few tokens, many features).  SPLIT: the blocks of a
-// cluster share a tile, each with a part of the depth, and add their sums
-// through shared memory.
-template <int QT, int CG, bool SPLIT>
+// QT: columns of the accumulator, at most for CG 2, where each tile has a
+// width of its own.  CG 2: a pair of blocks, 256 lanes, each loading half of a
+// tile's rows of Q.  CG 1: 128 lanes.  SPLIT: the blocks of a cluster share a
+// tile, each with a part of the depth, and add their sums through shared
+// memory.  ROWS: the output's rows are the lanes (CG 2), else the columns.
+template <int QT, int CG, bool SPLIT, bool ROWS>
 struct Shape {
     static constexpr int kQRows = QT / CG;                           // rows of Q that a block loads
     static constexpr int kPBytes = 128 * 128, kQBytes = kQRows * 128;
     static constexpr int kStageBytes = kPBytes + kQBytes;
-    static constexpr int kStages = CG == 2 ? 6 : QT == 128 ? (SPLIT ? 3 : 6) : QT == 64 ? 4 : 5;
+    static constexpr int kOutWarps = CG == 2 && !ROWS ? 8 : 4;  // that take results out
+    static constexpr int kThreads = 128 + 32 * kOutWarps;
+    static constexpr int kStages = CG == 2 ? (ROWS ? 6 : 5) : QT == 128 ? (SPLIT ? 3 : 6) : QT == 64 ? 4 : 5;
     static constexpr int kQAtoms = QT <= 128 ? 1 : QT / 128;         // 128 scales each
     static constexpr int kScaleBytes = 512 * (1 + kQAtoms);           // of four blocks
     static constexpr int kScaleColumns = 4 * (1 + kQAtoms);
@@ -324,25 +323,26 @@ struct Shape {
     static constexpr int kUsed = kScaleAt + kScaleParts * kScaleColumns;
     static constexpr int kColumns = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr int kPerSm = CG == 2 || (QT == 128 && !SPLIT) ? 1 : 2;  // shared and tensor memory have room for
-    static constexpr int kTranspose = CG == 2 ? 4 * 32 * 33 * 4 : 0;
+    static constexpr int kOutBytes = CG == 2 && !ROWS ? 2 * 64 * 128 * 2 : 0;  // bf16 results on their way out
+    static constexpr int kBox = CG == 2 ? 64 : QT;  // rows of Q in one copy
     static constexpr int kBarriers = 2 * kStages + 2 * kRing + 4 + 1;
     static size_t smem(int E) {
-        return 1024 + (size_t)kStages * kStageBytes + (size_t)kScaleParts * kScaleBytes + kTranspose + 8 * kBarriers + 16 +
+        return 1024 + (size_t)kStages * kStageBytes + (size_t)kScaleParts * kScaleBytes + kOutBytes + 8 * kBarriers + 16 +
                (E ? 8 * (size_t)(E + 1) : 0);
     }
 };
 
-template <int QT, int CG, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
+template <int QT, int CG, bool SPLIT, bool ROWS>
+__global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT, CG, SPLIT, ROWS>::kPerSm)
     matmul_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ Problem g, const uint32_t idesc, const int tile_count) {
-    using S = Shape<QT, CG, SPLIT>;
+    using S = Shape<QT, CG, SPLIT, ROWS>;
     constexpr int PT = 128 * CG;
     extern __shared__ uint8_t raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* scales = stages + S::kStages * S::kStageBytes;
-    float* transpose = reinterpret_cast<float*>(scales + S::kScaleParts * S::kScaleBytes);
-    uint8_t* bars = reinterpret_cast<uint8_t*>(transpose) + S::kTranspose;
+    [[maybe_unused]] uint16_t* outs = reinterpret_cast<uint16_t*>(scales + S::kScaleParts * S::kScaleBytes);  // [64][128]
+    uint8_t* bars = scales + S::kScaleParts * S::kScaleBytes + S::kOutBytes;
     volatile int* gave_up = reinterpret_cast<volatile int*>(bars + 8 * S::kBarriers);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 8 * S::kBarriers + 4);
     Ragged rag;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(acc_full + 8 * i, 1);
-                mbar_init(acc_empty + 8 * i, 4 * CG);
+                mbar_init(acc_empty + 8 * i, CG * S::kOutWarps);
             }
             mbar_init(drained, 1);
             *gave_up = 0;
@@ -380,8 +380,7 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
     } else if (warp == 1) {
         tmem_alloc<CG>(smem_u32(tmem_at), S::kColumns);
     } else if (warp == 2 && g.ragged != kNone) {
-        read_offsets(g, g.ragged == kDepth ? g.depth : g.ragged == kRowsOfP ? g.p_rows : g.q_rows,
-                     g.ragged == kRowsOfP ? PT : QT, rag);
+        read_offsets(g, g.ragged == kDepth ? g.depth : g.q_rows, QT, rag);
     }
     tc_fence_before();
     __syncthreads();
@@ -390,7 +389,6 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_at, 0);  // known to be the same in a warp: see elect_one()
 
     int tiles = tile_count;
-    if (g.ragged == kRowsOfP) tiles = rag.tiles[g.E] * g.q_tiles;
     if (g.ragged == kRowsOfQ) tiles = rag.tiles[g.E] * g.p_tiles;
     const int span = SPLIT ? (int)(gridDim.x) : (int)gridDim.x / CG;  // SPLIT: one tile per cluster
     int split = 1, first_tile = (int)blockIdx.x / CG;
@@ -419,23 +417,27 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
             const Tile c = tile_at<PT, QT>(g, rag, t);
             int kb0, kb1;
             depth_of(c, kb0, kb1);
-            const int p_row = c.p0 + 128 * (int)pair_rank, q_row = c.q0 + S::kQRows * (int)pair_rank;
-            const int pe = g.p_expert ? c.e : 0, qe = g.q_expert ? c.e : 0;
+            const int q_rows = CG == 2 ? c.columns / 2 : QT, q_boxes = g.q_mn ? 1 : (q_rows + S::kBox - 1) / S::kBox;
+            const int bytes = S::kPBytes + (g.q_mn ? S::kQBytes : q_boxes * S::kBox * 128);
+            const int p_row = c.p0 + 128 * (int)pair_rank, q_row = c.q0 + q_rows * (int)pair_rank;
+            const int pe = g.p_expert ? c.e : 0;
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = mbar_wait(empty + 8 * s, parity, gave_up);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t at = smem_u32(stages) + s * S::kStageBytes, bar = full + 8 * s;
-                    if (leader) mbar_expect_tx(bar, CG * S::kStageBytes);
+                    if (leader) mbar_expect_tx(bar, CG * bytes);
                     if (g.p_mn)
                         tma_load<CG == 2>(at, &p_map, bar, p_row, kb * 128, pe);
                     else
                         tma_load<CG == 2>(at, &p_map, bar, kb * 128, p_row, pe);
                     if (g.q_mn)
-                        tma_load<CG == 2>(at + S::kPBytes, &q_map, bar, q_row, kb * 128, qe);
+                        tma_load<CG == 2>(at + S::kPBytes, &q_map, bar, q_row, kb * 128, 0);
                     else
-                        tma_load<CG == 2>(at + S::kPBytes, &q_map, bar, kb * 128, q_row, qe);
+                        for (int i = 0; i < q_boxes; ++i)
+                            tma_load<CG == 2>(at + S::kPBytes + i * (S::kBox * 128), &q_map, bar, kb * 128,
+                                              q_row + i * S::kBox, 0);
                 }
                 __syncwarp();
                 ++n;
@@ -471,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
                 else
                     ok = it < 2 || mbar_wait(acc_empty + 8 * (it & 1), ((it >> 1) - 1) & 1, gave_up);
                 const uint32_t acc = tmem + (it & 1) * S::kAcc1;
+                const uint32_t tile_desc = idesc | instruction_columns(__shfl_sync(0xFFFFFFFFu, c.columns, 0));
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 // Copies the scales of group x of this block's.  That they have arrived says, too, that the
                 // products which used the same bytes and columns before are done.
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
                     const bool last = i + 1 == blocks;
                     if (elect_one()) {
                         const uint64_t dp = desc_p + ((s * S::kStageBytes) >> 4), dq = desc_q + ((s * S::kStageBytes) >> 4);
-                        const uint32_t id = idesc | scale_byte(j & 3);
+                        const uint32_t id = tile_desc | scale_byte(j & 3);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_block_scaled<CG>(acc, dp + k * step_p, dq + k * step_q, id, sfp, sfq, i > 0 || k > 0);
@@ -565,7 +568,6 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
         const uint32_t lanes = (uint32_t)(32 * band) << 16;
         const uint32_t release_at = CG == 2 ? map_rank(acc_empty, 0) : 0;
         constexpr int W = QT < 64 ? QT : 64;  // columns at a time
-        constexpr int kChunks = QT / W;
         int it = 0;
         bool ok = true;
         for (int t = first_tile; t < tiles; t += span) {
@@ -580,15 +582,20 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
                 tc_fence_after();
                 ++it;
             }
-            const int64_t base = g.ragged == kDepth ? c.e * g.out_expert : 0;
-            const int lane_row = c.p0 + 128 * (int)pair_rank + 32 * band + lane;
+            const int row = c.p0 + 128 * (int)pair_rank + 32 * band + lane;  // of P: a column of the output
+            const int64_t base = (g.ragged == kDepth ? c.e * g.out_expert : 0) + (ROWS ? row * g.ldo : row);
+            const int chunks = QT == 256 ? (c.columns + W - 1) / W : QT / W;
+            // eight warps: the even and the odd chunks have four each
+            constexpr int kHalves = S::kOutWarps / 4;
+            const int half = kHalves == 2 ? (warp - 4) >> 2 : 0;
+            bool held = !none;  // the accumulator's shared columns
 #pragma unroll 1
-            for (int x = 0; x < kChunks; ++x) {
-                // the columns that the two accumulators share come first (the second one's first, the first
-                // one's last): only they hold up the next tile
-                const int chunk = QT == 256 && a == 0 ? (x + kChunks - 1) % kChunks : x;
+            for (int x = half; x < chunks || held; x += kHalves) {
+                // The columns that the two accumulators share come first (the second one's first, the first
+                // one's last): only they hold up the next tile.
+                const int chunk = QT != 256 || a != 0 || chunks != 4 ? x : kHalves == 1 ? (x + 3) & 3 : half == 1 ? x ^ 2 : x;
                 uint32_t v[W];
-                if (!none && ok) {
+                if (!none && ok && x < chunks) {
                     const uint32_t from = tmem + lanes + a * S::kAcc1 + chunk * W;
                     if constexpr (W == 16) {
                         tmem_ld(v, from);
@@ -601,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
 #pragma unroll
                     for (int i = 0; i < W; ++i) v[i] = none ? 0u : 0x7FC00000u;
                 }
-                if (!none && x == (QT == 256 ? 0 : kChunks - 1)) {
+                if (held && (QT == 256 || x == chunks - 1)) {
+                    held = false;
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -612,68 +620,91 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
                             mbar_arrive(acc_empty + 8 * bar);
                     }
                 }
+                if (x >= chunks) break;
                 if constexpr (SPLIT) {
                     float* part = reinterpret_cast<float*>(stages);  // [QT][128]: every load and MMA is done
 #pragma unroll
                     for (int i = 0; i < W; ++i) part[(chunk * W + i) * 128 + 32 * band + lane] = __uint_as_float(v[i]);
-                } else if constexpr (CG == 1) {
-                    // rows of the output are columns here: 32 lanes store neighbours
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        const int row = c.q0 + chunk * W + i;
-                        if (row < c.q_end && lane_row < c.p_end) store_one(g, base + row * g.ldo + lane_row, v[i]);
-                    }
                 } else {
-                    const int col = c.q0 + chunk * W;
-                    if (g.wide && col + W <= c.q_end) {
-                        if (lane_row < c.p_end) {
+                    const int q0 = c.q0 + chunk * W, n = c.q_end - q0;
+                    uint32_t top = 0;  // NaN results are rare: look for any, then make them canonical
+#pragma unroll
+                    for (int i = 0; i < W; ++i) top = max(top, v[i] & 0x7FFFFFFFu);
+                    if (top > 0x7F800000u)
+#pragma unroll
+                        for (int i = 0; i < W; ++i) v[i] = canonical(v[i]);
+                    if constexpr (ROWS) {
+                        // a thread's 64 columns are neighbours: whole sectors of 32 bytes (launch_matmul sees to it that
+                        // they are aligned)
+                        if (row < g.p_rows) {
                             if (g.out_bf16) {
-                                uint16_t* to = static_cast<uint16_t*>(g.out) + base + lane_row * g.ldo + col;
+                                uint16_t* to = static_cast<uint16_t*>(g.out) + base + q0;
 #pragma unroll
                                 for (int h = 0; h < W / 16; ++h) {
-                                    uint32_t p[8];
+                                    uint32_t w[8];
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        p[i] = bf16_rne(canonical(v[16 * h + 2 * i])) |
-                                               (bf16_rne(canonical(v[16 * h + 2 * i + 1])) << 16);
-                                    st32(to + 16 * h, p);
+                                    for (int i = 0; i < 8; ++i) w[i] = bf16_rne(v[16 * h + 2 * i]) | bf16_rne(v[16 * h + 2 * i + 1]) << 16;
+                                    if (16 * h + 16 <= n)
+                                        st32(to + 16 * h, w);
+                                    else
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i)
+                                            if (16 * h + i < n) to[16 * h + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
                                 }
                             } else {
-                                uint32_t* to = static_cast<uint32_t*>(g.out) + base + lane_row * g.ldo + col;
+                                uint32_t* to = static_cast<uint32_t*>(g.out) + base + q0;
 #pragma unroll
                                 for (int h = 0; h < W / 8; ++h) {
-                                    uint32_t p[8];
+                                    if (8 * h + 8 <= n)
+                                        st32(to + 8 * h, reinterpret_cast<uint32_t(&)[8]>(v[8 * h]));
+                                    else
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) p[i] = canonical(v[8 * h + i]);
-                                    st32(to + 8 * h, p);
+                                        for (int i = 0; i < 8; ++i)
+                                            if (8 * h + i < n) to[8 * h + i] = v[8 * h + i];
                                 }
                             }
                         }
-                    } else {
-                        // through shared memory, so that neighbouring lanes store neighbouring columns
-                        uint32_t* buf = reinterpret_cast<uint32_t*>(transpose) + band * (32 * 33);
-                        const int row0 = lane_row - lane, rows = min(32, c.p_end - row0);
+                    } else if (!g.out_bf16) {  // a warp's 32 lanes store 128 neighbouring bytes
+                        uint32_t* to = static_cast<uint32_t*>(g.out) + base + q0 * g.ldo;
+                        if (row < g.p_rows) {
 #pragma unroll
-                        for (int h = 0; h < W / 32; ++h) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = v[32 * h + i];
-                            __syncwarp();
-                            const int at = col + 32 * h + lane;
-                            for (int i = 0; i < rows; ++i)
-                                if (at < c.q_end) store_one(g, base + (row0 + i) * g.ldo + at, buf[i * 33 + lane]);
-                            __syncwarp();
+                            for (int i = 0; i < W; ++i, to += g.ldo)
+                                if (i < n) *to = v[i];
                         }
+                    } else if (CG == 2 && g.wide) {
+                        // Through shared memory, so that a row's 128 features, 256 bytes, are stored together: the
+                        // 64 bytes of one warp's lanes make partial lines, and a 256x256 tile took 9.4 us so
+                        // (fp32, 128 bytes a warp: 3.1 us; this: STAGED us).
+                        uint16_t* buf = outs + half * (64 * 128);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) buf[128 * i + 32 * band + lane] = (uint16_t)bf16_rne(v[i]);
+                        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                        const int part = threadIdx.x & 15, feature = c.p0 + 128 * (int)pair_rank + 8 * part;
+                        uint16_t* to = static_cast<uint16_t*>(g.out) + base - row + feature + (int64_t)q0 * g.ldo;
+#pragma unroll
+                        for (int k = 0; k < W / 8; ++k) {
+                            const int i = 8 * k + ((threadIdx.x >> 4) & 7);
+                            const uint4 y = *reinterpret_cast<const uint4*>(buf + 128 * i + 8 * part);
+                            if (i < n && feature + 8 <= g.p_rows) *reinterpret_cast<uint4*>(to + i * g.ldo) = y;
+                            if (i < n && feature + 8 > g.p_rows)
+                                for (int f = 0; feature + f < g.p_rows; ++f) to[i * g.ldo + f] = buf[128 * i + 8 * part + f];
+                        }
+                        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                    } else {
+                        uint16_t* to = static_cast<uint16_t*>(g.out) + base + q0 * g.ldo;
+#pragma unroll
+                        for (int i = 0; i < W; ++i, to += g.ldo)
+                            if (i < n && row < g.p_rows) *to = (uint16_t)bf16_rne(v[i]);
                     }
                 }
             }
         }
         // rows that belong to no expert
-        if (g.ragged == kRowsOfP || g.ragged == kRowsOfQ) {
-            const int rows = g.ragged == kRowsOfP ? g.p_rows : g.q_rows, n = g.ragged == kRowsOfP ? g.q_rows : g.p_rows;
+        if (g.ragged == kRowsOfQ) {
             const int front = rag.bound[0], behind = rag.bound[g.E];
-            for (int64_t i = blockIdx.x; i < front + (rows - behind); i += gridDim.x) {
+            for (int64_t i = blockIdx.x; i < (int64_t)front + (g.q_rows - behind); i += gridDim.x) {
                 const int64_t row = i < front ? i : behind + (i - front);
-                for (int j = threadIdx.x - 128; j < n; j += 128) store_one(g, row * g.ldo + j, 0u);
+                for (int j = threadIdx.x - 128; j < g.p_rows; j += 32 * S::kOutWarps) store_one(g, row * g.ldo + j, 0u);
             }
         }
     }
@@ -687,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
             const uint32_t part = smem_u32(stages);
             const int j0 = QT * (int)rank / split, j1 = min(QT * ((int)rank + 1) / split, c.q_end - c.q0);
             // four neighbouring rows of P a thread, the sums of all blocks on their way together
-            for (int x = threadIdx.x; x < (j1 - j0) * 32; x += kThreads) {
+            for (int x = threadIdx.x; x < (j1 - j0) * 32; x += S::kThreads) {
                 const int j = j0 + (x >> 5), r = (x & 31) * 4;
                 float4 v[8];
 #pragma unroll
@@ -697,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, Shape<QT, CG, SPLIT>::kPerSm)
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
                     if (s < split) sum.x += v[s].x, sum.y += v[s].y, sum.z += v[s].z, sum.w += v[s].w;
-                store_four(g, base + (int64_t)(c.q0 + j) * g.ldo + c.p0 + r, c.p_end - (c.p0 + r), sum);
+                store_four(g, base + (int64_t)(c.q0 + j) * g.ldo + c.p0 + r, g.p_rows - (c.p0 + r), sum);
             }
         }
     }
@@ -766,10 +797,11 @@ ScaleSource scale_source(const MatOperand& o, int64_t depth) {
     return s;
 }
 
-template <int QT, int CG, bool SPLIT>
-cudaError_t launch(const MatmulArgs& m, const MatOperand& p, const MatOperand& q, int ragged, int split, cudaStream_t stream) {
-    using S = Shape<QT, CG, SPLIT>;
+template <int QT, int CG, bool SPLIT, bool ROWS>
+cudaError_t launch(const MatmulArgs& m, int ragged, int columns, int split, cudaStream_t stream) {
+    using S = Shape<QT, CG, SPLIT, ROWS>;
     constexpr int PT = 128 * CG;
+    const MatOperand &p = ROWS ? m.a : m.b, &q = ROWS ? m.b : m.a;
     Problem g{};
     g.sp = scale_source(p, m.depth);
     g.sq = scale_source(q, m.depth);
@@ -782,26 +814,24 @@ cudaError_t launch(const MatmulArgs& m, const MatOperand& p, const MatOperand& q
     g.p_rows = (int)p.rows;
     g.q_rows = (int)q.rows;
     g.p_tiles = (int)ceil_div(p.rows, PT);
-    g.q_tiles = (int)ceil_div(q.rows, QT);
+    g.columns = columns;
+    g.q_tiles = (int)ceil_div(q.rows, columns);
     g.ragged = ragged;
     g.p_mn = p.mn;
     g.q_mn = q.mn;
     g.p_expert = p.expert != 0;
-    g.q_expert = q.expert != 0;
     g.out_bf16 = m.out_bf16;
     const int64_t es = m.out_bf16 ? 2 : 4;
     g.wide = reinterpret_cast<uintptr_t>(m.out) % 32 == 0 && m.ldo * es % 32 == 0;
     CUtensorMap pm, qm;
-    if (!make_map(&pm, p, m.depth, m.E, 128) || !make_map(&qm, q, m.depth, m.E, q.mn ? 128 : S::kQRows))
+    if (!make_map(&pm, p, m.depth, m.E, 128) || !make_map(&qm, q, m.depth, m.E, q.mn ? 128 : S::kBox))
         return cudaErrorInvalidValue;
 
     int64_t tiles = (int64_t)g.p_tiles * g.q_tiles * (ragged == kDepth ? m.E : 1);
-    if (ragged == kRowsOfP || ragged == kRowsOfQ) {  // at most: every expert has a last, partial tile
-        const int64_t rows = ragged == kRowsOfP ? p.rows : q.rows, step = ragged == kRowsOfP ? PT : QT;
-        tiles = (rows / step + (m.E < rows ? m.E : rows)) * (ragged == kRowsOfP ? g.q_tiles : g.p_tiles);
-    }
+    if (ragged == kRowsOfQ)  // at most: every expert has a last, partial tile
+        tiles = (q.rows / QT + (m.E < q.rows ? m.E : q.rows)) * g.p_tiles;
     if (tiles > INT64_C(0x3FFFFFFF)) return cudaErrorInvalidValue;
-    auto kernel = matmul_kernel<QT, CG, SPLIT>;
+    auto kernel = matmul_kernel<QT, CG, SPLIT, ROWS>;
     const size_t smem = S::smem((int)m.E);
     // once a device: the most that any number of experts asks for
     static std::atomic<bool> allowed[64];
@@ -822,45 +852,48 @@ cudaError_t launch(const MatmulArgs& m, const MatOperand& p, const MatOperand& q
     const int64_t room = (int64_t)sm_count() * S::kPerSm / CG;
     const int64_t blocks = SPLIT ? tiles * split : (tiles < room ? tiles : room) * CG;
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &cluster;
     cfg.numAttrs = CG == 2 || SPLIT ? 1 : 0;
-    const uint32_t idesc = instruction_desc(PT, QT, p.mn, q.mn);
+    const uint32_t idesc = instruction_desc(PT, p.mn, q.mn);
     return cudaLaunchKernelEx(&cfg, kernel, pm, qm, g, idesc, (int)tiles);
 }
 
 }  // namespace
 
 cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
-    const bool grouped = m.grouping == Grouping::ROWS;
-    const int ragged = m.grouping == Grouping::DEPTH ? kDepth : kNone;
+    const int ragged = m.grouping == Grouping::DEPTH ? kDepth : m.grouping == Grouping::ROWS ? kRowsOfQ : kNone;
+    const int64_t features = m.b.rows, tokens = m.a.rows, blocks = ceil_div(m.depth, 128);
     cudaError_t e;
-    if (m.a.rows > 256 && m.b.rows > 128 && !(grouped && m.a.rows / m.E < 128)) {
-        e = launch<256, 2, false>(m, m.a, m.b, grouped ? kRowsOfP : ragged, 1, s);
+    if (tokens > 256 && features > 128 && !(ragged == kRowsOfQ && tokens / m.E < 64)) {
+        const int64_t es = m.out_bf16 ? 2 : 4;
+        const bool sectors = reinterpret_cast<uintptr_t>(m.out) % 32 == 0 && m.ldo * es % 32 == 0;
+        if (ragged != kRowsOfQ && sectors)
+            e = launch<256, 2, false, true>(m, ragged, 256, 1, s);
+        else
+            e = launch<256, 2, false, false>(m, ragged, 256, 1, s);
     } else {
-        // A's rows as columns
-        const int r = grouped ? kRowsOfQ : ragged;
-        const int64_t rows = grouped ? ceil_div(m.a.rows, m.E) : m.a.rows;
-        const int64_t qt = m.a.mn || rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
-        const int64_t tiles = ceil_div(m.b.rows, 128) * ceil_div(m.a.rows, qt), quads = ceil_div(m.depth, 512);
+        const int64_t rows = ragged == kRowsOfQ ? ceil_div(tokens, m.E) : tokens;
+        const int qt = m.a.mn || rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
+        const int64_t tiles = ceil_div(features, 128) * ceil_div(tokens, qt), quads = ceil_div(m.depth, 512);
         // as many blocks to a tile's depth as the device has room for at once (two a multiprocessor), and no more than
         // shorten the longest share
         int split = 1;
-        if (r == kNone)
+        if (ragged == kNone)
             for (int x = 2; x <= 8 && x <= quads && tiles * x <= 2 * sm_count(); ++x)
                 if (ceil_div(quads, x) < ceil_div(quads, split)) split = x;
         if (split > 1)
-            e = qt == 16   ? launch<16, 1, true>(m, m.b, m.a, r, split, s)
-                : qt == 32 ? launch<32, 1, true>(m, m.b, m.a, r, split, s)
-                : qt == 64 ? launch<64, 1, true>(m, m.b, m.a, r, split, s)
-                           : launch<128, 1, true>(m, m.b, m.a, r, split, s);
+            e = qt == 16   ? launch<16, 1, true, false>(m, ragged, qt, split, s)
+                : qt == 32 ? launch<32, 1, true, false>(m, ragged, qt, split, s)
+                : qt == 64 ? launch<64, 1, true, false>(m, ragged, qt, split, s)
+                           : launch<128, 1, true, false>(m, ragged, qt, split, s);
         else
-            e = qt == 16   ? launch<16, 1, false>(m, m.b, m.a, r, 1, s)
-                : qt == 32 ? launch<32, 1, false>(m, m.b, m.a, r, 1, s)
-                : qt == 64 ? launch<64, 1, false>(m, m.b, m.a, r, 1, s)
-                           : launch<128, 1, false>(m, m.b, m.a, r, 1, s);
+            e = qt == 16   ? launch<16, 1, false, false>(m, ragged, qt, 1, s)
+                : qt == 32 ? launch<32, 1, false, false>(m, ragged, qt, 1, s)
+                : qt == 64 ? launch<64, 1, false, false>(m, ragged, qt, 1, s)
+                           : launch<128, 1, false, false>(m, ragged, qt, 1, s);
     }
     if (e != cudaSuccess) cudaGetLastError();
     return e;

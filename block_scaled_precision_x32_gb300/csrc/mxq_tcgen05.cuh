@@ -215,10 +215,10 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 // Instruction descriptor of kind::mxf8f6f4: E4M3 x E4M3 (format fields 0), UE8M0 scales (bit 23), majors
 // (bits 15, 16: 1 = MN), N/8 (17..22), M/16 (24..28).  The scale bytes' place in their columns goes to
 // bits 29..30 (A) and 4..5 (B).
-__host__ __device__ constexpr uint32_t instruction_desc(int m, int n, bool a_mn, bool b_mn) {
-    return ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
-           ((uint32_t)(m >> 4) << 24);
+__host__ __device__ constexpr uint32_t instruction_desc(int m, bool a_mn, bool b_mn) {
+    return ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | (1u << 23) | ((uint32_t)(m >> 4) << 24);
 }
+__host__ __device__ constexpr uint32_t instruction_columns(int n) { return (uint32_t)(n >> 3) << 17; }
 __host__ __device__ constexpr uint32_t scale_byte(uint32_t j) { return (j << 29) | (j << 4); }
 
 }  // namespace mxq
