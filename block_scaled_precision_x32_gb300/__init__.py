@@ -847,16 +847,17 @@ class Library:
         _check_int32(ids, n, "ids")
         cap = n + min(num_experts, n) * (align - 1)  # mxq_moe_capacity
         need = self.L.mxq_moe_sort_workspace(T, topk, num_experts)
-        if order is None:  # one allocation for the results and the workspace, four-byte values all
-            buf = torch.empty(num_experts + 1 + cap + n + need // 4, dtype=torch.int32, device=ids.device)
-            offsets, source, slots, ws = buf.split_with_sizes((num_experts + 1, cap, n, need // 4))
-            order = MoeOrder(offsets, source, slots.view(T, topk))
+        if order is None:  # allocations of their own: views of one would take several times as long to make
+            dev_ = ids.device
+            order = MoeOrder(torch.empty(num_experts + 1, dtype=torch.int32, device=dev_),
+                             torch.empty(cap, dtype=torch.int32, device=dev_),
+                             torch.empty((T, topk), dtype=torch.int32, device=dev_))
         else:
             _same_device(dev, *order)
             _check_int32(order.offsets, num_experts + 1, "offsets")
             _check_int32(order.source, cap, "source")
             _check_int32(order.slots, n, "slots")
-            ws = torch.empty(need // 4, dtype=torch.int32, device=ids.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
         args = (ids.data_ptr(), T, topk, num_experts, align, order.offsets.data_ptr(), order.source.data_ptr(),
                 order.slots.data_ptr(), ws.data_ptr() if need else None, need, _raw_stream(dev))
         return args, order, ws
