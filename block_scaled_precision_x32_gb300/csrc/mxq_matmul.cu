@@ -39,6 +39,15 @@ constexpr int kMostExperts = 1024;
 constexpr int kGroup = 8;
 constexpr int kRing = 2;  // groups, both in shared and in tensor memory
 
+// The tensor core cuts off what a sum's 24 bits cannot hold instead of
+// rounding it, so that the error of a long sum grows with its length: 1.2e-6
+// of the result's norm at a depth of 8191, against 1e-7 for sums that are
+// rounded.  That is far below a bf16 result's own rounding, but not below
+// fp32's.  fp32 results are therefore summed in segments of at most 40 blocks,
+// 5120 of depth, which are added, rounded, to what the output holds: 5e-7 at
+// 8191, 7e-7 at 5119, the worst.  A multiple of kGroup.
+constexpr int kSegment = 40;
+
 // The operand whose rows are the accumulator's lanes is called P, the one
 // whose rows are its columns Q.  Lanes come 128 at a time, columns in any
 // multiple of 16.  Where tokens are few or an expert's, they are the columns:
@@ -70,6 +79,7 @@ struct Problem {
     int E, depth;
     int p_rows, q_rows, p_tiles, q_tiles;
     int columns;  // of the accumulator a tile takes, where experts' rows do not decide it
+    int segment;  // blocks of depth that one accumulation takes: see kSegment
     int ragged;
     bool p_mn, q_mn;   // the operand's depth runs across its rows in memory
     bool p_expert;     // P is a stack of experts' weights
@@ -298,6 +308,12 @@ __device__ __forceinline__ void store_four(const Problem& g, int64_t at, int n, 
         if (i < n) store_one(g, at + i, u[i]);
 }
 
+// Blocks to a segment: as even as groups allow.
+__device__ __forceinline__ int even_segment(const Problem& g, int depth) {
+    const int n = (depth + g.segment - 1) / g.segment;
+    return n <= 1 ? g.segment : ((depth + n - 1) / n + kGroup - 1) / kGroup * kGroup;
+}
+
 // QT: columns of the accumulator, at most for CG 2, where each tile has a
 // width of its own.  CG 2: a pair of blocks, 256 lanes, each loading half of a
 // tile's rows of Q.  CG 1: 128 lanes.  SPLIT: the blocks of a cluster share a
@@ -465,15 +481,17 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
                 const Tile c = tile_at<PT, QT>(g, rag, t);
                 int kb0, kb1;
                 depth_of(c, kb0, kb1);
-                const int blocks = __shfl_sync(0xFFFFFFFFu, kb1 - kb0, 0);
-                if (blocks <= 0) continue;
+                const int depth = __shfl_sync(0xFFFFFFFFu, kb1 - kb0, 0);
+                const uint32_t tile_desc = idesc | instruction_columns(__shfl_sync(0xFFFFFFFFu, c.columns, 0));
+                const int segment = even_segment(g, depth);
+                for (int at = 0; ok && at < depth; at += segment) {
+                const int blocks = min(segment, depth - at);
                 // the accumulator that this tile writes has been taken out
                 if constexpr (QT == 256)
                     ok = it < 1 || mbar_wait(acc_empty, (it - 1) & 1, gave_up);
                 else
                     ok = it < 2 || mbar_wait(acc_empty + 8 * (it & 1), ((it >> 1) - 1) & 1, gave_up);
                 const uint32_t acc = tmem + (it & 1) * S::kAcc1;
-                const uint32_t tile_desc = idesc | instruction_columns(__shfl_sync(0xFFFFFFFFu, c.columns, 0));
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 // Copies the scales of group x of this block's.  That they have arrived says, too, that the
                 // products which used the same bytes and columns before are done.
@@ -519,6 +537,7 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
                 if (!ok) break;
                 if (blocks % kGroup) ++group;
                 ++it;
+                }
             }
             if (!ok) {  // what has been issued ends before the block does
                 volatile int again = 0;
@@ -575,6 +594,9 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
             int kb0, kb1;
             depth_of(c, kb0, kb1);
             const bool none = kb0 >= kb1;  // a sum of nothing
+            const int segment = even_segment(g, kb1 - kb0);
+            for (int seg = kb0; none ? seg == kb0 : seg < kb1; seg += segment) {
+            const bool add = seg > kb0;
             const int a = it & 1;
             if (!none) {
                 ok = ok && mbar_wait(acc_full + 8 * a, (it >> 1) & 1, gave_up);
@@ -627,6 +649,29 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
                     for (int i = 0; i < W; ++i) part[(chunk * W + i) * 128 + 32 * band + lane] = __uint_as_float(v[i]);
                 } else {
                     const int q0 = c.q0 + chunk * W, n = c.q_end - q0;
+                    if (add && row < g.p_rows) {  // this thread's own stores of the segments before (fp32)
+                        const uint32_t* from = static_cast<const uint32_t*>(g.out) + base + (ROWS ? q0 : q0 * g.ldo);
+                        if constexpr (ROWS) {
+#pragma unroll
+                            for (int h = 0; h < W; h += 32) {
+                                uint32_t old[4][8];  // half of the chunk on its way at once
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    if (h + 8 * k + 8 <= n)
+                                        ld32(old[k], from + h + 8 * k);
+                                    else
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i) old[k][i] = h + 8 * k + i < n ? from[h + 8 * k + i] : 0u;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[h + i] = f32_add(v[h + i], old[i / 8][i % 8]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < W; ++i)
+                                if (i < n) v[i] = f32_add(v[i], from[i * g.ldo]);
+                        }
+                    }
                     uint32_t top = 0;  // NaN results are rare: look for any, then make them canonical
 #pragma unroll
                     for (int i = 0; i < W; ++i) top = max(top, v[i] & 0x7FFFFFFFu);
@@ -697,6 +742,7 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
                             if (i < n && row < g.p_rows) *to = (uint16_t)bf16_rne(v[i]);
                     }
                 }
+            }
             }
         }
         // rows that belong to no expert
@@ -815,6 +861,7 @@ cudaError_t launch(const MatmulArgs& m, int ragged, int columns, int split, cuda
     g.q_rows = (int)q.rows;
     g.p_tiles = (int)ceil_div(p.rows, PT);
     g.columns = columns;
+    g.segment = SPLIT || m.out_bf16 ? 1 << 26 : kSegment;
     g.q_tiles = (int)ceil_div(q.rows, columns);
     g.ragged = ragged;
     g.p_mn = p.mn;
@@ -884,6 +931,7 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
         if (ragged == kNone)
             for (int x = 2; x <= 8 && x <= quads && tiles * x <= 2 * sm_count(); ++x)
                 if (ceil_div(quads, x) < ceil_div(quads, split)) split = x;
+        if (!m.out_bf16 && ceil_div(quads, split) * 4 > kSegment) split = 1;  // a share of a cluster is one segment
         if (split > 1)
             e = qt == 16   ? launch<16, 1, true, false>(m, ragged, qt, split, s)
                 : qt == 32 ? launch<32, 1, true, false>(m, ragged, qt, split, s)

@@ -151,7 +151,7 @@ def call(mx, direction):
 
 SIZES = [(1, 1, 1), (1, 128, 128), (1, 1024, 2048), (2, 300, 144), (3, 17, 33), (16, 256, 512), (17, 129, 1040), (33, 640, 384), (64, 200, 4112),
          (65, 1000, 96), (127, 129, 130), (128, 128, 128), (129, 257, 255), (200, 4112, 272), (256, 256, 256), (300, 96, 2064), (385, 784, 656),
-         (513, 1040, 1552), (1100, 528, 912)]
+         (513, 1040, 1552), (1100, 528, 912), (300, 4240, 8336), (4200, 272, 288), (8400, 160, 304), (20, 9000, 300), (3, 304, 33000)]
 
 
 @pytest.mark.parametrize("direction", ["fwd", "dgrad", "wgrad"])
