@@ -147,10 +147,10 @@ __device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t
         }
         c.e = lo;
         t -= r.tiles[lo] * g.p_tiles;
-        const int n = r.tiles[lo + 1] - r.tiles[lo], rows = r.bound[lo + 1] - r.bound[lo];
-        c.columns = QT < 256 ? QT : ((rows + n - 1) / n + 15) & ~15;  // as even as they can be; none is left empty
-        c.q0 = r.bound[lo] + t % n * c.columns;
-        c.q_end = min(r.bound[lo + 1], c.q0 + c.columns);
+        const int n = r.tiles[lo + 1] - r.tiles[lo];
+        c.q0 = r.bound[lo] + t % n * QT;
+        c.q_end = min(r.bound[lo + 1], c.q0 + QT);
+        c.columns = QT < 256 ? QT : (c.q_end - c.q0 + 15) & ~15;  // a narrow last tile loads less than two even ones
         c.p0 = t / n * PT;
         return c;
     }
