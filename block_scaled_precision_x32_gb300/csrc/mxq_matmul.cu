@@ -28,6 +28,7 @@
 
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
+#include "mxq_launch.cuh"
 #include "mxq_tcgen05.cuh"
 
 namespace mxq {
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
     const uint32_t pair_rank = CG == 2 ? rank : 0;
     const bool leader = pair_rank == 0;
 
+    let_next_start();
     if (warp == 0) {
         if (lane == 0) {
             prefetch_map(&p_map);
@@ -396,8 +398,10 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
     } else if (warp == 1) {
         tmem_alloc<CG>(smem_u32(tmem_at), S::kColumns);
     } else if (warp == 2 && g.ragged != kNone) {
+        wait_for_stream();
         read_offsets(g, g.ragged == kDepth ? g.depth : g.q_rows, QT, rag);
     }
+    wait_for_stream();
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();  // its barriers take the other block's arrivals from here on
@@ -719,7 +723,7 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
                     } else if (CG == 2 && g.wide) {
                         // Through shared memory, so that a row's 128 features, 256 bytes, are stored together: the
                         // 64 bytes of one warp's lanes make partial lines, and a 256x256 tile took 9.4 us so
-                        // (fp32, 128 bytes a warp: 3.1 us; this: STAGED us).
+                        // (fp32, 128 bytes a warp: 3.1 us; this: 5.3 us).
                         uint16_t* buf = outs + half * (64 * 128);
 #pragma unroll
                         for (int i = 0; i < W; ++i) buf[128 * i + 32 * band + lane] = (uint16_t)bf16_rne(v[i]);
@@ -789,6 +793,8 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
 
 __global__ void __launch_bounds__(256) repack_kernel(const uint8_t* src, int64_t ld, int64_t rows, int64_t n,
                                                      uint8_t* dst, int64_t ldd) {
+    let_next_start();
+    wait_for_stream();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * ldd; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / ldd, c = i - r * ldd;
         dst[i] = c < n ? src[r * ld + c] : 0;
@@ -891,21 +897,11 @@ cudaError_t launch(const MatmulArgs& m, int ragged, int columns, int split, cuda
         if (device < 64) allowed[device].store(true, std::memory_order_relaxed);
     }
 
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute cluster{};
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = (unsigned)(CG == 2 ? 2 : split);
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
     const int64_t room = (int64_t)sm_count() * S::kPerSm / CG;
     const int64_t blocks = SPLIT ? tiles * split : (tiles < room ? tiles : room) * CG;
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &cluster;
-    cfg.numAttrs = CG == 2 || SPLIT ? 1 : 0;
     const uint32_t idesc = instruction_desc(PT, p.mn, q.mn);
-    return cudaLaunchKernelEx(&cfg, kernel, pm, qm, g, idesc, (int)tiles);
+    return launch_overlapped(kernel, dim3((unsigned)blocks), S::kThreads, smem, CG == 2 ? 2 : SPLIT ? split : 0, stream, pm, qm, g,
+                             idesc, (int)tiles);
 }
 
 }  // namespace
@@ -952,8 +948,8 @@ cudaError_t launch_repack(const uint8_t* src, int64_t ld, int64_t rows, int64_t 
     if (rows == 0) return cudaSuccess;
     const int64_t want = ceil_div(rows * ldd, 256);
     const int64_t most = (int64_t)sm_count() * 16;
-    repack_kernel<<<(unsigned)(want < most ? want : most), 256, 0, s>>>(src, ld, rows, n, dst, ldd);
-    return cudaGetLastError();
+    return launch_overlapped(repack_kernel, dim3((unsigned)(want < most ? want : most)), 256, 0, 0, s, src, ld, rows, n, dst,
+                             ldd);
 }
 
 }  // namespace mxq

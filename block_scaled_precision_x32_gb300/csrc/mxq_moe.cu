@@ -7,6 +7,7 @@
 
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
+#include "mxq_launch.cuh"
 
 namespace mxq {
 namespace {
@@ -43,6 +44,8 @@ __device__ __forceinline__ void count_chunk(const MoeSortArgs& a, int walkers, i
 
 __global__ void __launch_bounds__(1024) count_kernel(MoeSortArgs a, int walkers) {
     extern __shared__ int hist[];
+    let_next_start();
+    wait_for_stream();
     count_chunk<false>(a, walkers, hist);
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) a.counts[blockIdx.x * a.experts + e] = hist[e];
 }
@@ -53,6 +56,8 @@ __global__ void __launch_bounds__(1024) count_kernel(MoeSortArgs a, int walkers)
 // expert as the block has.
 __global__ void __launch_bounds__(1024) place_kernel(MoeSortArgs a, int chunks, int walkers) {
     extern __shared__ int smem[];
+    let_next_start();
+    wait_for_stream();
     const int E = (int)a.experts;
     int* hist = smem;                 // [walkers][E]
     int* begin = smem + walkers * E;  // [E + 1]
@@ -204,6 +209,8 @@ struct Piece {
 // One row of the order to blockIdx.x, a slice of its pieces to blockIdx.y.
 template <Elt ELT, int VEC>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
+    let_next_start();
+    wait_for_stream();
     const int64_t pieces = a.H / VEC;
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
         const int c = a.source[r];
@@ -224,6 +231,8 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
 // to blockIdx.y; the rows of four choices are loaded before they are added.
 template <Elt ELT, int VEC>
 __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(MoeRowsArgs a) {
+    let_next_start();
+    wait_for_stream();
     const int64_t pieces = a.H / VEC;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x)
         for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.y * kRowThreads) {
@@ -258,6 +267,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(MoeRowsArgs a) 
 // the tokens' clear the rows of no choice.
 template <Elt ELT, int VEC, int TG>
 __global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsArgs a, int64_t work, int64_t work_blocks) {
+    let_next_start();
+    wait_for_stream();
     const int64_t pieces = a.H / VEC, n = a.T * a.topk;
     if (blockIdx.x >= work_blocks) {
         // each thread looks at one of the block's next rows; those of no choice are cleared by the whole block
@@ -353,29 +364,31 @@ dim3 row_grid(int64_t rows, int64_t pieces) {
 template <Elt ELT, int VEC>
 cudaError_t rows_launch(int what, const MoeRowsArgs& a, cudaStream_t s) {
     if (what == 0) {
-        dispatch_kernel<ELT, VEC><<<row_grid(a.R, a.H / VEC), kRowThreads, 0, s>>>(a);
+        return launch_overlapped(dispatch_kernel<ELT, VEC>, row_grid(a.R, a.H / VEC), kRowThreads, 0, 0, s, a);
     } else if (what == 1) {
-        combine_kernel<ELT, VEC><<<row_grid(a.T, a.H / VEC), kRowThreads, 0, s>>>(a);
+        return launch_overlapped(combine_kernel<ELT, VEC>, row_grid(a.T, a.H / VEC), kRowThreads, 0, 0, s, a);
     } else {
-        // four choices to a block, or one where that leaves the device empty (64 tokens of 7184, topk 4, bf16: 10.3 us with
-        // four, GRADSMALL with one; 8191 tokens: 214 and 282)
+        // four choices to a block, or one where that leaves the device empty (64 tokens of 7184, topk 4, bf16: 6.8 us with
+        // four, 4.4 with one; 8191 tokens: 192 and 282)
         const int together = a.T * ceil_div(a.topk, kTogether) < 8 * (int64_t)sm_count() ? 1 : kTogether;
         const int64_t work = a.T * ceil_div(a.topk, together), work_blocks = work < (1 << 30) ? work : 1 << 30;
         const int64_t room = ceil_div(a.R, kGradThreads), clear = room < sm_count() ? room : sm_count();
         const unsigned grid = (unsigned)(work_blocks + clear);
         constexpr int V = VEC == 1 ? 1 : VEC / 2;
-        if (together == 1)
-            combine_grad_kernel<ELT, V, 1><<<grid, kGradThreads, 0, s>>>(a, work, work_blocks);
-        else
-            combine_grad_kernel<ELT, V, kTogether><<<grid, kGradThreads, 0, s>>>(a, work, work_blocks);
+        return together == 1
+                   ? launch_overlapped(combine_grad_kernel<ELT, V, 1>, dim3(grid), kGradThreads, 0, 0, s, a, work, work_blocks)
+                   : launch_overlapped(combine_grad_kernel<ELT, V, kTogether>, dim3(grid), kGradThreads, 0, 0, s, a, work,
+                                       work_blocks);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t rows_launch(int what, Elt elt, const MoeRowsArgs& a, cudaStream_t s) {
-    if (elt == Elt::BF16)
-        return whole_pieces<Elt::BF16>(a) ? rows_launch<Elt::BF16, 16>(what, a, s) : rows_launch<Elt::BF16, 1>(what, a, s);
-    return whole_pieces<Elt::FP32>(a) ? rows_launch<Elt::FP32, 8>(what, a, s) : rows_launch<Elt::FP32, 1>(what, a, s);
+    const cudaError_t e =
+        elt == Elt::BF16
+            ? (whole_pieces<Elt::BF16>(a) ? rows_launch<Elt::BF16, 16>(what, a, s) : rows_launch<Elt::BF16, 1>(what, a, s))
+            : (whole_pieces<Elt::FP32>(a) ? rows_launch<Elt::FP32, 8>(what, a, s) : rows_launch<Elt::FP32, 1>(what, a, s));
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -389,20 +402,17 @@ cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
     int walkers = (int)(INT64_C(128) * 1024 / (a.experts * 4));
     walkers = walkers < threads / 32 ? walkers : threads / 32;
     const int one = (int)a.experts * 4, hist = walkers * one, place = hist + (int)(3 * a.experts + 1) * 4;
-    if (place > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, place);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return e;
-        }
+    cudaError_t e = cudaSuccess;
+    if (place > 48 * 1024) e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, place);
+    if (e == cudaSuccess && chunks > 1) e = launch_overlapped(count_kernel, dim3(chunks), threads, one, 0, s, a, walkers);
+    if (e == cudaSuccess) {
+        // not overlapped with count_kernel: its blocks would take the multiprocessors' threads while that still runs
+        // (65536 x 8 over 256 experts: 14.0 us; overlapped 20)
+        place_kernel<<<chunks, threads, place, s>>>(a, chunks, walkers);
+        e = cudaGetLastError();
     }
-    if (chunks > 1) {
-        count_kernel<<<chunks, threads, one, s>>>(a, walkers);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    place_kernel<<<chunks, threads, place, s>>>(a, chunks, walkers);
-    return cudaGetLastError();
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_moe_dispatch(Elt elt, const MoeRowsArgs& a, cudaStream_t s) { return rows_launch(0, elt, a, s); }

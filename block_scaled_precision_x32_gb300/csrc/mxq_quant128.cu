@@ -8,6 +8,7 @@
 
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
+#include "mxq_launch.cuh"
 
 namespace mxq {
 namespace {
@@ -67,6 +68,8 @@ struct Unit {
 // 8192 x 7184 bf16: see the table of figures in the launcher's comment.
 template <Elt ELT, int UNITS>
 __global__ void __launch_bounds__(256) quant_rows_unit_kernel(Quant128Args a, int64_t nb) {
+    let_next_start();
+    wait_for_stream();
     const int64_t first = (int64_t)blockIdx.x * (256 * UNITS) + threadIdx.x, total = a.out_rows * nb * 8;
     Unit<ELT> u[UNITS];
     int64_t row[UNITS], b[UNITS];
@@ -107,6 +110,8 @@ __global__ void __launch_bounds__(256) quant_rows_unit_kernel(Quant128Args a, in
 // Any alignment and any K: one warp per 1x128 block, an element at a time.
 template <Elt ELT>
 __global__ void __launch_bounds__(256) quant_rows_kernel(Quant128Args a, int64_t nb) {
+    let_next_start();
+    wait_for_stream();
     const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32;
     if (unit >= a.out_rows * nb) return;
     int64_t r, b;
@@ -137,6 +142,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(Quant128Args a, int64_t
 // it) and shared memory.
 template <Elt ELT>
 __global__ void __launch_bounds__(256) quant_columns_tile_kernel(Quant128Args a) {
+    let_next_start();
+    wait_for_stream();
     constexpr int R = 4;
     __shared__ uint4 top[8][16];  // [warp][64 columns]
     __shared__ uint2 codes[8];    // 64 bytes
@@ -210,6 +217,8 @@ __global__ void __launch_bounds__(256) quant_columns_tile_kernel(Quant128Args a)
 // Any alignment and any K: one thread per 128x1 block.
 template <Elt ELT>
 __global__ void __launch_bounds__(128) quant_columns_kernel(Quant128Args a) {
+    let_next_start();
+    wait_for_stream();
     const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
     if (c >= a.K) return;
     const int64_t r0 = (int64_t)blockIdx.y * 128, r1 = min(r0 + 128, a.out_rows);
@@ -250,11 +259,9 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
             p.data = a.data + r0 * a.K;
             p.scales = a.scales + r0 / 128 * a.K;
             const unsigned y = (unsigned)ceil_div(p.out_rows, 128);
-            if (tiled)
-                quant_columns_tile_kernel<ELT><<<dim3((unsigned)ceil_div(a.K, 64), y), 256, 0, s>>>(p);
-            else
-                quant_columns_kernel<ELT><<<dim3((unsigned)ceil_div(a.K, 128), y), 128, 0, s>>>(p);
-            const cudaError_t e = cudaGetLastError();
+            const cudaError_t e =
+                tiled ? launch_overlapped(quant_columns_tile_kernel<ELT>, dim3((unsigned)ceil_div(a.K, 64), y), 256, 0, 0, s, p)
+                      : launch_overlapped(quant_columns_kernel<ELT>, dim3((unsigned)ceil_div(a.K, 128), y), 128, 0, 0, s, p);
             if (e != cudaSuccess) return e;
         }
         return cudaSuccess;
@@ -264,18 +271,18 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
     // units of 16 elements: 32-byte loads and 16-byte stores
     if (a.K % 16 == 0 && on(a.x, 32) && (one_row || a.ldx * es % 32 == 0) && on(a.data, 16)) {
         constexpr int units = 1;
-        quant_rows_unit_kernel<ELT, units>
-            <<<(unsigned)ceil_div(a.out_rows * nb * 8, 256 * units), 256, 0, s>>>(a, nb);
-        return cudaGetLastError();
+        return launch_overlapped(quant_rows_unit_kernel<ELT, units>, dim3((unsigned)ceil_div(a.out_rows * nb * 8, 256 * units)),
+                                 256, 0, 0, s, a, nb);
     }
-    quant_rows_kernel<ELT><<<(unsigned)ceil_div(a.out_rows * nb, 8), 256, 0, s>>>(a, nb);
-    return cudaGetLastError();
+    return launch_overlapped(quant_rows_kernel<ELT>, dim3((unsigned)ceil_div(a.out_rows * nb, 8)), 256, 0, 0, s, a, nb);
 }
 
 }  // namespace
 
 cudaError_t launch_quant128(Elt elt, bool columns, const Quant128Args& a, cudaStream_t s) {
-    return elt == Elt::BF16 ? launch<Elt::BF16>(columns, a, s) : launch<Elt::FP32>(columns, a, s);
+    const cudaError_t e = elt == Elt::BF16 ? launch<Elt::BF16>(columns, a, s) : launch<Elt::FP32>(columns, a, s);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
 }
 
 }  // namespace mxq
