@@ -79,7 +79,8 @@ mxq_status check_product(const mxq_fp8_product* p) {
         return MXQ_ERR_INVALID_ARG;
     const mxq_status st = check_dtype(p->out_dt);
     if (st != MXQ_OK) return st;
-    if (!valid_dim(p->M) || !valid_dim(p->N) || !valid_dim(p->K)) return MXQ_ERR_INVALID_ARG;
+    for (int64_t n : {p->M, p->N, p->K})
+        if (n < 0 || n > (INT64_C(1) << 30)) return MXQ_ERR_INVALID_ARG;
     if (p->offsets && (p->E < 1 || p->E > 1024 || !aligned(p->offsets, 4))) return MXQ_ERR_INVALID_ARG;
     const Operands o = operands(*p);
     if (!valid_ld(o.a_n, p->lda) || !valid_ld(o.b_n, p->ldb) || !valid_ld(o.out_n, p->ldo)) return MXQ_ERR_INVALID_ARG;

@@ -16,10 +16,27 @@
 // One thread block (or a pair of them, on two SMs) is a pipeline of warps:
 //   warp 0     TMA: boxes of both operands, 128 deep, into a ring of stages
 //   warp 1     one thread issues scale copies and MMAs
-//   warp 2, 3  gather the scale bytes of four blocks (512 of depth) of each operand
+//   warp 2, 3  gather the scale bytes of eight blocks (1024 of depth) of each operand
 //   warps 4..  take finished sums out of tensor memory, round and store them
 // Blocks walk over their tiles, so that loads and MMAs of the next tile run
 // while the last one is being stored.
+//
+// What bounds it (GB300; the tensor cores' own time for a 256x256 tile and 128
+// of depth is 497 clocks, 4.9 PFLOP/s at 2 GHz):
+//   8192^3                       0.305 ms, 3.6 PFLOP/s: the board's power.  On
+//                                operands of zeros 0.263 ms, 4.2 PFLOP/s.
+//   rows of 7184 bytes           a box of 128 bytes lies across two 128-byte
+//                                lines; the L2 serves five sectors for four:
+//                                16384x4096x7184 2.7 PFLOP/s, at 8192 deep 3.5.
+//   few rows                     the weight's bytes: one token through
+//                                8192x8192 15.1 us, 4.4 TB/s, of which 10.4 us
+//                                are the stream at 6.4 TB/s and the rest the
+//                                launch, the first loads and the sum over a
+//                                cluster; 48 tokens x 2 of 32 experts
+//                                (4096x7184 each) at 6 TB/s.
+// A pair's stages take 32 KB a block of depth on each SM, which at the tensor
+// cores' rate is 18 TB/s from the L2: wider sharing (clusters of four with
+// multicast) would relieve it, but only 144 of the 152 SMs hold such clusters.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -35,8 +52,8 @@ namespace mxq {
 namespace {
 
 constexpr int kMostExperts = 1024;
-// Scales move in groups of two words a row, eight blocks of depth: what a warp spends on a group (its loads, which the
-// proxy fence waits for, and the fence) is about 2000 clocks, as long as the products of four blocks.
+// Scales move in groups of two words a row, eight blocks of depth: a warp spends about 1000 clocks on a group (its loads,
+// which the proxy fence waits for, the words' order and the fence), the tensor cores 4000 on its products.
 constexpr int kGroup = 8;
 constexpr int kRing = 2;  // groups, both in shared and in tensor memory
 
@@ -136,7 +153,7 @@ __device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t
     Tile c;
     c.e = 0;
     c.kb0 = 0;
-    c.kb1 = (g.depth + 127) >> 7;
+    c.kb1 = (g.depth + 127) >> 7;  // sizes are at most 2^30
     if (g.ragged == kRowsOfQ) {
         int lo = 0, hi = g.E - 1;  // the last expert whose tiles begin at or before t
         while (lo < hi) {
@@ -489,58 +506,58 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
                 const uint32_t tile_desc = idesc | instruction_columns(__shfl_sync(0xFFFFFFFFu, c.columns, 0));
                 const int segment = even_segment(g, depth);
                 for (int at = 0; ok && at < depth; at += segment) {
-                const int blocks = min(segment, depth - at);
-                // the accumulator that this tile writes has been taken out
-                if constexpr (QT == 256)
-                    ok = it < 1 || mbar_wait(acc_empty, (it - 1) & 1, gave_up);
-                else
-                    ok = it < 2 || mbar_wait(acc_empty + 8 * (it & 1), ((it >> 1) - 1) & 1, gave_up);
-                const uint32_t acc = tmem + (it & 1) * S::kAcc1;
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                // Copies the scales of group x of this block's.  That they have arrived says, too, that the
-                // products which used the same bytes and columns before are done.
-                auto scales_of = [&](int x) {
-                    const int slot = x % kRing;
-                    const bool there = __all_sync(0xFFFFFFFFu, mbar_wait(sc_full + 8 * slot, (x / kRing) & 1, gave_up));
-                    tc_fence_after();
-                    if (there && elect_one()) {
-#pragma unroll
-                        for (int h = slot * (kGroup / 4), a = 0; a < (kGroup / 4) * (1 + S::kQAtoms); ++a)
-                            copy_scales<CG>(tmem + S::kScaleAt + h * S::kScaleColumns + 4 * a,
-                                            desc_s + ((h * S::kScaleBytes + 512 * a) >> 4));
-                    }
-                    __syncwarp();
-                    return there;
-                };
-                ok = ok && scales_of(group);
-                for (int i = 0; ok && i < blocks; ++i) {
-                    const uint32_t j = i % kGroup;
-                    const uint32_t sfp = tmem + S::kScaleAt + ((group % kRing) * (kGroup / 4) + j / 4) * S::kScaleColumns,
-                                   sfq = sfp + 4;
-                    ok = ok && mbar_wait(full + 8 * s, parity, gave_up);
+                    const int blocks = min(segment, depth - at);
+                    // the accumulator that this tile writes has been taken out
+                    if constexpr (QT == 256)
+                        ok = it < 1 || mbar_wait(acc_empty, (it - 1) & 1, gave_up);
+                    else
+                        ok = it < 2 || mbar_wait(acc_empty + 8 * (it & 1), ((it >> 1) - 1) & 1, gave_up);
+                    const uint32_t acc = tmem + (it & 1) * S::kAcc1;
                     ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const bool last = i + 1 == blocks;
-                    if (elect_one()) {
-                        const uint64_t dp = desc_p + ((s * S::kStageBytes) >> 4), dq = desc_q + ((s * S::kStageBytes) >> 4);
-                        const uint32_t id = tile_desc | scale_byte(j & 3);
+                    // Copies the scales of group x of this block's.  That they have arrived says, too, that the
+                    // products which used the same bytes and columns before are done.
+                    auto scales_of = [&](int x) {
+                        const int slot = x % kRing;
+                        const bool there = __all_sync(0xFFFFFFFFu, mbar_wait(sc_full + 8 * slot, (x / kRing) & 1, gave_up));
+                        tc_fence_after();
+                        if (there && elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_block_scaled<CG>(acc, dp + k * step_p, dq + k * step_q, id, sfp, sfq, i > 0 || k > 0);
-                        mma_commit<CG>(empty + 8 * s);
-                        if (j == kGroup - 1 || last) mma_commit<CG>(sc_empty + 8 * (group % kRing));
-                        if (last) mma_commit<CG>(acc_full + 8 * (it & 1));
+                            for (int h = slot * (kGroup / 4), a = 0; a < (kGroup / 4) * (1 + S::kQAtoms); ++a)
+                                copy_scales<CG>(tmem + S::kScaleAt + h * S::kScaleColumns + 4 * a,
+                                                desc_s + ((h * S::kScaleBytes + 512 * a) >> 4));
+                        }
+                        __syncwarp();
+                        return there;
+                    };
+                    ok = ok && scales_of(group);
+                    for (int i = 0; ok && i < blocks; ++i) {
+                        const uint32_t j = i % kGroup;
+                        const uint32_t sfp = tmem + S::kScaleAt + ((group % kRing) * (kGroup / 4) + j / 4) * S::kScaleColumns,
+                                       sfq = sfp + 4;
+                        ok = ok && mbar_wait(full + 8 * s, parity, gave_up);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const bool last = i + 1 == blocks;
+                        if (elect_one()) {
+                            const uint64_t dp = desc_p + ((s * S::kStageBytes) >> 4), dq = desc_q + ((s * S::kStageBytes) >> 4);
+                            const uint32_t id = tile_desc | scale_byte(j & 3);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_block_scaled<CG>(acc, dp + k * step_p, dq + k * step_q, id, sfp, sfq, i > 0 || k > 0);
+                            mma_commit<CG>(empty + 8 * s);
+                            if (j == kGroup - 1 || last) mma_commit<CG>(sc_empty + 8 * (group % kRing));
+                            if (last) mma_commit<CG>(acc_full + 8 * (it & 1));
+                        }
+                        __syncwarp();
+                        if (++s == S::kStages) s = 0, parity ^= 1;
+                        // copied well in front of the products that need them
+                        if (j == kGroup - 3 && i + 3 < blocks) ok = scales_of(group + 1);
+                        if (j == kGroup - 1) ++group;
                     }
-                    __syncwarp();
-                    if (++s == S::kStages) s = 0, parity ^= 1;
-                    // copied well in front of the products that need them
-                    if (j == kGroup - 3 && i + 3 < blocks) ok = scales_of(group + 1);
-                    if (j == kGroup - 1) ++group;
-                }
-                if (!ok) break;
-                if (blocks % kGroup) ++group;
-                ++it;
+                    if (!ok) break;
+                    if (blocks % kGroup) ++group;
+                    ++it;
                 }
             }
             if (!ok) {  // what has been issued ends before the block does
@@ -600,153 +617,153 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
             const bool none = kb0 >= kb1;  // a sum of nothing
             const int segment = even_segment(g, kb1 - kb0);
             for (int seg = kb0; none ? seg == kb0 : seg < kb1; seg += segment) {
-            const bool add = seg > kb0;
-            const int a = it & 1;
-            if (!none) {
-                ok = ok && mbar_wait(acc_full + 8 * a, (it >> 1) & 1, gave_up);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                tc_fence_after();
-                ++it;
-            }
-            const int row = c.p0 + 128 * (int)pair_rank + 32 * band + lane;  // of P: a column of the output
-            const int64_t base = (g.ragged == kDepth ? c.e * g.out_expert : 0) + (ROWS ? row * g.ldo : row);
-            const int chunks = QT == 256 ? (c.columns + W - 1) / W : QT / W;
-            // eight warps: the even and the odd chunks have four each
-            constexpr int kHalves = S::kOutWarps / 4;
-            const int half = kHalves == 2 ? (warp - 4) >> 2 : 0;
-            bool held = !none;  // the accumulator's shared columns
+                const bool add = seg > kb0;
+                const int a = it & 1;
+                if (!none) {
+                    ok = ok && mbar_wait(acc_full + 8 * a, (it >> 1) & 1, gave_up);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    tc_fence_after();
+                    ++it;
+                }
+                const int row = c.p0 + 128 * (int)pair_rank + 32 * band + lane;  // of P: a column of the output
+                const int64_t base = (g.ragged == kDepth ? c.e * g.out_expert : 0) + (ROWS ? row * g.ldo : row);
+                const int chunks = QT == 256 ? (c.columns + W - 1) / W : QT / W;
+                // eight warps: the even and the odd chunks have four each
+                constexpr int kHalves = S::kOutWarps / 4;
+                const int half = kHalves == 2 ? (warp - 4) >> 2 : 0;
+                bool held = !none;  // the accumulator's shared columns
 #pragma unroll 1
-            for (int x = half; x < chunks || held; x += kHalves) {
-                // The columns that the two accumulators share come first (the second one's first, the first
-                // one's last): only they hold up the next tile.
-                const int chunk = QT != 256 || a != 0 || chunks != 4 ? x : kHalves == 1 ? (x + 3) & 3 : half == 1 ? x ^ 2 : x;
-                uint32_t v[W];
-                if (!none && ok && x < chunks) {
-                    const uint32_t from = tmem + lanes + a * S::kAcc1 + chunk * W;
-                    if constexpr (W == 16) {
-                        tmem_ld(v, from);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < W / 32; ++h) tmem_ld(reinterpret_cast<uint32_t(&)[32]>(v[32 * h]), from + 32 * h);
-                    }
-                    tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) v[i] = none ? 0u : 0x7FC00000u;
-                }
-                if (held && (QT == 256 || x == chunks - 1)) {
-                    held = false;
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        const int bar = QT == 256 ? 0 : a;
-                        if constexpr (CG == 2)
-                            mbar_arrive_cluster(release_at + 8 * bar);
-                        else
-                            mbar_arrive(acc_empty + 8 * bar);
-                    }
-                }
-                if (x >= chunks) break;
-                if constexpr (SPLIT) {
-                    float* part = reinterpret_cast<float*>(stages);  // [QT][128]: every load and MMA is done
-#pragma unroll
-                    for (int i = 0; i < W; ++i) part[(chunk * W + i) * 128 + 32 * band + lane] = __uint_as_float(v[i]);
-                } else {
-                    const int q0 = c.q0 + chunk * W, n = c.q_end - q0;
-                    if (add && row < g.p_rows) {  // this thread's own stores of the segments before (fp32)
-                        const uint32_t* from = static_cast<const uint32_t*>(g.out) + base + (ROWS ? q0 : q0 * g.ldo);
-                        if constexpr (ROWS) {
-#pragma unroll
-                            for (int h = 0; h < W; h += 32) {
-                                uint32_t old[4][8];  // half of the chunk on its way at once
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    if (h + 8 * k + 8 <= n)
-                                        ld32(old[k], from + h + 8 * k);
-                                    else
-#pragma unroll
-                                        for (int i = 0; i < 8; ++i) old[k][i] = h + 8 * k + i < n ? from[h + 8 * k + i] : 0u;
-                                }
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[h + i] = f32_add(v[h + i], old[i / 8][i % 8]);
-                            }
+                for (int x = half; x < chunks || held; x += kHalves) {
+                    // The columns that the two accumulators share come first (the second one's first, the first
+                    // one's last): only they hold up the next tile.
+                    const int chunk = QT != 256 || a != 0 || chunks != 4 ? x : kHalves == 1 ? (x + 3) & 3 : half == 1 ? x ^ 2 : x;
+                    uint32_t v[W];
+                    if (!none && ok && x < chunks) {
+                        const uint32_t from = tmem + lanes + a * S::kAcc1 + chunk * W;
+                        if constexpr (W == 16) {
+                            tmem_ld(v, from);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < W; ++i)
-                                if (i < n) v[i] = f32_add(v[i], from[i * g.ldo]);
+                            for (int h = 0; h < W / 32; ++h) tmem_ld(reinterpret_cast<uint32_t(&)[32]>(v[32 * h]), from + 32 * h);
+                        }
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) v[i] = none ? 0u : 0x7FC00000u;
+                    }
+                    if (held && (QT == 256 || x == chunks - 1)) {
+                        held = false;
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            const int bar = QT == 256 ? 0 : a;
+                            if constexpr (CG == 2)
+                                mbar_arrive_cluster(release_at + 8 * bar);
+                            else
+                                mbar_arrive(acc_empty + 8 * bar);
                         }
                     }
-                    uint32_t top = 0;  // NaN results are rare: look for any, then make them canonical
+                    if (x >= chunks) break;
+                    if constexpr (SPLIT) {
+                        float* part = reinterpret_cast<float*>(stages);  // [QT][128]: every load and MMA is done
 #pragma unroll
-                    for (int i = 0; i < W; ++i) top = max(top, v[i] & 0x7FFFFFFFu);
-                    if (top > 0x7F800000u)
+                        for (int i = 0; i < W; ++i) part[(chunk * W + i) * 128 + 32 * band + lane] = __uint_as_float(v[i]);
+                    } else {
+                        const int q0 = c.q0 + chunk * W, n = c.q_end - q0;
+                        if (add && row < g.p_rows) {  // this thread's own stores of the segments before (fp32)
+                            const uint32_t* from = static_cast<const uint32_t*>(g.out) + base + (ROWS ? q0 : q0 * g.ldo);
+                            if constexpr (ROWS) {
 #pragma unroll
-                        for (int i = 0; i < W; ++i) v[i] = canonical(v[i]);
-                    if constexpr (ROWS) {
-                        // a thread's 64 columns are neighbours: whole sectors of 32 bytes (launch_matmul sees to it that
-                        // they are aligned)
-                        if (row < g.p_rows) {
-                            if (g.out_bf16) {
-                                uint16_t* to = static_cast<uint16_t*>(g.out) + base + q0;
+                                for (int h = 0; h < W; h += 32) {
+                                    uint32_t old[4][8];  // half of the chunk on its way at once
 #pragma unroll
-                                for (int h = 0; h < W / 16; ++h) {
-                                    uint32_t w[8];
+                                    for (int k = 0; k < 4; ++k) {
+                                        if (h + 8 * k + 8 <= n)
+                                            ld32(old[k], from + h + 8 * k);
+                                        else
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) w[i] = bf16_rne(v[16 * h + 2 * i]) | bf16_rne(v[16 * h + 2 * i + 1]) << 16;
-                                    if (16 * h + 16 <= n)
-                                        st32(to + 16 * h, w);
-                                    else
+                                            for (int i = 0; i < 8; ++i) old[k][i] = h + 8 * k + i < n ? from[h + 8 * k + i] : 0u;
+                                    }
 #pragma unroll
-                                        for (int i = 0; i < 16; ++i)
-                                            if (16 * h + i < n) to[16 * h + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                                    for (int i = 0; i < 32; ++i) v[h + i] = f32_add(v[h + i], old[i / 8][i % 8]);
                                 }
                             } else {
-                                uint32_t* to = static_cast<uint32_t*>(g.out) + base + q0;
 #pragma unroll
-                                for (int h = 0; h < W / 8; ++h) {
-                                    if (8 * h + 8 <= n)
-                                        st32(to + 8 * h, reinterpret_cast<uint32_t(&)[8]>(v[8 * h]));
-                                    else
-#pragma unroll
-                                        for (int i = 0; i < 8; ++i)
-                                            if (8 * h + i < n) to[8 * h + i] = v[8 * h + i];
-                                }
+                                for (int i = 0; i < W; ++i)
+                                    if (i < n) v[i] = f32_add(v[i], from[i * g.ldo]);
                             }
                         }
-                    } else if (!g.out_bf16) {  // a warp's 32 lanes store 128 neighbouring bytes
-                        uint32_t* to = static_cast<uint32_t*>(g.out) + base + q0 * g.ldo;
-                        if (row < g.p_rows) {
+                        uint32_t top = 0;  // NaN results are rare: look for any, then make them canonical
+#pragma unroll
+                        for (int i = 0; i < W; ++i) top = max(top, v[i] & 0x7FFFFFFFu);
+                        if (top > 0x7F800000u)
+#pragma unroll
+                            for (int i = 0; i < W; ++i) v[i] = canonical(v[i]);
+                        if constexpr (ROWS) {
+                            // a thread's 64 columns are neighbours: whole sectors of 32 bytes (launch_matmul sees to it that
+                            // they are aligned)
+                            if (row < g.p_rows) {
+                                if (g.out_bf16) {
+                                    uint16_t* to = static_cast<uint16_t*>(g.out) + base + q0;
+#pragma unroll
+                                    for (int h = 0; h < W / 16; ++h) {
+                                        uint32_t w[8];
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i) w[i] = bf16_rne(v[16 * h + 2 * i]) | bf16_rne(v[16 * h + 2 * i + 1]) << 16;
+                                        if (16 * h + 16 <= n)
+                                            st32(to + 16 * h, w);
+                                        else
+#pragma unroll
+                                            for (int i = 0; i < 16; ++i)
+                                                if (16 * h + i < n) to[16 * h + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                                    }
+                                } else {
+                                    uint32_t* to = static_cast<uint32_t*>(g.out) + base + q0;
+#pragma unroll
+                                    for (int h = 0; h < W / 8; ++h) {
+                                        if (8 * h + 8 <= n)
+                                            st32(to + 8 * h, reinterpret_cast<uint32_t(&)[8]>(v[8 * h]));
+                                        else
+#pragma unroll
+                                            for (int i = 0; i < 8; ++i)
+                                                if (8 * h + i < n) to[8 * h + i] = v[8 * h + i];
+                                    }
+                                }
+                            }
+                        } else if (!g.out_bf16) {  // a warp's 32 lanes store 128 neighbouring bytes
+                            uint32_t* to = static_cast<uint32_t*>(g.out) + base + q0 * g.ldo;
+                            if (row < g.p_rows) {
+#pragma unroll
+                                for (int i = 0; i < W; ++i, to += g.ldo)
+                                    if (i < n) *to = v[i];
+                            }
+                        } else if (CG == 2 && g.wide) {
+                            // Through shared memory, so that a row's 128 features, 256 bytes, are stored together: the
+                            // 64 bytes of one warp's lanes make partial lines, and a 256x256 tile took 9.4 us so
+                            // (fp32, 128 bytes a warp: 3.1 us; this: 5.3 us).
+                            uint16_t* buf = outs + half * (64 * 128);
+#pragma unroll
+                            for (int i = 0; i < W; ++i) buf[128 * i + 32 * band + lane] = (uint16_t)bf16_rne(v[i]);
+                            asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                            const int part = threadIdx.x & 15, feature = c.p0 + 128 * (int)pair_rank + 8 * part;
+                            uint16_t* to = static_cast<uint16_t*>(g.out) + base - row + feature + (int64_t)q0 * g.ldo;
+#pragma unroll
+                            for (int k = 0; k < W / 8; ++k) {
+                                const int i = 8 * k + ((threadIdx.x >> 4) & 7);
+                                const uint4 y = *reinterpret_cast<const uint4*>(buf + 128 * i + 8 * part);
+                                if (i < n && feature + 8 <= g.p_rows) *reinterpret_cast<uint4*>(to + i * g.ldo) = y;
+                                if (i < n && feature + 8 > g.p_rows)
+                                    for (int f = 0; feature + f < g.p_rows; ++f) to[i * g.ldo + f] = buf[128 * i + 8 * part + f];
+                            }
+                            asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                        } else {
+                            uint16_t* to = static_cast<uint16_t*>(g.out) + base + q0 * g.ldo;
 #pragma unroll
                             for (int i = 0; i < W; ++i, to += g.ldo)
-                                if (i < n) *to = v[i];
+                                if (i < n && row < g.p_rows) *to = (uint16_t)bf16_rne(v[i]);
                         }
-                    } else if (CG == 2 && g.wide) {
-                        // Through shared memory, so that a row's 128 features, 256 bytes, are stored together: the
-                        // 64 bytes of one warp's lanes make partial lines, and a 256x256 tile took 9.4 us so
-                        // (fp32, 128 bytes a warp: 3.1 us; this: 5.3 us).
-                        uint16_t* buf = outs + half * (64 * 128);
-#pragma unroll
-                        for (int i = 0; i < W; ++i) buf[128 * i + 32 * band + lane] = (uint16_t)bf16_rne(v[i]);
-                        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-                        const int part = threadIdx.x & 15, feature = c.p0 + 128 * (int)pair_rank + 8 * part;
-                        uint16_t* to = static_cast<uint16_t*>(g.out) + base - row + feature + (int64_t)q0 * g.ldo;
-#pragma unroll
-                        for (int k = 0; k < W / 8; ++k) {
-                            const int i = 8 * k + ((threadIdx.x >> 4) & 7);
-                            const uint4 y = *reinterpret_cast<const uint4*>(buf + 128 * i + 8 * part);
-                            if (i < n && feature + 8 <= g.p_rows) *reinterpret_cast<uint4*>(to + i * g.ldo) = y;
-                            if (i < n && feature + 8 > g.p_rows)
-                                for (int f = 0; feature + f < g.p_rows; ++f) to[i * g.ldo + f] = buf[128 * i + 8 * part + f];
-                        }
-                        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-                    } else {
-                        uint16_t* to = static_cast<uint16_t*>(g.out) + base + q0 * g.ldo;
-#pragma unroll
-                        for (int i = 0; i < W; ++i, to += g.ldo)
-                            if (i < n && row < g.p_rows) *to = (uint16_t)bf16_rne(v[i]);
                     }
                 }
-            }
             }
         }
         // rows that belong to no expert
@@ -910,9 +927,14 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
     const int ragged = m.grouping == Grouping::DEPTH ? kDepth : m.grouping == Grouping::ROWS ? kRowsOfQ : kNone;
     const int64_t features = m.b.rows, tokens = m.a.rows, blocks = ceil_div(m.depth, 128);
     cudaError_t e;
-    if (tokens > 256 && features > 128 && !(ragged == kRowsOfQ && tokens / m.E < 64)) {
+    // Pairs of blocks and 256x256 tiles where there are rows enough to fill them.  512x4096x4096: 17.6 us, 23.5 in tiles of
+    // 128x128 with the depth split; 256: 18.3 and 14.0.  32 experts of 4096x4096 with 50 rows each on average: 92 us, 102
+    // in single blocks; with 8: 64 in both.
+    if (tokens > 256 && features > 128 && !(ragged == kRowsOfQ && tokens / m.E < 16)) {
         const int64_t es = m.out_bf16 ? 2 : 4;
         const bool sectors = reinterpret_cast<uintptr_t>(m.out) % 32 == 0 && m.ldo * es % 32 == 0;
+        // 8192^3 with the rows as lanes 284 us, as columns 293; experts' rows are columns for their tiles' width (a
+        // 32-expert prompt of 16384 rows: 424 us, 477 as lanes), and so are rows that whole sectors cannot be stored of
         if (ragged != kRowsOfQ && sectors)
             e = launch<256, 2, false, true>(m, ragged, 256, 1, s);
         else

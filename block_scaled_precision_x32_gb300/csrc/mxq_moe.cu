@@ -53,7 +53,9 @@ __global__ void __launch_bounds__(1024) count_kernel(MoeSortArgs a, int walkers)
 // Every block finds all experts' totals and where each part begins, then the
 // rows of its own choices.  With one chunk the counts come from the block's
 // own histogram, else from count_kernel's, summed by as many threads an
-// expert as the block has.
+// expert as the block has.  Latency: 48 x 2 choices 3.4 us; 65536 x 8 over 256
+// experts 14.0 us in two launches, of which the scattered stores of `source`
+// and every block's sum over all chunks' counts take the most.
 __global__ void __launch_bounds__(1024) place_kernel(MoeSortArgs a, int chunks, int walkers) {
     extern __shared__ int smem[];
     let_next_start();
@@ -207,6 +209,8 @@ struct Piece {
 };
 
 // One row of the order to blockIdx.x, a slice of its pieces to blockIdx.y.
+// Memory-bound: 32764 rows of 7184 bf16 139 us, 6.8 TB/s of what is read and
+// written (a token is read for each of its choices).
 template <Elt ELT, int VEC>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
     let_next_start();
@@ -229,6 +233,8 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
 
 // out[t] = sum_j w_j y[slot_j]: one token to blockIdx.x, a slice of its pieces
 // to blockIdx.y; the rows of four choices are loaded before they are added.
+// Memory-bound; four blocks a multiprocessor, or the loads in flight do not
+// suffice: 8191 tokens x 4 of 7184 bf16 88.6 us, 6.6 TB/s (three blocks 111).
 template <Elt ELT, int VEC>
 __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(MoeRowsArgs a) {
     let_next_start();
@@ -264,7 +270,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(MoeRowsArgs a) 
 
 // TG choices of one token to a block.  The dot products are summed in a fixed
 // order: a thread's pieces, the warp's lanes, the warps.  The blocks behind
-// the tokens' clear the rows of no choice.
+// the tokens' clear the rows of no choice.  8191 tokens x 4 of 7184 bf16: 192
+// us, 5.5 TB/s: each piece's loads wait for the one before it, and more blocks
+// a multiprocessor leave too few registers for four rows (eight blocks of 128
+// threads; 16 bytes a piece, with 32 it took 239).
 template <Elt ELT, int VEC, int TG>
 __global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsArgs a, int64_t work, int64_t work_blocks) {
     let_next_start();

@@ -63,48 +63,40 @@ struct Unit {
 
 // Rows of 16-element units, eight lanes to a 1x128 block: 32 bytes (bf16) or
 // 64 (fp32) of loads and one 16-byte store a lane, the block's maximum by
-// three shuffles.  Memory-bound; UNITS units of a lane are loaded before the
-// first is used (4 of bf16, 2 of fp32: 128 bytes in flight a thread).
-// 8192 x 7184 bf16: see the table of figures in the launcher's comment.
-template <Elt ELT, int UNITS>
+// three shuffles.  Memory-bound: one unit a thread, so that registers leave
+// room for as many threads as there can be (8192 x 7184 bf16: 29.6 us, 5.98
+// TB/s; two units 31.7, four 34.8).
+template <Elt ELT>
 __global__ void __launch_bounds__(256) quant_rows_unit_kernel(Quant128Args a, int64_t nb) {
     let_next_start();
     wait_for_stream();
-    const int64_t first = (int64_t)blockIdx.x * (256 * UNITS) + threadIdx.x, total = a.out_rows * nb * 8;
-    Unit<ELT> u[UNITS];
-    int64_t row[UNITS], b[UNITS];
+    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x, total = a.out_rows * nb * 8;
+    int64_t row, b;
+    split_index(unit >> 3, nb, row, b);
+    const int64_t k = b * 128 + (threadIdx.x & 7) * 16;
+    const int64_t src = unit < total && k < a.K ? source_row(a, row) : -1;
+    Unit<ELT> u;
+    if (src >= 0)
+        u.load(a.x, src * a.ldx + k);
+    else
+        u.clear();
+    uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-        split_index((first + 256 * i) >> 3, nb, row[i], b[i]);
-        const int64_t k = b[i] * 128 + (threadIdx.x & 7) * 16;
-        const bool inside = first + 256 * i < total && k < a.K;
-        const int64_t src = inside ? source_row(a, row[i]) : -1;
-        if (src >= 0)
-            u[i].load(a.x, src * a.ldx + k);
-        else
-            u[i].clear();
+    for (int j = 0; j < 16; ++j) amax = max(amax, u.at(j) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+    const uint32_t code = scale_code128(amax), inv = inv_scale128(code);
+    if (unit >= total) return;
+    if ((threadIdx.x & 7) == 0) a.scales[row * nb + b] = (uint8_t)code;
+    if (k >= a.K) return;
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        o[j] = e4m3x2_from_f32(f32_mul(u.at(4 * j + 1), inv), f32_mul(u.at(4 * j), inv)) |
+               e4m3x2_from_f32(f32_mul(u.at(4 * j + 3), inv), f32_mul(u.at(4 * j + 2), inv)) << 16;
+        if (code == 255u) o[j] = 0x7F7F7F7Fu;
     }
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-        uint32_t amax = 0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) amax = max(amax, u[i].at(j) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int d = 1; d < 8; d *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        const uint32_t code = scale_code128(amax), inv = inv_scale128(code);
-        if (first + 256 * i >= total) continue;
-        const int64_t k = b[i] * 128 + (threadIdx.x & 7) * 16;
-        if ((threadIdx.x & 7) == 0) a.scales[row[i] * nb + b[i]] = (uint8_t)code;
-        if (k >= a.K) continue;
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            o[j] = e4m3x2_from_f32(f32_mul(u[i].at(4 * j + 1), inv), f32_mul(u[i].at(4 * j), inv)) |
-                   e4m3x2_from_f32(f32_mul(u[i].at(4 * j + 3), inv), f32_mul(u[i].at(4 * j + 2), inv)) << 16;
-            if (code == 255u) o[j] = 0x7F7F7F7Fu;
-        }
-        st16(a.data + row[i] * a.K + k, o[0], o[1], o[2], o[3]);
-    }
+    st16(a.data + row * a.K + k, o[0], o[1], o[2], o[3]);
 }
 
 // Any alignment and any K: one warp per 1x128 block, an element at a time.
@@ -139,7 +131,9 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(Quant128Args a, int64_t
 // 128 rows x 64 columns a block, 8 columns x 4 rows a thread, all in registers
 // between the maximum and the rounding: each element is read once.  The
 // maximum of a column goes through two shuffles (four threads of a warp share
-// it) and shared memory.
+// it) and shared memory.  4099 x 4096 fp32: 16.3 us, 5.2 TB/s, held back by
+// the two barriers and a last wave of half the device (512 threads of 2 rows
+// 18 to 22 us; one thread a column, reading twice, 44).
 template <Elt ELT>
 __global__ void __launch_bounds__(256) quant_columns_tile_kernel(Quant128Args a) {
     let_next_start();
@@ -267,12 +261,11 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
         return cudaSuccess;
     }
     const int64_t nb = ceil_div(a.K, 128);
-    if (ceil_div(a.out_rows * nb, 8) > INT64_C(0x7FFFFFFF)) return cudaErrorInvalidValue;
+    if (ceil_div(a.out_rows * nb, 8) > INT64_C(0x7FFFFFFF)) return cudaErrorInvalidValue;  // over 2 TB of elements
     // units of 16 elements: 32-byte loads and 16-byte stores
     if (a.K % 16 == 0 && on(a.x, 32) && (one_row || a.ldx * es % 32 == 0) && on(a.data, 16)) {
-        constexpr int units = 1;
-        return launch_overlapped(quant_rows_unit_kernel<ELT, units>, dim3((unsigned)ceil_div(a.out_rows * nb * 8, 256 * units)),
-                                 256, 0, 0, s, a, nb);
+        return launch_overlapped(quant_rows_unit_kernel<ELT>, dim3((unsigned)ceil_div(a.out_rows * nb * 8, 256)), 256, 0, 0, s, a,
+                                 nb);
     }
     return launch_overlapped(quant_rows_kernel<ELT>, dim3((unsigned)ceil_div(a.out_rows * nb, 8)), 256, 0, 0, s, a, nb);
 }

@@ -43,7 +43,7 @@ def test_the_binding_packs_the_struct():
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(dir=3), INVALID), (dict(M=-1), INVALID), (dict(K=1 << 31, lda=1 << 31, ldb=1 << 31), INVALID),
+    (dict(dir=3), INVALID), (dict(M=-1), INVALID), (dict(K=(1 << 30) + 1, lda=1 << 31, ldb=1 << 31), INVALID),
     (dict(out_dt=2), UNSUPPORTED), (dict(out_dt=5), INVALID), (dict(lda=127), INVALID), (dict(ldb=64), INVALID),
     (dict(ldo=255), INVALID), (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(a_scales=None), INVALID),
     (dict(b_scales=None), INVALID), (dict(b_scales=FAKE + 2), INVALID), (dict(out=None), INVALID),
