@@ -326,6 +326,28 @@ __device__ __forceinline__ void store_four(const Problem& g, int64_t at, int n, 
         if (i < n) store_one(g, at + i, u[i]);
 }
 
+// 128 bf16 values of a row of the output, the first `n` of them inside, by 16
+// threads: 16 aligned bytes a store, wherever the row begins.
+__device__ __forceinline__ void store_row(uint16_t* to, const uint16_t* from, int n, int part, bool aligned) {
+    if (aligned && 8 * part + 8 <= n) {
+        *reinterpret_cast<uint4*>(to + 8 * part) = *reinterpret_cast<const uint4*>(from + 8 * part);
+        return;
+    }
+    const int skip = (int)(reinterpret_cast<uintptr_t>(to) & 15u) / 2;  // values of the first 16 bytes that are not the row's
+    for (int f = 8 * part - skip; f < n; f += 128) {  // part 0 has the row's last few, too
+        if (f >= 0 && f + 8 <= n) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = from[f + 2 * i] | (uint32_t)from[f + 2 * i + 1] << 16;
+            *reinterpret_cast<uint4*>(to + f) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (f + i >= 0 && f + i < n) to[f + i] = from[f + i];
+        }
+    }
+}
+
 // Blocks to a segment: as even as groups allow.
 __device__ __forceinline__ int even_segment(const Problem& g, int depth) {
     const int n = (depth + g.segment - 1) / g.segment;
@@ -737,7 +759,7 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
                                 for (int i = 0; i < W; ++i, to += g.ldo)
                                     if (i < n) *to = v[i];
                             }
-                        } else if (CG == 2 && g.wide) {
+                        } else if (CG == 2) {
                             // Through shared memory, so that a row's 128 features, 256 bytes, are stored together: the
                             // 64 bytes of one warp's lanes make partial lines, and a 256x256 tile took 9.4 us so
                             // (fp32, 128 bytes a warp: 3.1 us; this: 5.3 us).
@@ -745,15 +767,12 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
 #pragma unroll
                             for (int i = 0; i < W; ++i) buf[128 * i + 32 * band + lane] = (uint16_t)bf16_rne(v[i]);
                             asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-                            const int part = threadIdx.x & 15, feature = c.p0 + 128 * (int)pair_rank + 8 * part;
-                            uint16_t* to = static_cast<uint16_t*>(g.out) + base - row + feature + (int64_t)q0 * g.ldo;
+                            const int part = threadIdx.x & 15, p0 = c.p0 + 128 * (int)pair_rank, left = min(128, g.p_rows - p0);
+                            uint16_t* to = static_cast<uint16_t*>(g.out) + base - row + p0 + (int64_t)q0 * g.ldo;
 #pragma unroll
                             for (int k = 0; k < W / 8; ++k) {
                                 const int i = 8 * k + ((threadIdx.x >> 4) & 7);
-                                const uint4 y = *reinterpret_cast<const uint4*>(buf + 128 * i + 8 * part);
-                                if (i < n && feature + 8 <= g.p_rows) *reinterpret_cast<uint4*>(to + i * g.ldo) = y;
-                                if (i < n && feature + 8 > g.p_rows)
-                                    for (int f = 0; feature + f < g.p_rows; ++f) to[i * g.ldo + f] = buf[128 * i + 8 * part + f];
+                                if (i < n) store_row(to + i * g.ldo, buf + 128 * i, left, part, g.wide);
                             }
                             asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
                         } else {
@@ -808,13 +827,34 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
     }
 }
 
+// Copies rows of n bytes to rows that begin on 16 bytes, 16 bytes a thread:
+// five aligned words of the source, shifted.  What lies behind a row's n bytes
+// in the copy is never read (the tensor map ends there).
 __global__ void __launch_bounds__(256) repack_kernel(const uint8_t* src, int64_t ld, int64_t rows, int64_t n,
                                                      uint8_t* dst, int64_t ldd) {
     let_next_start();
     wait_for_stream();
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * ldd; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / ldd, c = i - r * ldd;
-        dst[i] = c < n ? src[r * ld + c] : 0;
+    const int64_t pieces = ldd / 16, total = rows * pieces;
+    const uint8_t* const end = src + (rows - 1) * ld + n;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+        int64_t r, c;
+        split_index(u, pieces, r, c);
+        const uint8_t* from = src + r * ld + 16 * c;
+        const uint32_t skip = (uint32_t)(reinterpret_cast<uintptr_t>(from) & 3u);
+        uint32_t w[5] = {};
+        if (from - skip >= src && from - skip + 20 <= end) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = reinterpret_cast<const uint32_t*>(from - skip)[i];
+        } else {  // the matrix's ends, byte by byte into the same places
+#pragma unroll
+            for (int i = 0; i < 20; ++i) {
+                const int at = i - (int)skip;
+                if (at >= 0 && at < 16 && 16 * c + at < n) w[i / 4] |= (uint32_t)from[at] << (8 * (i & 3));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * skip);
+        *reinterpret_cast<uint4*>(dst + r * ldd + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -968,8 +1008,8 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
 cudaError_t launch_repack(const uint8_t* src, int64_t ld, int64_t rows, int64_t n, uint8_t* dst, int64_t ldd,
                           cudaStream_t s) {
     if (rows == 0) return cudaSuccess;
-    const int64_t want = ceil_div(rows * ldd, 256);
-    const int64_t most = (int64_t)sm_count() * 16;
+    const int64_t want = ceil_div(rows * (ldd / 16), 256);
+    const int64_t most = (int64_t)sm_count() * 32;
     return launch_overlapped(repack_kernel, dim3((unsigned)(want < most ? want : most)), 256, 0, 0, s, src, ld, rows, n, dst,
                              ldd);
 }

@@ -157,37 +157,60 @@ constexpr int kRowThreads = 256;
 constexpr int kGradThreads = 128;
 constexpr int kTogether = 4;  // choices of a token taken at a time
 
-// VEC consecutive elements: 32 bytes (bf16: 16, fp32: 8), or one where rows
-// do not begin on 32 bytes.
-template <Elt ELT, int VEC>
+// A thread's piece of a row of H elements: VEC consecutive ones, 16 or 32
+// bytes, or, where rows do not begin on 32 bytes (VEC 0), up to eight that
+// lie a block's threads apart, so that lanes still touch neighbours.
+template <Elt ELT, int VEC, int THREADS>
 struct Piece {
-    static constexpr int kWords = VEC == 1 ? 1 : VEC * (ELT == Elt::BF16 ? 2 : 4) / 4;
+    static constexpr int kBytes = ELT == Elt::BF16 ? 2 : 4;
+    static constexpr int kWords = VEC ? VEC * kBytes / 4 : 8;
+    static constexpr int kValues = VEC ? VEC : 8;
     uint32_t w[kWords];
 
-    __device__ __forceinline__ void read(const void* p, int64_t i) {
-        if constexpr (VEC == 1) {
-            if constexpr (ELT == Elt::BF16)
-                w[0] = static_cast<const uint16_t*>(p)[i];
-            else
-                w[0] = static_cast<const uint32_t*>(p)[i];
+    // Pieces of a row, and the first element of piece i (VEC 0: a multiple of
+    // THREADS pieces, the last ones reach behind the row).
+    static __device__ __forceinline__ int64_t count(int64_t H) {
+        return VEC ? H / (VEC ? VEC : 1) : (H + 8 * THREADS - 1) / (8 * THREADS) * THREADS;
+    }
+    static __device__ __forceinline__ int64_t first(int64_t i) {
+        return VEC ? i * VEC : i / THREADS * (8 * THREADS) + i % THREADS;
+    }
+    __device__ __forceinline__ void read(const void* row, int64_t i, int64_t H) {
+        const char* p = static_cast<const char*>(row) + first(i) * kBytes;
+        if constexpr (VEC == 0) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                w[q] = 0;
+                if (first(i) + q * THREADS < H) {
+                    if constexpr (ELT == Elt::BF16)
+                        w[q] = reinterpret_cast<const uint16_t*>(p)[q * THREADS];
+                    else
+                        w[q] = reinterpret_cast<const uint32_t*>(p)[q * THREADS];
+                }
+            }
         } else if constexpr (kWords == 4) {
             asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "l"(static_cast<const char*>(p) + i * (ELT == Elt::BF16 ? 2 : 4)));
+                         : "l"(p));
         } else {
-            ld32(w, static_cast<const char*>(p) + i * (ELT == Elt::BF16 ? 2 : 4));
+            ld32(w, p);
         }
     }
-    __device__ __forceinline__ void write(void* p, int64_t i) const {
-        if constexpr (VEC == 1) {
-            if constexpr (ELT == Elt::BF16)
-                static_cast<uint16_t*>(p)[i] = (uint16_t)w[0];
-            else
-                static_cast<uint32_t*>(p)[i] = w[0];
+    __device__ __forceinline__ void write(void* row, int64_t i, int64_t H) const {
+        char* p = static_cast<char*>(row) + first(i) * kBytes;
+        if constexpr (VEC == 0) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (first(i) + q * THREADS < H) {
+                    if constexpr (ELT == Elt::BF16)
+                        reinterpret_cast<uint16_t*>(p)[q * THREADS] = (uint16_t)w[q];
+                    else
+                        reinterpret_cast<uint32_t*>(p)[q * THREADS] = w[q];
+                }
         } else if constexpr (kWords == 4) {
-            st16(static_cast<char*>(p) + i * (ELT == Elt::BF16 ? 2 : 4), w[0], w[1], w[2], w[3]);
+            st16(p, w[0], w[1], w[2], w[3]);
         } else {
-            st32(static_cast<char*>(p) + i * (ELT == Elt::BF16 ? 2 : 4), w);
+            st32(p, w);
         }
     }
     __device__ __forceinline__ void clear() {
@@ -196,17 +219,29 @@ struct Piece {
     }
     __device__ __forceinline__ float at(int i) const {
         if constexpr (ELT == Elt::FP32) return __uint_as_float(w[i]);
+        else if constexpr (VEC == 0) return __uint_as_float(w[i] << 16);
         else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
     }
-    // Rounds element i to nearest even; every i in ascending order.
+    // Rounds value i to nearest even; every i in ascending order.
     __device__ __forceinline__ void set(int i, float v) {
         uint32_t u = __float_as_uint(v);
         if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0x7FC00000u;
         if constexpr (ELT == Elt::FP32) w[i] = u;
+        else if constexpr (VEC == 0) w[i] = bf16_rne(u);
         else if (i & 1) w[i / 2] |= bf16_rne(u) << 16;
         else w[i / 2] = bf16_rne(u);
     }
 };
+
+// Row r of a matrix of elements.
+template <Elt ELT>
+__device__ __forceinline__ const void* row_of(const void* p, int64_t r, int64_t ld) {
+    return static_cast<const char*>(p) + r * ld * (ELT == Elt::BF16 ? 2 : 4);
+}
+template <Elt ELT>
+__device__ __forceinline__ void* row_of(void* p, int64_t r, int64_t ld) {
+    return static_cast<char*>(p) + r * ld * (ELT == Elt::BF16 ? 2 : 4);
+}
 
 // One row of the order to blockIdx.x, a slice of its pieces to blockIdx.y.
 // Memory-bound: 32764 rows of 7184 bf16 139 us, 6.8 TB/s of what is read and
@@ -215,18 +250,19 @@ template <Elt ELT, int VEC>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
     let_next_start();
     wait_for_stream();
-    const int64_t pieces = a.H / VEC;
+    using P = Piece<ELT, VEC, kRowThreads>;
+    const int64_t pieces = P::count(a.H);
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
         const int c = a.source[r];
         const int64_t t = c < 0 ? -1 : c / a.topk;
         const bool there = t >= 0 && t < a.T;
         for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.y * kRowThreads) {
-            Piece<ELT, VEC> p;
+            P p;
             if (there)
-                p.read(a.tokens, t * a.ld_tokens + i * VEC);
+                p.read(row_of<ELT>(a.tokens, t, a.ld_tokens), i, a.H);
             else
                 p.clear();
-            p.write(a.out, r * a.H + i * VEC);
+            p.write(row_of<ELT>(a.out, r, a.H), i, a.H);
         }
     }
 }
@@ -239,12 +275,13 @@ template <Elt ELT, int VEC>
 __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(MoeRowsArgs a) {
     let_next_start();
     wait_for_stream();
-    const int64_t pieces = a.H / VEC;
+    using P = Piece<ELT, VEC, kRowThreads>;
+    const int64_t pieces = P::count(a.H);
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x)
         for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.y * kRowThreads) {
-            float sum[VEC] = {};
+            float sum[P::kValues] = {};
             for (int64_t j0 = 0; j0 < a.topk; j0 += kTogether) {
-                Piece<ELT, VEC> p[kTogether];
+                P p[kTogether];
                 bool there[kTogether];
                 float w[kTogether];
 #pragma unroll
@@ -253,18 +290,18 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(MoeRowsArgs a) 
                     const int64_t r = j0 + j < a.topk ? a.slots[c] : -1;
                     there[j] = r >= 0 && r < a.R;
                     w[j] = there[j] && a.weights ? a.weights[c] : 1.0f;
-                    if (there[j]) p[j].read(a.rows, r * a.ld_rows + i * VEC);
+                    if (there[j]) p[j].read(row_of<ELT>(a.rows, r, a.ld_rows), i, a.H);
                 }
 #pragma unroll
                 for (int j = 0; j < kTogether; ++j)
                     if (there[j])
 #pragma unroll
-                        for (int q = 0; q < VEC; ++q) sum[q] = fmaf(w[j], p[j].at(q), sum[q]);
+                        for (int q = 0; q < P::kValues; ++q) sum[q] = fmaf(w[j], p[j].at(q), sum[q]);
             }
-            Piece<ELT, VEC> o;
+            P o;
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) o.set(q, sum[q]);
-            o.write(a.out, t * a.H + i * VEC);
+            for (int q = 0; q < P::kValues; ++q) o.set(q, sum[q]);
+            o.write(row_of<ELT>(a.out, t, a.H), i, a.H);
         }
 }
 
@@ -278,7 +315,8 @@ template <Elt ELT, int VEC, int TG>
 __global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsArgs a, int64_t work, int64_t work_blocks) {
     let_next_start();
     wait_for_stream();
-    const int64_t pieces = a.H / VEC, n = a.T * a.topk;
+    using P = Piece<ELT, VEC, kGradThreads>;
+    const int64_t pieces = P::count(a.H), n = a.T * a.topk;
     if (blockIdx.x >= work_blocks) {
         // each thread looks at one of the block's next rows; those of no choice are cleared by the whole block
         __shared__ int empty[kGradThreads];
@@ -290,10 +328,10 @@ __global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsAr
             const int c = r < a.R ? a.source[r] : 0;
             if (c < 0 || c >= n) empty[atomicAdd(&found, 1)] = (int)threadIdx.x;
             __syncthreads();
-            Piece<ELT, VEC> zero;
+            P zero;
             zero.clear();
             for (int x = 0; x < found; ++x)
-                for (int64_t i = threadIdx.x; i < pieces; i += kGradThreads) zero.write(a.out, (r0 + empty[x]) * a.H + i * VEC);
+                for (int64_t i = threadIdx.x; i < pieces; i += kGradThreads) zero.write(row_of<ELT>(a.out, r0 + empty[x], a.H), i, a.H);
             __syncthreads();
         }
         return;
@@ -316,21 +354,21 @@ __global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsAr
         }
 #pragma unroll 1
         for (int64_t i = threadIdx.x; i < pieces; i += kGradThreads) {
-            Piece<ELT, VEC> g, y[TG];
-            g.read(a.tokens, t * a.ld_tokens + i * VEC);
+            P g, y[TG];
+            g.read(row_of<ELT>(a.tokens, t, a.ld_tokens), i, a.H);
 #pragma unroll
             for (int j = 0; j < TG; ++j)
-                if (row[j] >= 0) y[j].read(a.rows, row[j] * a.ld_rows + i * VEC);
+                if (row[j] >= 0) y[j].read(row_of<ELT>(a.rows, row[j], a.ld_rows), i, a.H);
 #pragma unroll
             for (int j = 0; j < TG; ++j)
                 if (row[j] >= 0) {
-                    Piece<ELT, VEC> o;
+                    P o;
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) {
+                    for (int q = 0; q < P::kValues; ++q) {
                         dot[j] = fmaf(g.at(q), y[j].at(q), dot[j]);
                         o.set(q, w[j] * g.at(q));
                     }
-                    o.write(a.out, row[j] * a.H + i * VEC);
+                    o.write(row_of<ELT>(a.out, row[j], a.H), i, a.H);
                 }
         }
 #pragma unroll
@@ -373,9 +411,9 @@ dim3 row_grid(int64_t rows, int64_t pieces) {
 template <Elt ELT, int VEC>
 cudaError_t rows_launch(int what, const MoeRowsArgs& a, cudaStream_t s) {
     if (what == 0) {
-        return launch_overlapped(dispatch_kernel<ELT, VEC>, row_grid(a.R, a.H / VEC), kRowThreads, 0, 0, s, a);
+        return launch_overlapped(dispatch_kernel<ELT, VEC>, row_grid(a.R, ceil_div(a.H, VEC ? VEC : 8)), kRowThreads, 0, 0, s, a);
     } else if (what == 1) {
-        return launch_overlapped(combine_kernel<ELT, VEC>, row_grid(a.T, a.H / VEC), kRowThreads, 0, 0, s, a);
+        return launch_overlapped(combine_kernel<ELT, VEC>, row_grid(a.T, ceil_div(a.H, VEC ? VEC : 8)), kRowThreads, 0, 0, s, a);
     } else {
         // four choices to a block, or one where that leaves the device empty (64 tokens of 7184, topk 4, bf16: 6.8 us with
         // four, 4.4 with one; 8191 tokens: 192 and 282)
@@ -383,7 +421,7 @@ cudaError_t rows_launch(int what, const MoeRowsArgs& a, cudaStream_t s) {
         const int64_t work = a.T * ceil_div(a.topk, together), work_blocks = work < (1 << 30) ? work : 1 << 30;
         const int64_t room = ceil_div(a.R, kGradThreads), clear = room < sm_count() ? room : sm_count();
         const unsigned grid = (unsigned)(work_blocks + clear);
-        constexpr int V = VEC == 1 ? 1 : VEC / 2;
+        constexpr int V = VEC / 2;
         return together == 1
                    ? launch_overlapped(combine_grad_kernel<ELT, V, 1>, dim3(grid), kGradThreads, 0, 0, s, a, work, work_blocks)
                    : launch_overlapped(combine_grad_kernel<ELT, V, kTogether>, dim3(grid), kGradThreads, 0, 0, s, a, work,
@@ -394,8 +432,8 @@ cudaError_t rows_launch(int what, const MoeRowsArgs& a, cudaStream_t s) {
 cudaError_t rows_launch(int what, Elt elt, const MoeRowsArgs& a, cudaStream_t s) {
     const cudaError_t e =
         elt == Elt::BF16
-            ? (whole_pieces<Elt::BF16>(a) ? rows_launch<Elt::BF16, 16>(what, a, s) : rows_launch<Elt::BF16, 1>(what, a, s))
-            : (whole_pieces<Elt::FP32>(a) ? rows_launch<Elt::FP32, 8>(what, a, s) : rows_launch<Elt::FP32, 1>(what, a, s));
+            ? (whole_pieces<Elt::BF16>(a) ? rows_launch<Elt::BF16, 16>(what, a, s) : rows_launch<Elt::BF16, 0>(what, a, s))
+            : (whole_pieces<Elt::FP32>(a) ? rows_launch<Elt::FP32, 8>(what, a, s) : rows_launch<Elt::FP32, 0>(what, a, s));
     if (e != cudaSuccess) cudaGetLastError();
     return e;
 }

@@ -99,33 +99,41 @@ __global__ void __launch_bounds__(256) quant_rows_unit_kernel(Quant128Args a, in
     st16(a.data + row * a.K + k, o[0], o[1], o[2], o[3]);
 }
 
-// Any alignment and any K: one warp per 1x128 block, an element at a time.
+// Any alignment and any K: a warp per four 1x128 blocks, an element at a time,
+// neighbours to neighbouring lanes; the loads of all four are on their way at once.
 template <Elt ELT>
 __global__ void __launch_bounds__(256) quant_rows_kernel(Quant128Args a, int64_t nb) {
     let_next_start();
     wait_for_stream();
-    const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32;
-    if (unit >= a.out_rows * nb) return;
-    int64_t r, b;
-    split_index(unit, nb, r, b);
+    constexpr int B = 4;
+    const int64_t first = ((int64_t)blockIdx.x * 8 + threadIdx.x / 32) * B;
     const int lane = threadIdx.x & 31;
-    const int64_t src = source_row(a, r);
-    const int64_t k0 = b * 128 + lane;
-    uint32_t v[4];
-    uint32_t amax = 0;
+    uint32_t v[B][4];
+    int64_t row[B], k0[B];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = src >= 0 && k0 + 32 * i < a.K ? load_f32<ELT>(a.x, src * a.ldx + k0 + 32 * i) : 0u;
-        amax = max(amax, v[i] & 0x7FFFFFFFu);
+    for (int i = 0; i < B; ++i) {
+        split_index(first + i, nb, row[i], k0[i]);
+        k0[i] = k0[i] * 128 + lane;
+        const int64_t src = row[i] < a.out_rows ? source_row(a, row[i]) : -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[i][j] = src >= 0 && k0[i] + 32 * j < a.K ? load_f32<ELT>(a.x, src * a.ldx + k0[i] + 32 * j) : 0u;
     }
-    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-    const uint32_t code = scale_code128(amax);
-    if (lane == 0) a.scales[r * nb + b] = (uint8_t)code;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (k0 + 32 * i < a.K)
-            a.data[r * a.K + k0 + 32 * i] =
-                code == 255u ? 0x7F : (uint8_t)e4m3x2_from_f32(0u, f32_mul(v[i], inv_scale128(code)));
+    for (int i = 0; i < B; ++i) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) amax = max(amax, v[i][j] & 0x7FFFFFFFu);
+        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+        if (row[i] >= a.out_rows) break;
+        const uint32_t code = scale_code128(amax);
+        if (lane == 0) a.scales[first + i] = (uint8_t)code;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (k0[i] + 32 * j < a.K)
+                a.data[row[i] * a.K + k0[i] + 32 * j] =
+                    code == 255u ? 0x7F : (uint8_t)e4m3x2_from_f32(0u, f32_mul(v[i][j], inv_scale128(code)));
+    }
 }
 
 // 128 rows x 64 columns a block, 8 columns x 4 rows a thread, all in registers
@@ -208,26 +216,37 @@ __global__ void __launch_bounds__(256) quant_columns_tile_kernel(Quant128Args a)
     }
 }
 
-// Any alignment and any K: one thread per 128x1 block.
+// Any alignment and any K: 128 rows x 64 columns a block, 16 rows of one column
+// a thread.
 template <Elt ELT>
-__global__ void __launch_bounds__(128) quant_columns_kernel(Quant128Args a) {
+__global__ void __launch_bounds__(512) quant_columns_kernel(Quant128Args a) {
     let_next_start();
     wait_for_stream();
-    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    constexpr int R = 16, Y = 8;
+    __shared__ uint32_t top[Y][64];
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + tx, r0 = (int64_t)blockIdx.y * 128 + ty;
+    uint32_t v[R], amax = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = r0 + Y * i;
+        const int64_t src = r < a.out_rows && c < a.K ? source_row(a, r) : -1;
+        v[i] = src >= 0 ? load_f32<ELT>(a.x, src * a.ldx + c) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) amax = max(amax, v[i] & 0x7FFFFFFFu);
+    top[ty][tx] = amax;
+    __syncthreads();
     if (c >= a.K) return;
-    const int64_t r0 = (int64_t)blockIdx.y * 128, r1 = min(r0 + 128, a.out_rows);
-    uint32_t amax = 0;
-    for (int64_t r = r0; r < r1; ++r) {
-        const int64_t src = source_row(a, r);
-        if (src >= 0) amax = max(amax, load_f32<ELT>(a.x, src * a.ldx + c) & 0x7FFFFFFFu);
-    }
+#pragma unroll
+    for (int y = 0; y < Y; ++y) amax = max(amax, top[y][tx]);
     const uint32_t code = scale_code128(amax);
-    a.scales[(int64_t)blockIdx.y * a.K + c] = (uint8_t)code;
-    for (int64_t r = r0; r < r1; ++r) {
-        const int64_t src = source_row(a, r);
-        const uint32_t v = src >= 0 ? load_f32<ELT>(a.x, src * a.ldx + c) : 0u;
-        a.data[r * a.K + c] = code == 255u ? 0x7F : (uint8_t)e4m3x2_from_f32(0u, f32_mul(v, inv_scale128(code)));
-    }
+    if (ty == 0) a.scales[(int64_t)blockIdx.y * a.K + c] = (uint8_t)code;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (r0 + Y * i < a.out_rows)
+            a.data[(r0 + Y * i) * a.K + c] =
+                code == 255u ? 0x7F : (uint8_t)e4m3x2_from_f32(0u, f32_mul(v[i], inv_scale128(code)));
 }
 
 bool on(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -255,7 +274,7 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
             const unsigned y = (unsigned)ceil_div(p.out_rows, 128);
             const cudaError_t e =
                 tiled ? launch_overlapped(quant_columns_tile_kernel<ELT>, dim3((unsigned)ceil_div(a.K, 64), y), 256, 0, 0, s, p)
-                      : launch_overlapped(quant_columns_kernel<ELT>, dim3((unsigned)ceil_div(a.K, 128), y), 128, 0, 0, s, p);
+                      : launch_overlapped(quant_columns_kernel<ELT>, dim3((unsigned)ceil_div(a.K, 64), y), 512, 0, 0, s, p);
             if (e != cudaSuccess) return e;
         }
         return cudaSuccess;
@@ -267,7 +286,7 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
         return launch_overlapped(quant_rows_unit_kernel<ELT>, dim3((unsigned)ceil_div(a.out_rows * nb * 8, 256)), 256, 0, 0, s, a,
                                  nb);
     }
-    return launch_overlapped(quant_rows_kernel<ELT>, dim3((unsigned)ceil_div(a.out_rows * nb, 8)), 256, 0, 0, s, a, nb);
+    return launch_overlapped(quant_rows_kernel<ELT>, dim3((unsigned)ceil_div(a.out_rows * nb, 32)), 256, 0, 0, s, a, nb);
 }
 
 }  // namespace
