@@ -6,7 +6,7 @@
 #include <cstdint>
 
 #include "../../include/mxq.h"
-#include "mxq_internal.h"
+#include "mxq_layer.h"
 
 namespace {
 

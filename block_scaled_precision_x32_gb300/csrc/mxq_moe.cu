@@ -6,7 +6,7 @@
 #include <cstdint>
 
 #include "mxq_device.cuh"
-#include "mxq_internal.h"
+#include "mxq_layer.h"
 #include "mxq_launch.cuh"
 
 namespace mxq {

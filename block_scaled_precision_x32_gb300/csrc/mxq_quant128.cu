@@ -7,7 +7,7 @@
 #include <cuda_bf16.h>
 
 #include "mxq_device.cuh"
-#include "mxq_internal.h"
+#include "mxq_layer.h"
 #include "mxq_launch.cuh"
 
 namespace mxq {
