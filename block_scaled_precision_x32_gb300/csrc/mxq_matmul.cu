@@ -23,7 +23,7 @@
 //
 // What bounds it (GB300; the tensor cores' own time for a 256x256 tile and 128
 // of depth is 497 clocks, 4.9 PFLOP/s at 2 GHz):
-//   8192^3                       0.305 ms, 3.6 PFLOP/s: the board's power.  On
+//   8192^3                       0.297 ms, 3.7 PFLOP/s: the board's power.  On
 //                                operands of zeros 0.263 ms, 4.2 PFLOP/s.
 //   rows of 7184 bytes           a box of 128 bytes lies across two 128-byte
 //                                lines; the L2 serves five sectors for four:
@@ -58,13 +58,15 @@ constexpr int kGroup = 8;
 constexpr int kRing = 2;  // groups, both in shared and in tensor memory
 
 // The tensor core cuts off what a sum's 24 bits cannot hold instead of
-// rounding it, so that the error of a long sum grows with its length: 1.2e-6
-// of the result's norm at a depth of 8191, against 1e-7 for sums that are
-// rounded.  That is far below a bf16 result's own rounding, but not below
-// fp32's.  fp32 results are therefore summed in segments of at most 40 blocks,
-// 5120 of depth, which are added, rounded, to what the output holds: 5e-7 at
-// 8191, 7e-7 at 5119, the worst.  A multiple of kGroup.
-constexpr int kSegment = 40;
+// rounding it, so that the error of a long sum grows with its length: 5e-7 to
+// 8e-7 of the result's norm at a depth of 4099, 1.2e-6 at 8191, against 1e-7
+// to 2e-7 for sums that are rounded.  That is far below a bf16 result's own
+// rounding, but not below fp32's.  fp32 results deeper than 36 blocks are
+// therefore summed in segments of about equal length, each added, rounded, to
+// what the output holds, which keeps them below 1e-6: 5e-7 at 8191.  A
+// segment more costs what its results' way to memory and back does (8192 x
+// 4096 x 4096: 101 us, as bf16 in one segment 85).
+constexpr int kSegment = 36;
 
 // The operand whose rows are the accumulator's lanes is called P, the one
 // whose rows are its columns Q.  Lanes come 128 at a time, columns in any
@@ -348,7 +350,7 @@ __device__ __forceinline__ void store_row(uint16_t* to, const uint16_t* from, in
     }
 }
 
-// Blocks to a segment: as even as groups allow.
+// Blocks to a segment: as even as whole groups allow.
 __device__ __forceinline__ int even_segment(const Problem& g, int depth) {
     const int n = (depth + g.segment - 1) / g.segment;
     return n <= 1 ? g.segment : ((depth + n - 1) / n + kGroup - 1) / kGroup * kGroup;
