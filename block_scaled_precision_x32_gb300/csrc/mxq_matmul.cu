@@ -29,10 +29,9 @@
 //                                lines; the L2 serves five sectors for four:
 //                                16384x4096x7184 2.7 PFLOP/s, at 8192 deep 3.5.
 //   few rows                     the weight's bytes: one token through
-//                                8192x8192 15.1 us, 4.4 TB/s, of which 10.4 us
-//                                are the stream at 6.4 TB/s and the rest the
-//                                launch, the first loads and the sum over a
-//                                cluster; 48 tokens x 2 of 32 experts
+//                                8192x8192 15.1 us, 4.4 TB/s, of which 11 us
+//                                are the stream at 6 TB/s and the rest the
+//                                launch and the sum over a cluster; 48 tokens x 2 of 32 experts
 //                                (4096x7184 each) at 6 TB/s.
 // A pair's stages take 32 KB a block of depth on each SM, which at the tensor
 // cores' rate is 18 TB/s from the L2: wider sharing (clusters of four with

@@ -288,6 +288,74 @@ def test_on_another_stream_and_in_a_graph(mx):
     close(out, want, S, 1040, F32)
 
 
+def test_dependent_calls_in_a_row(mx):
+    """Kernels start while the one in front of them in the stream is still running; a chain of dependent calls gives what the
+    same calls give one at a time."""
+    rng = np.random.default_rng(9)
+    w = [tuple(map(bytes_dev, (a[0], t[0] * np.float32(2.0**-4)))) for a, t in (make_weight(rng, 1, 384, 384) for _ in range(4))]
+    first = torch.from_numpy(rng.standard_normal((190, 384)).astype(np.float32)).to(BF16).cuda()
+    ids = torch.from_numpy(rng.integers(0, 4, (190, 1)).astype(np.int32)).cuda()
+
+    def chain(wait):
+        x, seen = first, []
+        for i in range(24):
+            order = mx.moe_sort(ids, 4)
+            wait()
+            rows = mx.moe_dispatch(x, order.source, 1)
+            wait()
+            q, s = mx.fp8_quant_1x128(rows)
+            wait()
+            y = mx.fp8_matmul(q, s, *w[i % 4]) if i % 2 else mx.fp8_matmul_dgrad(q, s, *w[i % 4])
+            wait()
+            x = mx.moe_combine(y, order.slots)
+            wait()
+            x = torch.nn.functional.normalize(x.float(), dim=1).to(BF16)
+            wait()
+            seen.append(x)
+        return torch.stack(seen)
+
+    apart = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        assert torch.equal(chain(lambda: None), apart)
+
+
+def test_more_outputs_than_32_bits_count(mx):
+    M, N, K = 70001, 32784, 128  # 2.3e9 outputs
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.randint(0, 127, (M, K), dtype=torch.uint8, device="cuda", generator=g)
+    w = torch.randint(0, 127, (N, K), dtype=torch.uint8, device="cuda", generator=g)
+    xs = torch.full((M, 1), 120, dtype=torch.uint8, device="cuda")
+    y = mx.fp8_matmul(x, xs, w, torch.full((257, 1), 2.0**-6, device="cuda"))
+    rows = [0, 1, 255, 256, 32767, 65535, 65536, 69888, 70000]
+    a = ref.e4m3_decode(x[rows].cpu().numpy()) * 2.0**-7
+    want, S = ref.product(a, ref.e4m3_decode(w.cpu().numpy()) * 2.0**-6)
+    close(y[rows], want, S, K, BF16)
+
+
+def test_more_elements_than_32_bits_count(mx):
+    T, H = 150001, 14336  # 2.15e9 elements
+    x = torch.empty(T, H, dtype=BF16, device="cuda")
+    x.view(torch.int16).random_(-(1 << 14), 1 << 14, generator=torch.Generator("cuda").manual_seed(2))
+    rows = [0, 127, 74999, 149796, 149999, 150000]
+    xr = f64(x[rows])
+    d, s = mx.fp8_quant_1x128(x)
+    want = ref.quant_rows(xr)
+    np.testing.assert_array_equal(host_bits(d[rows]), want[0])
+    np.testing.assert_array_equal(host_bits(s[rows]), want[1])
+    d, s = mx.fp8_quant_128x1(x)
+    tail = (T - 1) // 128 * 128
+    want = ref.quant_columns(f64(x[tail:]))
+    np.testing.assert_array_equal(host_bits(d[tail:]), want[0])
+    np.testing.assert_array_equal(host_bits(s[-1:]), want[1])
+    del d, s
+    slots = torch.tensor([[150000], [-1], [149796]], dtype=torch.int32, device="cuda")
+    np.testing.assert_array_equal(f64(mx.moe_combine(x, slots)), np.stack([xr[5], np.zeros(H), xr[3]]))
+    source = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    source[150000] = 149999
+    out = mx.moe_dispatch(x, source, 1)
+    np.testing.assert_array_equal(f64(out[149999:]), np.stack([np.zeros(H), xr[4]]))
+
+
 # ----------------------------------------------------------------- experts
 
 
