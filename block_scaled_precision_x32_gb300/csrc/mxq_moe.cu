@@ -154,7 +154,6 @@ __global__ void __launch_bounds__(1024) place_kernel(MoeSortArgs a, int chunks, 
 // ------------------------------------------------------------------- rows
 
 constexpr int kRowThreads = 256;
-constexpr int kGradThreads = 128;
 constexpr int kTogether = 4;  // choices of a token taken at a time
 
 // A thread's piece of a row of H elements: VEC consecutive ones, 16 or 32
@@ -307,21 +306,21 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(MoeRowsArgs a) 
 
 // TG choices of one token to a block.  The dot products are summed in a fixed
 // order: a thread's pieces, the warp's lanes, the warps.  The blocks behind
-// the tokens' clear the rows of no choice.  8191 tokens x 4 of 7184 bf16: 192
-// us, 5.5 TB/s: each piece's loads wait for the one before it, and more blocks
-// a multiprocessor leave too few registers for four rows (eight blocks of 128
-// threads; 16 bytes a piece, with 32 it took 239).
-template <Elt ELT, int VEC, int TG>
-__global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsArgs a, int64_t work, int64_t work_blocks) {
+// the tokens' clear the rows of no choice.  8191 tokens x 4 of 7184 bf16: 175
+// us, 6.05 TB/s.  A piece's loads wait for the one before, and the block for
+// its last thread: small blocks, 14 a multiprocessor, hide most of it (256
+// threads 213 us, 128 192, 32 184), pieces of 16 bytes leave registers for that.
+template <Elt ELT, int VEC, int TG, int THREADS>
+__global__ void __launch_bounds__(THREADS, 896 / THREADS) combine_grad_kernel(MoeRowsArgs a, int64_t work, int64_t work_blocks) {
     let_next_start();
     wait_for_stream();
-    using P = Piece<ELT, VEC, kGradThreads>;
+    using P = Piece<ELT, VEC, THREADS>;
     const int64_t pieces = P::count(a.H), n = a.T * a.topk;
     if (blockIdx.x >= work_blocks) {
         // each thread looks at one of the block's next rows; those of no choice are cleared by the whole block
-        __shared__ int empty[kGradThreads];
+        __shared__ int empty[THREADS];
         __shared__ int found;
-        for (int64_t r0 = (blockIdx.x - work_blocks) * kGradThreads; r0 < a.R; r0 += (gridDim.x - work_blocks) * kGradThreads) {
+        for (int64_t r0 = (blockIdx.x - work_blocks) * THREADS; r0 < a.R; r0 += (gridDim.x - work_blocks) * THREADS) {
             if (threadIdx.x == 0) found = 0;
             __syncthreads();
             const int64_t r = r0 + threadIdx.x;
@@ -331,12 +330,12 @@ __global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsAr
             P zero;
             zero.clear();
             for (int x = 0; x < found; ++x)
-                for (int64_t i = threadIdx.x; i < pieces; i += kGradThreads) zero.write(row_of<ELT>(a.out, r0 + empty[x], a.H), i, a.H);
+                for (int64_t i = threadIdx.x; i < pieces; i += THREADS) zero.write(row_of<ELT>(a.out, r0 + empty[x], a.H), i, a.H);
             __syncthreads();
         }
         return;
     }
-    __shared__ float part[kGradThreads / 32][TG];
+    __shared__ float part[THREADS / 32][TG];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int64_t groups = (a.topk + TG - 1) / TG;
     for (int64_t x = blockIdx.x; x < work; x += work_blocks) {
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsAr
             w[j] = row[j] >= 0 ? a.weights[c] : 0.0f;
         }
 #pragma unroll 1
-        for (int64_t i = threadIdx.x; i < pieces; i += kGradThreads) {
+        for (int64_t i = threadIdx.x; i < pieces; i += THREADS) {
             P g, y[TG];
             g.read(row_of<ELT>(a.tokens, t, a.ld_tokens), i, a.H);
 #pragma unroll
@@ -381,7 +380,7 @@ __global__ void __launch_bounds__(kGradThreads, 8) combine_grad_kernel(MoeRowsAr
         if (threadIdx.x < TG && j0 + threadIdx.x < a.topk) {
             float sum = 0.0f;
 #pragma unroll
-            for (int v = 0; v < kGradThreads / 32; ++v) sum += part[v][threadIdx.x];
+            for (int v = 0; v < THREADS / 32; ++v) sum += part[v][threadIdx.x];
             a.d_weights[t * a.topk + j0 + threadIdx.x] = sum;
         }
         __syncthreads();
@@ -415,17 +414,15 @@ cudaError_t rows_launch(int what, const MoeRowsArgs& a, cudaStream_t s) {
     } else if (what == 1) {
         return launch_overlapped(combine_kernel<ELT, VEC>, row_grid(a.T, ceil_div(a.H, VEC ? VEC : 8)), kRowThreads, 0, 0, s, a);
     } else {
-        // four choices to a block, or one where that leaves the device empty (64 tokens of 7184, topk 4, bf16: 6.8 us with
-        // four, 4.4 with one; 8191 tokens: 192 and 282)
-        const int together = a.T * ceil_div(a.topk, kTogether) < 8 * (int64_t)sm_count() ? 1 : kTogether;
-        const int64_t work = a.T * ceil_div(a.topk, together), work_blocks = work < (1 << 30) ? work : 1 << 30;
-        const int64_t room = ceil_div(a.R, kGradThreads), clear = room < sm_count() ? room : sm_count();
-        const unsigned grid = (unsigned)(work_blocks + clear);
+        // four choices to a block of 64 threads, or, where that leaves the device empty, one to a block of 128 (64 tokens of
+        // 7184, topk 4, bf16: 4.7 us, 6.8 as the others; 8191 tokens: 282 us, 175 as the others)
+        const bool few = a.T * ceil_div(a.topk, kTogether) < 8 * (int64_t)sm_count();
+        const int64_t work = a.T * ceil_div(a.topk, few ? 1 : kTogether), work_blocks = work < (1 << 30) ? work : 1 << 30;
+        const int64_t room = ceil_div(a.R, 64), clear = room < sm_count() ? room : sm_count();
+        const dim3 grid((unsigned)(work_blocks + clear));
         constexpr int V = VEC / 2;
-        return together == 1
-                   ? launch_overlapped(combine_grad_kernel<ELT, V, 1>, dim3(grid), kGradThreads, 0, 0, s, a, work, work_blocks)
-                   : launch_overlapped(combine_grad_kernel<ELT, V, kTogether>, dim3(grid), kGradThreads, 0, 0, s, a, work,
-                                       work_blocks);
+        return few ? launch_overlapped(combine_grad_kernel<ELT, V, 1, 128>, grid, 128, 0, 0, s, a, work, work_blocks)
+                   : launch_overlapped(combine_grad_kernel<ELT, V, kTogether, 64>, grid, 64, 0, 0, s, a, work, work_blocks);
     }
 }
 

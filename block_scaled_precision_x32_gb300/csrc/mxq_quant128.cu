@@ -136,25 +136,33 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(Quant128Args a, int64_t
     }
 }
 
-// 128 rows x 64 columns a block, 8 columns x 4 rows a thread, all in registers
-// between the maximum and the rounding: each element is read once.  The
-// maximum of a column goes through two shuffles (four threads of a warp share
-// it) and shared memory.  4099 x 4096 fp32: 16.3 us, 5.2 TB/s, held back by
-// the two barriers and a last wave of half the device (512 threads of 2 rows
-// 18 to 22 us; one thread a column, reading twice, 44).
+// Threads along a row, and rows a thread (bytes in flight are alike).
 template <Elt ELT>
-__global__ void __launch_bounds__(256) quant_columns_tile_kernel(Quant128Args a) {
+struct ColumnTile {
+    static constexpr int kX = 4, kRows = ELT == Elt::BF16 ? 8 : 4;
+    static constexpr int kY = 128 / kRows, kThreads = kX * kY;
+};
+
+// 128 rows x 32 columns a block, 8 columns of 4 (fp32) or 8 rows a thread, all
+// in registers between the maximum and the rounding: each element is read
+// once.  The maximum of a column goes through shuffles among the threads of a
+// warp that share it, and shared memory.  4099 x 4096 fp32: 14.8 us, 5.7 TB/s
+// (wider and narrower blocks 1 to 3 us more; one thread a column, reading
+// twice, 44), 8191 x 7184 bf16: 33.3 us, 5.3 TB/s: held back by the two
+// barriers of a block, the last wave of blocks and, for bf16, arithmetic.
+template <Elt ELT>
+__global__ void __launch_bounds__(ColumnTile<ELT>::kThreads) quant_columns_tile_kernel(Quant128Args a) {
     let_next_start();
     wait_for_stream();
-    constexpr int R = 4;
-    __shared__ uint4 top[8][16];  // [warp][64 columns]
-    __shared__ uint2 codes[8];    // 64 bytes
-    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
-    const int64_t c = (int64_t)blockIdx.x * 64 + tx * 8, r0 = (int64_t)blockIdx.y * 128 + ty;
+    constexpr int R = ColumnTile<ELT>::kRows, TX = ColumnTile<ELT>::kX, TY = ColumnTile<ELT>::kY, WARPS = TX * TY / 32;
+    __shared__ uint4 top[WARPS][2 * TX];  // [warp][columns]
+    __shared__ uint2 codes[TX];        // a byte a column
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+    const int64_t c = ((int64_t)blockIdx.x * TX + tx) * 8, r0 = (int64_t)blockIdx.y * 128 + ty;
     uint32_t v[R][ELT == Elt::BF16 ? 4 : 8];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int64_t r = r0 + 32 * i;
+        const int64_t r = r0 + TY * i;
         const int64_t src = r < a.out_rows && c < a.K ? source_row(a, r) : -1;
 #pragma unroll
         for (uint32_t& x : v[i]) x = 0;
@@ -177,42 +185,44 @@ __global__ void __launch_bounds__(256) quant_columns_tile_kernel(Quant128Args a)
         m[j] = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) m[j] = max(m[j], at(i, j) & 0x7FFFFFFFu);
-        m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 8));
-        m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+#pragma unroll
+        for (int d = TX; d < 32; d *= 2) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], d));
     }
-    if ((threadIdx.x & 31) < 8) {
+    if ((threadIdx.x & 31) < TX) {
         top[threadIdx.x / 32][2 * tx] = make_uint4(m[0], m[1], m[2], m[3]);
         top[threadIdx.x / 32][2 * tx + 1] = make_uint4(m[4], m[5], m[6], m[7]);
     }
     __syncthreads();
-    if (threadIdx.x < 64) {
+    if (threadIdx.x < 8 * TX) {
         uint32_t amax = 0;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) amax = max(amax, reinterpret_cast<const uint32_t*>(top[w])[threadIdx.x]);
+        for (int w = 0; w < WARPS; ++w) amax = max(amax, reinterpret_cast<const uint32_t*>(top[w])[threadIdx.x]);
         const uint8_t own = (uint8_t)scale_code128(amax);
         reinterpret_cast<uint8_t*>(codes)[threadIdx.x] = own;
-        const int64_t column = (int64_t)blockIdx.x * 64 + threadIdx.x;
+        const int64_t column = (int64_t)blockIdx.x * (8 * TX) + threadIdx.x;
         if (column < a.K) a.scales[(int64_t)blockIdx.y * a.K + column] = own;
     }
     __syncthreads();
     if (c >= a.K) return;
-    uint32_t code[8];
+    uint32_t inv[8], nan[2] = {};  // nan: bytes of poisoned columns
 #pragma unroll
-    for (int j = 0; j < 8; ++j) code[j] = ((j < 4 ? codes[tx].x : codes[tx].y) >> (8 * (j & 3))) & 0xFFu;
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t code = ((j < 4 ? codes[tx].x : codes[tx].y) >> (8 * (j & 3))) & 0xFFu;
+        inv[j] = inv_scale128(code);
+        nan[j / 4] |= code == 255u ? 0xFFu << (8 * (j & 3)) : 0u;
+    }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        if (r0 + 32 * i >= a.out_rows) break;
+        if (r0 + TY * i >= a.out_rows) break;
         uint32_t o[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int j = 4 * h;
-            o[h] = e4m3x2_from_f32(f32_mul(at(i, j + 1), inv_scale128(code[j + 1])), f32_mul(at(i, j), inv_scale128(code[j]))) |
-                   e4m3x2_from_f32(f32_mul(at(i, j + 3), inv_scale128(code[j + 3])), f32_mul(at(i, j + 2), inv_scale128(code[j + 2]))) << 16;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (code[j + q] == 255u) o[h] = (o[h] & ~(0xFFu << (8 * q))) | 0x7Fu << (8 * q);
+            const uint32_t lo = e4m3x2_from_f32(f32_mul(at(i, j + 1), inv[j + 1]), f32_mul(at(i, j), inv[j])),
+                           hi = e4m3x2_from_f32(f32_mul(at(i, j + 3), inv[j + 3]), f32_mul(at(i, j + 2), inv[j + 2]));
+            o[h] = lop_select(0x7F7F7F7Fu, lo | hi << 16, nan[h]);
         }
-        *reinterpret_cast<uint2*>(a.data + (r0 + 32 * i) * a.K + c) = make_uint2(o[0], o[1]);
+        *reinterpret_cast<uint2*>(a.data + (r0 + TY * i) * a.K + c) = make_uint2(o[0], o[1]);
     }
 }
 
@@ -273,7 +283,8 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
             p.scales = a.scales + r0 / 128 * a.K;
             const unsigned y = (unsigned)ceil_div(p.out_rows, 128);
             const cudaError_t e =
-                tiled ? launch_overlapped(quant_columns_tile_kernel<ELT>, dim3((unsigned)ceil_div(a.K, 64), y), 256, 0, 0, s, p)
+                tiled ? launch_overlapped(quant_columns_tile_kernel<ELT>, dim3((unsigned)ceil_div(a.K, 8 * ColumnTile<ELT>::kX), y),
+                                          ColumnTile<ELT>::kThreads, 0, 0, s, p)
                       : launch_overlapped(quant_columns_kernel<ELT>, dim3((unsigned)ceil_div(a.K, 64), y), 512, 0, 0, s, p);
             if (e != cudaSuccess) return e;
         }
