@@ -366,7 +366,7 @@ GROUPS = [  # rows of each expert
 
 @pytest.mark.parametrize("direction", ["fwd", "dgrad"])
 @pytest.mark.parametrize("counts", GROUPS)
-@pytest.mark.parametrize("N,K", [(272, 400), (128, 1040), (1000, 96)])
+@pytest.mark.parametrize("N,K", [(272, 400), (128, 1040), (1000, 96), (160, 9000), (5000, 160)])
 def test_grouped_product(mx, direction, counts, N, K):
     rng = np.random.default_rng(sum(counts) + N)
     E, front, behind = len(counts), 0, 7
@@ -419,7 +419,7 @@ def test_offsets_are_clamped(mx, off):
     close(mx.fp8_matmul(*map(bytes_dev, (x, xs, w, tile)), offsets=bytes_dev(off), out_dtype=F32), want, S, K, F32)
 
 
-@pytest.mark.parametrize("counts", [[128], [0, 256, 0, 128], [1, 130, 5, 128], [0, 0], [700, 3]])
+@pytest.mark.parametrize("counts", [[128], [0, 256, 0, 128], [1, 130, 5, 128], [0, 0], [700, 3], [5000, 130, 0, 9300]])
 @pytest.mark.parametrize("N,K", [(144, 272), (128, 128), (300, 97)])
 def test_grouped_weight_gradient(mx, counts, N, K):
     rng = np.random.default_rng(sum(counts) + N)
@@ -574,3 +574,68 @@ def test_slots_that_leave_the_rows_add_nothing(mx):
     slots = torch.tensor([[0, 4], [-1, 1 << 30], [3, -(1 << 31)]], dtype=torch.int32, device="cuda")
     assert mx.moe_combine(y, slots)[:, 0].tolist() == [1.0, 0.0, 1.0]
     assert mx.moe_dispatch(y, torch.tensor([8, 7, -1], dtype=torch.int32, device="cuda"), 2)[:, 0].tolist() == [0.0, 1.0, 0.0]
+
+
+# ---------------------------------------------------------------- refusals
+
+
+def test_refusals(mx):
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    f32 = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    x, xs, w, t = u8(40, 256), u8(40, 2), u8(384, 256), f32(3, 2)
+    mx.fp8_matmul(x, xs, w, t)
+    for bad in (
+        lambda: mx.fp8_matmul(x, u8(40, 1), w, t),                            # scales of another size
+        lambda: mx.fp8_matmul(x, xs.float(), w, t),                           # ... or type
+        lambda: mx.fp8_matmul(x, u8(40, 4)[:, ::2], w, t),                    # ... or not contiguous
+        lambda: mx.fp8_matmul(x, xs, w, f32(3, 1)),
+        lambda: mx.fp8_matmul(x, xs, w, t.double()),
+        lambda: mx.fp8_matmul(x, xs, u8(384, 128), t),                        # inner sizes
+        lambda: mx.fp8_matmul(x.to(BF16), xs, w, t),                          # no payload bytes
+        lambda: mx.fp8_matmul(x, xs, w.float(), t),
+        lambda: mx.fp8_matmul(x[:1].expand(40, 256), xs, w, t),               # rows that overlap
+        lambda: mx.fp8_matmul(x.t(), xs, w, t),
+        lambda: mx.fp8_matmul(x, xs, w, t, out=f32(40, 383)),
+        lambda: mx.fp8_matmul(x, xs, w, t, out=torch.zeros(40, 384)),         # on the CPU
+        lambda: mx.fp8_matmul(x.cpu(), xs, w, t),
+        lambda: mx.fp8_matmul(x, xs, w, t, offsets=i32(2)),                   # offsets without a stack
+        lambda: mx.fp8_matmul(x, xs, w.view(1, 384, 256), t),                 # a stack without offsets
+        lambda: mx.fp8_matmul(x, xs, w.view(1, 384, 256), t, offsets=i32(3)),
+        lambda: mx.fp8_matmul(x, xs, w.view(1, 384, 256), t, offsets=i32(2).long()),
+        lambda: mx.fp8_matmul(x, xs, w.view(1, 384, 256), t, offsets=i32(0)),
+        lambda: mx.fp8_matmul_wgrad(x, u8(1, 256), u8(41, 256), u8(1, 256)),  # rows
+        lambda: mx.fp8_matmul_wgrad(x, xs, x, u8(1, 256)),
+        lambda: mx.plan_fp8_matmul("forward", x, xs, w, t, f32(40, 384)),
+        lambda: mx.fp8_quant_1x128(f32(8, 4).t()),
+        lambda: mx.fp8_quant_1x128(f32(4, 8), index=i32(3).long()),
+        lambda: mx.fp8_quant_1x128(f32(4, 8), data=u8(4, 7)),
+        lambda: mx.fp8_quant_128x1(f32(4, 8), scales=u8(2, 8)),
+        lambda: mx.moe_sort(i32(8), 3),
+        lambda: mx.moe_sort(i32(8, 2).long(), 3),
+        lambda: mx.moe_sort(i32(8, 2), 0),
+        lambda: mx.moe_sort(i32(8, 2), 3, align=0),
+        lambda: mx.moe_sort(i32(8, 4)[:, ::2], 3),
+        lambda: mx.moe_dispatch(f32(4, 8), i32(4).long(), 1),
+        lambda: mx.moe_dispatch(f32(4, 8), i32(4), 1, out=f32(4, 7)),
+        lambda: mx.moe_dispatch(f32(4, 8, 1), i32(4), 1),
+        lambda: mx.moe_combine(f32(4, 8), i32(4)),
+        lambda: mx.moe_combine(f32(4, 8), i32(4, 2), f32(4, 1)),
+        lambda: mx.moe_combine(f32(4, 8), i32(4, 2), f32(4, 2).double()),
+        lambda: mx.moe_combine_grad(f32(4, 8), f32(6, 8), i32(5), i32(4, 2), f32(4, 2)),
+        lambda: mx.moe_combine_grad(f32(4, 8).to(BF16), f32(6, 8), i32(6), i32(4, 2), f32(4, 2)),
+    ):
+        with pytest.raises(ValueError):
+            bad()
+    for bad, status in (
+        (lambda: mx.fp8_quant_1x128(f32(4, 8).half()), 2),
+        (lambda: mx.fp8_matmul(x, xs, w, t, out_dtype=torch.float16), 2),
+        (lambda: mx.moe_combine(f32(4, 8).half(), i32(4, 2)), 2),
+        (lambda: mx.fp8_quant_1x128(f32(4, 8), index=i32(3), index_div=0), 1),
+        (lambda: mx.moe_sort(i32(8, 2), 2049), 1),
+        (lambda: mx.moe_dispatch(f32(4, 8), i32(4), 0), 1),
+        (lambda: mx.fp8_matmul(x, xs, u8(1025, 384, 256), f32(1025, 3, 2), offsets=i32(1026)), 1),
+    ):
+        with pytest.raises(mxq.MXQError) as e:
+            bad()
+        assert e.value.status == status
