@@ -29,7 +29,7 @@
 //                                lines; the L2 serves five sectors for four:
 //                                16384x4096x7184 2.7 PFLOP/s, at 8192 deep 3.5.
 //   few rows                     the weight's bytes: one token through
-//                                8192x8192 15.1 us, 4.4 TB/s, of which 11 us
+//                                8192x8192 15.0 us, 4.5 TB/s, of which 11 us
 //                                are the stream at 6 TB/s and the rest the
 //                                launch and the sum over a cluster; 48 tokens x 2 of 32 experts
 //                                (4096x7184 each) at 6 TB/s.
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
             const Tile c = tile_at<PT, QT>(g, rag, first_tile);
             const int64_t base = g.ragged == kDepth ? c.e * g.out_expert : 0;
             const uint32_t part = smem_u32(stages);
-            const int j0 = QT * (int)rank / split, j1 = min(QT * ((int)rank + 1) / split, c.q_end - c.q0);
+            const int width = c.q_end - c.q0, j0 = width * (int)rank / split, j1 = width * ((int)rank + 1) / split;
             // four neighbouring rows of P a thread, the sums of all blocks on their way together
             for (int x = threadIdx.x; x < (j1 - j0) * 32; x += S::kThreads) {
                 const int j = j0 + (x >> 5), r = (x & 31) * 4;
