@@ -99,6 +99,7 @@ struct Problem {
     int p_rows, q_rows, p_tiles, q_tiles;
     int columns;  // of the accumulator a tile takes, where experts' rows do not decide it
     int segment;  // blocks of depth that one accumulation takes: see kSegment
+    int whole;    // tiles in front of those that are taken in two halves (CG 2, kNone)
     int ragged;
     bool p_mn, q_mn;   // the operand's depth runs across its rows in memory
     bool p_expert;     // P is a stack of experts' weights
@@ -180,13 +181,22 @@ __device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t
         c.kb0 = (r.bound[c.e] + 127) >> 7;  // only `depth` itself is no multiple of 128: nothing begins there
         c.kb1 = (r.bound[c.e + 1] + 127) >> 7;
     }
+    // The last round's tiles come in halves of 128 columns where that fills it better.
+    const int half = QT == 256 && g.ragged == kNone && t >= g.whole ? (t - g.whole) & 1 : -1;
+    if (half >= 0) t = g.whole + ((t - g.whole) >> 1);
     constexpr int G = 16;  // 8192^3: 302 us; groups of eight 305, of four 307
     const int group = t / (G * g.q_tiles), first = group * G, n = min(G, g.p_tiles - first);
     t -= group * G * g.q_tiles;
     c.p0 = (first + t % n) * PT;
     c.q0 = t / n * g.columns;
-    c.q_end = min(g.q_rows, c.q0 + g.columns);
+    if (half > 0) c.q0 += 128;
+    c.q_end = min(g.q_rows, c.q0 + (half >= 0 ? 128 : g.columns));
     c.columns = QT < 256 ? QT : min(g.columns, (c.q_end - c.q0 + 31) & ~31);
+    if (c.q_end <= c.q0) {  // a half behind the last column: no work, and nothing to store
+        c.q_end = c.q0;
+        c.columns = 32;
+        c.kb1 = c.kb0;
+    }
     return c;
 }
 
@@ -941,7 +951,17 @@ cudaError_t launch(const MatmulArgs& m, int ragged, int columns, int split, cuda
     int64_t tiles = (int64_t)g.p_tiles * g.q_tiles * (ragged == kDepth ? m.E : 1);
     if (ragged == kRowsOfQ)  // at most: every expert has a last, partial tile
         tiles = (q.rows / QT + (m.E < q.rows ? m.E : q.rows)) * g.p_tiles;
-    if (tiles > INT64_C(0x3FFFFFFF)) return cudaErrorInvalidValue;
+    if (tiles > INT64_C(0x1FFFFFFF)) return cudaErrorInvalidValue;
+    g.whole = (int)tiles;
+    if (CG == 2 && ragged == kNone) {
+        // a half takes three quarters of a tile's time, and the last round is that much shorter (512x4096x4096 17.0 -> 15.3
+        // us, a weight gradient of 4096x4096 55.5 -> 52.8)
+        const int64_t pairs = sm_count() / 2, rest = tiles % pairs;
+        if (rest > 0 && 2 * rest <= pairs) {
+            g.whole = (int)(tiles - rest);
+            tiles += rest;
+        }
+    }
     auto kernel = matmul_kernel<QT, CG, SPLIT, ROWS>;
     const size_t smem = S::smem((int)m.E);
     // once a device: the most that any number of experts asks for
@@ -968,7 +988,7 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
     const int ragged = m.grouping == Grouping::DEPTH ? kDepth : m.grouping == Grouping::ROWS ? kRowsOfQ : kNone;
     const int64_t features = m.b.rows, tokens = m.a.rows, blocks = ceil_div(m.depth, 128);
     cudaError_t e;
-    // Pairs of blocks and 256x256 tiles where there are rows enough to fill them.  512x4096x4096: 17.6 us, 23.5 in tiles of
+    // Pairs of blocks and 256x256 tiles where there are rows enough to fill them.  512x4096x4096: 15.3 us, 23.5 in tiles of
     // 128x128 with the depth split; 256: 18.3 and 14.0.  32 experts of 4096x4096 with 50 rows each on average: 92 us, 102
     // in single blocks; with 8: 64 in both.
     if (tokens > 256 && features > 128 && !(ragged == kRowsOfQ && tokens / m.E < 16)) {
