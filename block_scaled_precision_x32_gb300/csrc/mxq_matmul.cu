@@ -954,8 +954,9 @@ cudaError_t launch(const MatmulArgs& m, int ragged, int columns, int split, cuda
     if (tiles > INT64_C(0x1FFFFFFF)) return cudaErrorInvalidValue;
     g.whole = (int)tiles;
     if (CG == 2 && ragged == kNone) {
-        // a half takes three quarters of a tile's time, and the last round is that much shorter (512x4096x4096 17.0 -> 15.3
-        // us, a weight gradient of 4096x4096 55.5 -> 52.8)
+        // a half takes three quarters of a tile's time, and the last round is that much shorter (512x4096x4096 17.0 -> 15.6
+        // us, 4099x4096x4096's weight gradient 53.9 -> 51.8, 4099x4096x7184's input gradient 85.2 -> 83.8: means of both sides
+        // run in turn, four times for the first and ten for the others)
         const int64_t pairs = sm_count() / 2, rest = tiles % pairs;
         if (rest > 0 && 2 * rest <= pairs) {
             g.whole = (int)(tiles - rest);
@@ -988,7 +989,7 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
     const int ragged = m.grouping == Grouping::DEPTH ? kDepth : m.grouping == Grouping::ROWS ? kRowsOfQ : kNone;
     const int64_t features = m.b.rows, tokens = m.a.rows, blocks = ceil_div(m.depth, 128);
     cudaError_t e;
-    // Pairs of blocks and 256x256 tiles where there are rows enough to fill them.  512x4096x4096: 15.3 us, 23.5 in tiles of
+    // Pairs of blocks and 256x256 tiles where there are rows enough to fill them.  512x4096x4096: 15.6 us, 23.5 in tiles of
     // 128x128 with the depth split; 256: 18.3 and 14.0.  32 experts of 4096x4096 with 50 rows each on average: 92 us, 102
     // in single blocks; with 8: 64 in both.
     if (tokens > 256 && features > 128 && !(ragged == kRowsOfQ && tokens / m.E < 16)) {
