@@ -168,6 +168,21 @@ def test_product(mx, direction, M, N, K, dtype):
 
 
 @pytest.mark.parametrize("direction", ["fwd", "dgrad", "wgrad"])
+@pytest.mark.parametrize("rows,features", [(257, 129), (273, 272), (383, 400), (384, 385), (641, 640), (2305, 2064), (2064, 2305), (2433, 2432)])
+@pytest.mark.parametrize("depth", [144, 1040])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_product_with_few_tiles_in_the_last_round(mx, direction, rows, features, depth, dtype):
+    """Tiles of 256x256 that are taken in halves: with a second half of nothing, of a column, of some and of all 128."""
+    M, N, K = {"fwd": (rows, features, depth), "dgrad": (rows, depth, features), "wgrad": (depth, rows, features)}[direction]
+    args, a, b = operands(np.random.default_rng(rows * 31 + features + depth), direction, M, N, K)
+    want, S = ref.product(a, b)
+    out = Guarded(want.shape, dtype)
+    call(mx, direction)(*args, out=out.t)
+    assert out.intact()
+    close(out.t, want, S, depth, dtype)
+
+
+@pytest.mark.parametrize("direction", ["fwd", "dgrad", "wgrad"])
 @pytest.mark.parametrize("shift,pad", [(0, 16), (16, 48), (1, 5), (0, 7), (8, 0)])
 def test_product_of_strided_operands(mx, direction, shift, pad):
     rng = np.random.default_rng(shift * 100 + pad)
