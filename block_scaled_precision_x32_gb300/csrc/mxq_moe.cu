@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(1024) place_kernel(MoeSortArgs a, int chunks, 
     // rows without a choice: behind each part (a warp each), and behind the last
     if (a.align > 1)
         for (int e = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; e < E; e += gridDim.x * (blockDim.x / 32))
-            for (int r = begin[e] + total[e] + (threadIdx.x & 31); r < begin[e + 1]; r += 32) a.source[r] = -1;
+            // 64 bits: a part may end within 32 rows of 2^31
+            for (int64_t r = (int64_t)begin[e] + total[e] + (threadIdx.x & 31); r < begin[e + 1]; r += 32) a.source[r] = -1;
     for (int64_t r = begin[E] + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.capacity;
          r += (int64_t)gridDim.x * blockDim.x)
         a.source[r] = -1;
