@@ -5,7 +5,10 @@
 // the one in front are still running.  (8192x8192 weight, one token, calls
 // back to back: 18.1 -> 15.6 us.)
 //
-// A kernel launched so calls wait_for_stream() before it touches memory.
+// A kernel launched so calls wait_for_stream() before it touches memory.  One
+// that allocates tensor memory calls let_next_start() after that: a block of
+// a kernel behind it that took the columns first, and then waited for this
+// one to end, would keep it from ever ending.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -424,7 +424,6 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
     const uint32_t pair_rank = CG == 2 ? rank : 0;
     const bool leader = pair_rank == 0;
 
-    let_next_start();
     if (warp == 0) {
         if (lane == 0) {
             prefetch_map(&p_map);
@@ -447,13 +446,14 @@ __global__ void __launch_bounds__(Shape<QT, CG, SPLIT, ROWS>::kThreads, Shape<QT
         }
     } else if (warp == 1) {
         tmem_alloc<CG>(smem_u32(tmem_at), S::kColumns);
-    } else if (warp == 2 && g.ragged != kNone) {
-        wait_for_stream();
-        read_offsets(g, g.ragged == kDepth ? g.depth : g.q_rows, QT, rag);
     }
     wait_for_stream();
+    if (warp == 2 && g.ragged != kNone) read_offsets(g, g.ragged == kDepth ? g.depth : g.q_rows, QT, rag);
     tc_fence_before();
     __syncthreads();
+    // The next kernel's blocks start once this grid's blocks hold their tensor memory, and not before: one of them that
+    // took the columns first, and then waited for this grid to end, would wait for ever.
+    let_next_start();
     if constexpr (CG == 2) cluster_sync();  // its barriers take the other block's arrivals from here on
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_at, 0);  // known to be the same in a warp: see elect_one()
