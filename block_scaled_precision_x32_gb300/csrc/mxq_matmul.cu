@@ -890,9 +890,11 @@ EncodeTiled encode_tiled() {
 // Boxes of 128 bytes of a row by `box` rows of one operand, of each expert where it is a stack.
 bool make_map(CUtensorMap* map, const MatOperand& o, int64_t depth, int64_t E, int box) {
     const int64_t inner = o.mn ? o.rows : depth, outer = o.mn ? depth : o.rows;
-    const int64_t ld = outer > 1 || o.expert ? o.ld : (inner + 15) / 16 * 16;
-    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)(o.expert ? E : 1)};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)(o.expert ? o.expert : ld)};
+    const int64_t experts = o.expert ? E : 1;
+    // strides are multiples of 16 bytes; one of a single row, or of a single expert, is not used and may be anything else
+    const int64_t ld = outer > 1 || experts > 1 ? o.ld : (inner + 15) / 16 * 16;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)experts};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)(experts > 1 ? o.expert : ld)};
     const cuuint32_t boxes[3] = {128, (cuuint32_t)box, 1}, steps[3] = {1, 1, 1};
     const EncodeTiled encode = encode_tiled();
     return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(o.data), dims, strides, boxes,

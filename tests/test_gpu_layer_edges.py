@@ -7,6 +7,7 @@ import torch
 
 import block_scaled_precision_x32_gb300 as mxq
 from tests import layer_ref as ref
+from tests.test_gpu_layer import BF16, F32, bytes_dev, call, close, make_rows, make_weight, operands
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,24 @@ def test_a_part_of_the_sort_that_ends_at_the_last_32_bit_row(mx):
     assert (room[:edge] == canary).all() and (room[edge + rows:] == canary).all()
     for piece in source[1:].split(1 << 28):
         assert (piece == -1).all()
+
+
+@pytest.mark.parametrize("direction", ["fwd", "dgrad"])
+@pytest.mark.parametrize("E,N", [(1, 1), (2, 1), (1, 2), (3, 5)])
+@pytest.mark.parametrize("K", [1, 16, 33, 100])
+@pytest.mark.parametrize("M", [1, 7, 300])
+def test_grouped_products_of_the_smallest_weights(mx, direction, E, N, K, M):
+    """Weights of one row, whose stride no copy uses and which need not be a multiple of anything."""
+    rng = np.random.default_rng(1000 * M + 10 * K + E + N)
+    off = np.linspace(0, M, E + 1).astype(np.int32)
+    x, xs = make_rows(rng, M, K if direction == "fwd" else N)
+    w, tile = make_weight(rng, E, N, K)
+    av = ref.decode_rows(x, xs)
+    n = N if direction == "fwd" else K
+    want, S = np.zeros((M, n)), np.zeros((M, n))
+    for e in range(E):
+        wd, sl = ref.decode_weight(w[e], tile[e]), slice(off[e], off[e + 1])
+        want[sl], S[sl] = ref.product(av[sl], wd if direction == "fwd" else wd.T)
+    for dtype in (BF16, F32):
+        y = call(mx, direction)(*map(bytes_dev, (x, xs, w, tile)), offsets=bytes_dev(off), out_dtype=dtype)
+        close(y, want, S, av.shape[1], dtype)
