@@ -13,6 +13,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace mxq {
 
 // The next kernel of the stream may start its blocks where this one's leave
@@ -20,6 +22,21 @@ namespace mxq {
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // ... and here waits until everything in front of it in the stream is done and visible.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Allows `kernel` up to `most` bytes of dynamic shared memory, once a device.
+// The limit belongs to the kernel on the device, whichever host thread sets
+// it: `most` is what the largest of all calls takes, so that no thread lowers
+// it between another one's setting and launch.
+constexpr int kDevices = 64;
+template <typename... Params>
+cudaError_t allow_shared_memory(void (*kernel)(Params...), size_t most, std::atomic<bool> (&allowed)[kDevices]) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess || (device < kDevices && allowed[device].load(std::memory_order_relaxed))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess && device < kDevices) allowed[device].store(true, std::memory_order_relaxed);
+    return e;
+}
 
 // cluster: 0 for a launch without clusters.
 template <typename... Params, typename... Args>

@@ -967,16 +967,9 @@ cudaError_t launch(const MatmulArgs& m, int ragged, int columns, int split, cuda
     }
     auto kernel = matmul_kernel<QT, CG, SPLIT, ROWS>;
     const size_t smem = S::smem((int)m.E);
-    // once a device: the most that any number of experts asks for
-    static std::atomic<bool> allowed[64];
-    int device = 0;
-    cudaError_t e = cudaGetDevice(&device);
+    static std::atomic<bool> allowed[kDevices];
+    const cudaError_t e = allow_shared_memory(kernel, S::smem(kMostExperts), allowed);
     if (e != cudaSuccess) return e;
-    if (device >= 64 || !allowed[device].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem(kMostExperts));
-        if (e != cudaSuccess) return e;
-        if (device < 64) allowed[device].store(true, std::memory_order_relaxed);
-    }
 
     const int64_t room = (int64_t)sm_count() * S::kPerSm / CG;
     const int64_t blocks = SPLIT ? tiles * split : (tiles < room ? tiles : room) * CG;

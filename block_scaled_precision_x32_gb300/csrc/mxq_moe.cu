@@ -3,6 +3,7 @@
 // the gradients of both.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "mxq_device.cuh"
@@ -15,6 +16,8 @@ namespace {
 // ------------------------------------------------------------------- sort
 
 constexpr int kChunk = 4096;  // choices per block
+constexpr int kHistograms = 128 * 1024;  // bytes of place_kernel's histograms, at most
+constexpr int kMostExperts = 2048;       // that mxq_moe_sort takes
 
 // Choices of the block that a walking warp takes: consecutive ones.
 __device__ __forceinline__ void warp_range(const MoeSortArgs& a, int walkers, int64_t& first, int64_t& end) {
@@ -444,11 +447,11 @@ cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
     const int chunks = (int)moe_sort_chunks(a.choices);
     // as many warps as have choices and as shared memory has room for histograms of
     const int threads = a.choices <= 1024 ? 256 : 1024;
-    int walkers = (int)(INT64_C(128) * 1024 / (a.experts * 4));
+    int walkers = kHistograms / ((int)a.experts * 4);
     walkers = walkers < threads / 32 ? walkers : threads / 32;
     const int one = (int)a.experts * 4, hist = walkers * one, place = hist + (int)(3 * a.experts + 1) * 4;
-    cudaError_t e = cudaSuccess;
-    if (place > 48 * 1024) e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, place);
+    static std::atomic<bool> allowed[kDevices];
+    cudaError_t e = allow_shared_memory(place_kernel, kHistograms + (3 * kMostExperts + 1) * 4, allowed);
     if (e == cudaSuccess && chunks > 1) e = launch_overlapped(count_kernel, dim3(chunks), threads, one, 0, s, a, walkers);
     if (e == cudaSuccess) {
         // not overlapped with count_kernel: its blocks would take the multiprocessors' threads while that still runs

@@ -1,6 +1,8 @@
 """The FP8 linear layer and the mixture-of-experts operators at the ends of their
 ranges, against 64-bit references from their definitions."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -52,3 +54,38 @@ def test_grouped_products_of_the_smallest_weights(mx, direction, E, N, K, M):
     for dtype in (BF16, F32):
         y = call(mx, direction)(*map(bytes_dev, (x, xs, w, tile)), offsets=bytes_dev(off), out_dtype=dtype)
         close(y, want, S, av.shape[1], dtype)
+
+
+def test_sorts_of_two_host_threads(mx):
+    """Sorts of 512 and of 2048 experts take different amounts of shared memory; threads that call both at once, each on a
+    stream of its own, get their results."""
+    rng = np.random.default_rng(41)
+    failed = []
+
+    def sorts(experts):
+        try:
+            ids = rng_ids[experts]
+            want = ref.moe_sort(ids, experts, 1)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                order = mxq.MoeOrder(*(torch.empty(n, dtype=torch.int32, device="cuda") for n in (experts + 1, ids.size, ids.shape)))
+                plan = mx.plan_moe_sort(bytes_dev(ids), experts, order)
+                ready.wait()
+                for _ in range(20):
+                    for _ in range(500):
+                        plan()
+                    torch.cuda.current_stream().synchronize()
+                for got, w in zip(order, want):
+                    np.testing.assert_array_equal(got.cpu().numpy(), w)
+        except BaseException as e:  # a thread's failure is the test's
+            failed.append((experts, e))
+            ready.abort()
+
+    rng_ids = {e: rng.integers(0, e, (1025, 1)).astype(np.int32) for e in (512, 2048)}
+    ready = threading.Barrier(2)
+    threads = [threading.Thread(target=sorts, args=(e,)) for e in rng_ids]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
