@@ -57,14 +57,18 @@ constexpr int kGroup = 8;
 constexpr int kRing = 2;  // groups, both in shared and in tensor memory
 
 // The tensor core cuts off what a sum's 24 bits cannot hold instead of
-// rounding it, so that the error of a long sum grows with its length: 5e-7 to
-// 8e-7 of the result's norm at a depth of 4099, 1.2e-6 at 8191, against 1e-7
-// to 2e-7 for sums that are rounded.  That is far below a bf16 result's own
-// rounding, but not below fp32's.  fp32 results deeper than 36 blocks are
-// therefore summed in segments of about equal length, each added, rounded, to
-// what the output holds, which keeps them below 1e-6: 5e-7 at 8191.  A
-// segment more costs what its results' way to memory and back does (8192 x
-// 4096 x 4096: 101 us, as bf16 in one segment 85).
+// rounding it, so that the error of a long sum grows with its length: in one
+// accumulation of normally distributed operands 2.2e-7 of the result's norm at
+// a depth of 4096, 2.5e-7 at 4608 and 3e-6 at 33000, where a sum that is
+// rounded has 1e-7 to 2e-7.  Operands of one sign have 1.4e-6 at 4096, those
+// whose magnitudes spread over 2^20 along the depth 2.4e-6.  That is far below
+// a bf16 result's own rounding (1.7e-3), but not below fp32's.  fp32 results
+// deeper than 36 blocks are therefore summed in segments of about equal length
+// (40 blocks at most), each added, rounded, to what the output holds, which
+// keeps the error where it is at one segment's depth: 2.2e-7 at 8191, 2.8e-7 at
+// 33000 (2.4e-6 and 2.9e-6 for the spread ones).  A segment more costs what its
+// results' way to memory and back does (8192 x 4096 x 4096: 101 us, as bf16 in
+// one segment 85).
 constexpr int kSegment = 36;
 
 // The operand whose rows are the accumulator's lanes is called P, the one

@@ -364,12 +364,18 @@ typedef struct {
     int64_t E;             /* 1 .. 1024 with offsets, ignored without */
 } mxq_fp8_product;
 
-/* out = the product described by p, accumulated in fp32 and rounded once
- * (round to nearest even) to out_dt.  The scales are applied as exact powers
- * of two to the products of each 128-block.  A block whose code is 0xFF, and
- * a payload NaN, make the sums that they enter NaN.  Results do not depend
- * on the order in which blocks of the grid run; their error is at most depth *
- * 2^-23 * sum |a b|, below 1e-6 of the result's norm for fp32 results.
+/* out = the product described by p, accumulated in fp32 on the tensor cores,
+ * which cut off what 24 bits of a running sum cannot hold.  A bf16 result is
+ * one such sum, rounded once (to nearest even); an fp32 result of a depth above
+ * 4608 is the sum of segments of 5120 at most, each added with one rounding.
+ * The scales are applied as exact powers of two to the products of each
+ * 128-block.  A block whose code is 0xFF, and a payload NaN, make the sums
+ * that they enter NaN.  Results do not depend on the order in which blocks of
+ * the grid run.
+ * Error: at most depth * 2^-23 * sum |a b|, plus the rounding to out_dt.
+ * Measured on fp32 results against their norm, at depths up to 40000: 3e-7
+ * for normally distributed operands (the tests hold it below 1e-6), 2e-6 for all
+ * of one sign, 3e-6 where magnitudes spread over 2^20 along the depth.
  * out must not overlap an operand.  Waits inside the kernel end after about
  * two seconds (a device fault, never expected) and leave NaN in the tiles
  * that were not finished.
