@@ -23,16 +23,24 @@
 //
 // What bounds it (GB300; the tensor cores' own time for a 256x256 tile and 128
 // of depth is 497 clocks, 4.9 PFLOP/s at 2 GHz):
-//   8192^3                       0.297 ms, 3.7 PFLOP/s: the board's power.  On
-//                                operands of zeros 0.263 ms, 4.2 PFLOP/s.
+//   8192^3                       0.299 ms, 3.7 PFLOP/s, in six calls in a row,
+//                                0.340 in 200: the board's power.  On operands
+//                                of zeros 0.281 ms, 3.9 PFLOP/s.
 //   rows of 7184 bytes           a box of 128 bytes lies across two 128-byte
 //                                lines; the L2 serves five sectors for four:
-//                                16384x4096x7184 2.7 PFLOP/s, at 8192 deep 3.5.
+//                                16384x4096x7184 2.7 PFLOP/s, at 8192 deep 3.6
+//                                (in 200 calls 2.7 and 3.2).
 //   few rows                     the weight's bytes: one token through
-//                                8192x8192 15.0 us, 4.5 TB/s, of which 11 us
+//                                8192x8192 15.1 us, 4.4 TB/s, of which 11 us
 //                                are the stream at 6 TB/s and the rest the
 //                                launch and the sum over a cluster; 48 tokens x 2 of 32 experts
-//                                (4096x7184 each) at 6 TB/s.
+//                                (4096x7184 each) at 5.6 TB/s of the weights that they chose.
+//   experts with uneven loads    no unit: 16384 rows over 32 experts, 24 of
+//                                which have fewer than 256, take 430 us, with the
+//                                tensor pipes busy 48% of the time, the L2 46%
+//                                and the HBM 35%.  An expert with few rows waits for
+//                                its weight, one with many for the tensor cores,
+//                                and their tiles come one expert after the other.
 // A pair's stages take 32 KB a block of depth on each SM, which at the tensor
 // cores' rate is 18 TB/s from the L2: wider sharing (clusters of four with
 // multicast) would relieve it, but only 144 of the 152 SMs hold such clusters.
@@ -188,7 +196,7 @@ __device__ __forceinline__ Tile tile_at(const Problem& g, const Ragged& r, int t
     // The last round's tiles come in halves of 128 columns where that fills it better.
     const int half = QT == 256 && g.ragged == kNone && t >= g.whole ? (t - g.whole) & 1 : -1;
     if (half >= 0) t = g.whole + ((t - g.whole) >> 1);
-    constexpr int G = 16;  // 8192^3: 302 us; groups of eight 305, of four 307
+    constexpr int G = 16;  // 8192^3: 299 us; groups of eight 303, of four 309
     const int group = t / (G * g.q_tiles), first = group * G, n = min(G, g.p_tiles - first);
     t -= group * G * g.q_tiles;
     c.p0 = (first + t % n) * PT;
@@ -988,20 +996,28 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
     const int ragged = m.grouping == Grouping::DEPTH ? kDepth : m.grouping == Grouping::ROWS ? kRowsOfQ : kNone;
     const int64_t features = m.b.rows, tokens = m.a.rows, blocks = ceil_div(m.depth, 128);
     cudaError_t e;
-    // Pairs of blocks and 256x256 tiles where there are rows enough to fill them.  512x4096x4096: 15.6 us, 23.5 in tiles of
-    // 128x128 with the depth split; 256: 18.3 and 14.0.  32 experts of 4096x4096 with 50 rows each on average: 92 us, 102
-    // in single blocks; with 8: 64 in both.
+    // Pairs of blocks and 256x256 tiles where there are rows enough to fill them.  512x4096x4096: 15.2 us, 23.5 in tiles of
+    // 128x128 with the depth split; 256: 18.3 and 14.0.  Experts by the rows that each has on average, uneven loads (some
+    // have ten times as many as others): 32 of 4096x7184 with 16 rows 150 us in pairs, 170 in single blocks, with 48 169
+    // and 212; 32 of 4096x4096 87 and 88, 97 and 101; with 8 rows 124 (4096x7184) and 68 in both, and 64 experts of
+    // 2048x2048 48 and 39.  Where every expert has the same number of rows, which a router does not see to, single blocks
+    // would stay ahead for longer: 32 of 4096x7184 with 16 rows 163 and 149, with 32 164 and 153, with 50 166 and 170.
     if (tokens > 256 && features > 128 && !(ragged == kRowsOfQ && tokens / m.E < 16)) {
         const int64_t es = m.out_bf16 ? 2 : 4;
         const bool sectors = reinterpret_cast<uintptr_t>(m.out) % 32 == 0 && m.ldo * es % 32 == 0;
-        // 8192^3 with the rows as lanes 284 us, as columns 293; experts' rows are columns for their tiles' width (a
-        // 32-expert prompt of 16384 rows: 424 us, 477 as lanes), and so are rows that whole sectors cannot be stored of
+        // 8192^3 with the rows as lanes 299 us, as columns 313; 8192x4096x4096 104 and 114 (to fp32 105 and 98); experts'
+        // rows are columns for their tiles' width (a 32-expert prompt of 16384 rows: 424 us, 477 as lanes), and so are rows
+        // that whole sectors cannot be stored of
         if (ragged != kRowsOfQ && sectors)
             e = launch<256, 2, false, true>(m, ragged, 256, 1, s);
         else
             e = launch<256, 2, false, false>(m, ragged, 256, 1, s);
     } else {
         const int64_t rows = ragged == kRowsOfQ ? ceil_div(tokens, m.E) : tokens;
+        // A tile as wide as the rows are many.  Through 8192x8192, 16 rows: 15.8 us in 16 columns, 15.9, 16.1 and 16.9 in 32,
+        // 64 and 128; 32 rows: 16.3 in 32, 18.4 in two tiles of 16, 16.6 and 17.4 in 64 and 128; 64 rows: 17.5 in 64, 19.2
+        // in two of 32, 18.2 in 128; 128 rows: 20.3 in 128, 21.4 in two of 64.  2048x7168 and 4096x4096 order them alike up
+        // to 64 rows, but have 128 in two tiles of 64 in 12.1 and 11.5 us, in one of 128 in 13.0 and 13.6.
         const int qt = m.a.mn || rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
         const int64_t tiles = ceil_div(features, 128) * ceil_div(tokens, qt), quads = ceil_div(m.depth, 512);
         // as many blocks to a tile's depth as the device has room for at once (two a multiprocessor), and no more than
@@ -1010,7 +1026,8 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
         if (ragged == kNone)
             for (int x = 2; x <= 8 && x <= quads && tiles * x <= 2 * sm_count(); ++x)
                 if (ceil_div(quads, x) < ceil_div(quads, split)) split = x;
-        if (!m.out_bf16 && ceil_div(quads, split) * 4 > kSegment) split = 1;  // a share of a cluster is one segment
+        // A share of a cluster is one segment; deeper fp32 results are not split (1x8192x28672: 68.7 us, as bf16, split, 39.6).
+        if (!m.out_bf16 && ceil_div(quads, split) * 4 > kSegment) split = 1;
         if (split > 1)
             e = qt == 16   ? launch<16, 1, true, false>(m, ragged, qt, split, s)
                 : qt == 32 ? launch<32, 1, true, false>(m, ragged, qt, split, s)

@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(1024) count_kernel(MoeSortArgs a, int walkers)
 // Every block finds all experts' totals and where each part begins, then the
 // rows of its own choices.  With one chunk the counts come from the block's
 // own histogram, else from count_kernel's, summed by as many threads an
-// expert as the block has.  Latency: 48 x 2 choices 3.4 us; 65536 x 8 over 256
-// experts 14.0 us in two launches, of which the scattered stores of `source`
+// expert as the block has.  Latency: 48 x 2 choices 3.5 us; 65536 x 8 over 256
+// experts 14.4 us in two launches, of which the scattered stores of `source`
 // and every block's sum over all chunks' counts take the most.
 __global__ void __launch_bounds__(1024) place_kernel(MoeSortArgs a, int chunks, int walkers) {
     extern __shared__ int smem[];
@@ -248,7 +248,7 @@ __device__ __forceinline__ void* row_of(void* p, int64_t r, int64_t ld) {
 
 // One row of the order to blockIdx.x, a slice of its pieces to blockIdx.y.
 // Memory-bound: 32764 rows of 7184 bf16 139 us, 6.8 TB/s of what is read and
-// written (a token is read for each of its choices).
+// written (a token is read for each of its choices; read once it would be 87).
 template <Elt ELT, int VEC>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
     let_next_start();
@@ -455,7 +455,7 @@ cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
     if (e == cudaSuccess && chunks > 1) e = launch_overlapped(count_kernel, dim3(chunks), threads, one, 0, s, a, walkers);
     if (e == cudaSuccess) {
         // not overlapped with count_kernel: its blocks would take the multiprocessors' threads while that still runs
-        // (65536 x 8 over 256 experts: 14.0 us; overlapped 20)
+        // (65536 x 8 over 256 experts: 14.4 us; overlapped 20)
         place_kernel<<<chunks, threads, place, s>>>(a, chunks, walkers);
         e = cudaGetLastError();
     }

@@ -65,7 +65,8 @@ struct Unit {
 // 64 (fp32) of loads and one 16-byte store a lane, the block's maximum by
 // three shuffles.  Memory-bound: one unit a thread, so that registers leave
 // room for as many threads as there can be (8192 x 7184 bf16: 29.6 us, 5.98
-// TB/s; two units 31.7, four 34.8).
+// TB/s; two units 31.7, four 34.8; fp32 42.7 us, 6.9 TB/s).  Gathered rows are
+// read and rounded once for each choice: 8191 x 4 of 7184 bf16 123 us.
 template <Elt ELT>
 __global__ void __launch_bounds__(256) quant_rows_unit_kernel(Quant128Args a, int64_t nb) {
     let_next_start();
@@ -100,7 +101,9 @@ __global__ void __launch_bounds__(256) quant_rows_unit_kernel(Quant128Args a, in
 }
 
 // Any alignment and any K: a warp per four 1x128 blocks, an element at a time,
-// neighbours to neighbouring lanes; the loads of all four are on their way at once.
+// neighbours to neighbouring lanes; the loads of all four are on their way at
+// once.  Bound by instructions, one load and one byte store an element: 4095 x
+// 7183 46 us as bf16, 36 as fp32 (4.1 TB/s).
 template <Elt ELT>
 __global__ void __launch_bounds__(256) quant_rows_kernel(Quant128Args a, int64_t nb) {
     let_next_start();
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(ColumnTile<ELT>::kThreads) quant_columns_tile_
 }
 
 // Any alignment and any K: 128 rows x 64 columns a block, 16 rows of one column
-// a thread.
+// a thread, an element at a time: 4095 x 7183 fp32 46 us, 3.2 TB/s.
 template <Elt ELT>
 __global__ void __launch_bounds__(512) quant_columns_kernel(Quant128Args a) {
     let_next_start();
