@@ -49,12 +49,13 @@ def whole_weight(rng, *shape):
             np.exp2(rng.integers(0, 3, tiles)).astype(np.float32))
 
 
-def check_exact(y, a, b):
-    """y is a b^T, rounded to nearest even where it is bf16."""
+def check_exact(ys, a, b):
+    """Each y is a b^T, rounded to nearest even where it is bf16."""
     want, S = ref.product(a, b)
     assert S.max(initial=0) < 1 << 24  # so every partial sum is below it
     want = torch.from_numpy(want).to(F32)  # exact
-    np.testing.assert_array_equal(f64(y), want.to(y.dtype).double().numpy())
+    for y in ys:
+        np.testing.assert_array_equal(f64(y), want.to(y.dtype).double().numpy())
 
 
 DEEP = [  # output rows, columns, depth
@@ -65,9 +66,7 @@ DEEP = [  # output rows, columns, depth
 
 @pytest.mark.parametrize("direction", ["fwd", "dgrad", "wgrad"])
 @pytest.mark.parametrize("rows,features,depth", DEEP)
-@pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("pad", [0, 3])
-def test_whole_numbers_are_exact(mx, direction, rows, features, depth, dtype, pad):
+def test_whole_numbers_are_exact(mx, direction, rows, features, depth):
     rng = np.random.default_rng(rows + 3 * features + 7 * depth)
     M, N, K = sizes(direction, rows, features, depth)
     if direction == "wgrad":
@@ -77,40 +76,39 @@ def test_whole_numbers_are_exact(mx, direction, rows, features, depth, dtype, pa
         p, q = whole_rows(rng, M, K if direction == "fwd" else N), whole_weight(rng, N, K)
         a, b = ref.decode_rows(*p), ref.decode_weight(*q)
         b = b if direction == "fwd" else b.T
-    wide = torch.full((rows, features + pad), 7.0, dtype=dtype, device="cuda")
-    y = wide[:, :features]
-    call(mx, direction)(*map(bytes_dev, (*p, *q)), out=y)
-    check_exact(y, a, b)
-    assert (wide[:, features:] == 7).all()
+    args = tuple(map(bytes_dev, (*p, *q)))
+    outs = [torch.full((rows, features + pad), 7.0, dtype=dtype, device="cuda") for dtype in (BF16, F32) for pad in (0, 3)]
+    for wide in outs:
+        call(mx, direction)(*args, out=wide[:, :features])
+        assert (wide[:, features:] == 7).all()
+    check_exact([wide[:, :features] for wide in outs], a, b)
 
 
 @pytest.mark.parametrize("direction", ["fwd", "dgrad"])
 @pytest.mark.parametrize("counts", [[3, 0, 1, 20], [300, 0, 17, 130, 60]])
 @pytest.mark.parametrize("features,depth", [(272, 4736), (200, 9216)])
-@pytest.mark.parametrize("dtype", [BF16, F32])
-def test_whole_numbers_per_expert_are_exact(mx, direction, counts, features, depth, dtype):
+def test_whole_numbers_per_expert_are_exact(mx, direction, counts, features, depth):
     rng = np.random.default_rng(sum(counts) + depth)
     off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     M, N, K = sizes(direction, int(off[-1]), features, depth)
     p, q = whole_rows(rng, M, K if direction == "fwd" else N), whole_weight(rng, len(counts), N, K)
-    y = call(mx, direction)(*map(bytes_dev, (*p, *q)), offsets=bytes_dev(off), out_dtype=dtype)
+    ys = [call(mx, direction)(*map(bytes_dev, (*p, *q)), offsets=bytes_dev(off), out_dtype=dtype) for dtype in (BF16, F32)]
     a, b = ref.decode_rows(*p), ref.decode_weight(*q)
     for e in range(len(counts)):
-        check_exact(y[off[e]:off[e + 1]], a[off[e]:off[e + 1]], b[e] if direction == "fwd" else b[e].T)
+        check_exact([y[off[e]:off[e + 1]] for y in ys], a[off[e]:off[e + 1]], b[e] if direction == "fwd" else b[e].T)
 
 
 @pytest.mark.parametrize("rooms", [[128, 0, 4736], [0, 9216, 128, 33024, 256]])
 @pytest.mark.parametrize("N,K", [(144, 272), (300, 97)])
-@pytest.mark.parametrize("dtype", [BF16, F32])
-def test_whole_numbers_of_an_experts_weight_gradient_are_exact(mx, rooms, N, K, dtype):
+def test_whole_numbers_of_an_experts_weight_gradient_are_exact(mx, rooms, N, K):
     rng = np.random.default_rng(sum(rooms) + N)
     off = np.concatenate([[0], np.cumsum(rooms)]).astype(np.int32)
     M = int(off[-1]) + 70
     p, q = whole_columns(rng, M, N), whole_columns(rng, M, K)
-    y = mx.fp8_matmul_wgrad(*map(bytes_dev, (*p, *q)), offsets=bytes_dev(off), out_dtype=dtype)
+    ys = [mx.fp8_matmul_wgrad(*map(bytes_dev, (*p, *q)), offsets=bytes_dev(off), out_dtype=dtype) for dtype in (BF16, F32)]
     a, b = ref.decode_columns(*p), ref.decode_columns(*q)
     for e in range(len(rooms)):
-        check_exact(y[e], a[off[e]:off[e + 1]].T, b[off[e]:off[e + 1]].T)
+        check_exact([y[e] for y in ys], a[off[e]:off[e + 1]].T, b[off[e]:off[e + 1]].T)
 
 
 def norm_error(y, want):
@@ -123,8 +121,7 @@ BOUND = {F32: 1e-6, BF16: 2.0**-9 + 1e-5}
 @pytest.mark.parametrize("direction", ["fwd", "dgrad", "wgrad"])
 @pytest.mark.parametrize("rows,features", [(3, 304), (100, 260), (300, 272)])
 @pytest.mark.parametrize("depth", [4480, 4608, 4736, 8191, 33000, 40000])
-@pytest.mark.parametrize("dtype", [BF16, F32])
-def test_error_of_normal_operands_against_the_norm(mx, direction, rows, features, depth, dtype):
+def test_error_of_normal_operands_against_the_norm(mx, direction, rows, features, depth):
     rng = np.random.default_rng(rows + depth)
     M, N, K = sizes(direction, rows, features, depth)
     normal = lambda *s: rng.standard_normal(s).astype(np.float32).astype(np.float64)  # noqa: E731
@@ -136,8 +133,9 @@ def test_error_of_normal_operands_against_the_norm(mx, direction, rows, features
         q = ref.e4m3_encode(normal(N, K) * 64), np.full((-(-N // 128), -(-K // 128)), 2.0**-6, np.float32)
         a, b = ref.decode_rows(*p), ref.decode_weight(*q)
         b = b if direction == "fwd" else b.T
-    y = call(mx, direction)(*map(bytes_dev, (*p, *q)), out_dtype=dtype)
-    assert norm_error(y, a @ b.T) < BOUND[dtype]
+    want = a @ b.T
+    for dtype, bound in BOUND.items():
+        assert norm_error(call(mx, direction)(*map(bytes_dev, (*p, *q)), out_dtype=dtype), want) < bound
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
