@@ -25,6 +25,13 @@ The FP8 linear layer on the 128x128 blockwise weights, and the mixture of expert
 * ``mxq_moe_sort``             a router's choices in the experts' order
 * ``mxq_moe_dispatch``, ``_dispatch_grad``  token rows to that order, and the gradient
 * ``mxq_moe_combine``, ``_combine_grad``    weighted sums of the experts' rows per token, and the gradients
+* ``mxq_fp8_dispatch``         quantized token rows to the experts' order
+
+What stands between those products in a transformer's mixture-of-experts block:
+
+* ``mxq_rmsnorm``, ``_grad``   root-mean-square norm of x plus a residual, as an FP8 operand, and its gradient
+* ``mxq_moe_route``, ``_grad`` a router's logits to experts and weights, and the gradient of the weights
+* ``mxq_silu_mul``, ``mxq_fp8_silu_mul_1x128`` / ``_128x1``, ``mxq_silu_mul_grad``  silu(gate) * up, plain or as an FP8 operand
 
 The ``skip=`` argument of the converters selects the ``*_update`` entry
 points: a device int32 tensor, read when the kernel runs; nonzero means the
@@ -53,6 +60,8 @@ __all__ = [
     "MoeOrder", "mxq_fp8_quant_1x128", "mxq_fp8_quant_128x1", "mxq_fp8_matmul", "mxq_fp8_matmul_dgrad",
     "mxq_fp8_matmul_wgrad", "mxq_fp8_grouped_matmul", "mxq_fp8_grouped_matmul_dgrad", "mxq_fp8_grouped_matmul_wgrad",
     "mxq_moe_sort", "mxq_moe_dispatch", "mxq_moe_dispatch_grad", "mxq_moe_combine", "mxq_moe_combine_grad",
+    "mxq_fp8_dispatch", "Normed", "mxq_rmsnorm", "mxq_rmsnorm_grad", "mxq_moe_route", "mxq_moe_route_grad", "mxq_silu_mul",
+    "mxq_fp8_silu_mul_1x128", "mxq_fp8_silu_mul_128x1", "mxq_silu_mul_grad",
 ]
 
 COMPACT, PADDED, SWIZZLED = 0, 1, 2
@@ -101,8 +110,23 @@ class MoeOrder(NamedTuple):
     slots: torch.Tensor    # int32 [tokens, topk], the row of each choice, -1 if dropped
 
 
+class Normed(NamedTuple):
+    """What mxq_rmsnorm gives; None for what was not asked for."""
+    data: Optional[torch.Tensor]    # E4M3 bytes of x's shape
+    scales: Optional[torch.Tensor]  # uint8 (*shape[:-1], ceil(K/128))
+    y: Optional[torch.Tensor]       # the norm in x's dtype
+    h: torch.Tensor                 # x + residual (x itself without one)
+    rstd: Optional[torch.Tensor]    # fp32 shape[:-1]
+
+
 # The C struct mxq_fp8_product: packing its bytes costs a fraction of filling a ctypes.Structure.
 _PRODUCT = struct.Struct("@i3qPqPPqPPiqPq").pack
+# The C structs mxq_norm, mxq_norm_grad and mxq_route
+_NORM = struct.Struct("@iiqqPqPqPfPqPPPP").pack
+_NORM_GRAD = struct.Struct("@iiqqPqPqPPPqPqP").pack
+_ROUTE = struct.Struct("@PiiqqqqqqqPif").pack
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GATE_FORMS = {None: "mxq_silu_mul", "1x128": "mxq_fp8_silu_mul_1x128", "128x1": "mxq_fp8_silu_mul_128x1"}
 _DIRECTIONS = {"fwd": _FWD, "dgrad": _DGRAD, "wgrad": _WGRAD}
 # PyTorch's own C entry points behind torch.cuda.current_stream() and current_device()
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -240,6 +264,19 @@ def _matrix(t: torch.Tensor, name: str, rank: int = 0):
     return rows, n, ld
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _like_rows(t, x, rows: int, K: int, name: str, dev: int):
+    """ld of an operand that has x's rows and dtype."""
+    _same_device(dev, t)
+    r, n, ld = _matrix(t, name)
+    if r != rows or n != K or t.dtype != x.dtype:
+        raise ValueError(f"{name} must have {rows} rows of {K} of dtype {x.dtype}")
+    return ld
+
+
 def _row_output(out, rows: int, H: int, like: torch.Tensor, name: str, dev: int):
     if out is None:
         return torch.empty((rows, H), dtype=like.dtype, device=like.device)
@@ -297,6 +334,20 @@ class Library:
         L.mxq_moe_dispatch.argtypes = [vp, ci, i64, i64, i64, vp, i64, i64, vp, vp]
         L.mxq_moe_combine.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, i64, vp, vp]
         L.mxq_moe_combine_grad.argtypes = [vp, vp, ci, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+        cp = ctypes.c_char_p
+        L.mxq_fp8_dispatch.argtypes = [vp, vp, i64, i64, i64, vp, i64, i64, vp, vp, vp]
+        L.mxq_rmsnorm.argtypes = [cp, vp]
+        L.mxq_rmsnorm_grad.argtypes = [cp, vp, sz, vp]
+        L.mxq_rmsnorm_grad_workspace.argtypes = [i64, i64]
+        L.mxq_rmsnorm_grad_workspace.restype = sz
+        L.mxq_moe_route.argtypes = [cp, vp, vp, vp]
+        L.mxq_moe_route_grad.argtypes = [vp, cp, vp, vp, vp]
+        L.mxq_silu_mul.argtypes = [vp, ci, i64, i64, i64, vp, vp]
+        L.mxq_fp8_silu_mul_1x128.argtypes = L.mxq_fp8_silu_mul_128x1.argtypes = [vp, ci, i64, i64, i64, vp, vp, vp]
+        L.mxq_silu_mul_grad.argtypes = [vp, vp, ci, i64, i64, i64, i64, vp, vp]
+        for fn in ("mxq_fp8_dispatch", "mxq_rmsnorm", "mxq_rmsnorm_grad", "mxq_moe_route", "mxq_moe_route_grad", "mxq_silu_mul",
+                   "mxq_fp8_silu_mul_1x128", "mxq_fp8_silu_mul_128x1", "mxq_silu_mul_grad"):
+            getattr(L, fn).restype = ci
         for fn in ("mxq_fake_quant_mxfp4", "mxq_mxfp8_row_direct", "mxq_fp8_block128_direct", "mxq_dequantize",
                    "mxq_export_mxfp8", "mxq_fake_quant_mxfp4_update", "mxq_mxfp8_row_direct_update",
                    "mxq_fp8_block128_direct_update", "mxq_mxfp4_pack", "mxq_mxfp8_col_direct",
@@ -959,6 +1010,289 @@ class Library:
         self._call(self.L.mxq_moe_combine_grad, args, "mxq_moe_combine_grad", g.get_device())
         return d_rows, d_weights
 
+    def _dispatch_fp8_args(self, data, scales, source, topk, out, out_scales):
+        dev = _cuda_index(data)
+        _same_device(dev, scales, source)
+        _check_fp8(data, "data")
+        T, K, ld = _matrix(data, "data", 2)
+        nb = _blocks(K)
+        _check_values(scales, torch.uint8, T * nb, "scales", "tokens * ceil(K/128)")
+        R = source.numel()
+        _check_int32(source, R, "source")
+        if out is None:
+            out = torch.empty((R, K), dtype=data.dtype, device=data.device)
+        else:
+            _same_device(dev, out)
+            if out.dtype != data.dtype or not out.is_contiguous() or tuple(out.shape) != (R, K):
+                raise ValueError(f"out must be a contiguous [{R}, {K}] tensor of dtype {data.dtype}")
+        if out_scales is None:
+            out_scales = torch.empty((R, nb), dtype=torch.uint8, device=data.device)
+        else:
+            _same_device(dev, out_scales)
+            _check_values(out_scales, torch.uint8, R * nb, "out_scales", "rows * ceil(K/128)")
+        return (data.data_ptr(), scales.data_ptr(), T, K, ld, source.data_ptr(), topk, R, out.data_ptr(), out_scales.data_ptr(),
+                _raw_stream(dev)), out, out_scales
+
+    def plan_fp8_dispatch(self, data: torch.Tensor, scales: torch.Tensor, source: torch.Tensor, topk: int, out: torch.Tensor,
+                          out_scales: torch.Tensor) -> "Call":
+        args, *_ = self._dispatch_fp8_args(data, scales, source, topk, out, out_scales)
+        return Call(self, self.L.mxq_fp8_dispatch, args, "mxq_fp8_dispatch", (data, scales, source, out, out_scales), data.device)
+
+    def fp8_dispatch(self, data: torch.Tensor, scales: torch.Tensor, source: torch.Tensor, topk: int,
+                     out: Optional[torch.Tensor] = None, out_scales: Optional[torch.Tensor] = None):
+        """Quantized token rows (data [tokens, K], scales [tokens, ceil(K/128)]
+        of fp8_quant_1x128 or rmsnorm) in the experts' order: row r is token
+        source[r] // topk, zeros where source is -1.  Returns (data, scales)."""
+        args, out, out_scales = self._dispatch_fp8_args(data, scales, source, topk, out, out_scales)
+        self._call(self.L.mxq_fp8_dispatch, args, "mxq_fp8_dispatch", data.get_device())
+        return out, out_scales
+
+    # -- between the products -------------------------------------------
+
+    def _norm_args(self, x, weight, residual, eps, h, y, data, scales, rstd):
+        dev = _cuda_index(x)
+        rows, K, ldx = _matrix(x, "x")
+        _same_device(dev, weight)
+        if weight.dim() != 1 or weight.shape[0] != K or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous vector of {K} values")
+        ldr = ldh = 0
+        if residual is not None:
+            ldr = _like_rows(residual, x, rows, K, "residual", dev)
+        if h is not None:
+            if residual is None:
+                raise ValueError("h is written only with a residual")
+            ldh = _like_rows(h, x, rows, K, "h", dev)
+        if y is not None and (_like_rows(y, x, rows, K, "y", dev) != K or not y.is_contiguous()):
+            raise ValueError("y must be contiguous")
+        if (data is None) != (scales is None):
+            raise ValueError("data and scales go together")
+        if data is not None:
+            _same_device(dev, data, scales)
+            if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != rows * K:
+                raise ValueError("data must be a contiguous uint8 tensor of one byte per element of x")
+            _check_values(scales, torch.uint8, rows * _blocks(K), "scales", "rows * ceil(K/128)")
+        if rstd is not None:
+            _same_device(dev, rstd)
+            _check_values(rstd, torch.float32, rows, "rstd", "rows")
+        return _NORM(_dt_code(x), _dt_code(weight), rows, K, x.data_ptr(), ldx, _ptr(residual) or 0, ldr, weight.data_ptr(), eps,
+                     _ptr(h) or 0, ldh, _ptr(y) or 0, _ptr(data) or 0, _ptr(scales) or 0, _ptr(rstd) or 0), _raw_stream(dev)
+
+    def plan_rmsnorm(self, x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+                     h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, data: Optional[torch.Tensor] = None,
+                     scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None) -> "Call":
+        """Writes those of h, y, (data, scales) and rstd that are given."""
+        args = self._norm_args(x, weight, residual, eps, h, y, data, scales, rstd)
+        return Call(self, self.L.mxq_rmsnorm, args, "mxq_rmsnorm", (x, weight, residual, h, y, data, scales, rstd), x.device)
+
+    def rmsnorm(self, x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                quantized: bool = True, normed: bool = False, stats: bool = False, h: Optional[torch.Tensor] = None) -> Normed:
+        """Root-mean-square norm of x + residual over the last dimension,
+        times weight.  ``quantized``: its E4M3 bytes and UE8M0 codes per 128
+        elements; ``normed``: the norm in x's dtype; ``stats``: 1 / rms of each
+        row, which rmsnorm_grad takes.  ``h`` receives x + residual, and may be
+        x or the residual itself (allocated when None)."""
+        new, nb = x.device, _blocks(x.shape[-1]) if x.dim() else 0
+        data = torch.empty(x.shape, dtype=torch.uint8, device=new) if quantized else None
+        scales = torch.empty(x.shape[:-1] + (nb,), dtype=torch.uint8, device=new) if quantized else None
+        y = torch.empty(x.shape, dtype=x.dtype, device=new) if normed else None
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=new) if stats else None
+        if h is None and residual is not None:
+            h = torch.empty(x.shape, dtype=x.dtype, device=new)
+        args = self._norm_args(x, weight, residual, eps, h, y, data, scales, rstd)
+        self._call(self.L.mxq_rmsnorm, args, "mxq_rmsnorm", x.get_device())
+        return Normed(data, scales, y, x if residual is None else h, rstd)
+
+    def _norm_grad_args(self, g, h, weight, rstd, g_h, d_h, d_weight):
+        dev = _cuda_index(g)
+        rows, K, ldg = _matrix(g, "g")
+        _same_device(dev, weight, rstd)
+        if weight.dim() != 1 or weight.shape[0] != K or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous vector of {K} values")
+        _check_values(rstd, torch.float32, rows, "rstd", "rows")
+        ldh = _like_rows(h, g, rows, K, "h", dev)
+        ldgh = _like_rows(g_h, g, rows, K, "g_h", dev) if g_h is not None else 0
+        ldd = _like_rows(d_h, g, rows, K, "d_h", dev)
+        ws, need = None, 0
+        if d_weight is not None:
+            _same_device(dev, d_weight)
+            _check_values(d_weight, torch.float32, K, "d_weight", "K")
+            need = self.L.mxq_rmsnorm_grad_workspace(rows, K)
+            ws = torch.empty(need, dtype=torch.uint8, device=g.device) if need else None
+        return (_NORM_GRAD(_dt_code(g), _dt_code(weight), rows, K, g.data_ptr(), ldg, h.data_ptr(), ldh, weight.data_ptr(),
+                           rstd.data_ptr(), _ptr(g_h) or 0, ldgh, d_h.data_ptr(), ldd, _ptr(d_weight) or 0), _ptr(ws), need,
+                _raw_stream(dev)), ws
+
+    def plan_rmsnorm_grad(self, g: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, d_h: torch.Tensor,
+                          d_weight: Optional[torch.Tensor] = None, g_h: Optional[torch.Tensor] = None) -> "Call":
+        args, ws = self._norm_grad_args(g, h, weight, rstd, g_h, d_h, d_weight)
+        return Call(self, self.L.mxq_rmsnorm_grad, args, "mxq_rmsnorm_grad", (g, h, weight, rstd, g_h, d_h, d_weight, ws), g.device)
+
+    def rmsnorm_grad(self, g: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     g_h: Optional[torch.Tensor] = None, weight_grad: bool = True, d_h: Optional[torch.Tensor] = None):
+        """Returns (d_h, d_weight) for the gradient g of rmsnorm's y: d_h is
+        the gradient of x and of the residual, with g_h, the gradient that
+        reaches h by another way, added; d_weight is fp32 (None unless
+        ``weight_grad``).  ``d_h`` may be given, and be g, h or g_h itself."""
+        if d_h is None:
+            d_h = torch.empty(g.shape, dtype=g.dtype, device=g.device)
+        d_weight = torch.empty(g.shape[-1:], dtype=torch.float32, device=g.device) if weight_grad else None
+        args, _ = self._norm_grad_args(g, h, weight, rstd, g_h, d_h, d_weight)
+        self._call(self.L.mxq_rmsnorm_grad, args, "mxq_rmsnorm_grad", g.get_device())
+        return d_h, d_weight
+
+    def _route_args(self, logits, topk, bias, score, groups, topk_groups, group_top, renormalize, scale):
+        dev = _cuda_index(logits)
+        T, E, ld = _matrix(logits, "logits", 2)
+        if score not in _SCORES:
+            raise ValueError('score must be "softmax" or "sigmoid"')
+        if bias is not None:
+            _same_device(dev, bias)
+            _check_values(bias, torch.float32, E, "bias", "experts")
+        if not (1 <= topk <= 32 and 1 <= E <= 1024 and topk <= E):
+            raise ValueError("1 to 1024 experts, and 1 to 32 choices of them, at most as many as there are")
+        if not (1 <= groups <= 32 and E % groups == 0 and 1 <= topk_groups <= groups and 1 <= group_top <= min(2, E // groups)
+                and topk <= topk_groups * (E // groups)):
+            raise ValueError("groups (at most 32) must divide the experts, group_top be 1 or 2 and at most a group's experts, and the "
+                             "topk_groups best groups hold topk experts")
+        return dev, T, E, _ROUTE(logits.data_ptr(), _dt_code(logits), _SCORES[score], T, E, ld, topk, groups, topk_groups, group_top,
+                                 _ptr(bias) or 0, 1 if renormalize else 0, scale)
+
+    def _route_outputs(self, logits, topk, dev, ids, weights):
+        T = logits.shape[0]
+        if ids is None:
+            ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+        if weights is None:
+            weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+        _same_device(dev, ids, weights)
+        _check_int32(ids, T * topk, "ids")
+        _check_values(weights, torch.float32, T * topk, "weights", "tokens * topk")
+        return ids, weights
+
+    def plan_moe_route(self, logits: torch.Tensor, topk: int, ids: torch.Tensor, weights: torch.Tensor,
+                       bias: Optional[torch.Tensor] = None, score: str = "softmax", groups: int = 1, topk_groups: int = 1,
+                       group_top: int = 1, renormalize: bool = True, scale: float = 1.0) -> "Call":
+        dev, _, _, p = self._route_args(logits, topk, bias, score, groups, topk_groups, group_top, renormalize, scale)
+        self._route_outputs(logits, topk, dev, ids, weights)
+        return Call(self, self.L.mxq_moe_route, (p, ids.data_ptr(), weights.data_ptr(), _raw_stream(dev)), "mxq_moe_route",
+                    (logits, bias, ids, weights), logits.device)
+
+    def moe_route(self, logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, score: str = "softmax", groups: int = 1,
+                  topk_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+        """A router's logits [tokens, experts] to (ids int32, weights fp32),
+        both [tokens, topk]: the topk experts with the largest score + bias
+        among the topk_groups best groups (a group counts the sum of its
+        group_top largest), and scale times their scores, divided by their sum
+        if ``renormalize``."""
+        dev, _, _, p = self._route_args(logits, topk, bias, score, groups, topk_groups, group_top, renormalize, scale)
+        ids, weights = self._route_outputs(logits, topk, dev, None, None)
+        self._call(self.L.mxq_moe_route, (p, ids.data_ptr(), weights.data_ptr(), _raw_stream(dev)), "mxq_moe_route", dev)
+        return ids, weights
+
+    def _route_grad_args(self, g, logits, ids, score, renormalize, scale, d_logits):
+        if ids.dim() != 2:
+            raise ValueError("ids must be [tokens, topk]")
+        topk = ids.shape[1]
+        dev, T, E, p = self._route_args(logits, topk, None, score, 1, 1, 1, renormalize, scale)
+        _same_device(dev, g, ids)
+        _check_int32(ids, T * topk, "ids")
+        _check_values(g, torch.float32, T * topk, "g", "tokens * topk")
+        d_logits = _row_output(d_logits, T, E, logits, "d_logits", dev)
+        return (g.data_ptr(), p, ids.data_ptr(), d_logits.data_ptr(), _raw_stream(dev)), d_logits
+
+    def plan_moe_route_grad(self, g: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, d_logits: torch.Tensor,
+                            score: str = "softmax", renormalize: bool = True, scale: float = 1.0) -> "Call":
+        args, d_logits = self._route_grad_args(g, logits, ids, score, renormalize, scale, d_logits)
+        return Call(self, self.L.mxq_moe_route_grad, args, "mxq_moe_route_grad", (g, logits, ids, d_logits), logits.device)
+
+    def moe_route_grad(self, g: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                       renormalize: bool = True, scale: float = 1.0, d_logits: Optional[torch.Tensor] = None):
+        """Gradient of the logits (their dtype) for the gradient g (fp32
+        [tokens, topk]) of moe_route's weights; the choice is constant."""
+        args, d_logits = self._route_grad_args(g, logits, ids, score, renormalize, scale, d_logits)
+        self._call(self.L.mxq_moe_route_grad, args, "mxq_moe_route_grad", logits.get_device())
+        return d_logits
+
+    def _gate_args(self, form, x, out, scales):
+        """(fn, args, name, out, scales) of silu_mul; form None, "1x128" or "128x1"."""
+        dev = _cuda_index(x)
+        rows, H2, ldx = _matrix(x, "x")
+        if H2 % 2:
+            raise ValueError("x must hold two halves of one size in its last dimension")
+        H = H2 // 2
+        dt = torch.uint8 if form else x.dtype
+        if out is None:
+            out = torch.empty((rows, H) if form == "128x1" else x.shape[:-1] + (H,), dtype=dt, device=x.device)
+        else:
+            _same_device(dev, out)
+            _check_values(out, dt, rows * H, "data" if form else "out", "rows * H")
+        name = _GATE_FORMS[form]
+        args = (x.data_ptr(), _dt_code(x), rows, H, ldx, out.data_ptr())
+        if form:
+            shape = (_blocks(rows), H) if form == "128x1" else x.shape[:-1] + (_blocks(H),)
+            if scales is None:
+                scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+            else:
+                _same_device(dev, scales)
+                _check_values(scales, torch.uint8, math.prod(shape), "scales",
+                              "ceil(rows/128) * H" if form == "128x1" else "rows * ceil(H/128)")
+            args += (scales.data_ptr(),)
+        return getattr(self.L, name), args + (_raw_stream(dev),), name, out, scales
+
+    def plan_silu_mul(self, x: torch.Tensor, out: torch.Tensor) -> "Call":
+        fn, args, name, *_ = self._gate_args(None, x, out, None)
+        return Call(self, fn, args, name, (x, out), x.device)
+
+    def plan_fp8_silu_mul_1x128(self, x: torch.Tensor, data: torch.Tensor, scales: torch.Tensor) -> "Call":
+        fn, args, name, *_ = self._gate_args("1x128", x, data, scales)
+        return Call(self, fn, args, name, (x, data, scales), x.device)
+
+    def plan_fp8_silu_mul_128x1(self, x: torch.Tensor, data: torch.Tensor, scales: torch.Tensor) -> "Call":
+        fn, args, name, *_ = self._gate_args("128x1", x, data, scales)
+        return Call(self, fn, args, name, (x, data, scales), x.device)
+
+    def silu_mul(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """silu(gate) * up in x's dtype, gate and up the halves of x's last dimension."""
+        fn, args, name, out, _ = self._gate_args(None, x, out, None)
+        self._call(fn, args, name, x.get_device())
+        return out
+
+    def fp8_silu_mul_1x128(self, x: torch.Tensor, data: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+        """silu(gate) * up as fp8_quant_1x128 quantizes: (E4M3 bytes
+        (*shape[:-1], H), UE8M0 codes (*shape[:-1], ceil(H/128)))."""
+        fn, args, name, data, scales = self._gate_args("1x128", x, data, scales)
+        self._call(fn, args, name, x.get_device())
+        return data, scales
+
+    def fp8_silu_mul_128x1(self, x: torch.Tensor, data: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+        """silu(gate) * up as fp8_quant_128x1 quantizes: (E4M3 bytes [rows,
+        H], UE8M0 codes [ceil(rows/128), H])."""
+        fn, args, name, data, scales = self._gate_args("128x1", x, data, scales)
+        self._call(fn, args, name, x.get_device())
+        return data, scales
+
+    def _gate_grad_args(self, g, x, d_x):
+        dev = _cuda_index(x)
+        rows, H2, ldx = _matrix(x, "x")
+        if H2 % 2:
+            raise ValueError("x must hold two halves of one size in its last dimension")
+        ldg = _like_rows(g, x, rows, H2 // 2, "g", dev)
+        if d_x is None:
+            d_x = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _same_device(dev, d_x)
+            _check_values(d_x, x.dtype, rows * H2, "d_x", "rows * 2H")
+        return (g.data_ptr(), x.data_ptr(), _dt_code(x), rows, H2 // 2, ldg, ldx, d_x.data_ptr(), _raw_stream(dev)), d_x
+
+    def plan_silu_mul_grad(self, g: torch.Tensor, x: torch.Tensor, d_x: torch.Tensor) -> "Call":
+        args, d_x = self._gate_grad_args(g, x, d_x)
+        return Call(self, self.L.mxq_silu_mul_grad, args, "mxq_silu_mul_grad", (g, x, d_x), x.device)
+
+    def silu_mul_grad(self, g: torch.Tensor, x: torch.Tensor, d_x: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Gradient of x for the gradient g of silu_mul's result."""
+        args, d_x = self._gate_grad_args(g, x, d_x)
+        self._call(self.L.mxq_silu_mul_grad, args, "mxq_silu_mul_grad", x.get_device())
+        return d_x
+
 
 class Call:
     """A prepared libmxq call (see Library.plan_*)."""
@@ -1081,6 +1415,42 @@ def mxq_moe_combine(y, slots, weights, out=None):
 
 def mxq_moe_combine_grad(g, y, source, slots, weights):
     return library().moe_combine_grad(g, y, source, slots, weights)
+
+
+def mxq_fp8_dispatch(data, scales, source, topk, out=None, out_scales=None):
+    return library().fp8_dispatch(data, scales, source, topk, out, out_scales)
+
+
+def mxq_rmsnorm(x, weight, residual=None, eps=1e-6, quantized=True, normed=False, stats=False, h=None):
+    return library().rmsnorm(x, weight, residual, eps, quantized, normed, stats, h)
+
+
+def mxq_rmsnorm_grad(g, h, weight, rstd, g_h=None, weight_grad=True, d_h=None):
+    return library().rmsnorm_grad(g, h, weight, rstd, g_h, weight_grad, d_h)
+
+
+def mxq_moe_route(logits, topk, bias=None, score="softmax", groups=1, topk_groups=1, group_top=1, renormalize=True, scale=1.0):
+    return library().moe_route(logits, topk, bias, score, groups, topk_groups, group_top, renormalize, scale)
+
+
+def mxq_moe_route_grad(g, logits, ids, score="softmax", renormalize=True, scale=1.0, d_logits=None):
+    return library().moe_route_grad(g, logits, ids, score, renormalize, scale, d_logits)
+
+
+def mxq_silu_mul(x, out=None):
+    return library().silu_mul(x, out)
+
+
+def mxq_fp8_silu_mul_1x128(x, data=None, scales=None):
+    return library().fp8_silu_mul_1x128(x, data, scales)
+
+
+def mxq_fp8_silu_mul_128x1(x, data=None, scales=None):
+    return library().fp8_silu_mul_128x1(x, data, scales)
+
+
+def mxq_silu_mul_grad(g, x, d_x=None):
+    return library().silu_mul_grad(g, x, d_x)
 
 
 def mxq_scale_bytes(rows, K, layout="compact"):

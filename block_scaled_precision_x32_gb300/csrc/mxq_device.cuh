@@ -75,6 +75,38 @@ __device__ __forceinline__ uint32_t f32_min(uint32_t a, uint32_t b) {
     asm("min.f32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+// The same on floats, so that nothing is contracted or flushed in any build.
+__device__ __forceinline__ float fmul(float a, float b) {
+    float d;
+    asm("mul.rn.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float fadd(float a, float b) {
+    float d;
+    asm("add.rn.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float ffma(float a, float b, float c) {
+    float d;
+    asm("fma.rn.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float fdiv(float a, float b) {
+    float d;
+    asm("div.rn.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float fsqrt(float a) {
+    float d;
+    asm("sqrt.rn.f32 %0, %1;" : "=f"(d) : "f"(a));
+    return d;
+}
+// Two fp32 values -> bf16x2, round to nearest even; `hi` goes to bits 31..16.
+__device__ __forceinline__ uint32_t bf16x2_from_f32(float hi, float lo) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
 // Two fp32 values -> two E4M3 bytes, round to nearest even, subnormals
 // included; `hi` goes to bits 15..8, `lo` to bits 7..0.
 __device__ __forceinline__ uint32_t e4m3x2_from_f32(uint32_t hi, uint32_t lo) {

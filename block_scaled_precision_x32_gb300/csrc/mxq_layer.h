@@ -63,6 +63,69 @@ struct MoeRowsArgs {
     float* d_weights;  // combine's gradient only
 };
 
+struct MoeFp8Args {
+    const uint8_t* data;    // [T, ld]
+    const uint8_t* scales;  // [T, nb]
+    int64_t T, topk, R, K, nb, ld;
+    const int32_t* source;
+    uint8_t* out;         // [R, K]
+    uint8_t* out_scales;  // [R, nb]
+};
+
+struct NormArgs {
+    const void* x;
+    const void* residual;  // optional
+    const void* weight;
+    Elt weight_elt;
+    int64_t rows, K, ldx, ldr, ldh;
+    float eps;
+    void* h;          // optional, with a residual
+    void* y;          // optional, contiguous
+    uint8_t* data;    // optional, with scales
+    uint8_t* scales;  // [rows, ceil(K/128)]
+    float* rstd;      // optional
+};
+
+// Sums over rows that the blocks of the norm's gradient leave for its second
+// kernel, at most: two blocks to each of a GB300's 152 multiprocessors.
+constexpr int64_t kNormParts = 304;
+
+struct NormGradArgs {
+    const void *g, *h, *weight;
+    Elt weight_elt;
+    const float* rstd;
+    const void* g_h;  // optional
+    int64_t rows, K, ldg, ldh, ldgh, ldd;
+    void* d_h;
+    float* d_weight;  // optional, with parts
+    float* parts;     // workspace [min(rows, kNormParts), K]
+};
+
+enum class GateForm { PLAIN, ROWS, COLUMNS, GRAD };
+
+struct GateArgs {
+    const void* x;  // [rows, ldx]: gate in columns 0..H-1, up in H..2H-1
+    int64_t rows, H, ldx;
+    const void* g;  // GRAD: [rows, ldg]
+    int64_t ldg;
+    void* out;        // PLAIN: [rows, H]; GRAD: [rows, 2H]
+    uint8_t* data;    // ROWS, COLUMNS: [rows, H]
+    uint8_t* scales;  // ROWS: [rows, ceil(H/128)]; COLUMNS: [ceil(rows/128), H]
+};
+
+struct RouteArgs {
+    const void* logits;  // [T, ld]
+    int64_t T, ld;
+    int E, topk, groups, topk_groups, group_top;
+    bool sigmoid, renorm;
+    float scale;
+    const float* bias;  // optional
+    int32_t* ids;       // [T, topk]; the gradient reads them
+    float* weights;     // [T, topk]
+    const float* g;     // gradient: of the weights
+    void* d_logits;     // gradient: [T, E]
+};
+
 // Each returns cudaSuccess or the launch error.
 cudaError_t launch_quant128(Elt elt, bool columns, const Quant128Args& a, cudaStream_t s);
 cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t s);
@@ -71,6 +134,11 @@ cudaError_t launch_repack(const uint8_t* src, int64_t ld, int64_t rows, int64_t 
 int64_t moe_sort_chunks(int64_t choices);
 cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s);
 cudaError_t launch_moe_dispatch(Elt elt, const MoeRowsArgs& a, cudaStream_t s);
+cudaError_t launch_moe_dispatch_fp8(const MoeFp8Args& a, cudaStream_t s);
+cudaError_t launch_norm(Elt elt, const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_grad(Elt elt, const NormGradArgs& a, cudaStream_t s);
+cudaError_t launch_gate(Elt elt, GateForm form, const GateArgs& a, cudaStream_t s);
+cudaError_t launch_route(Elt elt, bool grad, const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_moe_combine(Elt elt, const MoeRowsArgs& a, cudaStream_t s);
 cudaError_t launch_moe_combine_grad(Elt elt, const MoeRowsArgs& a, cudaStream_t s);
 

@@ -315,4 +315,217 @@ mxq_status mxq_moe_combine_grad(const void* g, const void* y, mxq_dtype dt, int6
     return launch_status(mxq::launch_moe_combine_grad(elt_of(dt), a, stream));
 }
 
+mxq_status mxq_fp8_dispatch(const uint8_t* data, const uint8_t* scales, int64_t tokens, int64_t K, int64_t ld,
+                            const int32_t* source, int64_t topk, int64_t rows, uint8_t* out, uint8_t* out_scales,
+                            cudaStream_t stream) {
+    if (!valid_dim(tokens) || !valid_dim(K) || !valid_dim(rows) || !valid_ld(K, ld) || topk < 1 || topk > kMaxDim)
+        return MXQ_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return MXQ_OK;
+    if ((tokens > 0 && (!data || !scales)) || !source || !out || !out_scales || !aligned(source, 4)) return MXQ_ERR_INVALID_ARG;
+    mxq::MoeFp8Args a{};
+    a.data = data;
+    a.scales = scales;
+    a.T = tokens;
+    a.topk = topk;
+    a.R = rows;
+    a.K = K;
+    a.nb = blocks(K);
+    a.ld = ld;
+    a.source = source;
+    a.out = out;
+    a.out_scales = out_scales;
+    return launch_status(mxq::launch_moe_dispatch_fp8(a, stream));
+}
+
+// ---- the norm
+
+mxq_status mxq_rmsnorm(const mxq_norm* p, cudaStream_t stream) {
+    if (!p) return MXQ_ERR_INVALID_ARG;
+    mxq_status st = check_dtype(p->dt);
+    if (st != MXQ_OK) return st;
+    st = check_dtype(p->weight_dt);
+    if (st != MXQ_OK) return st;
+    if (!valid_dim(p->rows) || !valid_dim(p->K) || !valid_ld(p->K, p->ldx) || !(p->eps >= 0.0f && p->eps <= 3.4e38f))
+        return MXQ_ERR_INVALID_ARG;
+    if ((p->residual && !valid_ld(p->K, p->ldr)) || (p->h && (!p->residual || !valid_ld(p->K, p->ldh))) || !p->data != !p->scales)
+        return MXQ_ERR_INVALID_ARG;
+    if (p->rows == 0 || p->K == 0) return MXQ_OK;
+    const size_t es = elt_size(p->dt);
+    if (!p->x || !p->weight || !aligned(p->x, es) || !aligned(p->residual, es) || !aligned(p->weight, elt_size(p->weight_dt)) ||
+        !aligned(p->h, es) || !aligned(p->y, es) || !aligned(p->rstd, 4))
+        return MXQ_ERR_INVALID_ARG;
+    // in place: the same rows
+    if (p->rows > 1 && ((p->h == p->x && p->h && p->ldh != p->ldx) || (p->h && p->h == p->residual && p->ldh != p->ldr)))
+        return MXQ_ERR_INVALID_ARG;
+    if (!p->h && !p->y && !p->data && !p->rstd) return MXQ_OK;
+    mxq::NormArgs a{};
+    a.x = p->x;
+    a.residual = p->residual;
+    a.weight = p->weight;
+    a.weight_elt = elt_of(p->weight_dt);
+    a.rows = p->rows;
+    a.K = p->K;
+    a.ldx = p->ldx;
+    a.ldr = p->ldr;
+    a.ldh = p->ldh;
+    a.eps = p->eps;
+    a.h = p->h;
+    a.y = p->y;
+    a.data = p->data;
+    a.scales = p->scales;
+    a.rstd = p->rstd;
+    return launch_status(mxq::launch_norm(elt_of(p->dt), a, stream));
+}
+
+size_t mxq_rmsnorm_grad_workspace(int64_t rows, int64_t K) {
+    if (!valid_dim(rows) || !valid_dim(K)) return 0;
+    return (size_t)((rows < mxq::kNormParts ? rows : mxq::kNormParts) * K) * 4;
+}
+
+mxq_status mxq_rmsnorm_grad(const mxq_norm_grad* p, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!p) return MXQ_ERR_INVALID_ARG;
+    mxq_status st = check_dtype(p->dt);
+    if (st != MXQ_OK) return st;
+    st = check_dtype(p->weight_dt);
+    if (st != MXQ_OK) return st;
+    if (!valid_dim(p->rows) || !valid_dim(p->K) || !valid_ld(p->K, p->ldg) || !valid_ld(p->K, p->ldh) ||
+        (p->g_h && !valid_ld(p->K, p->ldgh)) || !valid_ld(p->K, p->ldd) || !aligned(p->d_weight, 4))
+        return MXQ_ERR_INVALID_ARG;
+    if (p->K == 0) return MXQ_OK;
+    if (p->rows == 0)
+        return p->d_weight ? launch_status(cudaMemsetAsync(p->d_weight, 0, (size_t)p->K * 4, stream)) : MXQ_OK;
+    const size_t es = elt_size(p->dt);
+    if (!p->g || !p->h || !p->weight || !p->rstd || !p->d_h || !aligned(p->g, es) || !aligned(p->h, es) ||
+        !aligned(p->weight, elt_size(p->weight_dt)) || !aligned(p->rstd, 4) || !aligned(p->g_h, es) || !aligned(p->d_h, es))
+        return MXQ_ERR_INVALID_ARG;
+    if (p->rows > 1 && ((p->d_h == p->g && p->ldd != p->ldg) || (p->d_h == p->h && p->ldd != p->ldh) ||
+                        (p->d_h == p->g_h && p->ldd != p->ldgh)))
+        return MXQ_ERR_INVALID_ARG;
+    const size_t need = p->d_weight ? mxq_rmsnorm_grad_workspace(p->rows, p->K) : 0;
+    if (need && (!workspace || workspace_bytes < need)) return MXQ_ERR_BUFFER_TOO_SMALL;
+    if (need && !aligned(workspace, 16)) return MXQ_ERR_INVALID_ARG;
+    mxq::NormGradArgs a{};
+    a.g = p->g;
+    a.h = p->h;
+    a.weight = p->weight;
+    a.weight_elt = elt_of(p->weight_dt);
+    a.rstd = p->rstd;
+    a.g_h = p->g_h;
+    a.rows = p->rows;
+    a.K = p->K;
+    a.ldg = p->ldg;
+    a.ldh = p->ldh;
+    a.ldgh = p->ldgh;
+    a.ldd = p->ldd;
+    a.d_h = p->d_h;
+    a.d_weight = p->d_weight;
+    a.parts = need ? static_cast<float*>(workspace) : nullptr;
+    return launch_status(mxq::launch_norm_grad(elt_of(p->dt), a, stream));
+}
+
+// ---- the gated activation
+
+static mxq_status gate(mxq::GateForm form, const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx, const void* g, int64_t ldg,
+                       void* out, uint8_t* data, uint8_t* scales, cudaStream_t stream) {
+    const mxq_status st = check_dtype(dt);
+    if (st != MXQ_OK) return st;
+    const bool grad = form == mxq::GateForm::GRAD, quant = form == mxq::GateForm::ROWS || form == mxq::GateForm::COLUMNS;
+    if (!valid_dim(rows) || H < 0 || H > kMaxDim / 2 || !valid_ld(2 * H, ldx) || (grad && !valid_ld(H, ldg))) return MXQ_ERR_INVALID_ARG;
+    if (rows == 0 || H == 0) return MXQ_OK;
+    const size_t es = elt_size(dt);
+    if (!x || !aligned(x, es) || (grad && (!g || !aligned(g, es)))) return MXQ_ERR_INVALID_ARG;
+    if (quant ? (!data || !scales) : (!out || !aligned(out, es))) return MXQ_ERR_INVALID_ARG;
+    mxq::GateArgs a{};
+    a.x = x;
+    a.rows = rows;
+    a.H = H;
+    a.ldx = ldx;
+    a.g = g;
+    a.ldg = ldg;
+    a.out = out;
+    a.data = data;
+    a.scales = scales;
+    return launch_status(mxq::launch_gate(elt_of(dt), form, a, stream));
+}
+
+mxq_status mxq_silu_mul(const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx, void* out, cudaStream_t stream) {
+    return gate(mxq::GateForm::PLAIN, x, dt, rows, H, ldx, nullptr, 0, out, nullptr, nullptr, stream);
+}
+
+mxq_status mxq_fp8_silu_mul_1x128(const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx, uint8_t* data,
+                                  uint8_t* scales, cudaStream_t stream) {
+    return gate(mxq::GateForm::ROWS, x, dt, rows, H, ldx, nullptr, 0, nullptr, data, scales, stream);
+}
+
+mxq_status mxq_fp8_silu_mul_128x1(const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx, uint8_t* data,
+                                  uint8_t* scales, cudaStream_t stream) {
+    return gate(mxq::GateForm::COLUMNS, x, dt, rows, H, ldx, nullptr, 0, nullptr, data, scales, stream);
+}
+
+mxq_status mxq_silu_mul_grad(const void* g, const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldg, int64_t ldx,
+                             void* d_x, cudaStream_t stream) {
+    return gate(mxq::GateForm::GRAD, x, dt, rows, H, ldx, g, ldg, d_x, nullptr, nullptr, stream);
+}
+
+// ---- the router
+
+static bool valid_route(int64_t tokens, int64_t experts, int64_t ld, int64_t topk, int score, float scale) {
+    return valid_dim(tokens) && experts >= 1 && experts <= 1024 && valid_ld(experts, ld) && topk >= 1 && topk <= 32 && topk <= experts &&
+           tokens <= kMaxDim / topk && (score == MXQ_SCORE_SOFTMAX || score == MXQ_SCORE_SIGMOID) && scale >= -3.4e38f && scale <= 3.4e38f;
+}
+
+mxq_status mxq_moe_route(const mxq_route* p, int32_t* ids, float* weights, cudaStream_t stream) {
+    if (!p) return MXQ_ERR_INVALID_ARG;
+    const mxq_status st = check_dtype(p->dt);
+    if (st != MXQ_OK) return st;
+    if (!valid_route(p->tokens, p->experts, p->ld, p->topk, p->score, p->scale)) return MXQ_ERR_INVALID_ARG;
+    if (p->groups < 1 || p->groups > 32 || p->experts % p->groups || p->topk_groups < 1 || p->topk_groups > p->groups || p->group_top < 1 ||
+        p->group_top > 2 || p->group_top > p->experts / p->groups || p->topk > p->topk_groups * (p->experts / p->groups))
+        return MXQ_ERR_INVALID_ARG;
+    if (p->tokens == 0) return MXQ_OK;
+    if (!p->logits || !aligned(p->logits, elt_size(p->dt)) || !aligned(p->bias, 4) || !ids || !aligned(ids, 4) || !weights ||
+        !aligned(weights, 4))
+        return MXQ_ERR_INVALID_ARG;
+    mxq::RouteArgs a{};
+    a.logits = p->logits;
+    a.T = p->tokens;
+    a.ld = p->ld;
+    a.E = (int)p->experts;
+    a.topk = (int)p->topk;
+    a.groups = (int)p->groups;
+    a.topk_groups = (int)p->topk_groups;
+    a.group_top = (int)p->group_top;
+    a.sigmoid = p->score == MXQ_SCORE_SIGMOID;
+    a.renorm = p->renormalize != 0;
+    a.scale = p->scale;
+    a.bias = p->bias;
+    a.ids = ids;
+    a.weights = weights;
+    return launch_status(mxq::launch_route(elt_of(p->dt), false, a, stream));
+}
+
+mxq_status mxq_moe_route_grad(const float* g, const mxq_route* p, const int32_t* ids, void* d_logits, cudaStream_t stream) {
+    if (!p) return MXQ_ERR_INVALID_ARG;
+    const mxq_status st = check_dtype(p->dt);
+    if (st != MXQ_OK) return st;
+    if (!valid_route(p->tokens, p->experts, p->ld, p->topk, p->score, p->scale)) return MXQ_ERR_INVALID_ARG;
+    if (p->tokens == 0) return MXQ_OK;
+    const size_t es = elt_size(p->dt);
+    if (!g || !aligned(g, 4) || !p->logits || !aligned(p->logits, es) || !ids || !aligned(ids, 4) || !d_logits || !aligned(d_logits, es))
+        return MXQ_ERR_INVALID_ARG;
+    mxq::RouteArgs a{};
+    a.logits = p->logits;
+    a.T = p->tokens;
+    a.ld = p->ld;
+    a.E = (int)p->experts;
+    a.topk = (int)p->topk;
+    a.sigmoid = p->score == MXQ_SCORE_SIGMOID;
+    a.renorm = p->renormalize != 0;
+    a.scale = p->scale;
+    a.ids = const_cast<int32_t*>(ids);
+    a.g = g;
+    a.d_logits = d_logits;
+    return launch_status(mxq::launch_route(elt_of(p->dt), true, a, stream));
+}
+
 }  // extern "C"

@@ -5,6 +5,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "mxq_device.cuh"
 #include "mxq_layer.h"
@@ -270,6 +271,28 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
     }
 }
 
+// Quantized rows to the experts' order, K payload bytes and nb scale codes of
+// each, in pieces of BYTES; one row to blockIdx.x, a slice of its pieces to
+// blockIdx.y.
+template <int BYTES>
+__global__ void __launch_bounds__(kRowThreads) dispatch_fp8_kernel(MoeFp8Args a) {
+    let_next_start();
+    wait_for_stream();
+    using W = typename std::conditional<BYTES == 16, uint4, typename std::conditional<BYTES == 4, uint32_t, uint8_t>::type>::type;
+    const int64_t pieces = a.K / BYTES;
+    for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
+        const int c = a.source[r];
+        const int64_t t = c < 0 ? -1 : c / a.topk;
+        const bool there = t >= 0 && t < a.T;
+        const W* from = reinterpret_cast<const W*>(a.data + (there ? t * a.ld : 0));
+        W* to = reinterpret_cast<W*>(a.out + r * a.K);
+        for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.y * kRowThreads)
+            to[i] = there ? from[i] : W{};
+        for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < a.nb; i += (int64_t)gridDim.y * kRowThreads)
+            a.out_scales[r * a.nb + i] = there ? a.scales[t * a.nb + i] : 0;
+    }
+}
+
 // out[t] = sum_j w_j y[slot_j]: one token to blockIdx.x, a slice of its pieces
 // to blockIdx.y; the rows of four choices are loaded before they are added.
 // Memory-bound; four blocks a multiprocessor, or the loads in flight do not
@@ -439,6 +462,15 @@ cudaError_t rows_launch(int what, Elt elt, const MoeRowsArgs& a, cudaStream_t s)
     return e;
 }
 
+cudaError_t dispatch_fp8(const MoeFp8Args& a, cudaStream_t s) {
+    const auto on = [&](int64_t n) {
+        return (reinterpret_cast<uintptr_t>(a.data) | reinterpret_cast<uintptr_t>(a.out)) % n == 0 && a.K % n == 0 && (a.T <= 1 || a.ld % n == 0);
+    };
+    if (on(16)) return launch_overlapped(dispatch_fp8_kernel<16>, row_grid(a.R, a.K / 16), kRowThreads, 0, 0, s, a);
+    if (on(4)) return launch_overlapped(dispatch_fp8_kernel<4>, row_grid(a.R, a.K / 4), kRowThreads, 0, 0, s, a);
+    return launch_overlapped(dispatch_fp8_kernel<1>, row_grid(a.R, a.K), kRowThreads, 0, 0, s, a);
+}
+
 }  // namespace
 
 int64_t moe_sort_chunks(int64_t choices) { return ceil_div(choices, kChunk); }
@@ -464,6 +496,11 @@ cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_moe_dispatch(Elt elt, const MoeRowsArgs& a, cudaStream_t s) { return rows_launch(0, elt, a, s); }
+cudaError_t launch_moe_dispatch_fp8(const MoeFp8Args& a, cudaStream_t s) {
+    const cudaError_t e = dispatch_fp8(a, s);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
 cudaError_t launch_moe_combine(Elt elt, const MoeRowsArgs& a, cudaStream_t s) { return rows_launch(1, elt, a, s); }
 cudaError_t launch_moe_combine_grad(Elt elt, const MoeRowsArgs& a, cudaStream_t s) { return rows_launch(2, elt, a, s); }
 

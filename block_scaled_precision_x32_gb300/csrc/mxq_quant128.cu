@@ -1,34 +1,14 @@
 // mxq_quant128.cu -- activations and gradients to E4M3 with one power-of-two
 // scale per 128 elements, along the rows (1x128) or down the columns (128x1).
-//
-// For a block with largest magnitude amax = (1 + f) 2^E the scale is the
-// least power of two that keeps amax / 2^s within E4M3's largest value
-// 448 = 1.75 * 2^8: s = E - 8, and one more if f > 0.75.
 #include <cuda_bf16.h>
 
 #include "mxq_device.cuh"
+#include "mxq_e4m3.cuh"
 #include "mxq_layer.h"
 #include "mxq_launch.cuh"
 
 namespace mxq {
 namespace {
-
-// UE8M0 code of a block from the bits of its fp32 amax; 255 for NaN and Inf.
-__device__ __forceinline__ uint32_t scale_code128(uint32_t amax) {
-    const int E = (int)(amax >> 23);
-    if (E == 255) return 255u;
-    const int s = E - 135 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return (uint32_t)(max(s, -127) + 127);  // s <= 120: no upper clamp is reached
-}
-
-// 2^-s for a code below 255: s in [-127, 120].
-__device__ __forceinline__ uint32_t inv_scale128(uint32_t code) { return (254u - code) << 23; }
-
-template <Elt ELT>
-__device__ __forceinline__ uint32_t load_f32(const void* x, int64_t i) {
-    if constexpr (ELT == Elt::BF16) return (uint32_t)static_cast<const uint16_t*>(x)[i] << 16;
-    return static_cast<const uint32_t*>(x)[i];
-}
 
 // Source row of output row r, -1 for a row of zeros.
 __device__ __forceinline__ int64_t source_row(const Quant128Args& a, int64_t r) {
@@ -37,29 +17,6 @@ __device__ __forceinline__ int64_t source_row(const Quant128Args& a, int64_t r) 
     const int64_t t = i < 0 ? -1 : i / a.index_div;
     return t < a.rows ? t : -1;
 }
-
-// 16 consecutive elements as fp32 patterns, 32-byte loads.
-template <Elt ELT>
-struct Unit {
-    uint32_t w[ELT == Elt::BF16 ? 8 : 16];
-
-    __device__ __forceinline__ void load(const void* x, int64_t i) {
-        if constexpr (ELT == Elt::BF16) {
-            ld32(w, static_cast<const uint16_t*>(x) + i);
-        } else {
-            ld32(reinterpret_cast<uint32_t(&)[8]>(w[0]), static_cast<const uint32_t*>(x) + i);
-            ld32(reinterpret_cast<uint32_t(&)[8]>(w[8]), static_cast<const uint32_t*>(x) + i + 8);
-        }
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (uint32_t& v : w) v = 0;
-    }
-    __device__ __forceinline__ uint32_t at(int i) const {
-        if constexpr (ELT == Elt::BF16) return i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16;
-        return w[i];
-    }
-};
 
 // Rows of 16-element units, eight lanes to a 1x128 block: 32 bytes (bf16) or
 // 64 (fp32) of loads and one 16-byte store a lane, the block's maximum by
@@ -262,16 +219,14 @@ __global__ void __launch_bounds__(512) quant_columns_kernel(Quant128Args a) {
                 code == 255u ? 0x7F : (uint8_t)e4m3x2_from_f32(0u, f32_mul(v[i], inv_scale128(code)));
 }
 
-bool on(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-
 template <Elt ELT>
 cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
     constexpr int64_t es = ELT == Elt::BF16 ? 2 : 4;
     const bool one_row = a.rows <= 1;  // then the stride is not used
     if (columns) {
         // 8 columns: 16 bytes of bf16, 32 of fp32, 8 of payload and scales
-        const bool tiled = a.K % 8 == 0 && on(a.x, 8 * es) && (one_row || a.ldx * es % (8 * es) == 0) && on(a.data, 8) &&
-                           on(a.scales, 8);
+        const bool tiled = a.K % 8 == 0 && on_bytes(a.x, 8 * es) && (one_row || a.ldx * es % (8 * es) == 0) && on_bytes(a.data, 8) &&
+                           on_bytes(a.scales, 8);
         // blockIdx.y reaches 65535: 2^23 rows at a time
         for (int64_t r0 = 0; r0 < a.out_rows; r0 += INT64_C(128) * 65535) {
             Quant128Args p = a;
@@ -296,7 +251,7 @@ cudaError_t launch(bool columns, const Quant128Args& a, cudaStream_t s) {
     const int64_t nb = ceil_div(a.K, 128);
     if (ceil_div(a.out_rows * nb, 8) > INT64_C(0x7FFFFFFF)) return cudaErrorInvalidValue;  // over 2 TB of elements
     // units of 16 elements: 32-byte loads and 16-byte stores
-    if (a.K % 16 == 0 && on(a.x, 32) && (one_row || a.ldx * es % 32 == 0) && on(a.data, 16)) {
+    if (a.K % 16 == 0 && on_bytes(a.x, 32) && (one_row || a.ldx * es % 32 == 0) && on_bytes(a.data, 16)) {
         return launch_overlapped(quant_rows_unit_kernel<ELT>, dim3((unsigned)ceil_div(a.out_rows * nb * 8, 256)), 256, 0, 0, s, a,
                                  nb);
     }

@@ -433,6 +433,145 @@ MXQ_API mxq_status mxq_moe_combine_grad(const void* g, const void* y, mxq_dtype 
                                         const int32_t* slots, const float* weights, void* d_rows, float* d_weights,
                                         cudaStream_t stream);
 
+/* Quantized token rows to the sorted order: out[r] and out_scales[r] are those
+ * of token source[r] / topk, zeros (a block of zeros: code 0) where source[r]
+ * is negative or leaves the tokens.  What mxq_fp8_quant_1x128 with `index`
+ * gives, for rows that are quantized already: each token is rounded once.
+ *   data:   [tokens, ld] E4M3 bytes; scales: [tokens, ceil(K/128)] codes.
+ *   source: int32 [rows], of mxq_moe_sort; topk >= 1.
+ *   out:    [rows, K]; out_scales: [rows, ceil(K/128)].
+ * Errors: INVALID_ARG. */
+MXQ_API mxq_status mxq_fp8_dispatch(const uint8_t* data, const uint8_t* scales, int64_t tokens, int64_t K, int64_t ld,
+                                    const int32_t* source, int64_t topk, int64_t rows, uint8_t* out,
+                                    uint8_t* out_scales, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * What stands between those products in a transformer's mixture-of-experts
+ * block: the norm in front of it, the router, the gated activation.
+ * Arithmetic, sums and statistics are fp32, with one rounding to the result's
+ * type; none of these calls uses atomics, and results do not depend on the
+ * order in which blocks of the grid run.
+ * ------------------------------------------------------------------------ */
+
+/* Root-mean-square norm of x plus a residual:
+ *   h = RN(x + residual) in dt (h = x without one)
+ *   rstd = 1 / sqrt(mean_k h_k^2 + eps)
+ *   y_k = (h_k * rstd) * weight_k
+ * and y as the operand of the next product, as mxq_fp8_quant_1x128 quantizes,
+ * from the fp32 y, which is not rounded to dt before.  A row that holds a NaN
+ * comes out NaN; one whose squares overflow fp32 (an infinity among them) has
+ * rstd = 0. */
+typedef struct {
+    mxq_dtype dt;          /* x, residual, h, y */
+    mxq_dtype weight_dt;
+    int64_t rows, K;
+    const void* x;         /* [rows, ldx] */
+    int64_t ldx;
+    const void* residual;  /* [rows, ldr], or NULL */
+    int64_t ldr;
+    const void* weight;    /* [K] */
+    float eps;             /* >= 0, finite */
+    void* h;               /* [rows, ldh], or NULL: not written; only with a residual.  May be x or the residual
+                              (the same rows), any other overlap is undefined. */
+    int64_t ldh;
+    void* y;               /* [rows, K] contiguous, or NULL */
+    uint8_t* data;         /* [rows, K] E4M3 bytes, or NULL (then scales is NULL too) */
+    uint8_t* scales;       /* [rows, ceil(K/128)] UE8M0 codes */
+    float* rstd;           /* [rows], or NULL */
+} mxq_norm;
+/* Errors: INVALID_ARG, UNSUPPORTED_DTYPE. */
+MXQ_API mxq_status mxq_rmsnorm(const mxq_norm* p, cudaStream_t stream);
+
+/* Its gradient, for the gradient g of y.  With n = h * rstd:
+ *   d_h = rstd * (g * weight - n * mean_k(g * weight * n)) + g_h
+ *   d_weight = sum over the rows of g * n (fp32)
+ * d_h is the gradient of x and of the residual alike; g_h is the gradient
+ * that reaches h along the residual's path (NULL: none). */
+typedef struct {
+    mxq_dtype dt;        /* g, h, g_h, d_h */
+    mxq_dtype weight_dt;
+    int64_t rows, K;
+    const void* g;       /* [rows, ldg] */
+    int64_t ldg;
+    const void* h;       /* [rows, ldh]: the norm's h (its x without a residual) */
+    int64_t ldh;
+    const void* weight;  /* [K] */
+    const float* rstd;   /* [rows], of mxq_rmsnorm */
+    const void* g_h;     /* [rows, ldgh], or NULL */
+    int64_t ldgh;
+    void* d_h;           /* [rows, ldd].  May be g, h or g_h (the same rows), any other overlap is undefined. */
+    int64_t ldd;
+    float* d_weight;     /* [K], or NULL: not computed, no workspace needed */
+} mxq_norm_grad;
+/* workspace: mxq_rmsnorm_grad_workspace(rows, K) bytes, 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED_DTYPE, BUFFER_TOO_SMALL (workspace). */
+MXQ_API mxq_status mxq_rmsnorm_grad(const mxq_norm_grad* p, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+MXQ_API size_t mxq_rmsnorm_grad_workspace(int64_t rows, int64_t K);
+
+/* A router's logits to experts and weights.
+ *   s = softmax(logits of a token), or 1 / (1 + exp(-logit))
+ *   c = s + bias (bias chooses, it does not enter the weights)
+ * The experts are cut into `groups` equal, consecutive groups; a group's score
+ * is the sum of the group_top largest c of those of its experts that can be
+ * chosen.  Chosen are the topk largest c among the experts of the topk_groups
+ * best groups, in descending order; equal ones by the lowest index, groups too.
+ * The order is that of exact arithmetic (c that fp32 cannot tell apart are
+ * compared in 64 bits).  Weights: scale * s, or, renormalized, scale * s / (sum
+ * of the chosen s), also where the scores themselves underflow.
+ * An expert whose logit or bias is -inf cannot be chosen; where fewer than
+ * topk can, the last ids are -1 (mxq_moe_sort drops them) and their weights 0.
+ * A token with a NaN among its logits or in the bias, or an infinite
+ * softmax logit, has ids 0..topk-1 and NaN weights. */
+typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 } mxq_score;
+typedef struct {
+    const void* logits;  /* [tokens, ld] */
+    mxq_dtype dt;
+    mxq_score score;
+    int64_t tokens, experts, ld; /* experts 1 .. 1024 */
+    int64_t topk;                /* 1 .. min(32, experts that the kept groups have); tokens * topk fits in int32 */
+    int64_t groups;              /* 1 .. 32, divides experts */
+    int64_t topk_groups;         /* 1 .. groups */
+    int64_t group_top;           /* 1 or 2, at most a group's experts */
+    const float* bias;           /* fp32 [experts], or NULL */
+    int renormalize;
+    float scale;
+} mxq_route;
+/* ids: int32 [tokens, topk]; weights: fp32 [tokens, topk].
+ * Errors: INVALID_ARG, UNSUPPORTED_DTYPE. */
+MXQ_API mxq_status mxq_moe_route(const mxq_route* p, int32_t* ids, float* weights, cudaStream_t stream);
+
+/* Gradient of the weights (fp32 [tokens, topk]) with regard to the logits; the
+ * choice itself is constant.  p as in the call above, of which groups,
+ * topk_groups, group_top and bias are not looked at; ids outside
+ * 0..experts-1 have no part in it.  An id that a token has twice gets the sum.
+ *   d_logits: [tokens, experts] contiguous, in p->dt.
+ * Errors: INVALID_ARG, UNSUPPORTED_DTYPE. */
+MXQ_API mxq_status mxq_moe_route_grad(const float* g, const mxq_route* p, const int32_t* ids, void* d_logits,
+                                      cudaStream_t stream);
+
+/* Gated activation between an expert's two products: a[r, k] = silu(x[r, k]) *
+ * x[r, H + k] with silu(v) = v / (1 + exp(-v)); x [rows, ldx] holds the gate in
+ * its first H columns and the other factor in the next H (ldx >= 2H), as a
+ * product with both weights in one stack [2H, K] leaves them.
+ * mxq_silu_mul writes a in dt ([rows, H] contiguous); the fp8 forms quantize
+ * the fp32 a, as mxq_fp8_quant_1x128 does for the second product and
+ * mxq_fp8_quant_128x1 for its weight's gradient: data [rows, H]; scales [rows,
+ * ceil(H/128)] or [ceil(rows/128), H].
+ * silu(-inf) is NaN (0 * inf).
+ * Errors: INVALID_ARG, UNSUPPORTED_DTYPE. */
+MXQ_API mxq_status mxq_silu_mul(const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx, void* out,
+                                cudaStream_t stream);
+MXQ_API mxq_status mxq_fp8_silu_mul_1x128(const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx,
+                                          uint8_t* data, uint8_t* scales, cudaStream_t stream);
+MXQ_API mxq_status mxq_fp8_silu_mul_128x1(const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx,
+                                          uint8_t* data, uint8_t* scales, cudaStream_t stream);
+/* Gradient of x for the gradient g [rows, ldg] of a: with s = 1 / (1 +
+ * exp(-gate)), d_gate = g up s (1 + gate (1 - s)) and d_up = g gate s; d_x [rows, 2H]
+ * contiguous, all dt.  Errors as above. */
+MXQ_API mxq_status mxq_silu_mul_grad(const void* g, const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldg,
+                                     int64_t ldx, void* d_x, cudaStream_t stream);
+
 /* Static description of a status code. */
 MXQ_API const char* mxq_status_string(mxq_status s);
 
