@@ -33,6 +33,18 @@ __host__ __device__ constexpr int64_t elt_bytes() {
     return ELT == Elt::BF16 ? 2 : 4;
 }
 
+// A word of one fp32 or two bf16 elements, NaN made canonical.
+template <Elt ELT>
+__device__ __forceinline__ uint32_t canonical_word(uint32_t v) {
+    if constexpr (ELT == Elt::BF16) {
+        if ((v & 0x7FFFu) > 0x7F80u) v = (v & 0xFFFF0000u) | 0x7FC0u;
+        if ((v & 0x7FFFFFFFu) > 0x7F80FFFFu) v = (v & 0xFFFFu) | 0x7FC00000u;
+    } else if ((v & 0x7FFFFFFFu) > 0x7F800000u) {
+        v = 0x7FC00000u;
+    }
+    return v;
+}
+
 // 16 consecutive elements as fp32 patterns, 32-byte loads.
 template <Elt ELT>
 struct Unit {
@@ -69,6 +81,7 @@ struct Unit {
         return w[i];
     }
     __device__ __forceinline__ float f(int i) const { return __uint_as_float(at(i)); }
+    __device__ __forceinline__ float2 f2(int j) const { return make_float2(f(2 * j), f(2 * j + 1)); }
     // Rounds values 2j and 2j + 1; NaN is left as the conversion makes it.
     __device__ __forceinline__ void set2(int j, float lo, float hi) {
         if constexpr (ELT == Elt::BF16) {
@@ -81,14 +94,7 @@ struct Unit {
     // NaN elements to the canonical NaN.
     __device__ __forceinline__ void canonical() {
 #pragma unroll
-        for (uint32_t& v : w) {
-            if constexpr (ELT == Elt::BF16) {
-                if ((v & 0x7FFFu) > 0x7F80u) v = (v & 0xFFFF0000u) | 0x7FC0u;
-                if ((v & 0x7FFFFFFFu) > 0x7F80FFFFu) v = (v & 0xFFFFu) | 0x7FC00000u;
-            } else if ((v & 0x7FFFFFFFu) > 0x7F800000u) {
-                v = 0x7FC00000u;
-            }
-        }
+        for (uint32_t& v : w) v = canonical_word<ELT>(v);
     }
 };
 
@@ -109,34 +115,51 @@ __device__ __forceinline__ uint32_t amax16(const float (&v)[16]) {
     return m;
 }
 
-// 16 E4M3 payloads of a block with scale code `code`.
-__device__ __forceinline__ void e4m3_store16(uint8_t* p, const float (&v)[16], uint32_t code) {
-    const uint32_t inv = inv_scale128(code);
-    const auto at = [&](int i) { return f32_mul(__float_as_uint(v[i]), inv); };
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        o[j] = e4m3x2_from_f32(at(4 * j + 1), at(4 * j)) | e4m3x2_from_f32(at(4 * j + 3), at(4 * j + 2)) << 16;
-        if (code == 255u) o[j] = 0x7F7F7F7Fu;
-    }
-    st16(p, o[0], o[1], o[2], o[3]);
-}
-
 __device__ __forceinline__ uint8_t e4m3_byte(float v, uint32_t code) {
     return code == 255u ? 0x7F : (uint8_t)e4m3x2_from_f32(0u, f32_mul(__float_as_uint(v), inv_scale128(code)));
+}
+
+// Two floats in one 64-bit register: one instruction for both.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float ex2_approx(float t) {
+    float p;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return p;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+    return a;
 }
 
 // exp(-a) for a >= 0, off by 3e-7 of itself at most.  exp(-a) = 2^t with
 // t = -a log2(e); the product is kept to twice its bits, t + r, so that its
 // rounding does not grow with a, and 2^(t + r) = 2^t (1 + r ln 2) for the
-// small r.  Beyond 160 the result is zero either way.  NaN stays NaN.
+// small r.  a is cut off at 160, where the result is zero either way: the
+// caller of exp_neg2 does that.  NaN stays NaN.
+constexpr float kExpHi = -1.4426950216293335f, kExpLo = -1.9259629911e-8f, kLn2 = 0.6931471805599453f, kExpEnd = 160.0f;
 __device__ __forceinline__ float exp_neg(float a) {
-    constexpr float kHi = -1.4426950216293335f, kLo = -1.9259629911e-8f, kLn2 = 0.6931471805599453f;
-    asm("min.NaN.f32 %0, %0, 0f43200000;" : "+f"(a));
-    const float t = fmul(a, kHi), r = ffma(a, kLo, ffma(a, kHi, -t));
-    float p;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(t));
+    a = min_nan(a, kExpEnd);
+    const float t = fmul(a, kExpHi), r = ffma(a, kExpLo, ffma(a, kExpHi, -t)), p = ex2_approx(t);
     return ffma(fmul(p, kLn2), r, p);
+}
+__device__ __forceinline__ float2 exp_neg2(float2 a) {
+    const float2 t = mul2(a, both(-kExpHi));  // -t
+    const float2 r = fma2(a, both(kExpLo), fma2(a, both(kExpHi), t));
+    const float2 p = make_float2(ex2_approx(-t.x), ex2_approx(-t.y));
+    return fma2(mul2(p, both(kLn2)), r, p);
 }
 
 __device__ __forceinline__ float rcp_approx(float v) {
@@ -155,6 +178,35 @@ struct Sigmoid {
         rest = neg ? inv : low;
     }
 };
+
+// silu(x) = x / (1 + exp(-x)) of two values: with h = |x| and e = exp(-h),
+// 1 / (1 + exp(-x)) is 1 - e / (1 + e) for x >= 0 and e / (1 + e) below, so
+// that silu(x) = max(x, 0) - h e / (1 + e) for both: no choice to be made.
+// h comes cut off at kExpEnd, relu is max(x, 0).  Off by 11 units of 2^-24 of
+// itself: e / (1 + e) by 10, and it is at most one half.
+__device__ __forceinline__ float2 silu2(float2 h, float2 relu) {
+    const float2 e = exp_neg2(h), d = fma2(e, both(-1.0f), both(-1.0f));
+    return fma2(h, mul2(e, make_float2(rcp_approx(d.x), rcp_approx(d.y))), relu);
+}
+
+// Largest magnitude of `m` and two more values; NaN if one of them is.
+__device__ __forceinline__ float absmax3(float m, float a, float b) {
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// 16 E4M3 payloads of a block with scale code `code`.
+__device__ __forceinline__ void e4m3_store16(uint8_t* p, const float (&v)[16], uint32_t code) {
+    const float2 inv = both(__uint_as_float(inv_scale128(code)));
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 lo = mul2(make_float2(v[4 * j], v[4 * j + 1]), inv), hi = mul2(make_float2(v[4 * j + 2], v[4 * j + 3]), inv);
+        o[j] = e4m3x2_from_f32(__float_as_uint(lo.y), __float_as_uint(lo.x)) | e4m3x2_from_f32(__float_as_uint(hi.y), __float_as_uint(hi.x)) << 16;
+        if (code == 255u) o[j] = 0x7F7F7F7Fu;
+    }
+    st16(p, o[0], o[1], o[2], o[3]);
+}
 
 inline bool on_bytes(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 

@@ -12,43 +12,214 @@
 
 namespace mxq {
 namespace {
+#ifndef GN
+#define GN 16
+#define MINB 6
+#endif
 
-__device__ __forceinline__ float gated(float gate, float up) { return fmul(fmul(gate, Sigmoid(gate).s), up); }
+// N = 2, 4, ... values of a: gate and up as Unit's words hold them.  Bound by
+// instructions as much as by memory, so two values go through each.
+// -inf, whose silu is 0 / 0 by its definition, is looked for once for all.
+template <Elt ELT, int N>
+__device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, float* v) {
+    if constexpr (ELT == Elt::BF16) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            const uint32_t mag = gate[j] & 0x7FFF7FFFu;
+            uint32_t h, relu;
+            asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(h) : "r"(mag), "r"(0x43204320u));  // kExpEnd
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(relu) : "r"(gate[j]), "r"(0u));
+            top = u16x2_max(top, mag);
+            const auto two = [](uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
+            const float2 r = mul2(silu2(two(h), two(relu)), two(up[j]));
+            v[2 * j] = r.x, v[2 * j + 1] = r.y;
+        }
+        if ((top & 0x7FFFu) >= 0x7F80u || top >= 0x7F800000u) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if ((gate[j / 2] >> (16 * (j & 1)) & 0xFFFFu) == 0xFF80u) v[j] = __uint_as_float(0x7FC00000u);
+        }
+    } else {
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            const float2 g = make_float2(__uint_as_float(gate[2 * j]), __uint_as_float(gate[2 * j + 1]));
+            float2 relu;
+            asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(relu.x) : "f"(g.x));
+            asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(relu.y) : "f"(g.y));
+            top = absmax3(top, g.x, g.y);
+            const float2 r = mul2(silu2(make_float2(min_nan(fabsf(g.x), kExpEnd), min_nan(fabsf(g.y), kExpEnd)), relu),
+                                  make_float2(__uint_as_float(up[2 * j]), __uint_as_float(up[2 * j + 1])));
+            v[2 * j] = r.x, v[2 * j + 1] = r.y;
+        }
+        if (__float_as_uint(top) >= 0x7F800000u) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (gate[j] == 0xFF800000u) v[j] = __uint_as_float(0x7FC00000u);
+        }
+    }
+}
 
-// Rows of 16-element units, eight lanes to a 1x128 block.
-template <Elt ELT, bool QUANT>
-__global__ void __launch_bounds__(256) gate_rows_kernel(GateArgs a, int64_t nb) {
+// 4 or a multiple of 8 words.
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t* w, const char* p) {
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; j += 8) ld32(*reinterpret_cast<uint32_t(*)[8]>(w + j), p + 4 * j);
+    }
+}
+
+// Largest magnitude of N values, as a pattern; above 0x7F800000 for a NaN among them.
+template <int N>
+__device__ __forceinline__ uint32_t amax_of(const float* v) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) m = absmax3(m, v[j], v[j + 1]);
+    return __float_as_uint(m) & 0x7FFFFFFFu;
+}
+
+// Rows of units of N elements, 128 / N lanes to a 1x128 block.
+template <Elt ELT, bool QUANT, int N>
+__global__ void __launch_bounds__(256, MINB) gate_rows_kernel(GateArgs a, int64_t nb) {
     let_next_start();
     wait_for_stream();
+    constexpr int LANES = 128 / N, W = N * elt_bytes<ELT>() / 4;
     const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
     int64_t row, b;
-    split_index(unit >> 3, nb, row, b);
-    const int64_t k = b * 128 + (threadIdx.x & 7) * 16;
+    split_index(unit / LANES, nb, row, b);
+    const int64_t k = b * 128 + (threadIdx.x % LANES) * N;
     const bool there = row < a.rows && k < a.H;
-    Unit<ELT> gate, up;
-    gate.clear(), up.clear();
-    if (there) {
-        gate.load(a.x, row * a.ldx + k);
-        up.load(a.x, row * a.ldx + a.H + k);
-    }
-    float v[16];
+    uint32_t gate[W], up[W];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = gated(gate.f(j), up.f(j));
-    uint32_t amax = amax16(v);
+    for (int j = 0; j < W; ++j) gate[j] = up[j] = 0;
+    if (there) {
+        const char* p = static_cast<const char*>(a.x) + (row * a.ldx + k) * elt_bytes<ELT>();
+        load_words<W>(gate, p);
+        load_words<W>(up, p + a.H * elt_bytes<ELT>());
+    }
+    float v[N];
+    gated<ELT, N>(gate, up, v);
+    uint32_t amax = amax_of<N>(v);
     if constexpr (QUANT) {
 #pragma unroll
-        for (int d = 1; d < 8; d *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        for (int d = 1; d < LANES; d *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
         const uint32_t code = scale_code128(amax);
         if (!there) return;
-        if ((threadIdx.x & 7) == 0) a.scales[row * nb + b] = (uint8_t)code;
-        e4m3_store16(a.data + row * a.H + k, v, code);
+        if (threadIdx.x % LANES == 0) a.scales[row * nb + b] = (uint8_t)code;
+        const float2 inv = both(__uint_as_float(inv_scale128(code)));
+        uint32_t o[N / 4];
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+            const float2 lo = mul2(make_float2(v[4 * j], v[4 * j + 1]), inv), hi = mul2(make_float2(v[4 * j + 2], v[4 * j + 3]), inv);
+            o[j] = e4m3x2_from_f32(__float_as_uint(lo.y), __float_as_uint(lo.x)) | e4m3x2_from_f32(__float_as_uint(hi.y), __float_as_uint(hi.x)) << 16;
+            if (code == 255u) o[j] = 0x7F7F7F7Fu;
+        }
+        uint8_t* p = a.data + row * a.H + k;
+        if constexpr (N == 16) st16(p, o[0], o[1], o[2], o[3]);
+        else *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
     } else {
         if (!there) return;
-        Unit<ELT> o;
+        char* p = static_cast<char*>(a.out) + (row * a.H + k) * elt_bytes<ELT>();
+        const bool nan = amax > 0x7F800000u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.set2(j, v[2 * j], v[2 * j + 1]);
-        if (amax > 0x7F800000u) o.canonical();
-        o.store(a.out, row * a.H + k);
+        for (int j = 0; j < W; ++j) {
+            if constexpr (ELT == Elt::BF16) gate[j] = bf16x2_from_f32(v[2 * j + 1], v[2 * j]);
+            else gate[j] = __float_as_uint(v[j]);
+            if (nan) gate[j] = canonical_word<ELT>(gate[j]);
+        }
+        if constexpr (W % 8 == 0) {
+#pragma unroll
+            for (int j = 0; j < W; j += 8) st32(p + 4 * j, *reinterpret_cast<const uint32_t(*)[8]>(gate + j));
+        } else {
+            st16(p, gate[0], gate[1], gate[2], gate[3]);
+        }
+    }
+}
+
+// 128 rows x 8 TX columns a block, 8 columns of R rows a thread, in registers
+// between the maximum and the rounding: each element is read once.
+template <Elt ELT, int TX, int R>
+__global__ void __launch_bounds__(TX * 128 / R) gate_columns_tile_kernel(GateArgs a) {
+    let_next_start();
+    wait_for_stream();
+    constexpr int TY = 128 / R, WARPS = TX * TY / 32, W = ELT == Elt::BF16 ? 4 : 8;
+    __shared__ uint4 top[WARPS][2 * TX];  // [warp][columns]
+    __shared__ uint2 codes[TX];           // a byte a column
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+    const int64_t c = ((int64_t)blockIdx.x * TX + tx) * 8, r0 = (int64_t)blockIdx.y * 128 + ty;
+    uint32_t gate[R][W], up[R][W];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = r0 + TY * i;
+#pragma unroll
+        for (int j = 0; j < W; ++j) gate[i][j] = up[i][j] = 0;
+        if (r < a.rows && c < a.H) {
+            const char* p = static_cast<const char*>(a.x) + (r * a.ldx + c) * elt_bytes<ELT>();
+            const char* q = p + a.H * elt_bytes<ELT>();
+            if constexpr (ELT == Elt::BF16) {
+                const uint4 g = *reinterpret_cast<const uint4*>(p), u = *reinterpret_cast<const uint4*>(q);
+                gate[i][0] = g.x, gate[i][1] = g.y, gate[i][2] = g.z, gate[i][3] = g.w;
+                up[i][0] = u.x, up[i][1] = u.y, up[i][2] = u.z, up[i][3] = u.w;
+            } else {
+                ld32(gate[i], p);
+                ld32(up[i], q);
+            }
+        }
+    }
+    float v[R][8];
+    uint32_t m[8] = {};
+#pragma unroll
+    for (int i = 0; i < R; ++i) gated<ELT, 8>(gate[i], up[i], v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < R; i += 2) t = absmax3(t, v[i][j], v[i + 1][j]);
+        m[j] = __float_as_uint(t) & 0x7FFFFFFFu;
+#pragma unroll
+        for (int d = TX; d < 32; d *= 2) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], d));
+    }
+    if ((threadIdx.x & 31) < TX) {
+        top[threadIdx.x / 32][2 * tx] = make_uint4(m[0], m[1], m[2], m[3]);
+        top[threadIdx.x / 32][2 * tx + 1] = make_uint4(m[4], m[5], m[6], m[7]);
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 * TX) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) amax = max(amax, reinterpret_cast<const uint32_t*>(top[w])[threadIdx.x]);
+        const uint8_t own = (uint8_t)scale_code128(amax);
+        reinterpret_cast<uint8_t*>(codes)[threadIdx.x] = own;
+        const int64_t column = (int64_t)blockIdx.x * (8 * TX) + threadIdx.x;
+        if (column < a.H) a.scales[(int64_t)blockIdx.y * a.H + column] = own;
+    }
+    __syncthreads();
+    if (c >= a.H) return;
+    float2 inv[4];
+    uint32_t nan[2] = {};  // bytes of poisoned columns
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t code = ((j < 4 ? codes[tx].x : codes[tx].y) >> (8 * (j & 3))) & 0xFFu;
+        (j & 1 ? inv[j / 2].y : inv[j / 2].x) = __uint_as_float(inv_scale128(code));
+        nan[j / 4] |= code == 255u ? 0xFFu << (8 * (j & 3)) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (r0 + TY * i >= a.rows) break;
+        uint32_t o[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 lo = mul2(make_float2(v[i][4 * h], v[i][4 * h + 1]), inv[2 * h]),
+                         hi = mul2(make_float2(v[i][4 * h + 2], v[i][4 * h + 3]), inv[2 * h + 1]);
+            const uint32_t w = e4m3x2_from_f32(__float_as_uint(lo.y), __float_as_uint(lo.x)) |
+                               e4m3x2_from_f32(__float_as_uint(hi.y), __float_as_uint(hi.x)) << 16;
+            o[h] = lop_select(0x7F7F7F7Fu, w, nan[h]);
+        }
+        *reinterpret_cast<uint2*>(a.data + (r0 + TY * i) * a.H + c) = make_uint2(o[0], o[1]);
     }
 }
 
@@ -78,12 +249,8 @@ __global__ void __launch_bounds__(256) gate_any_kernel(GateArgs a, int64_t nb) {
     for (int i = 0; i < B; ++i) {
         if (row[i] >= a.rows) break;
         float v[4];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = gated(__uint_as_float(gate[i][j]), __uint_as_float(up[i][j]));
-            amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        }
+        gated<Elt::FP32, 4>(gate[i], up[i], v);
+        uint32_t amax = amax_of<4>(v);
         if constexpr (QUANT) amax = __reduce_max_sync(0xFFFFFFFFu, amax);
         const uint32_t code = scale_code128(amax);
         if (QUANT && lane == 0) a.scales[first + i] = (uint8_t)code;
@@ -107,17 +274,17 @@ __global__ void __launch_bounds__(512) gate_columns_kernel(GateArgs a) {
     __shared__ uint32_t top[Y][64];
     const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + tx, r0 = (int64_t)blockIdx.y * 128 + ty;
-    float v[R];
-    uint32_t amax = 0;
+    uint32_t gate[R], up[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int64_t r = r0 + Y * i;
         const bool there = r < a.rows && c < a.H;
-        const uint32_t gate = there ? load_f32<ELT>(a.x, r * a.ldx + c) : 0u, up = there ? load_f32<ELT>(a.x, r * a.ldx + a.H + c) : 0u;
-        v[i] = gated(__uint_as_float(gate), __uint_as_float(up));
+        gate[i] = there ? load_f32<ELT>(a.x, r * a.ldx + c) : 0u;
+        up[i] = there ? load_f32<ELT>(a.x, r * a.ldx + a.H + c) : 0u;
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    float v[R];
+    gated<Elt::FP32, R>(gate, up, v);
+    uint32_t amax = amax_of<R>(v);
     top[ty][tx] = amax;
     __syncthreads();
     if (c >= a.H) return;
@@ -182,6 +349,10 @@ __global__ void __launch_bounds__(256) gate_grad_any_kernel(GateArgs a) {
     store_f32<ELT>(a.out, row * 2 * a.H + a.H + k, d.up);
 }
 
+#ifndef GTX
+#define GTX 4
+#define GR 4
+#endif
 constexpr int64_t kMostBlocks = INT64_C(0x7FFFFFFF);
 
 template <Elt ELT>
@@ -200,6 +371,9 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
         return launch_overlapped(gate_grad_any_kernel<ELT>, dim3((unsigned)grid), 256, 0, 0, s, a);
     }
     if (form == GateForm::COLUMNS) {
+        // 8 columns: 16 bytes of bf16, 32 of fp32, 8 of payload and scales
+        constexpr int64_t bytes = 8 * elt_bytes<ELT>();
+        const bool tiled = a.H % 8 == 0 && on_bytes(a.x, bytes) && (a.rows <= 1 || a.ldx % 8 == 0) && on_bytes(a.data, 8) && on_bytes(a.scales, 8);
         // blockIdx.y reaches 65535: 2^23 rows at a time
         for (int64_t r0 = 0; r0 < a.rows; r0 += INT64_C(128) * 65535) {
             GateArgs p = a;
@@ -207,8 +381,10 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
             p.x = static_cast<const char*>(a.x) + r0 * a.ldx * elt_bytes<ELT>();
             p.data = a.data + r0 * a.H;
             p.scales = a.scales + r0 / 128 * a.H;
-            const cudaError_t e = launch_overlapped(gate_columns_kernel<ELT>,
-                                                    dim3((unsigned)ceil_div(a.H, 64), (unsigned)ceil_div(p.rows, 128)), 512, 0, 0, s, p);
+            const unsigned y = (unsigned)ceil_div(p.rows, 128);
+            const cudaError_t e =
+                tiled ? launch_overlapped(gate_columns_tile_kernel<ELT, GTX, GR>, dim3((unsigned)ceil_div(a.H, 8 * GTX), y), GTX * 128 / GR, 0, 0, s, p)
+                      : launch_overlapped(gate_columns_kernel<ELT>, dim3((unsigned)ceil_div(a.H, 64), y), 512, 0, 0, s, p);
             if (e != cudaSuccess) return e;
         }
         return cudaSuccess;
@@ -216,9 +392,9 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
     const bool quant = form == GateForm::ROWS;
     if (ceil_div(a.rows * nb, 16) > kMostBlocks) return cudaErrorInvalidValue;
     if (units && (quant ? on_bytes(a.data, 16) : on_bytes(a.out, 32))) {
-        const dim3 grid((unsigned)ceil_div(a.rows * nb * 8, 256));
-        return quant ? launch_overlapped(gate_rows_kernel<ELT, true>, grid, 256, 0, 0, s, a, nb)
-                     : launch_overlapped(gate_rows_kernel<ELT, false>, grid, 256, 0, 0, s, a, nb);
+        const dim3 grid((unsigned)ceil_div(a.rows * nb * (128 / GN), 256));
+        return quant ? launch_overlapped(gate_rows_kernel<ELT, true, GN>, grid, 256, 0, 0, s, a, nb)
+                     : launch_overlapped(gate_rows_kernel<ELT, false, GN>, grid, 256, 0, 0, s, a, nb);
     }
     const dim3 grid((unsigned)ceil_div(a.rows * nb, 16));
     return quant ? launch_overlapped(gate_any_kernel<ELT, true>, grid, 256, 0, 0, s, a, nb)

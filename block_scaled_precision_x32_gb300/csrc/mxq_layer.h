@@ -124,6 +124,9 @@ struct RouteArgs {
     float* weights;     // [T, topk]
     const float* g;     // gradient: of the weights
     void* d_logits;     // gradient: [T, E]
+    // set by the launcher: 16-byte accesses; experts of a group, and the binary logarithm of its lanes
+    bool vector;
+    int group_size, group_shift;
 };
 
 // Each returns cudaSuccess or the launch error.

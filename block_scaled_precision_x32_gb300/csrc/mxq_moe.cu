@@ -272,10 +272,11 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
 }
 
 // Quantized rows to the experts' order, K payload bytes and nb scale codes of
-// each, in pieces of BYTES; one row to blockIdx.x, a slice of its pieces to
-// blockIdx.y.
+// each, in pieces of BYTES, kFlight of them loaded before the first is stored;
+// one row to blockIdx.x, a slice of its pieces to blockIdx.y.
+constexpr int kFp8Threads = 128, kFlight = 4;
 template <int BYTES>
-__global__ void __launch_bounds__(kRowThreads) dispatch_fp8_kernel(MoeFp8Args a) {
+__global__ void __launch_bounds__(kFp8Threads) dispatch_fp8_kernel(MoeFp8Args a) {
     let_next_start();
     wait_for_stream();
     using W = typename std::conditional<BYTES == 16, uint4, typename std::conditional<BYTES == 4, uint32_t, uint8_t>::type>::type;
@@ -286,10 +287,16 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_fp8_kernel(MoeFp8Args a)
         const bool there = t >= 0 && t < a.T;
         const W* from = reinterpret_cast<const W*>(a.data + (there ? t * a.ld : 0));
         W* to = reinterpret_cast<W*>(a.out + r * a.K);
-        for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.y * kRowThreads)
-            to[i] = there ? from[i] : W{};
-        for (int64_t i = (int64_t)blockIdx.y * kRowThreads + threadIdx.x; i < a.nb; i += (int64_t)gridDim.y * kRowThreads)
-            a.out_scales[r * a.nb + i] = there ? a.scales[t * a.nb + i] : 0;
+        for (int64_t i0 = (int64_t)blockIdx.y * (kFp8Threads * kFlight) + threadIdx.x; i0 < pieces; i0 += (int64_t)gridDim.y * (kFp8Threads * kFlight)) {
+            W w[kFlight];
+#pragma unroll
+            for (int q = 0; q < kFlight; ++q) w[q] = there && i0 + q * kFp8Threads < pieces ? from[i0 + q * kFp8Threads] : W{};
+#pragma unroll
+            for (int q = 0; q < kFlight; ++q)
+                if (i0 + q * kFp8Threads < pieces) to[i0 + q * kFp8Threads] = w[q];
+        }
+        if (blockIdx.y == 0)
+            for (int64_t i = threadIdx.x; i < a.nb; i += kFp8Threads) a.out_scales[r * a.nb + i] = there ? a.scales[t * a.nb + i] : 0;
     }
 }
 
@@ -466,9 +473,14 @@ cudaError_t dispatch_fp8(const MoeFp8Args& a, cudaStream_t s) {
     const auto on = [&](int64_t n) {
         return (reinterpret_cast<uintptr_t>(a.data) | reinterpret_cast<uintptr_t>(a.out)) % n == 0 && a.K % n == 0 && (a.T <= 1 || a.ld % n == 0);
     };
-    if (on(16)) return launch_overlapped(dispatch_fp8_kernel<16>, row_grid(a.R, a.K / 16), kRowThreads, 0, 0, s, a);
-    if (on(4)) return launch_overlapped(dispatch_fp8_kernel<4>, row_grid(a.R, a.K / 4), kRowThreads, 0, 0, s, a);
-    return launch_overlapped(dispatch_fp8_kernel<1>, row_grid(a.R, a.K), kRowThreads, 0, 0, s, a);
+    const int64_t pieces = on(16) ? a.K / 16 : on(4) ? a.K / 4 : a.K, slices = ceil_div(pieces, kFp8Threads * kFlight);
+    // few rows are cut into slices so that the device is full
+    const int64_t wanted = ceil_div((int64_t)sm_count() * 16, a.R);
+    const dim3 grid((unsigned)(a.R < kMostBlocks ? a.R : kMostBlocks),
+                    (unsigned)(wanted < 1 ? 1 : wanted < slices ? wanted : slices < 65535 ? slices : 65535));
+    return on(16) ? launch_overlapped(dispatch_fp8_kernel<16>, grid, kFp8Threads, 0, 0, s, a)
+           : on(4) ? launch_overlapped(dispatch_fp8_kernel<4>, grid, kFp8Threads, 0, 0, s, a)
+                   : launch_overlapped(dispatch_fp8_kernel<1>, grid, kFp8Threads, 0, 0, s, a);
 }
 
 }  // namespace

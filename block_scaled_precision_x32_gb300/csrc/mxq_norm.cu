@@ -6,6 +6,8 @@
 // The statistics are those of h as it is stored, so that the gradient, which
 // has h alone, is that of what was computed.  y is quantized before it is
 // rounded to x's type.  Sums and statistics are fp32.
+#include <atomic>
+
 #include "mxq_device.cuh"
 #include "mxq_e4m3.cuh"
 #include "mxq_layer.h"
@@ -207,69 +209,178 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(NormArgs a, int64
 // d_w is summed by each block over its rows, and the blocks' sums in a fixed
 // order by a second kernel: no atomics.
 
-// Rows of units: a block takes every gridDim.x-th row and keeps its columns'
-// part of d_w in registers.
-template <Elt ELT, Elt WELT, int U>
-__global__ void __launch_bounds__(U == 1 ? 512 : 1024) norm_grad_rows_kernel(NormGradArgs a, float* parts) {
-    __shared__ float part[2][32];
+// Rows on 16 bytes: one persistent block to a multiprocessor, row_threads
+// threads to a row and as many rows at a time as it has threads for.  A thread
+// has P pieces of 16 bytes of a row, row_threads pieces apart.  Its part of the
+// rows that come next is on its way into its own slots of shared memory
+// (cp.async) while it works on one: only that keeps enough bytes in flight, as
+// a block has to wait for a row's sum between reading and writing it.  The
+// columns' part of d_w stays in registers.
+constexpr int kRingBytes = 220 * 1024, kRingMost = 8;
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_but(int left) {
+    if constexpr (N == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (left == N) asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    else copies_but<N - 1>(left);
+}
+
+// Values 2j and 2j + 1 of pieces.
+template <Elt ELT>
+__device__ __forceinline__ float2 pair_of(const uint32_t* w, int j) {
+    if constexpr (ELT == Elt::BF16) return make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+    return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+}
+
+template <Elt ELT, Elt WELT, int P>
+__global__ void __launch_bounds__(512) norm_grad_rows_kernel(NormGradArgs a, int row_threads, int stages) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ __align__(16) float part[2][16];
     let_next_start();
     wait_for_stream();
-    Unit<WELT> w[U];
-    float dw[U][16] = {};
+    constexpr int E = 16 / (int)elt_bytes<ELT>(), kPairs = P * E / 2;  // elements of a piece, pairs of them a thread
+    const int operands = a.g_h ? 3 : 2, rows_at_once = blockDim.x / row_threads;
+    const int tid = threadIdx.x % row_threads, mine = threadIdx.x / row_threads;
+    const int64_t first = (int64_t)blockIdx.x * rows_at_once + mine, step = (int64_t)gridDim.x * rows_at_once;
+    bool there[P];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t k = ((int64_t)u * blockDim.x + threadIdx.x) * 16;
-        w[u].clear();
-        if (k < a.K) w[u].load_shared(a.weight, k);
-    }
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        Unit<ELT> g[U], h[U];
-        const float r = a.rstd[row];
-        float dot = 0.0f;
+    for (int p = 0; p < P; ++p) there[p] = ((int64_t)p * row_threads + tid) * E < a.K;
+    // piece p of operand o of this thread in stage s lies at ((s * operands + o) * P + p) * blockDim.x * 16 + threadIdx.x * 16
+    const uint32_t slots = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+    const char* from[3] = {at_row<ELT>(a.g, first, a.ldg) + tid * 16, at_row<ELT>(a.h, first, a.ldh) + tid * 16,
+                           at_row<ELT>(a.g_h ? a.g_h : a.g, first, a.ldgh) + tid * 16};
+    const int64_t stride[3] = {step * a.ldg * elt_bytes<ELT>(), step * a.ldh * elt_bytes<ELT>(), step * a.ldgh * elt_bytes<ELT>()};
+    int64_t next = first;
+    const auto fetch = [&](int stage) {  // row `next`
+        if (next < a.rows) {
+            uint32_t to = slots + (uint32_t)(stage * operands * P) * blockDim.x * 16;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = ((int64_t)u * blockDim.x + threadIdx.x) * 16;
-            g[u].clear(), h[u].clear();
-            if (k < a.K) {
-                g[u].load(at_row<ELT>(a.g, row, a.ldg), k);
-                h[u].load(at_row<ELT>(a.h, row, a.ldh), k);
+            for (int o = 0; o < 3; ++o) {
+                if (o >= operands) break;
+#pragma unroll
+                for (int p = 0; p < P; ++p, to += blockDim.x * 16)
+                    if (there[p]) copy16(to, from[o] + p * row_threads * 16);
+                from[o] += stride[o];
             }
         }
+        next += step;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const auto read = [&](uint32_t (&v)[4 * P], int stage, int o) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int p = 0; p < P; ++p) {
+            const uint4 w = *reinterpret_cast<const uint4*>(ring + ((size_t)((stage * operands + o) * P + p) * blockDim.x + threadIdx.x) * 16);
+            v[4 * p] = w.x, v[4 * p + 1] = w.y, v[4 * p + 2] = w.z, v[4 * p + 3] = w.w;
+        }
+    };
+    for (int s = 0; s < stages; ++s) fetch(s);
+    if (threadIdx.x < 16 && threadIdx.x >= blockDim.x / 32) part[0][threadIdx.x] = part[1][threadIdx.x] = 0.0f;  // of no warp
+    constexpr int kWeightWords = P * E * (int)elt_bytes<WELT>() / 4;
+    uint32_t w[kWeightWords];
+    float2 dw[kPairs] = {};
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float n = fmul(h[u].f(j), r);
-                dot = ffma(fmul(g[u].f(j), w[u].f(j)), n, dot);
-                dw[u][j] = ffma(g[u].f(j), n, dw[u][j]);
-            }
-        const float c = fdiv(block_sum(dot, part[turn]), (float)a.K);
+    for (int p = 0; p < P; ++p) {
+        constexpr int N = kWeightWords / P;  // words of a piece's weights: 2, 4 or 8
+        const uint2* from_w = reinterpret_cast<const uint2*>(static_cast<const char*>(a.weight) + ((int64_t)p * row_threads + tid) * E * elt_bytes<WELT>());
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = ((int64_t)u * blockDim.x + threadIdx.x) * 16;
-            if (k >= a.K) continue;
-            Unit<ELT> o, add;
-            add.clear();
-            if (a.g_h) add.load(at_row<ELT>(a.g_h, row, a.ldgh), k);
-            const auto value = [&](int j) {
-                const float d = ffma(fmul(h[u].f(j), r), -c, fmul(g[u].f(j), w[u].f(j)));
-                return ffma(d, r, add.f(j));
-            };
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o.set2(j, value(2 * j), value(2 * j + 1));
-            if (!(fabsf(c) <= 3.4028235e38f)) o.canonical();
-            o.store(at_row<ELT>(a.d_h, row, a.ldd), k);
+        for (int q = 0; q < N; q += 2) {
+            const uint2 v = there[p] ? __ldg(from_w + q / 2) : make_uint2(0u, 0u);
+            w[p * N + q] = v.x, w[p * N + q + 1] = v.y;
         }
     }
-    if (!parts) return;
+    const float per_k = fdiv(1.0f, (float)a.K);
+    const int64_t turns = (a.rows + step - 1) / step;  // the same for every thread: each one meets every barrier
+    int stage = 0;
+    float next_r = first < a.rows ? a.rstd[first] : 0.0f;
+    for (int64_t turn = 0; turn < turns; ++turn) {
+        const int64_t row = first + turn * step;
+        const float r = next_r;
+        next_r = row + step < a.rows ? a.rstd[row + step] : 0.0f;
+        copies_but<kRingMost - 1>(stages - 1);
+        uint32_t g[4 * P], h[4 * P], add[4 * P];
+        read(g, stage, 0);
+        read(h, stage, 1);
+        if (a.g_h) read(add, stage, 2);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t k = ((int64_t)u * blockDim.x + threadIdx.x) * 16;
-        if (k >= a.K) continue;
-        float4* p = reinterpret_cast<float4*>(parts + blockIdx.x * a.K + k);
+        for (int i = 0; i < 4 * P; ++i) {
+            if (!there[i / 4] || row >= a.rows) g[i] = h[i] = 0;
+            if (!a.g_h) add[i] = 0;
+        }
+        float2 dot2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = make_float4(dw[u][4 * j], dw[u][4 * j + 1], dw[u][4 * j + 2], dw[u][4 * j + 3]);
+        for (int j = 0; j < kPairs; ++j) {
+            dot2 = fma2(mul2(pair_of<ELT>(g, j), pair_of<WELT>(w, j)), pair_of<ELT>(h, j), dot2);
+            dw[j] = fma2(pair_of<ELT>(g, j), mul2(pair_of<ELT>(h, j), both(r)), dw[j]);
+        }
+        float dot = warp_sum(fadd(dot2.x, dot2.y));
+        float* sums = part[turn & 1];
+        if ((threadIdx.x & 31) == 0) sums[threadIdx.x / 32] = dot;
+        __syncthreads();
+        fetch(stage);  // what was here is in registers
+        stage = stage + 1 < stages ? stage + 1 : 0;
+        if (row_threads > 256) {
+            // the row's warps; behind the block's last there are zeros
+            dot = 0.0f;
+#pragma unroll
+            for (int v = 0; v < 16; v += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(sums + v);
+                dot = fadd(dot, fadd(fadd(q.x, q.y), fadd(q.z, q.w)));
+            }
+        } else if (row_threads > 32) {
+            dot = 0.0f;
+#pragma unroll 4
+            for (int v = mine * (row_threads / 32); v < (mine + 1) * (row_threads / 32); ++v) dot = fadd(dot, sums[v]);
+        }
+        if (row >= a.rows) continue;
+        const float rc = -fmul(r, fmul(fmul(r, dot), per_k));  // d_h = r g w - (r h) (r c) + g_h
+        float top = 0.0f;
+        uint32_t o[4 * P];
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const float2 d = fma2(mul2(pair_of<ELT>(g, j), pair_of<WELT>(w, j)), both(r),
+                                  fma2(mul2(pair_of<ELT>(h, j), both(r)), both(rc), pair_of<ELT>(add, j)));
+            if constexpr (ELT == Elt::BF16) o[j] = bf16x2_from_f32(d.y, d.x);
+            else o[2 * j] = __float_as_uint(d.x), o[2 * j + 1] = __float_as_uint(d.y);
+            top = absmax3(top, d.x, d.y);
+        }
+        if (top != top)
+#pragma unroll
+            for (uint32_t& v : o) v = canonical_word<ELT>(v);
+        char* to = at_row<ELT>(a.d_h, row, a.ldd) + tid * 16;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (there[p]) st16(to + p * row_threads * 16, o[4 * p], o[4 * p + 1], o[4 * p + 2], o[4 * p + 3]);
+    }
+    if (!a.parts) return;
+    // the rows that ran side by side add up in their order
+    float2* sums = reinterpret_cast<float2*>(ring);
+    copies_but<0>(0);
+    for (int v = 1; v < rows_at_once; ++v) {
+        __syncthreads();
+        if (mine == v)
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) sums[j * row_threads + tid] = dw[j];
+        __syncthreads();
+        if (mine == 0)
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                const float2 o = sums[j * row_threads + tid];
+                dw[j] = make_float2(fadd(dw[j].x, o.x), fadd(dw[j].y, o.y));
+            }
+    }
+    if (mine != 0) return;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        if (!there[p]) continue;
+        float4* to = reinterpret_cast<float4*>(a.parts + blockIdx.x * a.K + ((int64_t)p * row_threads + tid) * E);
+#pragma unroll
+        for (int q = 0; q < E / 4; ++q) {
+            const float2 x = dw[p * E / 2 + 2 * q], y = dw[p * E / 2 + 2 * q + 1];
+            to[q] = make_float4(x.x, x.y, y.x, y.y);
+        }
     }
 }
 
@@ -363,22 +474,53 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
     return a.weight_elt == Elt::BF16 ? rows_launch<ELT, Elt::BF16, RES>(a, s) : rows_launch<ELT, Elt::FP32, RES>(a, s);
 }
 
+// Stages of the ring that shared memory has room for, 0 where rows are too long for it.
+struct RingShape {
+    int wide, row_threads, threads, stages;
+    size_t bytes;
+};
+template <Elt ELT>
+RingShape ring_shape(const NormGradArgs& a) {
+    RingShape r{};
+    r.wide = a.K > 8192;  // 16 elements a thread, or 32
+    r.row_threads = (int)unit_threads(a.K, r.wide ? 2 : 1);
+    if (r.row_threads > 512) return r;
+    r.threads = 512 / r.row_threads * r.row_threads;
+    const size_t elements = (size_t)r.threads * (r.wide ? 32 : 16), stage = (a.g_h ? 3 : 2) * elements * elt_bytes<ELT>();
+    r.stages = (int)(kRingBytes / stage < kRingMost ? kRingBytes / stage : kRingMost);
+    if (r.stages < 2) r.stages = 0;
+    const size_t sums = (size_t)r.row_threads * (r.wide ? 32 : 16) * 4;
+    r.bytes = r.stages * stage > sums ? r.stages * stage : sums;
+    return r;
+}
+
+template <Elt ELT, Elt WELT, int P>
+cudaError_t grad_rows_launch(const NormGradArgs& a, const RingShape& r, unsigned blocks, cudaStream_t s) {
+    static std::atomic<bool> allowed[kDevices];
+    const cudaError_t e = allow_shared_memory(norm_grad_rows_kernel<ELT, WELT, P>, kRingBytes, allowed);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(norm_grad_rows_kernel<ELT, WELT, P>, dim3(blocks), r.threads, r.bytes, 0, s, a, r.row_threads, r.stages);
+}
 template <Elt ELT, Elt WELT>
-cudaError_t grad_rows_launch(const NormGradArgs& a, unsigned blocks, cudaStream_t s) {
-    if (a.K <= 8192)
-        return launch_overlapped(norm_grad_rows_kernel<ELT, WELT, 1>, dim3(blocks), unit_threads(a.K, 1), 0, 0, s, a, a.parts);
-    return launch_overlapped(norm_grad_rows_kernel<ELT, WELT, 2>, dim3(blocks), unit_threads(a.K, 2), 0, 0, s, a, a.parts);
+cudaError_t grad_rows_launch(const NormGradArgs& a, const RingShape& r, unsigned blocks, cudaStream_t s) {
+    constexpr int P = (int)elt_bytes<ELT>();  // pieces of 16 elements
+    return r.wide ? grad_rows_launch<ELT, WELT, 2 * P>(a, r, blocks, s) : grad_rows_launch<ELT, WELT, P>(a, r, blocks, s);
 }
 
 template <Elt ELT>
 cudaError_t grad_launch(const NormGradArgs& a, cudaStream_t s) {
-    const bool units = a.K % 16 == 0 && a.K <= 16384 && unit_rows<ELT>(a.g, a.rows, a.ldg) && unit_rows<ELT>(a.h, a.rows, a.ldh) &&
-                       unit_rows<ELT>(a.g_h, a.rows, a.ldgh) && unit_rows<ELT>(a.d_h, a.rows, a.ldd) && on_bytes(a.weight, 16);
-    const unsigned blocks = (unsigned)(a.rows < kNormParts ? a.rows : kNormParts);
+    const auto on16 = [&](const void* p, int64_t ld) { return on_bytes(p, 16) && (a.rows <= 1 || ld * elt_bytes<ELT>() % 16 == 0); };
+    const bool pieces = a.K * elt_bytes<ELT>() % 16 == 0 && a.K <= 16384 && on16(a.g, a.ldg) && on16(a.h, a.ldh) && on16(a.g_h, a.ldgh) &&
+                        on16(a.d_h, a.ldd) && on_bytes(a.weight, 16);
+    const RingShape ring = pieces ? ring_shape<ELT>(a) : RingShape{};
+    unsigned blocks;
     cudaError_t e;
-    if (units) {
-        e = a.weight_elt == Elt::BF16 ? grad_rows_launch<ELT, Elt::BF16>(a, blocks, s) : grad_rows_launch<ELT, Elt::FP32>(a, blocks, s);
+    if (ring.stages) {
+        const int64_t groups = ceil_div(a.rows, ring.threads / ring.row_threads), most = sm_count() < kNormParts ? sm_count() : kNormParts;
+        blocks = (unsigned)(groups < most ? groups : most);
+        e = a.weight_elt == Elt::BF16 ? grad_rows_launch<ELT, Elt::BF16>(a, ring, blocks, s) : grad_rows_launch<ELT, Elt::FP32>(a, ring, blocks, s);
     } else {
+        blocks = (unsigned)(a.rows < kNormParts ? a.rows : kNormParts);
         e = cudaSuccess;
         if (a.parts)  // ahead of d_h, which may lie over g
             e = launch_overlapped(norm_weight_any_kernel<ELT>, dim3((unsigned)ceil_div(a.K, kAnyThreads), blocks), kAnyThreads, 0, 0, s, a,

@@ -30,15 +30,15 @@ __device__ __forceinline__ float lane_sum(float v) {
     return v;
 }
 
-// Numbers as keys of the same order: a larger number has a larger key, -inf
-// the least one, above 0, which stands for "not to be chosen".
+// Numbers as keys of the same order: a larger number has a larger key, -0 that
+// of 0, -inf the least one, above 0, which stands for "not to be chosen".
 __device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t u = __float_as_uint(v);
+    const uint32_t u = __float_as_uint(fadd(v, 0.0f));
     return u ^ ((int32_t)u < 0 ? 0xFFFFFFFFu : 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^ ((int32_t)k < 0 ? 0x80000000u : 0xFFFFFFFFu)); }
 __device__ __forceinline__ uint64_t key_of(double v) {
-    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint64_t u = (uint64_t)__double_as_longlong(v == 0.0 ? 0.0 : v);
     return u ^ ((int64_t)u < 0 ? ~0ull : 1ull << 63);
 }
 __device__ __forceinline__ double of_key(uint64_t k) {
@@ -50,83 +50,144 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
     const uint32_t lo = warp_max((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
     return (uint64_t)hi << 32 | lo;
 }
-__device__ __forceinline__ float warp_max(float v) { return of_key(warp_max(key_of(v))); }
+__device__ __forceinline__ float warp_max(float v) {
+    asm volatile("redux.sync.max.f32 %0, %0, 0xFFFFFFFF;" : "+f"(v));
+    return v;
+}
+__device__ __forceinline__ double warp_max(double v) { return of_key(warp_max(key_of(v))); }
 
+// The two largest of some numbers.
 template <typename Real>
 struct Top2 {
     Real a = (Real)-kInf, b = (Real)-kInf;
     __device__ __forceinline__ void add(Real v) {
-        b = v > a ? a : v > b ? v : b;
-        a = v > a ? v : a;
+        b = max(b, min(a, v));
+        a = max(a, v);
+    }
+    __device__ __forceinline__ void add(const Top2& o) {
+        b = max(max(b, o.b), min(a, o.a));
+        a = max(a, o.a);
     }
     __device__ __forceinline__ void merge(int d) {
-        const Real oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
-        add(oa);
-        add(ob);
+        Top2 o;
+        o.a = __shfl_xor_sync(kAll, a, d);
+        o.b = __shfl_xor_sync(kAll, b, d);
+        add(o);
     }
     // The group's score; -inf where no expert of it can be chosen.
     __device__ __forceinline__ Real score(int top) const { return top == 1 || b == (Real)-kInf ? a : a + b; }
+    __device__ __forceinline__ Real size() const {
+        return (a == (Real)-kInf ? (Real)0 : fabs(a)) + (b == (Real)-kInf ? (Real)0 : fabs(b));
+    }
 };
+template <int N, typename Real>
+__device__ __forceinline__ Top2<Real> top2_of(const Real* c) {
+    Top2<Real> t;
+    if constexpr (N == 1) {
+        t.a = c[0];
+    } else {
+        t = top2_of<N / 2>(c);
+        t.add(top2_of<N / 2>(c + N / 2));
+    }
+    return t;
+}
 
 template <Elt ELT>
 __device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
-    return fadd(__uint_as_float(load_f32<ELT>(a.logits, t * a.ld + e)), 0.0f);  // -0 becomes 0, which is its equal
+    return __uint_as_float(load_f32<ELT>(a.logits, t * a.ld + e));
 }
 
 // VPL consecutive logits, -inf behind the last expert.
 template <Elt ELT, int VPL>
 __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int lane, float (&x)[VPL]) {
+    constexpr int kWords = VPL * (ELT == Elt::BF16 ? 2 : 4) / 16;  // 16-byte words of a lane
+    if (kWords > 0 && a.vector) {
+        if (lane * VPL < a.E) {
+            uint32_t w[kWords ? 4 * kWords : 1];
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.logits) + (t * a.ld + lane * VPL) * elt_bytes<ELT>());
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) x[i] = lane * VPL + i < a.E ? logit<ELT>(a, t, lane * VPL + i) : -kInf;
+            for (int q = 0; q < kWords; ++q) {
+                const uint4 v = __ldg(p + q);
+                w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                x[i] = __uint_as_float(ELT == Elt::FP32 ? w[kWords ? i : 0] : i & 1 ? w[kWords ? i / 2 : 0] & 0xFFFF0000u : w[kWords ? i / 2 : 0] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) x[i] = -kInf;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) x[i] = lane * VPL + i < a.E ? logit<ELT>(a, t, lane * VPL + i) : -kInf;
+    }
 }
 
-// The topk largest of c in the best groups: lane j's result is the j-th, -1
-// for none.  c is -inf for what cannot be chosen.  err: how far a c may be
-// off what exact arithmetic gives; two that cannot be told apart set `unsure`.
-// A negative err: c is taken as it is.
-template <Elt ELT, int VPL, typename Real>
-__device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lane, Real (&c)[VPL], Real err, bool& unsure) {
-    using Key = decltype(key_of(Real()));
+// How the experts' groups lie: none, a power of two of whole lanes each, or otherwise.
+enum Groups { NONE, LANES, ANY };
+
+// Takes the experts of all but the best groups out (c = -inf).
+template <int VPL, Groups GROUPS, typename Real>
+__device__ __forceinline__ void best_groups(const RouteArgs& a, int lane, Real (&c)[VPL], Real err, bool& unsure) {
     constexpr Real kRound = (Real)(1.0 / (1 << 22));
-    if (a.groups > 1) {
-        const int size = a.E / a.groups, lanes = size / VPL;
-        // a lane's group and its score; every lane of a group the same
-        Real mine = (Real)-kInf;
-        int group = lane, step = 1;
-        if (lanes * VPL == size && (lanes & (lanes - 1)) == 0) {
-            group = lane / lanes, step = lanes;
-            Top2<Real> top;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) top.add(c[i]);
-            for (int d = 1; d < lanes; d *= 2) top.merge(d);
-            mine = top.score(a.group_top);
-        } else {
-            for (int g = 0; g < a.groups; ++g) {
-                Top2<Real> top;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if ((lane * VPL + i) / size == g) top.add(c[i]);
-                for (int d = 1; d < 32; d *= 2) top.merge(d);
-                if (lane == g) mine = top.score(a.group_top);
-            }
-        }
-        int ahead = 0;
+    Top2<Real> top;
+    int group = lane, shift = 0, ahead = 0;
+    if constexpr (GROUPS == LANES) {
+        shift = a.group_shift;
+        group = lane >> shift;
+        top = top2_of<VPL>(c);
+        for (int d = 1; d < 1 << shift; d *= 2) top.merge(d);
+    } else {
         for (int g = 0; g < a.groups; ++g) {
-            const Real other = __shfl_sync(kAll, mine, g * step);
-            ahead += other > mine || (other == mine && g < group) ? 1 : 0;
+            Top2<Real> of;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (lane * VPL + i >= g * a.group_size && lane * VPL + i < (g + 1) * a.group_size) of.add(c[i]);
+            for (int d = 1; d < 32; d *= 2) of.merge(d);
+            if (lane == g) top = of;
         }
-        const bool real = group < a.groups && lane == group * step, kept = real && ahead < a.topk_groups;
-        if (err >= (Real)0 && a.topk_groups < a.groups) {
-            const Real least = -of_key(warp_max(key_of(kept ? -mine : (Real)-kInf)));
-            const Real next = of_key(warp_max(key_of(real && !kept ? mine : (Real)-kInf)));
-            const Real tol = 2 * a.group_top * err + kRound * max(fabs(least), fabs(next));
-            if (next > (Real)-kInf && least - next <= tol) unsure = true;
-        }
+    }
+    const Real mine = top.score(a.group_top);
+    // a group's lanes share the comparisons with the others
+    for (int g0 = 0; g0 < a.groups; g0 += 1 << shift) {
+        const int g = g0 + (lane & ((1 << shift) - 1));
+        const Real other = __shfl_sync(kAll, mine, (g << shift) & 31);
+        ahead += g < a.groups && (other > mine || (other == mine && g < group)) ? 1 : 0;
+    }
+    for (int d = 1; d < 1 << shift; d *= 2) ahead += __shfl_xor_sync(kAll, ahead, d);
+    const bool real = group < a.groups, kept = real && ahead < a.topk_groups;
+    if (err >= (Real)0 && a.topk_groups < a.groups) {
+        const Real least = -warp_max(kept ? -mine : (Real)-kInf), next = warp_max(real && !kept ? mine : (Real)-kInf);
+        const Real tol = 2 * a.group_top * err + kRound * warp_max(top.size());
+        if (next > (Real)-kInf && least - next <= tol) unsure = true;
+    }
+    if constexpr (GROUPS == LANES) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = kept ? c[i] : (Real)-kInf;
+    } else {
         const unsigned mask = __ballot_sync(kAll, kept);
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (lane * VPL + i >= a.E || !(mask >> ((lane * VPL + i) / size * step) & 1)) c[i] = (Real)-kInf;
+            if (lane * VPL + i >= a.E || !(mask >> ((lane * VPL + i) / a.group_size) & 1)) c[i] = (Real)-kInf;
     }
+}
+
+// Can two neighbours of the order, last in front of e, not be told apart?
+// Equal logits with equal biases are ties, which the index decides.
+template <Elt ELT, typename Real>
+__device__ __forceinline__ bool too_near(const RouteArgs& a, int64_t t, Real err, Real last_c, int last, Real c, int e) {
+    constexpr Real kRound = (Real)(1.0 / (1 << 22));
+    return last_c - c <= 2 * err + kRound * max(fabs(last_c), fabs(c)) &&
+           !(logit<ELT>(a, t, last) == logit<ELT>(a, t, e) && (!a.bias || a.bias[last] == a.bias[e]));
+}
+
+// The topk largest of c, one after the other: lane j's result is the j-th, -1
+// for none.  c is -inf for what cannot be chosen.  err: how far a c may be
+// off what exact arithmetic gives, besides its last rounding; neighbours that
+// cannot be told apart set `unsure`.  A negative err: c is taken as it is.
+template <Elt ELT, int VPL, typename Real>
+__device__ __forceinline__ int choose_in_turn(const RouteArgs& a, int64_t t, int lane, const Real (&c)[VPL], Real err, bool& unsure) {
+    using Key = decltype(key_of(Real()));
     Key key[VPL], top = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -158,9 +219,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lane, R
         if (j < a.topk && lane == j) id = e;
         if (err >= (Real)0) {
             const Real now = of_key(best);
-            if (j && last_c - now <= 2 * err + kRound * max(fabs(last_c), fabs(now)) &&
-                !(logit<ELT>(a, t, last) == logit<ELT>(a, t, e) && (!a.bias || a.bias[last] == a.bias[e])))
-                unsure = true;
+            if (j && too_near<ELT>(a, t, err, last_c, last, now, e)) unsure = true;
             last = e;
             last_c = now;
         }
@@ -168,8 +227,119 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lane, R
     return id;
 }
 
-// The same in 64 bits.
+// The same for fp32 in fewer steps.  The topk + 1 largest are among the values
+// that reach the (topk + 1)-th largest of the lanes' own largest ones: a dozen
+// for topk 8.  Those go to shared memory, one to a lane, and each counts how
+// many are ahead of it.  More than 32 of them are chosen in turn.
 template <Elt ELT, int VPL>
+__device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, int lane, const float (&c)[VPL], float err, bool& unsure, uint64_t* list) {
+    float left = c[0], from = -kInf;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) left = max(left, c[i]);
+    const int rounds = a.topk + (err >= 0.0f ? 1 : 0);
+#pragma unroll 1
+    for (int j = 0; j < rounds; ++j) {
+        from = warp_max(left);
+        left = left == from ? -kInf : left;
+    }
+    from = max(from, -3.4028235e38f);  // with fewer lanes than rounds, all that can be chosen
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mine += c[i] >= from ? 1 : 0;
+    int at = 0, n = 0;
+#pragma unroll
+    for (int b = 0; (1 << b) <= VPL; ++b) {
+        const unsigned bit = __ballot_sync(kAll, mine >> b & 1);
+        at += __popc(bit & ((1u << lane) - 1)) << b;
+        n += __popc(bit) << b;
+    }
+    if (n > 32) return choose_in_turn<ELT, VPL, float>(a, t, lane, c, err, unsure);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (c[i] >= from) list[at++] = (uint64_t)__float_as_uint(c[i]) << 32 | (uint32_t)(lane * VPL + i);
+    __syncwarp();
+    uint64_t own = 0;
+    if (lane < n) {  // the order of the keys: by value, then the lower index first
+        own = list[lane];
+        own = (uint64_t)key_of(__uint_as_float((uint32_t)(own >> 32))) << 32 | (uint32_t)~(uint32_t)own;
+    }
+    list[lane] = own;
+    __syncwarp();
+    int rank = 0;
+#pragma unroll 2
+    for (int j = 0; j < n; j += 2) {  // behind the last there are zeros
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(list + j);
+        rank += k.x > own ? 1 : 0;
+        rank += k.y > own ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < n) list[rank] = own;
+    __syncwarp();
+    int id = -1;
+    if (lane < a.topk && lane < n) {
+        const uint64_t k = list[lane];
+        id = (int)~(uint32_t)k;
+        if (err >= 0.0f && lane + 1 < n) {
+            const uint64_t l = list[lane + 1];
+            unsure |= too_near<ELT>(a, t, err, of_key((uint32_t)(k >> 32)), id, of_key((uint32_t)(l >> 32)), (int)~(uint32_t)l);
+        }
+    }
+    return id;
+}
+
+// The largest; NaN if one is.
+template <int N>
+__device__ __forceinline__ float max_nan(const float (&v)[N]) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < N; i += 2) asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[i]), "f"(v[i + 1 < N ? i + 1 : i]));
+    return m;
+}
+
+template <int VPL>
+__device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&b)[VPL]) {
+    if (VPL % 4 == 0 && a.vector) {
+        if (lane * VPL < a.E) {
+            const float4* p = reinterpret_cast<const float4*>(a.bias + lane * VPL);
+#pragma unroll
+            for (int q = 0; q < VPL / 4; ++q) {
+                const float4 v = __ldg(p + q);
+                b[4 * q] = v.x, b[4 * q + 1] = v.y, b[4 * q + 2] = v.z, b[4 * q + 3] = v.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (lane * VPL + i < a.E) b[i] = __ldg(a.bias + lane * VPL + i);
+    }
+}
+
+// Scores of VPL logits: 1 / (1 + exp(-x)), or exp(x - m) for the softmax; 0 for -inf.
+template <int VPL>
+__device__ __forceinline__ void scores(const RouteArgs& a, const float (&x)[VPL], float m, float (&s)[VPL]) {
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += 2) {
+            const int j = VPL > 1 ? i + 1 : i;
+            const float2 e = exp_neg2(make_float2(min_nan(fabsf(x[i]), kExpEnd), min_nan(fabsf(x[j]), kExpEnd)));
+            const float2 inv = make_float2(rcp_approx(fadd(1.0f, e.x)), rcp_approx(fadd(1.0f, e.y))), low = mul2(e, inv);
+            s[i] = x[i] < 0.0f ? low.x : inv.x;
+            s[j] = x[j] < 0.0f ? low.y : inv.y;
+        }
+    } else {
+        const float from = m == -kInf ? 0.0f : m;  // a row of -inf alone
+#pragma unroll
+        for (int i = 0; i < VPL; i += 2) {
+            const int j = VPL > 1 ? i + 1 : i;
+            const float2 e = exp_neg2(make_float2(min_nan(from - x[i], kExpEnd), min_nan(from - x[j], kExpEnd)));
+            s[i] = e.x;
+            s[j] = e.y;
+        }
+    }
+}
+
+// The same in 64 bits.
+template <Elt ELT, int VPL, Groups GROUPS>
 __device__ __noinline__ int choose64(const RouteArgs& a, int64_t t, int lane) {
     float x[VPL];
     load_logits<ELT, VPL>(a, t, lane, x);
@@ -191,7 +361,8 @@ __device__ __noinline__ int choose64(const RouteArgs& a, int64_t t, int lane) {
         if (x[i] == -kInf) c[i] = -(double)kInf;
     }
     bool unsure = false;
-    return choose<ELT, VPL, double>(a, t, lane, c, -1.0, unsure);
+    if constexpr (GROUPS != NONE) best_groups<VPL, GROUPS, double>(a, lane, c, -1.0, unsure);
+    return choose_in_turn<ELT, VPL, double>(a, t, lane, c, -1.0, unsure);
 }
 
 // The chosen experts' scores up to a common factor of the row, lane j for
@@ -216,8 +387,9 @@ struct Chosen {
     }
 };
 
-template <Elt ELT, int VPL>
+template <Elt ELT, int VPL, Groups GROUPS>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
+    __shared__ __align__(16) uint64_t lists[kWarps][32];
     let_next_start();
     wait_for_stream();
     const int lane = threadIdx.x & 31;
@@ -225,64 +397,66 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     if (t >= a.T) return;
     float c[VPL];
     load_logits<ELT, VPL>(a, t, lane, c);
-    bool bad = false;
-    float m = -kInf;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        bad |= c[i] != c[i];
-        m = max(m, c[i]);
+    float m = max_nan<VPL>(c);
+    bool bad = m != m;
+    if (!a.sigmoid) {
+        m = warp_max(m);
+        bad |= m == kInf;
     }
-    m = warp_max(m);
-    bad |= !a.sigmoid && m == kInf;
     float total = 0.0f, err = -1.0f;
-    const bool scored = a.bias || (a.groups > 1 && a.group_top > 1);
+    const bool scored = a.bias || (GROUPS != NONE && a.group_top > 1);
     if (scored || !(a.sigmoid || a.renorm)) {
         float s[VPL];
+        scores<VPL>(a, c, m, s);
+        if (!a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            s[i] = c[i] == -kInf ? 0.0f : a.sigmoid ? Sigmoid(c[i]).s : exp_neg(m - c[i]);
-            total = fadd(total, s[i]);
+            for (int i = 0; i < VPL; ++i) total = fadd(total, s[i]);
+            total = lane_sum(total);
         }
-        total = lane_sum(total);
         if (scored) {
             // in units of 2^-24 of the largest score: two of exp_neg and the sum, or the reciprocal, and a sum's VPL + 5 terms
             const float most = a.sigmoid ? 1.0f : fdiv(1.0f, total);
-            constexpr float kStep = 5.9604645e-8f;
-            err = (a.sigmoid ? 10.0f : VPL + 20.0f) * kStep * most;
-            float size = 0.0f;
+            err = (a.sigmoid ? 10.0f : VPL + 20.0f) * 5.9604645e-8f * most;
+            float b[VPL];
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) b[i] = 0.0f;
+            if (a.bias) {
+                load_bias<VPL>(a, lane, b);
+                const float top = max_nan<VPL>(b);
+                bad |= top != top;
+            }
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                const float b = a.bias && lane * VPL + i < a.E ? a.bias[lane * VPL + i] : 0.0f;
-                bad |= b != b;
-                if (c[i] > -kInf) c[i] = fadd(a.sigmoid ? s[i] : fmul(s[i], most), b);
-                if (c[i] > -kInf) size = max(size, fabsf(c[i]));
+                const float v = fadd(a.sigmoid ? s[i] : fmul(s[i], most), b[i]);
+                c[i] = c[i] > -kInf ? v : c[i];
             }
-            err += kStep * warp_max(size);  // the rounding of score + bias
         }
     }
-    int id;
+    bad = __any_sync(kAll, bad);
+    int id = lane;  // a row that cannot be scored: valid experts, and NaN as their weights
     float x = -kInf;
-    if (__any_sync(kAll, bad)) {  // a row that cannot be scored: valid experts, and NaN as their weights
-        id = lane;
-    } else {
+    if (!bad) {
         bool unsure = false;
-        id = choose<ELT, VPL, float>(a, t, lane, c, err, unsure);
-        if (__any_sync(kAll, unsure)) id = choose64<ELT, VPL>(a, t, lane);
+        if constexpr (GROUPS != NONE) best_groups<VPL, GROUPS, float>(a, lane, c, err, unsure);
+        id = choose32<ELT, VPL>(a, t, lane, c, err, unsure, lists[threadIdx.x / 32]);
+        if (__any_sync(kAll, unsure)) id = choose64<ELT, VPL, GROUPS>(a, t, lane);
         if (id >= 0) x = logit<ELT>(a, t, id);
     }
-    const Chosen chosen(x, a.sigmoid);
-    float w;
+    float w = x == -kInf ? 0.0f : a.sigmoid ? Sigmoid(x).s : exp_neg(m - x);
     if (a.renorm) {
-        w = chosen.u > 0.0f ? fmul(a.scale, fdiv(chosen.u, chosen.sum)) : 0.0f;
-    } else if (a.sigmoid) {
-        w = x == -kInf ? 0.0f : fmul(a.scale, Sigmoid(x).s);
-    } else {
-        w = x == -kInf ? 0.0f : fmul(a.scale, fdiv(exp_neg(m - x), total));
+        float sum = lane_sum(w);
+        if (sum < 1e-3f) {  // the chosen scores are small, or underflow
+            const Chosen chosen(x, a.sigmoid);
+            w = chosen.u;
+            sum = chosen.sum;
+        }
+        w = sum > 0.0f ? fdiv(w, sum) : 0.0f;
+    } else if (!a.sigmoid) {
+        w = total > 0.0f ? fdiv(w, total) : 0.0f;
     }
-    if (__any_sync(kAll, bad)) w = __uint_as_float(0x7FC00000u);
     if (lane < a.topk) {
         a.ids[t * a.topk + lane] = id;
-        a.weights[t * a.topk + lane] = w;
+        a.weights[t * a.topk + lane] = bad ? __uint_as_float(0x7FC00000u) : fmul(a.scale, w);
     }
 }
 
@@ -293,6 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 // g_j s_j (1 - s_j) for sigmoid.  A warp to a token.
 template <Elt ELT, int VPL>
 __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_constant__ RouteArgs a) {
+    __shared__ __align__(16) float rows[kWarps][32 * VPL];
     let_next_start();
     wait_for_stream();
     const int lane = threadIdx.x & 31;
@@ -318,38 +493,69 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
         if (id < 0 || x == -kInf) v = 0.0f;
     } else {
         load_logits<ELT, VPL>(a, t, lane, d);
-        float m = -kInf, total = 0.0f;
+        float m = max_nan<VPL>(d);
+        m = __any_sync(kAll, m != m) ? __uint_as_float(0x7FC00000u) : warp_max(m);
+        float total = 0.0f;
+        scores<VPL>(a, d, m, d);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) m = max(m, d[i]);
-        m = warp_max(m);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            d[i] = d[i] == -kInf ? 0.0f : exp_neg(m - d[i]);
-            total = fadd(total, d[i]);
-        }
+        for (int i = 0; i < VPL; ++i) total = fadd(total, d[i]);
         const float inv = fdiv(1.0f, lane_sum(total));
         v = x == -kInf ? 0.0f : fmul(g, fmul(exp_neg(m - x), inv));
         const float all = fmul(inv, lane_sum(v));
 #pragma unroll
         for (int i = 0; i < VPL; ++i) d[i] = d[i] == 0.0f ? 0.0f : -fmul(d[i], all);
     }
+    // the row goes through shared memory, where the chosen experts' parts are added: of the choices of one expert (there may
+    // be more than one) the first adds all, in their order
+    float* row = rows[threadIdx.x / 32];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) row[lane * VPL + i] = d[i];
+    float sum = 0.0f;
+    bool first = id >= 0;
     for (int j = 0; j < a.topk; ++j) {
         const int e = __shfl_sync(kAll, id, j);
         const float add = __shfl_sync(kAll, v, j);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (e == lane * VPL + i) d[i] = fadd(d[i], add);
+        if (e == id) {
+            sum = fadd(sum, add);
+            first &= j >= lane;
+        }
     }
+    __syncwarp();
+    if (first) row[id] = fadd(row[id], sum);
+    __syncwarp();
+    constexpr int kPer = ELT == Elt::BF16 ? 8 : 4;  // 16 bytes
+    // NaN comes out canonical: only a row with a NaN or an infinity can have one
+    const bool odd = __any_sync(kAll, !(fabsf(v) < kInf) || !(fabsf(d[0]) < kInf));
+    if (a.vector && !odd) {
+        for (int e = lane * kPer; e < a.E; e += 32 * kPer) {
+            uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (lane * VPL + i < a.E) store_f32<ELT>(a.d_logits, t * a.E + lane * VPL + i, d[i]);
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (ELT == Elt::BF16) w[i] = bf16x2_from_f32(row[e + 2 * i + 1], row[e + 2 * i]);
+                else w[i] = __float_as_uint(row[e + i]);
+            }
+            *reinterpret_cast<uint4*>(static_cast<char*>(a.d_logits) + (t * a.E + e) * elt_bytes<ELT>()) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+        for (int e = lane; e < a.E; e += 32) store_f32<ELT>(a.d_logits, t * a.E + e, row[e]);
+    }
 }
 
 template <Elt ELT, int VPL>
-cudaError_t launch(bool grad, const RouteArgs& a, cudaStream_t s) {
+cudaError_t launch(bool grad, RouteArgs a, cudaStream_t s) {
+    // whole lanes of 16-byte words in, and out for the gradient
+    a.vector = a.E % VPL == 0 && on_bytes(a.logits, 16) && (a.T <= 1 || a.ld * elt_bytes<ELT>() % 16 == 0) && on_bytes(a.bias, 16) &&
+               (!grad || (a.E * elt_bytes<ELT>() % 16 == 0 && on_bytes(a.d_logits, 16)));
     const dim3 grid((unsigned)ceil_div(a.T, kWarps));
-    return grad ? launch_overlapped(route_grad_kernel<ELT, VPL>, grid, kWarps * 32, 0, 0, s, a)
-                : launch_overlapped(route_kernel<ELT, VPL>, grid, kWarps * 32, 0, 0, s, a);
+    if (grad) return launch_overlapped(route_grad_kernel<ELT, VPL>, grid, kWarps * 32, 0, 0, s, a);
+    if (a.groups == 1) return launch_overlapped(route_kernel<ELT, VPL, NONE>, grid, kWarps * 32, 0, 0, s, a);
+    a.group_size = a.E / a.groups;
+    for (int shift = 0; shift < 6; ++shift)
+        if (VPL << shift == a.group_size) {
+            a.group_shift = shift;
+            return launch_overlapped(route_kernel<ELT, VPL, LANES>, grid, kWarps * 32, 0, 0, s, a);
+        }
+    return launch_overlapped(route_kernel<ELT, VPL, ANY>, grid, kWarps * 32, 0, 0, s, a);
 }
 
 template <Elt ELT>
