@@ -91,6 +91,16 @@ struct Unit {
             w[2 * j + 1] = __float_as_uint(hi);
         }
     }
+    // Adds, each sum rounded once.
+    __device__ __forceinline__ void add(const Unit& o) {
+        if constexpr (ELT == Elt::BF16) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = bf2_add(w[j], o.w[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = f32_add(w[j], o.w[j]);
+        }
+    }
     // NaN elements to the canonical NaN.
     __device__ __forceinline__ void canonical() {
 #pragma unroll
@@ -119,6 +129,10 @@ __device__ __forceinline__ uint8_t e4m3_byte(float v, uint32_t code) {
     return code == 255u ? 0x7F : (uint8_t)e4m3x2_from_f32(0u, f32_mul(__float_as_uint(v), inv_scale128(code)));
 }
 
+// 16 bytes into shared memory, asynchronously; past L1.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 // Two floats in one 64-bit register: one instruction for both.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
@@ -184,8 +198,8 @@ struct Sigmoid {
 // that silu(x) = max(x, 0) - h e / (1 + e) for both: no choice to be made.
 // h comes cut off at kExpEnd, relu is max(x, 0).  Off by 11 units of 2^-24 of
 // itself: e / (1 + e) by 10, and it is at most one half.
-__device__ __forceinline__ float2 silu2(float2 h, float2 relu) {
-    const float2 e = exp_neg2(h), d = fma2(e, both(-1.0f), both(-1.0f));
+__device__ __forceinline__ float2 silu2(float2 h, float2 e, float2 relu) {
+    const float2 d = fma2(e, both(-1.0f), both(-1.0f));
     return fma2(h, mul2(e, make_float2(rcp_approx(d.x), rcp_approx(d.y))), relu);
 }
 

@@ -12,28 +12,49 @@
 
 namespace mxq {
 namespace {
-#ifndef GN
-#define GN 16
-#define MINB 6
-#endif
 
 // N = 2, 4, ... values of a: gate and up as Unit's words hold them.  Bound by
 // instructions as much as by memory, so two values go through each.
-// -inf, whose silu is 0 / 0 by its definition, is looked for once for all.
-template <Elt ELT, int N>
+//
+// The exponential of a bf16 gate takes fewer of them than exp_neg2: log2(e) is
+// cut into K1 of 16 bits, whose product with the gate's 8 is exact, and the
+// rest K2 = 7.1e-6: exp(-h) = 2^(-h K1) (1 - h K2 ln 2), off by (h K2)^2 / 4 <
+// 1.5 units of 2^-24 for the second order left out, up to h = 88, and 5 with
+// the rest.
+//
+// To be quantized, silu(x) is taken as x / (1 + exp(-x)), which needs no choice
+// by the sign but a bound below: a gate under -87 counts as -87, which is off by
+// 1.5e-36 |up| at most; and an infinite gate, of either sign, gives NaN: its
+// block is poisoned as it would be by an infinity.  Otherwise -inf, whose silu is
+// 0 * inf by its definition, is looked for once for all.
+template <Elt ELT, int N, bool QUANT>
 __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, float* v) {
     if constexpr (ELT == Elt::BF16) {
+        constexpr float K1 = 47274.0f / 32768.0f, K2 = 7.0526077e-6f * kLn2;
+        const auto two = [](uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
+        const auto exp_of = [&](float2 h) {  // exp(-h)
+            const float2 t = mul2(h, both(K1));
+            return mul2(make_float2(ex2_approx(-t.x), ex2_approx(-t.y)), fma2(h, both(-K2), both(1.0f)));
+        };
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
-            const uint32_t mag = gate[j] & 0x7FFF7FFFu;
-            uint32_t h, relu;
-            asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(h) : "r"(mag), "r"(0x43204320u));  // kExpEnd
-            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(relu) : "r"(gate[j]), "r"(0u));
-            top = u16x2_max(top, mag);
-            const auto two = [](uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
-            const float2 r = mul2(silu2(two(h), two(relu)), two(up[j]));
-            v[2 * j] = r.x, v[2 * j + 1] = r.y;
+            if constexpr (QUANT) {
+                uint32_t cut;
+                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(cut) : "r"(gate[j]), "r"(0xC2AEC2AEu));       // -87
+                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(cut) : "r"(gate[j]), "r"(0u));  // NaN for infinities
+                const float2 x = two(cut), d = fma2(exp_of(x), both(1.0f), both(1.0f));
+                const float2 r = mul2(mul2(x, make_float2(rcp_approx(d.x), rcp_approx(d.y))), two(up[j]));
+                v[2 * j] = r.x, v[2 * j + 1] = r.y;
+            } else {
+                const uint32_t mag = gate[j] & 0x7FFF7FFFu;
+                uint32_t cut, relu;
+                asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(cut) : "r"(mag), "r"(0x43204320u));  // kExpEnd
+                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(relu) : "r"(gate[j]), "r"(0u));
+                top = u16x2_max(top, mag);
+                const float2 r = mul2(silu2(two(cut), exp_of(two(cut)), two(relu)), two(up[j]));
+                v[2 * j] = r.x, v[2 * j + 1] = r.y;
+            }
         }
         if ((top & 0x7FFFu) >= 0x7F80u || top >= 0x7F800000u) {
 #pragma unroll
@@ -49,8 +70,8 @@ __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, 
             asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(relu.x) : "f"(g.x));
             asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(relu.y) : "f"(g.y));
             top = absmax3(top, g.x, g.y);
-            const float2 r = mul2(silu2(make_float2(min_nan(fabsf(g.x), kExpEnd), min_nan(fabsf(g.y), kExpEnd)), relu),
-                                  make_float2(__uint_as_float(up[2 * j]), __uint_as_float(up[2 * j + 1])));
+            const float2 h = make_float2(min_nan(fabsf(g.x), kExpEnd), min_nan(fabsf(g.y), kExpEnd));
+            const float2 r = mul2(silu2(h, exp_neg2(h), relu), make_float2(__uint_as_float(up[2 * j]), __uint_as_float(up[2 * j + 1])));
             v[2 * j] = r.x, v[2 * j + 1] = r.y;
         }
         if (__float_as_uint(top) >= 0x7F800000u) {
@@ -82,12 +103,12 @@ __device__ __forceinline__ uint32_t amax_of(const float* v) {
     return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
-// Rows of units of N elements, 128 / N lanes to a 1x128 block.
-template <Elt ELT, bool QUANT, int N>
-__global__ void __launch_bounds__(256, MINB) gate_rows_kernel(GateArgs a, int64_t nb) {
+// Rows of units of 16 elements, eight lanes to a 1x128 block.
+template <Elt ELT, bool QUANT>
+__global__ void __launch_bounds__(256, ELT == Elt::FP32 ? 4 : QUANT ? 7 : 5) gate_rows_kernel(GateArgs a, int64_t nb) {
     let_next_start();
     wait_for_stream();
-    constexpr int LANES = 128 / N, W = N * elt_bytes<ELT>() / 4;
+    constexpr int N = 16, LANES = 128 / N, W = N * elt_bytes<ELT>() / 4;
     const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
     int64_t row, b;
     split_index(unit / LANES, nb, row, b);
@@ -102,7 +123,7 @@ __global__ void __launch_bounds__(256, MINB) gate_rows_kernel(GateArgs a, int64_
         load_words<W>(up, p + a.H * elt_bytes<ELT>());
     }
     float v[N];
-    gated<ELT, N>(gate, up, v);
+    gated<ELT, N, QUANT>(gate, up, v);
     uint32_t amax = amax_of<N>(v);
     if constexpr (QUANT) {
 #pragma unroll
@@ -142,11 +163,12 @@ __global__ void __launch_bounds__(256, MINB) gate_rows_kernel(GateArgs a, int64_
 
 // 128 rows x 8 TX columns a block, 8 columns of R rows a thread, in registers
 // between the maximum and the rounding: each element is read once.
-template <Elt ELT, int TX, int R>
-__global__ void __launch_bounds__(TX * 128 / R) gate_columns_tile_kernel(GateArgs a) {
+constexpr int kTileX = 4, kTileRows = 4;
+template <Elt ELT>
+__global__ void __launch_bounds__(kTileX * 128 / kTileRows, 7) gate_columns_tile_kernel(GateArgs a) {
     let_next_start();
     wait_for_stream();
-    constexpr int TY = 128 / R, WARPS = TX * TY / 32, W = ELT == Elt::BF16 ? 4 : 8;
+    constexpr int TX = kTileX, R = kTileRows, TY = 128 / R, WARPS = TX * TY / 32, W = ELT == Elt::BF16 ? 4 : 8;
     __shared__ uint4 top[WARPS][2 * TX];  // [warp][columns]
     __shared__ uint2 codes[TX];           // a byte a column
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
@@ -173,7 +195,7 @@ __global__ void __launch_bounds__(TX * 128 / R) gate_columns_tile_kernel(GateArg
     float v[R][8];
     uint32_t m[8] = {};
 #pragma unroll
-    for (int i = 0; i < R; ++i) gated<ELT, 8>(gate[i], up[i], v[i]);
+    for (int i = 0; i < R; ++i) gated<ELT, 8, true>(gate[i], up[i], v[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         float t = 0.0f;
@@ -249,7 +271,7 @@ __global__ void __launch_bounds__(256) gate_any_kernel(GateArgs a, int64_t nb) {
     for (int i = 0; i < B; ++i) {
         if (row[i] >= a.rows) break;
         float v[4];
-        gated<Elt::FP32, 4>(gate[i], up[i], v);
+        gated<Elt::FP32, 4, QUANT>(gate[i], up[i], v);
         uint32_t amax = amax_of<4>(v);
         if constexpr (QUANT) amax = __reduce_max_sync(0xFFFFFFFFu, amax);
         const uint32_t code = scale_code128(amax);
@@ -283,7 +305,7 @@ __global__ void __launch_bounds__(512) gate_columns_kernel(GateArgs a) {
         up[i] = there ? load_f32<ELT>(a.x, r * a.ldx + a.H + c) : 0u;
     }
     float v[R];
-    gated<Elt::FP32, R>(gate, up, v);
+    gated<Elt::FP32, R, true>(gate, up, v);
     uint32_t amax = amax_of<R>(v);
     top[ty][tx] = amax;
     __syncthreads();
@@ -349,10 +371,6 @@ __global__ void __launch_bounds__(256) gate_grad_any_kernel(GateArgs a) {
     store_f32<ELT>(a.out, row * 2 * a.H + a.H + k, d.up);
 }
 
-#ifndef GTX
-#define GTX 4
-#define GR 4
-#endif
 constexpr int64_t kMostBlocks = INT64_C(0x7FFFFFFF);
 
 template <Elt ELT>
@@ -383,7 +401,7 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
             p.scales = a.scales + r0 / 128 * a.H;
             const unsigned y = (unsigned)ceil_div(p.rows, 128);
             const cudaError_t e =
-                tiled ? launch_overlapped(gate_columns_tile_kernel<ELT, GTX, GR>, dim3((unsigned)ceil_div(a.H, 8 * GTX), y), GTX * 128 / GR, 0, 0, s, p)
+                tiled ? launch_overlapped(gate_columns_tile_kernel<ELT>, dim3((unsigned)ceil_div(a.H, 8 * kTileX), y), kTileX * 128 / kTileRows, 0, 0, s, p)
                       : launch_overlapped(gate_columns_kernel<ELT>, dim3((unsigned)ceil_div(a.H, 64), y), 512, 0, 0, s, p);
             if (e != cudaSuccess) return e;
         }
@@ -392,9 +410,9 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
     const bool quant = form == GateForm::ROWS;
     if (ceil_div(a.rows * nb, 16) > kMostBlocks) return cudaErrorInvalidValue;
     if (units && (quant ? on_bytes(a.data, 16) : on_bytes(a.out, 32))) {
-        const dim3 grid((unsigned)ceil_div(a.rows * nb * (128 / GN), 256));
-        return quant ? launch_overlapped(gate_rows_kernel<ELT, true, GN>, grid, 256, 0, 0, s, a, nb)
-                     : launch_overlapped(gate_rows_kernel<ELT, false, GN>, grid, 256, 0, 0, s, a, nb);
+        const dim3 grid((unsigned)ceil_div(a.rows * nb * 8, 256));
+        return quant ? launch_overlapped(gate_rows_kernel<ELT, true>, grid, 256, 0, 0, s, a, nb)
+                     : launch_overlapped(gate_rows_kernel<ELT, false>, grid, 256, 0, 0, s, a, nb);
     }
     const dim3 grid((unsigned)ceil_div(a.rows * nb, 16));
     return quant ? launch_overlapped(gate_any_kernel<ELT, true>, grid, 256, 0, 0, s, a, nb)

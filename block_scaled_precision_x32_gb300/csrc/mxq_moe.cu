@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kFp8Threads) dispatch_fp8_kernel(MoeFp8Args a)
     const int64_t pieces = a.K / BYTES;
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
         const int c = a.source[r];
-        const int64_t t = c < 0 ? -1 : c / a.topk;
+        const int64_t t = c < 0 ? -1 : c / (int)a.topk;  // both are ints: a division of 64 bits takes several times as long
         const bool there = t >= 0 && t < a.T;
         const W* from = reinterpret_cast<const W*>(a.data + (there ? t * a.ld : 0));
         W* to = reinterpret_cast<W*>(a.out + r * a.K);

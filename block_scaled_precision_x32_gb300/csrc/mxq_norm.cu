@@ -7,6 +7,7 @@
 // has h alone, is that of what was computed.  y is quantized before it is
 // rounded to x's type.  Sums and statistics are fp32.
 #include <atomic>
+#include <type_traits>
 
 #include "mxq_device.cuh"
 #include "mxq_e4m3.cuh"
@@ -24,14 +25,18 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Sum over the block, the same in every thread: lanes, then warps, in a fixed
 // order.  `part` is written by this call alone until the block's next barrier.
-__device__ __forceinline__ float block_sum(float v, float (&part)[32]) {
+template <int WARPS>
+__device__ __forceinline__ float block_sum(float v, float (&part)[WARPS]) {
     v = warp_sum(v);
-    const int warps = blockDim.x / 32;
-    if (warps == 1) return v;
+    if (threadIdx.x < WARPS && threadIdx.x >= blockDim.x / 32) part[threadIdx.x] = 0.0f;  // of no warp
     if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
     float sum = 0.0f;
-    for (int w = 0; w < warps; ++w) sum = fadd(sum, part[w]);
+#pragma unroll
+    for (int w = 0; w < WARPS; w += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(part + w);
+        sum = fadd(sum, fadd(fadd(q.x, q.y), fadd(q.z, q.w)));
+    }
     return sum;
 }
 
@@ -51,13 +56,13 @@ __device__ __forceinline__ const char* at_row(const void* p, int64_t r, int64_t 
 // One row to a block, U units of 16 elements to a thread, eight lanes to a
 // 1x128 block; the row stays in registers between its sum and its rounding.
 template <Elt ELT, Elt WELT, bool RES, int U>
-__global__ void __launch_bounds__(U == 1 ? 512 : 1024) norm_rows_kernel(NormArgs a, int64_t nb) {
-    __shared__ float part[32];
+__global__ void __launch_bounds__(U == 1 ? 512 : 1024, U == 1 && ELT == Elt::BF16 ? 3 : 1) norm_rows_kernel(NormArgs a, int64_t nb) {
+    __shared__ __align__(16) float part[U == 1 ? 16 : 32];
     let_next_start();
     wait_for_stream();
     const int64_t row = blockIdx.x;
     Unit<ELT> h[U];
-    float sum = 0.0f;
+    float2 squares = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t k = ((int64_t)u * blockDim.x + threadIdx.x) * 16;
@@ -67,12 +72,11 @@ __global__ void __launch_bounds__(U == 1 ? 512 : 1024) norm_rows_kernel(NormArgs
             if constexpr (RES) {
                 Unit<ELT> r;
                 r.load(at_row<ELT>(a.residual, row, a.ldr), k);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[u].set2(j, fadd(h[u].f(2 * j), r.f(2 * j)), fadd(h[u].f(2 * j + 1), r.f(2 * j + 1)));
+                h[u].add(r);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum = ffma(h[u].f(j), h[u].f(j), sum);
+        for (int j = 0; j < 8; ++j) squares = fma2(h[u].f2(j), h[u].f2(j), squares);
     }
     Unit<WELT> w[U];
 #pragma unroll
@@ -81,21 +85,25 @@ __global__ void __launch_bounds__(U == 1 ? 512 : 1024) norm_rows_kernel(NormArgs
         w[u].clear();
         if (k < a.K) w[u].load_shared(a.weight, k);
     }
-    sum = block_sum(sum, part);
+    const float sum = block_sum(fadd(squares.x, squares.y), part);
     const float rstd = rstd_of(sum, a.K, a.eps);
     if (a.rstd && threadIdx.x == 0) store_f32<Elt::FP32>(a.rstd, row, rstd);
     const bool strange = !(sum <= 3.4028235e38f);  // a NaN or an infinity in the row, or squares that overflow
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t i = (int64_t)u * blockDim.x + threadIdx.x, k = i * 16;
-        float y[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = fmul(fmul(h[u].f(j), rstd), w[u].f(j));
-        uint32_t amax = amax16(y);
         if constexpr (RES) {
             if (strange) h[u].canonical();
             if (a.h && k < a.K) h[u].store(at_row<ELT>(a.h, row, a.ldh), k);
         }
+        float y[16], top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 v = mul2(mul2(h[u].f2(j), both(rstd)), w[u].f2(j));
+            y[2 * j] = v.x, y[2 * j + 1] = v.y;
+            top = absmax3(top, v.x, v.y);
+        }
+        uint32_t amax = __float_as_uint(top) & 0x7FFFFFFFu;
         if (a.y && k < a.K) {
             Unit<ELT> o;
 #pragma unroll
@@ -117,12 +125,19 @@ __global__ void __launch_bounds__(U == 1 ? 512 : 1024) norm_rows_kernel(NormArgs
 
 constexpr int kAnyThreads = 256, kAnyWarps = kAnyThreads / 32, kHeld = 8;
 
+template <Elt ELT>
+__device__ __forceinline__ float value_at(const void* p, int64_t k) {
+    return __uint_as_float(load_f32<ELT>(p, k));
+}
+
 // Any alignment and any K: one row to a block, 1x128 blocks to its warps in
-// turn, neighbours to neighbouring lanes.  The first kHeld blocks of a warp
-// (rows of 8192) stay in registers, what is behind them is read again.
-template <Elt ELT, bool RES>
-__global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(NormArgs a, int64_t nb, bool w_bf16) {
-    __shared__ float part[32];
+// turn, neighbours to neighbouring lanes: an element at a time, so that
+// instructions bound it; whole blocks go without a check for each element.
+// The first kHeld blocks of a warp (rows of 8192) stay in registers, what is
+// behind them is read again.
+template <Elt ELT, Elt WELT, bool RES>
+__global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(NormArgs a, int64_t nb) {
+    __shared__ __align__(16) float part[kAnyWarps];
     let_next_start();
     wait_for_stream();
     const int64_t row = blockIdx.x;
@@ -130,75 +145,87 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(NormArgs a, int64
     const void* x = at_row<ELT>(a.x, row, a.ldx);
     const void* res = RES ? at_row<ELT>(a.residual, row, a.ldr) : nullptr;
     void* hp = RES && a.h ? at_row<ELT>(a.h, row, a.ldh) : nullptr;
+    void* yp = a.y ? at_row<ELT>(a.y, row, a.K) : nullptr;
+    uint8_t* data = a.data ? a.data + row * a.K : nullptr;
     const auto sum_at = [&](int64_t k) {
-        float v = __uint_as_float(load_f32<ELT>(x, k));
+        float v = value_at<ELT>(x, k);
         if constexpr (RES) {
-            v = fadd(v, __uint_as_float(load_f32<ELT>(res, k)));
+            v = fadd(v, value_at<ELT>(res, k));
             if constexpr (ELT == Elt::BF16) v = __uint_as_float(bf16x2_from_f32(v, 0.0f) & 0xFFFF0000u);
         }
         return v;
     };
-    float held[kHeld][4];
-    float sum = 0.0f;
+    // the lane's four elements of block b, zeros behind the row
+    const auto read = [&](int64_t b, float (&v)[4]) {
+        const int64_t k = b * 128 + lane;
+        if (b * 128 + 128 <= a.K) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = sum_at(k + 32 * q);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = k + 32 * q < a.K ? sum_at(k + 32 * q) : 0.0f;
+        }
+    };
+    const auto keep = [&](int64_t b, const float (&v)[4], float sum) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (hp && b * 128 + lane + 32 * q < a.K) store_f32<ELT>(hp, b * 128 + lane + 32 * q, v[q]);
+            sum = ffma(v[q], v[q], sum);
+        }
+        return sum;
+    };
+    float held[kHeld][4], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) read((int64_t)i * kAnyWarps + warp, held[i]);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t k = ((int64_t)i * kAnyWarps + warp) * 128 + lane + 32 * q;
-            held[i][q] = k < a.K ? sum_at(k) : 0.0f;
-        }
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t k = ((int64_t)i * kAnyWarps + warp) * 128 + lane + 32 * q;
-            if (hp && k < a.K) store_f32<ELT>(hp, k, held[i][q]);
-            sum = ffma(held[i][q], held[i][q], sum);
-        }
-    for (int64_t b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t k = b * 128 + lane + 32 * q;
-            const float v = k < a.K ? sum_at(k) : 0.0f;
-            if (hp && k < a.K) store_f32<ELT>(hp, k, v);
-            sum = ffma(v, v, sum);
-        }
+        if ((int64_t)i * kAnyWarps + warp < nb) sum = keep((int64_t)i * kAnyWarps + warp, held[i], sum);
+    for (int64_t b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps) {
+        float v[4];
+        read(b, v);
+        sum = keep(b, v, sum);
+    }
     const float rstd = rstd_of(block_sum(sum, part), a.K, a.eps);
     if (a.rstd && threadIdx.x == 0) store_f32<Elt::FP32>(a.rstd, row, rstd);
-    const auto finish = [&](int64_t b, const float (&v)[4]) {
+    const auto finish = [&](int64_t b, const float (&v)[4], auto whole) {
+        const int64_t k = b * 128 + lane;
         float y[4];
         uint32_t amax = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int64_t k = b * 128 + lane + 32 * q;
-            const float w = k >= a.K ? 0.0f
-                                     : __uint_as_float(w_bf16 ? load_f32<Elt::BF16>(a.weight, k) : load_f32<Elt::FP32>(a.weight, k));
-            y[q] = k < a.K ? fmul(fmul(v[q], rstd), w) : 0.0f;
+            const bool there = decltype(whole)::value || k + 32 * q < a.K;
+            y[q] = there ? fmul(fmul(v[q], rstd), value_at<WELT>(a.weight, k + 32 * q)) : 0.0f;
             amax = max(amax, __float_as_uint(y[q]) & 0x7FFFFFFFu);
-            if (a.y && k < a.K) store_f32<ELT>(at_row<ELT>(a.y, row, a.K), k, y[q]);
+            if (yp && there) store_f32<ELT>(yp, k + 32 * q, y[q]);
         }
-        if (!a.data) return;
+        if (!data) return;
         amax = __reduce_max_sync(0xFFFFFFFFu, amax);
         const uint32_t code = scale_code128(amax);
         if (lane == 0) a.scales[row * nb + b] = (uint8_t)code;
+        const float inv = __uint_as_float(inv_scale128(code));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t k = b * 128 + lane + 32 * q;
-            if (k < a.K) a.data[row * a.K + k] = e4m3_byte(y[q], code);
+        for (int q = 0; q < 4; q += 2) {
+            uint32_t two = e4m3x2_from_f32(__float_as_uint(fmul(y[q + 1], inv)), __float_as_uint(fmul(y[q], inv)));
+            if (code == 255u) two = 0x7F7Fu;
+            if (decltype(whole)::value || k + 32 * q < a.K) data[k + 32 * q] = (uint8_t)two;
+            if (decltype(whole)::value || k + 32 * q + 32 < a.K) data[k + 32 * q + 32] = (uint8_t)(two >> 8);
         }
     };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        if ((int64_t)i * kAnyWarps + warp < nb) finish((int64_t)i * kAnyWarps + warp, held[i]);
+    for (int i = 0; i < kHeld; ++i) {
+        const int64_t b = (int64_t)i * kAnyWarps + warp;
+        if (b * 128 + 128 <= a.K) finish(b, held[i], std::true_type());
+        else if (b < nb) finish(b, held[i], std::false_type());
+    }
     for (int64_t b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps) {
         float v[4];
+        // h may lie over x or the residual: what this thread wrote there is read back
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int64_t k = b * 128 + lane + 32 * q;
-            // h may lie over x or the residual: what this thread wrote there is read back
-            v[q] = k >= a.K ? 0.0f : hp ? __uint_as_float(load_f32<ELT>(hp, k)) : sum_at(k);
+            v[q] = k >= a.K ? 0.0f : hp ? value_at<ELT>(hp, k) : sum_at(k);
         }
-        finish(b, v);
+        finish(b, v, std::false_type());
     }
 }
 
@@ -218,9 +245,6 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(NormArgs a, int64
 // columns' part of d_w stays in registers.
 constexpr int kRingBytes = 220 * 1024, kRingMost = 8;
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void copies_but(int left) {
     if constexpr (N == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -392,7 +416,7 @@ __device__ __forceinline__ float weight_at(const void* w, int64_t k, bool bf16) 
 // Any alignment and any K: d_h, one row to a block, read twice ...
 template <Elt ELT>
 __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(NormGradArgs a, bool w_bf16) {
-    __shared__ float part[32];
+    __shared__ __align__(16) float part[kAnyWarps];
     let_next_start();
     wait_for_stream();
     const int64_t row = blockIdx.x;
@@ -469,8 +493,9 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
                        (!RES || (unit_rows<ELT>(a.residual, a.rows, a.ldr) && unit_rows<ELT>(a.h, a.rows, a.ldh))) &&
                        unit_rows<ELT>(a.y, a.rows, a.K) && on_bytes(a.data, 16);
     if (!units)
-        return launch_overlapped(norm_any_kernel<ELT, RES>, dim3((unsigned)a.rows), kAnyThreads, 0, 0, s, a, ceil_div(a.K, 128),
-                                 a.weight_elt == Elt::BF16);
+        return a.weight_elt == Elt::BF16
+                   ? launch_overlapped(norm_any_kernel<ELT, Elt::BF16, RES>, dim3((unsigned)a.rows), kAnyThreads, 0, 0, s, a, ceil_div(a.K, 128))
+                   : launch_overlapped(norm_any_kernel<ELT, Elt::FP32, RES>, dim3((unsigned)a.rows), kAnyThreads, 0, 0, s, a, ceil_div(a.K, 128));
     return a.weight_elt == Elt::BF16 ? rows_launch<ELT, Elt::BF16, RES>(a, s) : rows_launch<ELT, Elt::FP32, RES>(a, s);
 }
 
