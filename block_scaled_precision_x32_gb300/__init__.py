@@ -1049,33 +1049,39 @@ class Library:
 
     # -- between the products -------------------------------------------
 
-    def _norm_args(self, x, weight, residual, eps, h, y, data, scales, rstd):
+    def _norm_args(self, x, weight, residual, eps, h, y, data, scales, rstd, new=False):
+        """``new``: y, data, scales and rstd were made for this call."""
         dev = _cuda_index(x)
         rows, K, ldx = _matrix(x, "x")
-        _same_device(dev, weight)
-        if weight.dim() != 1 or weight.shape[0] != K or not weight.is_contiguous():
-            raise ValueError(f"weight must be a contiguous vector of {K} values")
-        ldr = ldh = 0
+        if weight.get_device() != dev or weight.dim() != 1 or weight.shape[0] != K or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous vector of {K} values on x's device")
+        ldr = ldh = pr = ph = py = pd = ps = pst = 0
         if residual is not None:
-            ldr = _like_rows(residual, x, rows, K, "residual", dev)
+            ldr, pr = _like_rows(residual, x, rows, K, "residual", dev), residual.data_ptr()
         if h is not None:
             if residual is None:
                 raise ValueError("h is written only with a residual")
-            ldh = _like_rows(h, x, rows, K, "h", dev)
-        if y is not None and (_like_rows(y, x, rows, K, "y", dev) != K or not y.is_contiguous()):
-            raise ValueError("y must be contiguous")
+            ldh, ph = _like_rows(h, x, rows, K, "h", dev), h.data_ptr()
         if (data is None) != (scales is None):
             raise ValueError("data and scales go together")
+        if y is not None:
+            if not new and (_like_rows(y, x, rows, K, "y", dev) != K or not y.is_contiguous()):
+                raise ValueError("y must be contiguous")
+            py = y.data_ptr()
         if data is not None:
-            _same_device(dev, data, scales)
-            if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != rows * K:
-                raise ValueError("data must be a contiguous uint8 tensor of one byte per element of x")
-            _check_values(scales, torch.uint8, rows * _blocks(K), "scales", "rows * ceil(K/128)")
+            if not new:
+                _same_device(dev, data, scales)
+                if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != rows * K:
+                    raise ValueError("data must be a contiguous uint8 tensor of one byte per element of x")
+                _check_values(scales, torch.uint8, rows * _blocks(K), "scales", "rows * ceil(K/128)")
+            pd, ps = data.data_ptr(), scales.data_ptr()
         if rstd is not None:
-            _same_device(dev, rstd)
-            _check_values(rstd, torch.float32, rows, "rstd", "rows")
-        return _NORM(_dt_code(x), _dt_code(weight), rows, K, x.data_ptr(), ldx, _ptr(residual) or 0, ldr, weight.data_ptr(), eps,
-                     _ptr(h) or 0, ldh, _ptr(y) or 0, _ptr(data) or 0, _ptr(scales) or 0, _ptr(rstd) or 0), _raw_stream(dev)
+            if not new:
+                _same_device(dev, rstd)
+                _check_values(rstd, torch.float32, rows, "rstd", "rows")
+            pst = rstd.data_ptr()
+        return _NORM(_dt_code(x), _dt_code(weight), rows, K, x.data_ptr(), ldx, pr, ldr, weight.data_ptr(), eps, ph, ldh, py, pd, ps,
+                     pst), _raw_stream(dev)
 
     def plan_rmsnorm(self, x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
                      h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, data: Optional[torch.Tensor] = None,
@@ -1091,14 +1097,19 @@ class Library:
         elements; ``normed``: the norm in x's dtype; ``stats``: 1 / rms of each
         row, which rmsnorm_grad takes.  ``h`` receives x + residual, and may be
         x or the residual itself (allocated when None)."""
-        new, nb = x.device, _blocks(x.shape[-1]) if x.dim() else 0
-        data = torch.empty(x.shape, dtype=torch.uint8, device=new) if quantized else None
-        scales = torch.empty(x.shape[:-1] + (nb,), dtype=torch.uint8, device=new) if quantized else None
-        y = torch.empty(x.shape, dtype=x.dtype, device=new) if normed else None
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=new) if stats else None
+        device, shape = x.device, x.shape
+        if not shape:
+            raise ValueError("x needs at least one dimension")
+        data = scales = None
+        if quantized:
+            data = torch.empty(shape, dtype=torch.uint8, device=device)
+            per_row = _blocks(shape[-1])
+            scales = torch.empty((shape[0], per_row) if len(shape) == 2 else shape[:-1] + (per_row,), dtype=torch.uint8, device=device)
+        y = torch.empty(shape, dtype=x.dtype, device=device) if normed else None
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device) if stats else None
         if h is None and residual is not None:
-            h = torch.empty(x.shape, dtype=x.dtype, device=new)
-        args = self._norm_args(x, weight, residual, eps, h, y, data, scales, rstd)
+            h = torch.empty(shape, dtype=x.dtype, device=device)
+        args = self._norm_args(x, weight, residual, eps, h, y, data, scales, rstd, True)
         self._call(self.L.mxq_rmsnorm, args, "mxq_rmsnorm", x.get_device())
         return Normed(data, scales, y, x if residual is None else h, rstd)
 
@@ -1160,9 +1171,8 @@ class Library:
     def _route_outputs(self, logits, topk, dev, ids, weights):
         T = logits.shape[0]
         if ids is None:
-            ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-        if weights is None:
-            weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+            device = logits.device
+            return torch.empty((T, topk), dtype=torch.int32, device=device), torch.empty((T, topk), dtype=torch.float32, device=device)
         _same_device(dev, ids, weights)
         _check_int32(ids, T * topk, "ids")
         _check_values(weights, torch.float32, T * topk, "weights", "tokens * topk")
@@ -1218,24 +1228,25 @@ class Library:
         rows, H2, ldx = _matrix(x, "x")
         if H2 % 2:
             raise ValueError("x must hold two halves of one size in its last dimension")
-        H = H2 // 2
+        H, device = H2 // 2, x.device
+        lead = (rows,) if form == "128x1" or x.dim() == 2 else x.shape[:-1]
         dt = torch.uint8 if form else x.dtype
         if out is None:
-            out = torch.empty((rows, H) if form == "128x1" else x.shape[:-1] + (H,), dtype=dt, device=x.device)
+            out = torch.empty(lead + (H,), dtype=dt, device=device)
         else:
             _same_device(dev, out)
             _check_values(out, dt, rows * H, "data" if form else "out", "rows * H")
-        name = _GATE_FORMS[form]
         args = (x.data_ptr(), _dt_code(x), rows, H, ldx, out.data_ptr())
         if form:
-            shape = (_blocks(rows), H) if form == "128x1" else x.shape[:-1] + (_blocks(H),)
+            shape = (_blocks(rows), H) if form == "128x1" else lead + (_blocks(H),)
             if scales is None:
-                scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+                scales = torch.empty(shape, dtype=torch.uint8, device=device)
             else:
                 _same_device(dev, scales)
                 _check_values(scales, torch.uint8, math.prod(shape), "scales",
                               "ceil(rows/128) * H" if form == "128x1" else "rows * ceil(H/128)")
             args += (scales.data_ptr(),)
+        name = _GATE_FORMS[form]
         return getattr(self.L, name), args + (_raw_stream(dev),), name, out, scales
 
     def plan_silu_mul(self, x: torch.Tensor, out: torch.Tensor) -> "Call":

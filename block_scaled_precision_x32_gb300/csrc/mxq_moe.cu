@@ -5,7 +5,6 @@
 
 #include <atomic>
 #include <cstdint>
-#include <type_traits>
 
 #include "mxq_device.cuh"
 #include "mxq_layer.h"
@@ -272,31 +271,60 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
 }
 
 // Quantized rows to the experts' order, K payload bytes and nb scale codes of
-// each, in pieces of BYTES, kFlight of them loaded before the first is stored;
-// one row to blockIdx.x, a slice of its pieces to blockIdx.y.
+// each: one row to blockIdx.x, a slice of it to blockIdx.y, kFlight 16-byte
+// pieces of it loaded by a thread before it stores the first.  SHIFT: rows
+// that do not begin on 16 bytes; the pieces are those of the output, put
+// together from the five words of the token that they lie across, and the
+// bytes in front of the first and behind the last go one by one.
 constexpr int kFp8Threads = 128, kFlight = 4;
-template <int BYTES>
+template <bool SHIFT>
 __global__ void __launch_bounds__(kFp8Threads) dispatch_fp8_kernel(MoeFp8Args a) {
     let_next_start();
     wait_for_stream();
-    using W = typename std::conditional<BYTES == 16, uint4, typename std::conditional<BYTES == 4, uint32_t, uint8_t>::type>::type;
-    const int64_t pieces = a.K / BYTES;
+    const int K = (int)a.K, nb = (int)a.nb;
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
         const int c = a.source[r];
-        const int64_t t = c < 0 ? -1 : c / (int)a.topk;  // both are ints: a division of 64 bits takes several times as long
+        const int t = c < 0 ? -1 : c / (int)a.topk;
         const bool there = t >= 0 && t < a.T;
-        const W* from = reinterpret_cast<const W*>(a.data + (there ? t * a.ld : 0));
-        W* to = reinterpret_cast<W*>(a.out + r * a.K);
-        for (int64_t i0 = (int64_t)blockIdx.y * (kFp8Threads * kFlight) + threadIdx.x; i0 < pieces; i0 += (int64_t)gridDim.y * (kFp8Threads * kFlight)) {
-            W w[kFlight];
+        const uint8_t* from = a.data + (there ? t * a.ld : 0);
+        uint8_t* to = a.out + r * a.K;
+        // bytes of the row in front of the output's first 16-byte boundary
+        const int head = SHIFT ? min((int)(-reinterpret_cast<uintptr_t>(to) & 15), K) : 0, pieces = (K - head) / 16;
+        if (SHIFT && blockIdx.y == 0 && threadIdx.x < 32) {
+            const int tail = head + pieces * 16, i = threadIdx.x < 16 ? (int)threadIdx.x : tail + (int)threadIdx.x - 16;
+            if (threadIdx.x < 16 ? i < head : i < K) to[i] = there ? from[i] : 0;
+        }
+        from += head, to += head;
+        const int off = (int)(reinterpret_cast<uintptr_t>(from) & 3), last = (K - head + off) / 4;  // whole words of the row from `off` on
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(from - off);
+        for (int i0 = blockIdx.y * (kFp8Threads * kFlight) + threadIdx.x; i0 < pieces; i0 += gridDim.y * (kFp8Threads * kFlight)) {
+            uint4 w[kFlight];
 #pragma unroll
-            for (int q = 0; q < kFlight; ++q) w[q] = there && i0 + q * kFp8Threads < pieces ? from[i0 + q * kFp8Threads] : W{};
+            for (int q = 0; q < kFlight; ++q) {
+                const int i = i0 + q * kFp8Threads;
+                w[q] = make_uint4(0u, 0u, 0u, 0u);
+                if (!there || i >= pieces) continue;
+                if constexpr (!SHIFT) {
+                    w[q] = reinterpret_cast<const uint4*>(from)[i];
+                } else if ((off == 0 || i > 0 || head >= off) && 4 * i + 5 <= last) {
+                    uint32_t x[5];
+#pragma unroll
+                    for (int j = 0; j < 5; ++j) x[j] = words[4 * i + j];
+                    w[q] = make_uint4(__funnelshift_r(x[0], x[1], 8 * off), __funnelshift_r(x[1], x[2], 8 * off),
+                                      __funnelshift_r(x[2], x[3], 8 * off), __funnelshift_r(x[3], x[4], 8 * off));
+                } else {  // a word of the piece lies across the row's end
+                    uint32_t x[4] = {};
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j / 4] |= (uint32_t)from[16 * i + j] << (8 * (j & 3));
+                    w[q] = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            }
 #pragma unroll
             for (int q = 0; q < kFlight; ++q)
-                if (i0 + q * kFp8Threads < pieces) to[i0 + q * kFp8Threads] = w[q];
+                if (i0 + q * kFp8Threads < pieces) st16(to + (int64_t)(i0 + q * kFp8Threads) * 16, w[q].x, w[q].y, w[q].z, w[q].w);
         }
         if (blockIdx.y == 0)
-            for (int64_t i = threadIdx.x; i < a.nb; i += kFp8Threads) a.out_scales[r * a.nb + i] = there ? a.scales[t * a.nb + i] : 0;
+            for (int i = threadIdx.x; i < nb; i += kFp8Threads) a.out_scales[r * nb + i] = there ? a.scales[t * a.nb + i] : 0;
     }
 }
 
@@ -470,17 +498,15 @@ cudaError_t rows_launch(int what, Elt elt, const MoeRowsArgs& a, cudaStream_t s)
 }
 
 cudaError_t dispatch_fp8(const MoeFp8Args& a, cudaStream_t s) {
-    const auto on = [&](int64_t n) {
-        return (reinterpret_cast<uintptr_t>(a.data) | reinterpret_cast<uintptr_t>(a.out)) % n == 0 && a.K % n == 0 && (a.T <= 1 || a.ld % n == 0);
-    };
-    const int64_t pieces = on(16) ? a.K / 16 : on(4) ? a.K / 4 : a.K, slices = ceil_div(pieces, kFp8Threads * kFlight);
+    const bool whole = (reinterpret_cast<uintptr_t>(a.data) | reinterpret_cast<uintptr_t>(a.out)) % 16 == 0 && a.K % 16 == 0 &&
+                       (a.T <= 1 || a.ld % 16 == 0);
+    const int64_t slices = ceil_div(ceil_div(a.K, 16), kFp8Threads * kFlight);
     // few rows are cut into slices so that the device is full
     const int64_t wanted = ceil_div((int64_t)sm_count() * 16, a.R);
     const dim3 grid((unsigned)(a.R < kMostBlocks ? a.R : kMostBlocks),
                     (unsigned)(wanted < 1 ? 1 : wanted < slices ? wanted : slices < 65535 ? slices : 65535));
-    return on(16) ? launch_overlapped(dispatch_fp8_kernel<16>, grid, kFp8Threads, 0, 0, s, a)
-           : on(4) ? launch_overlapped(dispatch_fp8_kernel<4>, grid, kFp8Threads, 0, 0, s, a)
-                   : launch_overlapped(dispatch_fp8_kernel<1>, grid, kFp8Threads, 0, 0, s, a);
+    return whole ? launch_overlapped(dispatch_fp8_kernel<false>, grid, kFp8Threads, 0, 0, s, a)
+                 : launch_overlapped(dispatch_fp8_kernel<true>, grid, kFp8Threads, 0, 0, s, a);
 }
 
 }  // namespace

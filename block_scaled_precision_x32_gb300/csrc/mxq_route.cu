@@ -499,42 +499,56 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
         scores<VPL>(a, d, m, d);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) total = fadd(total, d[i]);
-        const float inv = fdiv(1.0f, lane_sum(total));
+        total = lane_sum(total);
+        const float inv = total == 0.0f ? 0.0f : fdiv(1.0f, total);
         v = x == -kInf ? 0.0f : fmul(g, fmul(exp_neg(m - x), inv));
-        const float all = fmul(inv, lane_sum(v));
+        const float all = -fmul(inv, lane_sum(v));
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) d[i] = d[i] == 0.0f ? 0.0f : -fmul(d[i], all);
+        for (int i = 0; i < VPL; ++i) d[i] = fmul(d[i], all);
     }
-    // the row goes through shared memory, where the chosen experts' parts are added: of the choices of one expert (there may
-    // be more than one) the first adds all, in their order
     float* row = rows[threadIdx.x / 32];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) row[lane * VPL + i] = d[i];
-    float sum = 0.0f;
+    // a choice that is its token's only one of an expert adds to what the others leave; of several of one expert the first adds
+    // all, in their order
+    if (id >= 0) row[id] = __uint_as_float(lane);
+    __syncwarp();
     bool first = id >= 0;
-    for (int j = 0; j < a.topk; ++j) {
-        const int e = __shfl_sync(kAll, id, j);
-        const float add = __shfl_sync(kAll, v, j);
-        if (e == id) {
-            sum = fadd(sum, add);
-            first &= j >= lane;
+    if (__any_sync(kAll, first && __float_as_uint(row[id]) != lane)) {
+        float sum = 0.0f;
+        for (int j = 0; j < a.topk; ++j) {
+            const int e = __shfl_sync(kAll, id, j);
+            const float add = __shfl_sync(kAll, v, j);
+            if (e == id) {
+                sum = fadd(sum, add);
+                first &= j >= lane;
+            }
         }
+        v = sum;
     }
     __syncwarp();
-    if (first) row[id] = fadd(row[id], sum);
+    if constexpr (VPL % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4) *reinterpret_cast<float4*>(row + lane * VPL + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) row[lane * VPL + i] = d[i];
+    }
+    __syncwarp();
+    if (first) row[id] = fadd(row[id], v);
     __syncwarp();
     constexpr int kPer = ELT == Elt::BF16 ? 8 : 4;  // 16 bytes
     // NaN comes out canonical: only a row with a NaN or an infinity can have one
     const bool odd = __any_sync(kAll, !(fabsf(v) < kInf) || !(fabsf(d[0]) < kInf));
     if (a.vector && !odd) {
         for (int e = lane * kPer; e < a.E; e += 32 * kPer) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (ELT == Elt::BF16) w[i] = bf16x2_from_f32(row[e + 2 * i + 1], row[e + 2 * i]);
-                else w[i] = __float_as_uint(row[e + i]);
+            const float4 p = *reinterpret_cast<const float4*>(row + e);
+            uint4 w;
+            if constexpr (ELT == Elt::BF16) {
+                const float4 q = *reinterpret_cast<const float4*>(row + e + 4);
+                w = make_uint4(bf16x2_from_f32(p.y, p.x), bf16x2_from_f32(p.w, p.z), bf16x2_from_f32(q.y, q.x), bf16x2_from_f32(q.w, q.z));
+            } else {
+                w = make_uint4(__float_as_uint(p.x), __float_as_uint(p.y), __float_as_uint(p.z), __float_as_uint(p.w));
             }
-            *reinterpret_cast<uint4*>(static_cast<char*>(a.d_logits) + (t * a.E + e) * elt_bytes<ELT>()) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(static_cast<char*>(a.d_logits) + (t * a.E + e) * elt_bytes<ELT>()) = w;
         }
     } else {
         for (int e = lane; e < a.E; e += 32) store_f32<ELT>(a.d_logits, t * a.E + e, row[e]);
