@@ -558,3 +558,62 @@ def test_the_fast_math_build_gives_the_same(mx):
     fast = mxq.Library(fastmath=True)
     for a, b in zip(small_run(fast, *inputs(6)), small_run(mx, *inputs(6))):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------- routers of many tokens
+
+MANY = [
+    dict(E=256, topk=8, score="sigmoid", bias=True, groups=8, topk_groups=4, group_top=2, scale=2.5),
+    dict(E=256, topk=8, score="softmax", renormalize=False),
+    dict(E=256, topk=6, score="softmax", bias=True, groups=16, topk_groups=5, group_top=2),
+    dict(E=256, topk=1, score="sigmoid", groups=4, topk_groups=1),
+    dict(E=192, topk=7, score="sigmoid", bias=True),
+    dict(E=160, topk=6, score="softmax", groups=10, topk_groups=3, renormalize=False),
+    dict(E=132, topk=8, score="softmax", bias=True),
+    dict(E=128, topk=8, score="softmax", bias=True),
+    dict(E=128, topk=4, score="sigmoid", bias=True, groups=8, topk_groups=2, group_top=2),
+    dict(E=128, topk=2, score="softmax", groups=4, topk_groups=2, group_top=2),
+    dict(E=96, topk=5, score="sigmoid", renormalize=False),
+    dict(E=64, topk=6, score="softmax"),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(str(v) for v in c.values()))
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_route_of_many_tokens(mx, case, dtype):
+    """Ordinary rows, and among them rows with experts out of service, ties, values that 32 bits cannot tell apart, NaN,
+    infinities, and scores that underflow."""
+    kw = dict(case)
+    E, topk, bias = kw.pop("E"), kw.pop("topk"), kw.pop("bias", False)
+    rng = np.random.default_rng(E + topk)
+    T = 16389
+    x = 1.5 * normal(rng, T, E)
+    b = 0.05 * normal(rng, E) if bias else None
+    x[5::97, ::3] = -np.inf
+    x[7::97, 2:] = -np.inf
+    x[9::97] = -np.inf
+    x[11::97] = 0.25                                   # every expert alike
+    x[13::97, : E // 2] = 2.0                          # many alike
+    x[15::97, 4], x[17::97, E - 1], x[19::97, 1] = np.nan, np.inf, 3e38
+    x[21::97] -= np.float32(500.0)
+    x[23::97, 8:16] = 4.0 + 1e-6 * normal(rng, len(x[23::97]), 8)
+    logits = dev(x, dtype)
+    check_route(mx, logits, topk, None if b is None else dev(b), **kw)
+    if bias:
+        b[3::7] = -np.inf
+        check_route(mx, logits, topk, dev(b), **kw)
+        s = bref.scores(x[:1].astype(np.float64), kw.get("score", "softmax"))[0]
+        near_ties = dev(np.repeat(x[:1], T, 0) + np.float32(1e-6) * normal(rng, T, E))
+        check_route(mx, near_ties, topk, dev((0.7 - s).astype(np.float32)), **kw)
+
+
+def test_route_of_many_tokens_gives_what_few_do(mx):
+    """A token's choice does not depend on how many there are with it."""
+    x = torch.randn(20000, 256, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    bias = 0.1 * torch.randn(256, device="cuda", generator=torch.Generator("cuda").manual_seed(4))
+    kw = dict(bias=bias, score="sigmoid", groups=8, topk_groups=4, group_top=2)
+    ids, w = mx.moe_route(x, 8, **kw)
+    for a in range(0, 20000, 1000):
+        i, v = mx.moe_route(x[a:a + 1000], 8, **kw)
+        assert torch.equal(i, ids[a:a + 1000])
+        near(v, f64(w[a:a + 1000]), 100 * U * f64(w[a:a + 1000]))
