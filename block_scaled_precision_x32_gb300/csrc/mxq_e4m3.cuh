@@ -111,18 +111,9 @@ struct Unit {
 // One element, rounded to nearest even; NaN comes out canonical.
 template <Elt ELT>
 __device__ __forceinline__ void store_f32(void* p, int64_t i, float v) {
-    uint32_t u = __float_as_uint(v);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0x7FC00000u;
-    if constexpr (ELT == Elt::BF16) static_cast<uint16_t*>(p)[i] = (uint16_t)bf16_rne(u);
-    else static_cast<uint32_t*>(p)[i] = u;
-}
-
-// Largest magnitude of 16 values, as a pattern; above 0x7F800000 for a NaN among them.
-__device__ __forceinline__ uint32_t amax16(const float (&v)[16]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (float x : v) m = max(m, __float_as_uint(x) & 0x7FFFFFFFu);
-    return m;
+    const bool nan = (__float_as_uint(v) & 0x7FFFFFFFu) > 0x7F800000u;
+    if constexpr (ELT == Elt::BF16) static_cast<uint16_t*>(p)[i] = nan ? 0x7FC0 : (uint16_t)bf16x2_from_f32(0.0f, v);
+    else static_cast<uint32_t*>(p)[i] = nan ? 0x7FC00000u : __float_as_uint(v);
 }
 
 __device__ __forceinline__ uint8_t e4m3_byte(float v, uint32_t code) {

@@ -82,6 +82,22 @@ __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, 
     }
 }
 
+// The same for elements that came one by one, as load_f32 leaves them.
+template <Elt ELT, int N, bool QUANT>
+__device__ __forceinline__ void gated_loose(const uint32_t* gate, const uint32_t* up, float* v) {
+    if constexpr (ELT == Elt::BF16) {
+        uint32_t g[N / 2], u[N / 2];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            g[j] = prmt(gate[2 * j], gate[2 * j + 1], 0x7632u);
+            u[j] = prmt(up[2 * j], up[2 * j + 1], 0x7632u);
+        }
+        gated<ELT, N, QUANT>(g, u, v);
+    } else {
+        gated<ELT, N, QUANT>(gate, up, v);
+    }
+}
+
 // 4 or a multiple of 8 words.
 template <int W>
 __device__ __forceinline__ void load_words(uint32_t* w, const char* p) {
@@ -245,44 +261,73 @@ __global__ void __launch_bounds__(kTileX * 128 / kTileRows, 7) gate_columns_tile
     }
 }
 
-// Any alignment and any H: a warp per two 1x128 blocks, an element at a time,
+struct GateGrad {
+    float gate, up;
+    // d_up = g silu(gate);  d_gate = g up (s + silu(gate) (1 - s))
+    __device__ __forceinline__ GateGrad(float g, float x, float u) {
+        const Sigmoid s(x);
+        const float silu = fmul(x, s.s);
+        up = fmul(g, silu);
+        gate = fmul(fmul(g, u), ffma(silu, s.rest, s.s));
+    }
+};
+
+// Any alignment and any H, every form but COLUMNS: one row to blockIdx.x, its
+// 1x128 blocks to the warps of blockIdx.y in turn, an element at a time,
 // neighbours to neighbouring lanes.
-template <Elt ELT, bool QUANT>
-__global__ void __launch_bounds__(256) gate_any_kernel(GateArgs a, int64_t nb) {
+template <Elt ELT, GateForm FORM>
+__global__ void __launch_bounds__(256) gate_any_kernel(GateArgs a, int nb) {
     let_next_start();
     wait_for_stream();
-    constexpr int B = 2;
-    const int64_t first = ((int64_t)blockIdx.x * 8 + threadIdx.x / 32) * B;
-    const int lane = threadIdx.x & 31;
-    uint32_t gate[B][4], up[B][4];
-    int64_t row[B], k0[B];
+    const int lane = threadIdx.x & 31, H = (int)a.H;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const char* x = static_cast<const char*>(a.x) + row * a.ldx * elt_bytes<ELT>();
+        const char* u = x + a.H * elt_bytes<ELT>();
+        const char* g = FORM == GateForm::GRAD ? static_cast<const char*>(a.g) + row * a.ldg * elt_bytes<ELT>() : nullptr;
+        for (int b = blockIdx.y * 8 + threadIdx.x / 32; b < nb; b += gridDim.y * 8) {
+            const int k = b * 128 + lane;
+            uint32_t gate[4], up[4], of[4];
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-        split_index(first + i, nb, row[i], k0[i]);
-        k0[i] = k0[i] * 128 + lane;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool there = row[i] < a.rows && k0[i] + 32 * j < a.H;
-            gate[i][j] = there ? load_f32<ELT>(a.x, row[i] * a.ldx + k0[i] + 32 * j) : 0u;
-            up[i][j] = there ? load_f32<ELT>(a.x, row[i] * a.ldx + a.H + k0[i] + 32 * j) : 0u;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-        if (row[i] >= a.rows) break;
-        float v[4];
-        gated<Elt::FP32, 4, QUANT>(gate[i], up[i], v);
-        uint32_t amax = amax_of<4>(v);
-        if constexpr (QUANT) amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-        const uint32_t code = scale_code128(amax);
-        if (QUANT && lane == 0) a.scales[first + i] = (uint8_t)code;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (k0[i] + 32 * j < a.H) {
-                const int64_t at = row[i] * a.H + k0[i] + 32 * j;
-                if constexpr (QUANT) a.data[at] = e4m3_byte(v[j], code);
-                else store_f32<ELT>(a.out, at, v[j]);
+            for (int q = 0; q < 4; ++q) {
+                const bool there = k + 32 * q < H;
+                gate[q] = there ? load_f32<ELT>(x, k + 32 * q) : 0u;
+                up[q] = there ? load_f32<ELT>(u, k + 32 * q) : 0u;
+                of[q] = FORM == GateForm::GRAD && there ? load_f32<ELT>(g, k + 32 * q) : 0u;
             }
+            if constexpr (FORM == GateForm::GRAD) {
+                char* to = static_cast<char*>(a.out) + row * 2 * a.H * elt_bytes<ELT>();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const GateGrad d(__uint_as_float(of[q]), __uint_as_float(gate[q]), __uint_as_float(up[q]));
+                    if (k + 32 * q < H) {
+                        store_f32<ELT>(to, k + 32 * q, d.gate);
+                        store_f32<ELT>(to, H + (int64_t)k + 32 * q, d.up);
+                    }
+                }
+            } else {
+                constexpr bool QUANT = FORM == GateForm::ROWS;
+                float v[4];
+                gated_loose<ELT, 4, QUANT>(gate, up, v);
+                if constexpr (QUANT) {
+                    const uint32_t code = scale_code128(__reduce_max_sync(0xFFFFFFFFu, amax_of<4>(v)));
+                    if (lane == 0) a.scales[row * nb + b] = (uint8_t)code;
+                    const float2 inv = both(__uint_as_float(inv_scale128(code)));
+                    uint8_t* to = a.data + row * a.H;
+#pragma unroll
+                    for (int q = 0; q < 4; q += 2) {
+                        const float2 p = mul2(make_float2(v[q], v[q + 1]), inv);
+                        const uint32_t two = code == 255u ? 0x7F7Fu : e4m3x2_from_f32(__float_as_uint(p.y), __float_as_uint(p.x));
+                        if (k + 32 * q < H) to[k + 32 * q] = (uint8_t)two;
+                        if (k + 32 * q + 32 < H) to[k + 32 * q + 32] = (uint8_t)(two >> 8);
+                    }
+                } else {
+                    char* to = static_cast<char*>(a.out) + row * a.H * elt_bytes<ELT>();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (k + 32 * q < H) store_f32<ELT>(to, k + 32 * q, v[q]);
+                }
+            }
+        }
     }
 }
 
@@ -305,7 +350,7 @@ __global__ void __launch_bounds__(512) gate_columns_kernel(GateArgs a) {
         up[i] = there ? load_f32<ELT>(a.x, r * a.ldx + a.H + c) : 0u;
     }
     float v[R];
-    gated<Elt::FP32, R, true>(gate, up, v);
+    gated_loose<ELT, R, true>(gate, up, v);
     uint32_t amax = amax_of<R>(v);
     top[ty][tx] = amax;
     __syncthreads();
@@ -318,17 +363,6 @@ __global__ void __launch_bounds__(512) gate_columns_kernel(GateArgs a) {
     for (int i = 0; i < R; ++i)
         if (r0 + Y * i < a.rows) a.data[(r0 + Y * i) * a.H + c] = e4m3_byte(v[i], code);
 }
-
-struct GateGrad {
-    float gate, up;
-    // d_up = g silu(gate);  d_gate = g up (s + silu(gate) (1 - s))
-    __device__ __forceinline__ GateGrad(float g, float x, float u) {
-        const Sigmoid s(x);
-        const float silu = fmul(x, s.s);
-        up = fmul(g, silu);
-        gate = fmul(fmul(g, u), ffma(silu, s.rest, s.s));
-    }
-};
 
 // A unit of 16 elements of both halves a thread.
 template <Elt ELT>
@@ -357,21 +391,16 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(GateArgs a, int64_t nu) 
     up.store(a.out, row * 2 * a.H + a.H + k);
 }
 
-// Any alignment and any H: an element a thread.
-template <Elt ELT>
-__global__ void __launch_bounds__(256) gate_grad_any_kernel(GateArgs a) {
-    let_next_start();
-    wait_for_stream();
-    int64_t row, k;
-    split_index((int64_t)blockIdx.x * 256 + threadIdx.x, a.H, row, k);
-    if (row >= a.rows) return;
-    const GateGrad d(__uint_as_float(load_f32<ELT>(a.g, row * a.ldg + k)), __uint_as_float(load_f32<ELT>(a.x, row * a.ldx + k)),
-                     __uint_as_float(load_f32<ELT>(a.x, row * a.ldx + a.H + k)));
-    store_f32<ELT>(a.out, row * 2 * a.H + k, d.gate);
-    store_f32<ELT>(a.out, row * 2 * a.H + a.H + k, d.up);
-}
-
 constexpr int64_t kMostBlocks = INT64_C(0x7FFFFFFF);
+
+template <Elt ELT, GateForm FORM>
+cudaError_t any_launch(const GateArgs& a, cudaStream_t s) {
+    // few rows are cut into slices so that the device is full
+    const int64_t nb = ceil_div(a.H, 128), slices = ceil_div(nb, 8), wanted = ceil_div((int64_t)sm_count() * 8, a.rows);
+    const dim3 grid((unsigned)(a.rows < kMostBlocks ? a.rows : kMostBlocks),
+                    (unsigned)(wanted < 1 ? 1 : wanted < slices ? wanted : slices < 65535 ? slices : 65535));
+    return launch_overlapped(gate_any_kernel<ELT, FORM>, grid, 256, 0, 0, s, a, (int)nb);
+}
 
 template <Elt ELT>
 cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
@@ -384,9 +413,7 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
             if (grid > kMostBlocks) return cudaErrorInvalidValue;
             return launch_overlapped(gate_grad_kernel<ELT>, dim3((unsigned)grid), 256, 0, 0, s, a, a.H / 16);
         }
-        const int64_t grid = ceil_div(a.rows * a.H, 256);
-        if (grid > kMostBlocks) return cudaErrorInvalidValue;
-        return launch_overlapped(gate_grad_any_kernel<ELT>, dim3((unsigned)grid), 256, 0, 0, s, a);
+        return any_launch<ELT, GateForm::GRAD>(a, s);
     }
     if (form == GateForm::COLUMNS) {
         // 8 columns: 16 bytes of bf16, 32 of fp32, 8 of payload and scales
@@ -414,9 +441,7 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
         return quant ? launch_overlapped(gate_rows_kernel<ELT, true>, grid, 256, 0, 0, s, a, nb)
                      : launch_overlapped(gate_rows_kernel<ELT, false>, grid, 256, 0, 0, s, a, nb);
     }
-    const dim3 grid((unsigned)ceil_div(a.rows * nb, 16));
-    return quant ? launch_overlapped(gate_any_kernel<ELT, true>, grid, 256, 0, 0, s, a, nb)
-                 : launch_overlapped(gate_any_kernel<ELT, false>, grid, 256, 0, 0, s, a, nb);
+    return quant ? any_launch<ELT, GateForm::ROWS>(a, s) : any_launch<ELT, GateForm::PLAIN>(a, s);
 }
 
 }  // namespace

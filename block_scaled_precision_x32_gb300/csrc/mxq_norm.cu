@@ -144,100 +144,121 @@ __device__ __forceinline__ float value_at(const void* p, int64_t k) {
 
 // Any alignment and any K: one row to a block, 1x128 blocks to its warps in
 // turn, neighbours to neighbouring lanes: an element at a time, so that
-// instructions bound it; whole blocks go without a check for each element.
-// The first kHeld blocks of a warp (rows of 8192) stay in registers, what is
-// behind them is read again.
+// instructions bound it.  The first kHeld blocks of a warp (rows of 8192) stay
+// in registers, what is behind them is read again.
 template <Elt ELT, Elt WELT, bool RES>
-__global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(NormArgs a, int64_t nb) {
+__global__ void __launch_bounds__(kAnyThreads, 4) norm_any_kernel(NormArgs a, int nb) {
     __shared__ __align__(16) float part[kAnyWarps];
     let_next_start();
     wait_for_stream();
     const int64_t row = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, K = (int)a.K;
     const void* x = at_row<ELT>(a.x, row, a.ldx);
     const void* res = RES ? at_row<ELT>(a.residual, row, a.ldr) : nullptr;
     void* hp = RES && a.h ? at_row<ELT>(a.h, row, a.ldh) : nullptr;
     void* yp = a.y ? at_row<ELT>(a.y, row, a.K) : nullptr;
     uint8_t* data = a.data ? a.data + row * a.K : nullptr;
-    const auto sum_at = [&](int64_t k) {
-        float v = value_at<ELT>(x, k);
-        if constexpr (RES) {
-            v = fadd(v, value_at<ELT>(res, k));
-            if constexpr (ELT == Elt::BF16) v = __uint_as_float(bf16x2_from_f32(v, 0.0f) & 0xFFFF0000u);
-        }
-        return v;
-    };
     // the lane's four elements of block b, zeros behind the row
-    const auto read = [&](int64_t b, float (&v)[4]) {
-        const int64_t k = b * 128 + lane;
-        if (b * 128 + 128 <= a.K) {
+    const auto read = [&](int b, float (&v)[4]) {
+        const int k = b * 128 + lane;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = sum_at(k + 32 * q);
-        } else {
+        for (int q = 0; q < 4; ++q) v[q] = k + 32 * q < K ? value_at<ELT>(x, k + 32 * q) : 0.0f;
+        if constexpr (RES) {
+            float r[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = k + 32 * q < a.K ? sum_at(k + 32 * q) : 0.0f;
+            for (int q = 0; q < 4; ++q) r[q] = k + 32 * q < K ? value_at<ELT>(res, k + 32 * q) : 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+                v[q] = fadd(v[q], r[q]), v[q + 1] = fadd(v[q + 1], r[q + 1]);
+                if constexpr (ELT == Elt::BF16) {
+                    const uint32_t two = bf16x2_from_f32(v[q + 1], v[q]);
+                    v[q] = __uint_as_float(two << 16), v[q + 1] = __uint_as_float(two & 0xFFFF0000u);
+                }
+            }
         }
     };
-    const auto keep = [&](int64_t b, const float (&v)[4], float sum) {
+    const auto keep = [&](int b, const float (&v)[4], float sum) {
+        const int k = b * 128 + lane;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (hp && b * 128 + lane + 32 * q < a.K) store_f32<ELT>(hp, b * 128 + lane + 32 * q, v[q]);
+            if (hp && k + 32 * q < K) store_f32<ELT>(hp, k + 32 * q, v[q]);
             sum = ffma(v[q], v[q], sum);
         }
         return sum;
     };
     float held[kHeld][4], sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) read((int64_t)i * kAnyWarps + warp, held[i]);
+    for (int i = 0; i < kHeld; ++i) read(i * kAnyWarps + warp, held[i]);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-        if ((int64_t)i * kAnyWarps + warp < nb) sum = keep((int64_t)i * kAnyWarps + warp, held[i], sum);
-    for (int64_t b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps) {
+        if (i * kAnyWarps + warp < nb) sum = keep(i * kAnyWarps + warp, held[i], sum);
+    for (int b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps) {
         float v[4];
         read(b, v);
         sum = keep(b, v, sum);
     }
     const float rstd = rstd_of(row_sum(sum, part, 0, kAnyWarps), a.K, a.eps);
     if (a.rstd && threadIdx.x == 0) store_f32<Elt::FP32>(a.rstd, row, rstd);
-    const auto finish = [&](int64_t b, const float (&v)[4], auto whole) {
-        const int64_t k = b * 128 + lane;
-        float y[4];
-        uint32_t amax = 0;
+    // weights of the lane's four elements of block b; any value behind the row
+    const auto weights = [&](int b, float (&w)[4]) {
+        const int k = b * 128 + lane;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const bool there = decltype(whole)::value || k + 32 * q < a.K;
-            y[q] = there ? fmul(fmul(v[q], rstd), value_at<WELT>(a.weight, k + 32 * q)) : 0.0f;
-            amax = max(amax, __float_as_uint(y[q]) & 0x7FFFFFFFu);
-            if (yp && there) store_f32<ELT>(yp, k + 32 * q, y[q]);
-        }
-        if (!data) return;
-        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-        const uint32_t code = scale_code128(amax);
-        if (lane == 0) a.scales[row * nb + b] = (uint8_t)code;
-        const float inv = __uint_as_float(inv_scale128(code));
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-            uint32_t two = e4m3x2_from_f32(__float_as_uint(fmul(y[q + 1], inv)), __float_as_uint(fmul(y[q], inv)));
-            if (code == 255u) two = 0x7F7Fu;
-            if (decltype(whole)::value || k + 32 * q < a.K) data[k + 32 * q] = (uint8_t)two;
-            if (decltype(whole)::value || k + 32 * q + 32 < a.K) data[k + 32 * q + 32] = (uint8_t)(two >> 8);
+            const int i = k + 32 * q < K ? k + 32 * q : 0;
+            if constexpr (WELT == Elt::BF16) w[q] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.weight) + i) << 16);
+            else w[q] = __ldg(static_cast<const float*>(a.weight) + i);
         }
     };
+    const auto finish = [&](int b, const float (&v)[4], const float (&w)[4]) {
+        const int k = b * 128 + lane;
+        const bool there[4] = {k < K, k + 32 < K, k + 64 < K, k + 96 < K};
+        float2 y[2];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int64_t b = (int64_t)i * kAnyWarps + warp;
-        if (b * 128 + 128 <= a.K) finish(b, held[i], std::true_type());
-        else if (b < nb) finish(b, held[i], std::false_type());
-    }
-    for (int64_t b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps) {
-        float v[4];
-        // h may lie over x or the residual: what this thread wrote there is read back
+        for (int q = 0; q < 2; ++q) y[q] = mul2(mul2(make_float2(v[2 * q], v[2 * q + 1]), both(rstd)), make_float2(w[2 * q], w[2 * q + 1]));
+        if (!there[3]) y[1].y = 0.0f;
+        if (!there[2]) y[1].x = 0.0f;
+        if (!there[1]) y[0].y = 0.0f;
+        if (!there[0]) y[0].x = 0.0f;
+        const float top = absmax3(absmax3(0.0f, y[0].x, y[0].y), y[1].x, y[1].y);
+        if (yp)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t k = b * 128 + lane + 32 * q;
-            v[q] = k >= a.K ? 0.0f : hp ? value_at<ELT>(hp, k) : sum_at(k);
+            for (int q = 0; q < 4; ++q) {
+                const float f = q & 1 ? y[q / 2].y : y[q / 2].x;
+                if (there[q]) store_f32<ELT>(yp, k + 32 * q, f);
+            }
+        if (!data) return;
+        const uint32_t code = scale_code128(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top) & 0x7FFFFFFFu));
+        if (lane == 0) a.scales[row * nb + b] = (uint8_t)code;
+        const float2 inv = both(__uint_as_float(inv_scale128(code)));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float2 p = mul2(y[q], inv);
+            const uint32_t two = code == 255u ? 0x7F7Fu : e4m3x2_from_f32(__float_as_uint(p.y), __float_as_uint(p.x));
+            if (there[2 * q]) data[k + 64 * q] = (uint8_t)two;
+            if (there[2 * q + 1]) data[k + 64 * q + 32] = (uint8_t)(two >> 8);
         }
-        finish(b, v, std::false_type());
+    };
+    // the weights of four blocks are on their way at once
+#pragma unroll
+    for (int i0 = 0; i0 < kHeld; i0 += 4) {
+        float w[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) weights((i0 + i) * kAnyWarps + warp, w[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((i0 + i) * kAnyWarps + warp < nb) finish((i0 + i) * kAnyWarps + warp, held[i0 + i], w[i]);
+    }
+    for (int b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps) {
+        float v[4], w[4];
+        weights(b, w);
+        // h may lie over x or the residual: what this thread wrote there is read back
+        if (hp) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = b * 128 + lane + 32 * q < K ? value_at<ELT>(hp, b * 128 + lane + 32 * q) : 0.0f;
+        } else {
+            read(b, v);
+        }
+        finish(b, v, w);
     }
 }
 
@@ -420,6 +441,70 @@ __global__ void __launch_bounds__(512) norm_grad_rows_kernel(NormGradArgs a, int
     }
 }
 
+// Rows of up to 8192 elements that do not lie on 16 bytes: a persistent block
+// to a multiprocessor, every 1024th element of a row to a thread, the next row's
+// on their way while it works on one.
+constexpr int kLooseThreads = 1024, kLoose = 8;
+template <Elt ELT>
+__global__ void __launch_bounds__(kLooseThreads) norm_grad_loose_kernel(NormGradArgs a, bool w_bf16) {
+    __shared__ __align__(16) float part[2][kLooseThreads / 32];
+    let_next_start();
+    wait_for_stream();
+    const int K = (int)a.K;
+    // what is on its way stays as it is in memory: to touch it would be to wait for it
+    using Raw = typename std::conditional<ELT == Elt::BF16, uint16_t, uint32_t>::type;
+    const auto f32_of = [](Raw v) { return __uint_as_float(ELT == Elt::BF16 ? (uint32_t)v << 16 : (uint32_t)v); };
+    float w[kLoose], dw[kLoose] = {};
+    Raw next_g[kLoose], next_h[kLoose];
+#pragma unroll
+    for (int i = 0; i < kLoose; ++i) {
+        const int k = i * kLooseThreads + threadIdx.x;
+        w[i] = k >= K ? 0.0f : w_bf16 ? value_at<Elt::BF16>(a.weight, k) : value_at<Elt::FP32>(a.weight, k);
+    }
+    const auto fetch = [&](int64_t row) {
+        const Raw* g = reinterpret_cast<const Raw*>(at_row<ELT>(a.g, row, a.ldg));
+        const Raw* h = reinterpret_cast<const Raw*>(at_row<ELT>(a.h, row, a.ldh));
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) {
+            const int k = i * kLooseThreads + threadIdx.x;
+            const bool there = row < a.rows && k < K;
+            next_g[i] = there ? g[k] : (Raw)0;
+            next_h[i] = there ? h[k] : (Raw)0;
+        }
+    };
+    const float per_k = fdiv(1.0f, (float)K);
+    fetch(blockIdx.x);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const float r = a.rstd[row];
+        float g[kLoose], h[kLoose], dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) {
+            g[i] = f32_of(next_g[i]);
+            h[i] = fmul(f32_of(next_h[i]), r);
+            dw[i] = ffma(g[i], h[i], dw[i]);
+            g[i] = fmul(g[i], w[i]);
+            dot = ffma(g[i], h[i], dot);
+        }
+        fetch(row + gridDim.x);
+        const float c = fmul(row_sum(dot, part[turn], 0, kLooseThreads / 32), per_k);
+        const Raw* add = a.g_h ? reinterpret_cast<const Raw*>(at_row<ELT>(a.g_h, row, a.ldgh)) : nullptr;
+        Raw more[kLoose];  // all of them ahead of the first store, which may go to the same memory
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) more[i] = add && i * kLooseThreads + (int)threadIdx.x < K ? add[i * kLooseThreads + threadIdx.x] : (Raw)0;
+        void* to = at_row<ELT>(a.d_h, row, a.ldd);
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) {
+            const int k = i * kLooseThreads + threadIdx.x;
+            if (k < K) store_f32<ELT>(to, k, ffma(ffma(h[i], -c, g[i]), r, f32_of(more[i])));
+        }
+    }
+    if (!a.parts) return;
+#pragma unroll
+    for (int i = 0; i < kLoose; ++i)
+        if (i * kLooseThreads + (int)threadIdx.x < K) a.parts[blockIdx.x * a.K + i * kLooseThreads + threadIdx.x] = dw[i];
+}
+
 template <Elt ELT>
 __device__ __forceinline__ float weight_at(const void* w, int64_t k, bool bf16) {
     return __uint_as_float(bf16 ? load_f32<Elt::BF16>(w, k) : load_f32<Elt::FP32>(w, k));
@@ -509,8 +594,8 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
                        unit_rows<ELT>(a.y, a.rows, a.K) && on_bytes(a.data, 16);
     if (!units)
         return a.weight_elt == Elt::BF16
-                   ? launch_overlapped(norm_any_kernel<ELT, Elt::BF16, RES>, dim3((unsigned)a.rows), kAnyThreads, 0, 0, s, a, ceil_div(a.K, 128))
-                   : launch_overlapped(norm_any_kernel<ELT, Elt::FP32, RES>, dim3((unsigned)a.rows), kAnyThreads, 0, 0, s, a, ceil_div(a.K, 128));
+                   ? launch_overlapped(norm_any_kernel<ELT, Elt::BF16, RES>, dim3((unsigned)a.rows), kAnyThreads, 0, 0, s, a, (int)ceil_div(a.K, 128))
+                   : launch_overlapped(norm_any_kernel<ELT, Elt::FP32, RES>, dim3((unsigned)a.rows), kAnyThreads, 0, 0, s, a, (int)ceil_div(a.K, 128));
     return a.weight_elt == Elt::BF16 ? rows_launch<ELT, Elt::BF16, RES>(a, s) : rows_launch<ELT, Elt::FP32, RES>(a, s);
 }
 
@@ -559,6 +644,10 @@ cudaError_t grad_launch(const NormGradArgs& a, cudaStream_t s) {
         const int64_t groups = ceil_div(a.rows, ring.threads / ring.row_threads), most = sm_count() < kNormParts ? sm_count() : kNormParts;
         blocks = (unsigned)(groups < most ? groups : most);
         e = a.weight_elt == Elt::BF16 ? grad_rows_launch<ELT, Elt::BF16>(a, ring, blocks, s) : grad_rows_launch<ELT, Elt::FP32>(a, ring, blocks, s);
+    } else if (a.K <= kLoose * kLooseThreads) {
+        const int64_t most = sm_count() < kNormParts ? sm_count() : kNormParts;
+        blocks = (unsigned)(a.rows < most ? a.rows : most);
+        e = launch_overlapped(norm_grad_loose_kernel<ELT>, dim3(blocks), kLooseThreads, 0, 0, s, a, a.weight_elt == Elt::BF16);
     } else {
         blocks = (unsigned)(a.rows < kNormParts ? a.rows : kNormParts);
         e = cudaSuccess;
