@@ -1055,6 +1055,8 @@ class Library:
         rows, K, ldx = _matrix(x, "x")
         if weight.get_device() != dev or weight.dim() != 1 or weight.shape[0] != K or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous vector of {K} values on x's device")
+        if not 0.0 <= eps <= 3.4e38:
+            raise ValueError("eps must be finite and not negative")
         ldr = ldh = pr = ph = py = pd = ps = pst = 0
         if residual is not None:
             ldr, pr = _like_rows(residual, x, rows, K, "residual", dev), residual.data_ptr()
@@ -1159,6 +1161,8 @@ class Library:
         if bias is not None:
             _same_device(dev, bias)
             _check_values(bias, torch.float32, E, "bias", "experts")
+        if not -3.4e38 <= scale <= 3.4e38:
+            raise ValueError("scale must be finite")
         if not (1 <= topk <= 32 and 1 <= E <= 1024 and topk <= E):
             raise ValueError("1 to 1024 experts, and 1 to 32 choices of them, at most as many as there are")
         if not (1 <= groups <= 32 and E % groups == 0 and 1 <= topk_groups <= groups and 1 <= group_top <= min(2, E // groups)

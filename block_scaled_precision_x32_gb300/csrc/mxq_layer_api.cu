@@ -26,6 +26,7 @@ mxq::Elt elt_of(mxq_dtype dt) { return dt == MXQ_BF16 ? mxq::Elt::BF16 : mxq::El
 mxq_status launch_status(cudaError_t e) { return e == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA; }
 
 bool valid_dim(int64_t n) { return n >= 0 && n <= kMaxDim; }
+bool valid_width(int64_t n) { return n >= 0 && n <= (INT64_C(1) << 30); }  // of a row that is indexed in 32 bits
 bool valid_ld(int64_t n, int64_t ld) { return ld >= n && ld <= kMaxLd; }
 
 mxq_status quant128(bool columns, const void* x, mxq_dtype dt, int64_t rows, int64_t K, int64_t ldx,
@@ -318,7 +319,7 @@ mxq_status mxq_moe_combine_grad(const void* g, const void* y, mxq_dtype dt, int6
 mxq_status mxq_fp8_dispatch(const uint8_t* data, const uint8_t* scales, int64_t tokens, int64_t K, int64_t ld,
                             const int32_t* source, int64_t topk, int64_t rows, uint8_t* out, uint8_t* out_scales,
                             cudaStream_t stream) {
-    if (!valid_dim(tokens) || !valid_dim(K) || !valid_dim(rows) || !valid_ld(K, ld) || topk < 1 || topk > kMaxDim)
+    if (!valid_dim(tokens) || !valid_width(K) || !valid_dim(rows) || !valid_ld(K, ld) || topk < 1 || topk > kMaxDim)
         return MXQ_ERR_INVALID_ARG;
     if (rows == 0 || K == 0) return MXQ_OK;
     if ((tokens > 0 && (!data || !scales)) || !source || !out || !out_scales || !aligned(source, 4)) return MXQ_ERR_INVALID_ARG;
@@ -345,11 +346,13 @@ mxq_status mxq_rmsnorm(const mxq_norm* p, cudaStream_t stream) {
     if (st != MXQ_OK) return st;
     st = check_dtype(p->weight_dt);
     if (st != MXQ_OK) return st;
-    if (!valid_dim(p->rows) || !valid_dim(p->K) || !valid_ld(p->K, p->ldx) || !(p->eps >= 0.0f && p->eps <= 3.4e38f))
+    if (!valid_dim(p->rows) || !valid_width(p->K) || !valid_ld(p->K, p->ldx) || !(p->eps >= 0.0f && p->eps <= 3.4e38f))
         return MXQ_ERR_INVALID_ARG;
     if ((p->residual && !valid_ld(p->K, p->ldr)) || (p->h && (!p->residual || !valid_ld(p->K, p->ldh))) || !p->data != !p->scales)
         return MXQ_ERR_INVALID_ARG;
-    if (p->rows == 0 || p->K == 0) return MXQ_OK;
+    if (p->rows == 0) return MXQ_OK;
+    if (p->K == 0)  // the mean of nothing
+        return p->rstd ? launch_status(cudaMemsetAsync(p->rstd, 0xFF, (size_t)p->rows * 4, stream)) : MXQ_OK;
     const size_t es = elt_size(p->dt);
     if (!p->x || !p->weight || !aligned(p->x, es) || !aligned(p->residual, es) || !aligned(p->weight, elt_size(p->weight_dt)) ||
         !aligned(p->h, es) || !aligned(p->y, es) || !aligned(p->rstd, 4))
@@ -378,7 +381,7 @@ mxq_status mxq_rmsnorm(const mxq_norm* p, cudaStream_t stream) {
 }
 
 size_t mxq_rmsnorm_grad_workspace(int64_t rows, int64_t K) {
-    if (!valid_dim(rows) || !valid_dim(K)) return 0;
+    if (!valid_dim(rows) || !valid_width(K)) return 0;
     return (size_t)((rows < mxq::kNormParts ? rows : mxq::kNormParts) * K) * 4;
 }
 
@@ -388,7 +391,7 @@ mxq_status mxq_rmsnorm_grad(const mxq_norm_grad* p, void* workspace, size_t work
     if (st != MXQ_OK) return st;
     st = check_dtype(p->weight_dt);
     if (st != MXQ_OK) return st;
-    if (!valid_dim(p->rows) || !valid_dim(p->K) || !valid_ld(p->K, p->ldg) || !valid_ld(p->K, p->ldh) ||
+    if (!valid_dim(p->rows) || !valid_width(p->K) || !valid_ld(p->K, p->ldg) || !valid_ld(p->K, p->ldh) ||
         (p->g_h && !valid_ld(p->K, p->ldgh)) || !valid_ld(p->K, p->ldd) || !aligned(p->d_weight, 4))
         return MXQ_ERR_INVALID_ARG;
     if (p->K == 0) return MXQ_OK;
@@ -430,7 +433,7 @@ static mxq_status gate(mxq::GateForm form, const void* x, mxq_dtype dt, int64_t 
     const mxq_status st = check_dtype(dt);
     if (st != MXQ_OK) return st;
     const bool grad = form == mxq::GateForm::GRAD, quant = form == mxq::GateForm::ROWS || form == mxq::GateForm::COLUMNS;
-    if (!valid_dim(rows) || H < 0 || H > kMaxDim / 2 || !valid_ld(2 * H, ldx) || (grad && !valid_ld(H, ldg))) return MXQ_ERR_INVALID_ARG;
+    if (!valid_dim(rows) || !valid_width(2 * H) || !valid_ld(2 * H, ldx) || (grad && !valid_ld(H, ldg))) return MXQ_ERR_INVALID_ARG;
     if (rows == 0 || H == 0) return MXQ_OK;
     const size_t es = elt_size(dt);
     if (!x || !aligned(x, es) || (grad && (!g || !aligned(g, es)))) return MXQ_ERR_INVALID_ARG;

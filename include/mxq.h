@@ -450,7 +450,8 @@ MXQ_API mxq_status mxq_fp8_dispatch(const uint8_t* data, const uint8_t* scales, 
  * block: the norm in front of it, the router, the gated activation.
  * Arithmetic, sums and statistics are fp32, with one rounding to the result's
  * type; none of these calls uses atomics, and results do not depend on the
- * order in which blocks of the grid run.
+ * order in which blocks of the grid run.  A row has at most 2^30 elements.
+ * Outputs must not overlap inputs but where it is said.
  * ------------------------------------------------------------------------ */
 
 /* Root-mean-square norm of x plus a residual:
@@ -460,7 +461,8 @@ MXQ_API mxq_status mxq_fp8_dispatch(const uint8_t* data, const uint8_t* scales, 
  * and y as the operand of the next product, as mxq_fp8_quant_1x128 quantizes,
  * from the fp32 y, which is not rounded to dt before.  A row that holds a NaN
  * comes out NaN; one whose squares overflow fp32 (an infinity among them) has
- * rstd = 0. */
+ * rstd = 0, and y = 0 but for NaN in the infinity's place.  rstd of rows of no
+ * elements is NaN. */
 typedef struct {
     mxq_dtype dt;          /* x, residual, h, y */
     mxq_dtype weight_dt;
@@ -558,7 +560,9 @@ MXQ_API mxq_status mxq_moe_route_grad(const float* g, const mxq_route* p, const 
  * the fp32 a, as mxq_fp8_quant_1x128 does for the second product and
  * mxq_fp8_quant_128x1 for its weight's gradient: data [rows, H]; scales [rows,
  * ceil(H/128)] or [ceil(rows/128), H].
- * silu(-inf) is NaN (0 * inf).
+ * silu(-inf) is NaN (0 * inf); an infinite bf16 gate of either sign poisons its
+ * block, as an infinity does.  A bf16 gate below -87 counts as -87 in the fp8
+ * forms, which is off by 1.5e-36 |up| at most.
  * Errors: INVALID_ARG, UNSUPPORTED_DTYPE. */
 MXQ_API mxq_status mxq_silu_mul(const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx, void* out,
                                 cudaStream_t stream);

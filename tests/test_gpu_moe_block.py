@@ -617,3 +617,61 @@ def test_route_of_many_tokens_gives_what_few_do(mx):
         i, v = mx.moe_route(x[a:a + 1000], 8, **kw)
         assert torch.equal(i, ids[a:a + 1000])
         near(v, f64(w[a:a + 1000]), 100 * U * f64(w[a:a + 1000]))
+
+
+# ----------------------------------------------------- ends of the ranges
+
+
+def test_offsets_beyond_32_bits(mx):
+    """Tensors of more than 2^31 elements: their last rows are those of a small call."""
+    rows, K = 262400, 8192
+    x = torch.empty(rows, K, dtype=BF16, device="cuda")
+    x[-300:] = torch.randn(300, K, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    x[:-300] = 1.0
+    w = torch.ones(K, dtype=BF16, device="cuda")
+    whole, few = mx.rmsnorm(x, w, stats=True), mx.rmsnorm(x[-300:], w, stats=True)
+    for a, b in ((whole.data, few.data), (whole.scales, few.scales), (whole.rstd, few.rstd)):
+        assert torch.equal(a[-300:], b)
+    d, _ = mx.rmsnorm_grad(x, x, w, whole.rstd, weight_grad=False)
+    assert torch.equal(d[-300:], mx.rmsnorm_grad(x[-300:], x[-300:], w, few.rstd, weight_grad=False)[0])
+    source = torch.arange(rows - 1, rows - 301, -1, dtype=torch.int32, device="cuda")
+    got = mx.fp8_dispatch(whole.data, whole.scales, source, 1)
+    assert torch.equal(got[0], few.data.flip(0)) and torch.equal(got[1], few.scales.flip(0))
+    del d, whole
+    for f in (mx.fp8_silu_mul_1x128, mx.silu_mul, lambda t: mx.silu_mul_grad(t[:, : K // 2], t)):
+        a, b = f(x), f(x[-300:])
+        for p, q in zip(a if isinstance(a, tuple) else (a,), b if isinstance(b, tuple) else (b,)):
+            assert torch.equal(p[-300:], q)
+    a, b = mx.fp8_silu_mul_128x1(x), mx.fp8_silu_mul_128x1(x[-256:])  # rows is a multiple of 128
+    assert torch.equal(a[0][-256:], b[0]) and torch.equal(a[1][-2:], b[1])
+
+
+def test_rows_of_no_elements(mx):
+    x, w = torch.empty(3, 0, device="cuda"), torch.empty(0, device="cuda")
+    r = mx.rmsnorm(x, w, stats=True, normed=True)
+    assert r.data.shape == (3, 0) and r.scales.shape == (3, 0) and torch.isnan(r.rstd).all()
+    d, dw = mx.rmsnorm_grad(x, x, w, r.rstd)
+    assert d.shape == (3, 0) and dw.shape == (0,)
+    assert mx.silu_mul(x).shape == (3, 0) and mx.fp8_silu_mul_128x1(x)[1].shape == (1, 0)
+
+
+def test_refusals_of_the_binding(mx):
+    x, w, res = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda"), torch.ones(4, 64, device="cuda", dtype=BF16)
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    g = torch.ones(4, 2, device="cuda")
+    for f in (lambda: mx.rmsnorm(x, w[:63]), lambda: mx.rmsnorm(x, w.cpu()), lambda: mx.rmsnorm(x, w, res), lambda: mx.rmsnorm(x, w, x[:3]),
+              lambda: mx.rmsnorm(x, w, eps=-1.0), lambda: mx.rmsnorm(x, w, eps=float("nan")), lambda: mx.rmsnorm(x, w, eps=1e39), lambda: mx.rmsnorm(x, w, h=x),
+              lambda: mx.rmsnorm(x.t(), w[:4]), lambda: mx.rmsnorm(x, w.expand(2, 64)), lambda: mx.rmsnorm_grad(x, res, w, w[:4]),
+              lambda: mx.rmsnorm_grad(x, x, w, w[:5]), lambda: mx.rmsnorm_grad(x, x, w, w[:4], g_h=x[:, :32]), lambda: mx.moe_route(x, 0), lambda: mx.moe_route(x, 33),
+              lambda: mx.moe_route(x, 65), lambda: mx.moe_route(x, 2, score="tanh"), lambda: mx.moe_route(x, 2, groups=3), lambda: mx.moe_route(x, 2, groups=4, topk_groups=5),
+              lambda: mx.moe_route(x, 8, groups=32), lambda: mx.moe_route(x, 2, group_top=3), lambda: mx.moe_route(x, 2, bias=w.cpu()), lambda: mx.moe_route(x, 2, bias=w[:5]),
+              lambda: mx.moe_route(x, 2, scale=float("inf")), lambda: mx.moe_route(x[0], 2), lambda: mx.moe_route_grad(g, x, ids.long()), lambda: mx.moe_route_grad(g[:3], x, ids),
+              lambda: mx.moe_route_grad(g, x, ids[:3]), lambda: mx.silu_mul(x[:, :63]), lambda: mx.silu_mul_grad(x, x), lambda: mx.silu_mul_grad(res[:, :32], x),
+              lambda: mx.fp8_silu_mul_1x128(x, data=torch.empty(4, 31, dtype=torch.uint8, device="cuda")),
+              lambda: mx.fp8_dispatch(x, x, ids.view(-1), 2), lambda: mx.fp8_dispatch(res.view(torch.uint8), ids.view(torch.uint8)[:, :1], ids.view(-1), 2)):
+        with pytest.raises(ValueError):
+            f()
+    half = x.half()
+    for f in (lambda: mx.rmsnorm(half, w), lambda: mx.rmsnorm(x, w.half()), lambda: mx.moe_route(half, 2), lambda: mx.silu_mul(half)):
+        with pytest.raises(mxq.MXQError):
+            f()

@@ -63,7 +63,7 @@ NAN, INF = float("nan"), float("inf")
     (dict(h=FAKE, ldh=32), INVALID), (dict(residual=FAKE, ldr=32, h=FAKE, ldh=31), INVALID), (dict(scales=None), INVALID), (dict(data=None), INVALID),
     (dict(x=None), INVALID), (dict(weight=None), INVALID), (dict(x=FAKE + 1), INVALID), (dict(weight=FAKE + 1), INVALID), (dict(y=FAKE + 1), INVALID),
     (dict(rstd=FAKE + 2), INVALID), (dict(residual=FAKE + 64, ldr=32, h=FAKE + 64, ldh=48), INVALID), (dict(residual=FAKE + 64, ldr=32, h=FAKE, ldh=48), INVALID),
-    (dict(rows=0), OK), (dict(K=0, ldx=0), OK), (dict(data=None, scales=None), OK),
+    (dict(K=(1 << 30) + 1, ldx=1 << 31), INVALID), (dict(rows=0), OK), (dict(K=0, ldx=0), OK), (dict(data=None, scales=None), OK),
 ])
 def test_norm_refusals(lib, change, status):
     assert lib.L.mxq_rmsnorm(norm(**change), None) == status
@@ -133,7 +133,7 @@ def test_gate_refusals(lib):
     assert L.mxq_silu_mul(FAKE, 5, 4, 32, 64, FAKE, None) == INVALID
     assert L.mxq_silu_mul(FAKE, 0, 4, 32, 63, FAKE, None) == INVALID  # ldx < 2H
     assert L.mxq_silu_mul(FAKE, 0, -4, 32, 64, FAKE, None) == INVALID
-    assert L.mxq_silu_mul(FAKE, 0, 4, 1 << 30, 1 << 31, FAKE, None) == INVALID
+    assert L.mxq_silu_mul(FAKE, 0, 4, (1 << 29) + 1, 1 << 31, FAKE, None) == INVALID
     assert L.mxq_silu_mul(None, 0, 4, 32, 64, FAKE, None) == INVALID
     assert L.mxq_silu_mul(FAKE, 0, 4, 32, 64, None, None) == INVALID
     assert L.mxq_silu_mul(FAKE, 0, 4, 32, 64, FAKE + 1, None) == INVALID
