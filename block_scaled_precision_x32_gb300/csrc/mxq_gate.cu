@@ -98,10 +98,13 @@ __device__ __forceinline__ void gated_loose(const uint32_t* gate, const uint32_t
     }
 }
 
-// 4 or a multiple of 8 words.
+// 2, 4 or a multiple of 8 words.
 template <int W>
 __device__ __forceinline__ void load_words(uint32_t* w, const char* p) {
-    if constexpr (W == 4) {
+    if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else if constexpr (W == 4) {
         const uint4 v = *reinterpret_cast<const uint4*>(p);
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
@@ -177,43 +180,45 @@ __global__ void __launch_bounds__(256, ELT == Elt::FP32 ? 4 : QUANT ? 7 : 5) gat
     }
 }
 
-// 128 rows x 8 TX columns a block, 8 columns of R rows a thread, in registers
-// between the maximum and the rounding: each element is read once.
-constexpr int kTileX = 4, kTileRows = 4;
+// Tiles of 128 rows x C TX columns a block, C columns of R rows a thread, in
+// registers between the maximum and the rounding: each element is read once.
+// bf16: few columns of many rows, since each column's maximum costs shuffles
+// and its scale unpacking, and 64 registers: 16379 x 4096 52.3 us, 6.4 TB/s
+// (eight columns of four rows 63 to 73, seven blocks a multiprocessor 54.6, 16
+// threads a row 54.6).  fp32: wide loads count for more, 8191 x 4096 45.8 us, 6.6
+// TB/s (four columns of eight rows 57 to 66).
 template <Elt ELT>
-__global__ void __launch_bounds__(kTileX * 128 / kTileRows, 7) gate_columns_tile_kernel(GateArgs a) {
+struct GateTile {
+    static constexpr bool kBf16 = ELT == Elt::BF16;
+    static constexpr int kC = kBf16 ? 4 : 8, kX = kBf16 ? 8 : 4, kRows = kBf16 ? 8 : 4, kBlocks = kBf16 ? 8 : 7;
+    static constexpr int kThreads = kX * 128 / kRows;
+};
+template <Elt ELT>
+__global__ void __launch_bounds__(GateTile<ELT>::kThreads, GateTile<ELT>::kBlocks) gate_columns_tile_kernel(GateArgs a) {
     let_next_start();
     wait_for_stream();
-    constexpr int TX = kTileX, R = kTileRows, TY = 128 / R, WARPS = TX * TY / 32, W = ELT == Elt::BF16 ? 4 : 8;
-    __shared__ uint4 top[WARPS][2 * TX];  // [warp][columns]
-    __shared__ uint2 codes[TX];           // a byte a column
+    constexpr int TX = GateTile<ELT>::kX, R = GateTile<ELT>::kRows, C = GateTile<ELT>::kC, TY = 128 / R, WARPS = TX * TY / 32, W = C * (int)elt_bytes<ELT>() / 4;
+    __shared__ __align__(16) uint32_t top[WARPS][C * TX];
+    __shared__ __align__(8) uint8_t codes[C * TX];
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    const int64_t c = ((int64_t)blockIdx.x * TX + tx) * 8, r0 = (int64_t)blockIdx.y * 128 + ty;
+    const int64_t c = ((int64_t)blockIdx.x * TX + tx) * C, r0 = (int64_t)blockIdx.y * 128 + ty;
     uint32_t gate[R][W], up[R][W];
+    const char* p = static_cast<const char*>(a.x) + (r0 * a.ldx + c) * elt_bytes<ELT>();
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int64_t r = r0 + TY * i;
+    for (int i = 0; i < R; ++i, p += TY * a.ldx * elt_bytes<ELT>()) {
 #pragma unroll
         for (int j = 0; j < W; ++j) gate[i][j] = up[i][j] = 0;
-        if (r < a.rows && c < a.H) {
-            const char* p = static_cast<const char*>(a.x) + (r * a.ldx + c) * elt_bytes<ELT>();
-            const char* q = p + a.H * elt_bytes<ELT>();
-            if constexpr (ELT == Elt::BF16) {
-                const uint4 g = *reinterpret_cast<const uint4*>(p), u = *reinterpret_cast<const uint4*>(q);
-                gate[i][0] = g.x, gate[i][1] = g.y, gate[i][2] = g.z, gate[i][3] = g.w;
-                up[i][0] = u.x, up[i][1] = u.y, up[i][2] = u.z, up[i][3] = u.w;
-            } else {
-                ld32(gate[i], p);
-                ld32(up[i], q);
-            }
+        if (r0 + TY * i < a.rows && c < a.H) {
+            load_words<W>(gate[i], p);
+            load_words<W>(up[i], p + a.H * elt_bytes<ELT>());
         }
     }
-    float v[R][8];
-    uint32_t m[8] = {};
+    float v[R][C];
+    uint32_t m[C];
 #pragma unroll
-    for (int i = 0; i < R; ++i) gated<ELT, 8, true>(gate[i], up[i], v[i]);
+    for (int i = 0; i < R; ++i) gated<ELT, C, true>(gate[i], up[i], v[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < C; ++j) {
         float t = 0.0f;
 #pragma unroll
         for (int i = 0; i < R; i += 2) t = absmax3(t, v[i][j], v[i + 1][j]);
@@ -221,43 +226,44 @@ __global__ void __launch_bounds__(kTileX * 128 / kTileRows, 7) gate_columns_tile
 #pragma unroll
         for (int d = TX; d < 32; d *= 2) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], d));
     }
-    if ((threadIdx.x & 31) < TX) {
-        top[threadIdx.x / 32][2 * tx] = make_uint4(m[0], m[1], m[2], m[3]);
-        top[threadIdx.x / 32][2 * tx + 1] = make_uint4(m[4], m[5], m[6], m[7]);
-    }
+    if ((threadIdx.x & 31) < TX)
+#pragma unroll
+        for (int j = 0; j < C; j += 4) *reinterpret_cast<uint4*>(&top[threadIdx.x / 32][C * tx + j]) = make_uint4(m[j], m[j + 1], m[j + 2], m[j + 3]);
     __syncthreads();
-    if (threadIdx.x < 8 * TX) {
+    if (threadIdx.x < C * TX) {
         uint32_t amax = 0;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) amax = max(amax, reinterpret_cast<const uint32_t*>(top[w])[threadIdx.x]);
+        for (int w = 0; w < WARPS; ++w) amax = max(amax, top[w][threadIdx.x]);
         const uint8_t own = (uint8_t)scale_code128(amax);
-        reinterpret_cast<uint8_t*>(codes)[threadIdx.x] = own;
-        const int64_t column = (int64_t)blockIdx.x * (8 * TX) + threadIdx.x;
+        codes[threadIdx.x] = own;
+        const int64_t column = (int64_t)blockIdx.x * (C * TX) + threadIdx.x;
         if (column < a.H) a.scales[(int64_t)blockIdx.y * a.H + column] = own;
     }
     __syncthreads();
     if (c >= a.H) return;
-    float2 inv[4];
-    uint32_t nan[2] = {};  // bytes of poisoned columns
+    float2 inv[C / 2];
+    uint32_t nan[C / 4] = {};  // bytes of poisoned columns
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t code = ((j < 4 ? codes[tx].x : codes[tx].y) >> (8 * (j & 3))) & 0xFFu;
+    for (int j = 0; j < C; ++j) {
+        const uint32_t code = *reinterpret_cast<const uint32_t*>(codes + C * tx + j / 4 * 4) >> (8 * (j & 3)) & 0xFFu;
         (j & 1 ? inv[j / 2].y : inv[j / 2].x) = __uint_as_float(inv_scale128(code));
         nan[j / 4] |= code == 255u ? 0xFFu << (8 * (j & 3)) : 0u;
     }
+    uint8_t* to = a.data + r0 * a.H + c;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
+    for (int i = 0; i < R; ++i, to += TY * a.H) {
         if (r0 + TY * i >= a.rows) break;
-        uint32_t o[2];
+        uint32_t o[C / 4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < C / 4; ++h) {
             const float2 lo = mul2(make_float2(v[i][4 * h], v[i][4 * h + 1]), inv[2 * h]),
                          hi = mul2(make_float2(v[i][4 * h + 2], v[i][4 * h + 3]), inv[2 * h + 1]);
             const uint32_t w = e4m3x2_from_f32(__float_as_uint(lo.y), __float_as_uint(lo.x)) |
                                e4m3x2_from_f32(__float_as_uint(hi.y), __float_as_uint(hi.x)) << 16;
             o[h] = lop_select(0x7F7F7F7Fu, w, nan[h]);
         }
-        *reinterpret_cast<uint2*>(a.data + (r0 + TY * i) * a.H + c) = make_uint2(o[0], o[1]);
+        if constexpr (C == 8) *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[C / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(to) = o[0];
     }
 }
 
@@ -416,9 +422,9 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
         return any_launch<ELT, GateForm::GRAD>(a, s);
     }
     if (form == GateForm::COLUMNS) {
-        // 8 columns: 16 bytes of bf16, 32 of fp32, 8 of payload and scales
-        constexpr int64_t bytes = 8 * elt_bytes<ELT>();
-        const bool tiled = a.H % 8 == 0 && on_bytes(a.x, bytes) && (a.rows <= 1 || a.ldx % 8 == 0) && on_bytes(a.data, 8) && on_bytes(a.scales, 8);
+        using Tile = GateTile<ELT>;
+        constexpr int64_t bytes = Tile::kC * elt_bytes<ELT>();  // of a thread's columns
+        const bool tiled = a.H % Tile::kC == 0 && on_bytes(a.x, bytes) && (a.rows <= 1 || a.ldx % Tile::kC == 0) && on_bytes(a.data, Tile::kC);
         // blockIdx.y reaches 65535: 2^23 rows at a time
         for (int64_t r0 = 0; r0 < a.rows; r0 += INT64_C(128) * 65535) {
             GateArgs p = a;
@@ -428,7 +434,7 @@ cudaError_t launch(GateForm form, const GateArgs& a, cudaStream_t s) {
             p.scales = a.scales + r0 / 128 * a.H;
             const unsigned y = (unsigned)ceil_div(p.rows, 128);
             const cudaError_t e =
-                tiled ? launch_overlapped(gate_columns_tile_kernel<ELT>, dim3((unsigned)ceil_div(a.H, 8 * kTileX), y), kTileX * 128 / kTileRows, 0, 0, s, p)
+                tiled ? launch_overlapped(gate_columns_tile_kernel<ELT>, dim3((unsigned)ceil_div(a.H, Tile::kC * Tile::kX), y), Tile::kThreads, 0, 0, s, p)
                       : launch_overlapped(gate_columns_kernel<ELT>, dim3((unsigned)ceil_div(a.H, 64), y), 512, 0, 0, s, p);
             if (e != cudaSuccess) return e;
         }

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(MoeRowsArgs a) {
 // that do not begin on 16 bytes; the pieces are those of the output, put
 // together from the five words of the token that they lie across, and the
 // bytes in front of the first and behind the last go one by one.
-constexpr int kFp8Threads = 128, kFlight = 4;
+constexpr int kFp8Threads = 64, kFlight = 8;
 template <bool SHIFT>
 __global__ void __launch_bounds__(kFp8Threads) dispatch_fp8_kernel(MoeFp8Args a) {
     let_next_start();

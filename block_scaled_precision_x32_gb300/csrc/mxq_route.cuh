@@ -962,12 +962,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
     if (t >= a.T) return;
-    int id = lane < a.topk ? a.ids[t * a.topk + lane] : -1;
-    if (id >= a.E) id = -1;
-    const float g = id >= 0 ? fmul(a.scale, a.g[t * a.topk + lane]) : 0.0f;
-    const float x = id >= 0 ? logit<ELT>(a, t, id) : -kInf;
+    const bool dense = !a.sigmoid && !a.renorm;
     float d[VPL], v;
-    if (a.sigmoid || a.renorm) {
+    if (dense) load_logits<ELT, VPL>(a, t, lane, d);  // ahead of what has to wait for the ids
+    int id = lane < a.topk ? a.ids[t * a.topk + lane] : -1;
+    float g = lane < a.topk ? a.g[t * a.topk + lane] : 0.0f;
+    if (id < 0 || id >= a.E) id = -1, g = 0.0f;
+    g = fmul(a.scale, g);
+    const float x = id >= 0 ? logit<ELT>(a, t, id) : -kInf;
+    if (!dense) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
         const Chosen chosen(x, a.sigmoid);
@@ -981,7 +984,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
         }
         if (id < 0 || x == -kInf) v = 0.0f;
     } else {
-        load_logits<ELT, VPL>(a, t, lane, d);
         float m = max_nan<VPL>(d);
         m = __any_sync(kAll, m != m) ? __uint_as_float(0x7FC00000u) : warp_max(m);
         float total = 0.0f;
