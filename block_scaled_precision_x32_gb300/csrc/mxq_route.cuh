@@ -14,6 +14,8 @@
 // A warp to a token, VPL consecutive experts to a lane, in registers.
 #pragma once
 
+#include <type_traits>
+
 #include "mxq_device.cuh"
 #include "mxq_e4m3.cuh"
 #include "mxq_layer.h"
@@ -229,10 +231,22 @@ enum Groups { NONE, LANES, ANY };
 
 // Takes the experts of all but the best groups out (c = -inf).
 template <int VPL, Groups GROUPS, typename Real>
-__device__ __forceinline__ void best_groups(const RouteArgs& a, int lane, Real (&c)[VPL], float err, bool& unsure) {
+__device__ __forceinline__ void best_groups(const RouteArgs& a, int lane, Real (&c)[VPL], float err, bool& unsure, float* stage = nullptr) {
     Top2<Real> top;
     int group = lane, shift = 0, ahead = 0;
-    if constexpr (GROUPS == LANES) {
+    if constexpr (GROUPS == ANY && std::is_same<Real, float>::value) {
+        // through shared memory, as many lanes to a group as there are for each
+        shift = a.group_shift;
+        group = lane >> shift;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) stage[lane * VPL + i] = c[i];
+        __syncwarp();
+        if (group < a.groups)
+            for (int e = group * a.group_size + (lane & ((1 << shift) - 1)); e < (group + 1) * a.group_size; e += 1 << shift) top.add(stage[e]);
+        __syncwarp();
+#pragma unroll 1
+        for (int d = 1; d < 1 << shift; d *= 2) top.merge(d);
+    } else if constexpr (GROUPS == LANES) {
         shift = a.group_shift;
         group = lane >> shift;
         top = top2_of<VPL>(c);
@@ -273,9 +287,13 @@ __device__ __forceinline__ void best_groups(const RouteArgs& a, int lane, Real (
         for (int i = 0; i < VPL; ++i) c[i] = kept ? c[i] : of<Real>(-kInf);
     } else {
         const unsigned mask = __ballot_sync(kAll, kept);
+        int g = lane * VPL / a.group_size;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (lane * VPL + i >= a.E || !(mask >> ((lane * VPL + i) / a.group_size) & 1)) c[i] = of<Real>(-kInf);
+        for (int i = 0; i < VPL; ++i) {
+            const int e = lane * VPL + i;
+            g += e >= (g + 1) * a.group_size ? 1 : 0;  // the next expert's group is the same or the next
+            if (e >= a.E || !(mask >> (g << shift) & 1)) c[i] = of<Real>(-kInf);
+        }
     }
 }
 
@@ -617,7 +635,7 @@ struct Chosen {
 
 // One token to a warp, from its logits to its outputs.
 template <Elt ELT, int VPL, Groups GROUPS>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, uint64_t* list) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, uint64_t* list, float* stage = nullptr) {
     float c[VPL];
     load_logits<ELT, VPL>(a, t, lane, c);
     float m = max_nan<VPL>(c);
@@ -662,7 +680,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
     float x = -kInf;
     if (!bad) {
         bool unsure = false;
-        if constexpr (GROUPS != NONE) best_groups<VPL, GROUPS, float>(a, lane, c, err, unsure);
+        if constexpr (GROUPS != NONE) best_groups<VPL, GROUPS, float>(a, lane, c, err, unsure, stage);
         id = choose32<ELT, VPL>(a, t, lane, c, err, unsure, list);
         if (__any_sync(kAll, unsure)) {
             id = choose48<ELT, VPL, GROUPS>(a, t, lane);
@@ -691,10 +709,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
 template <Elt ELT, int VPL, Groups GROUPS>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
     __shared__ __align__(16) uint64_t lists[kWarps][32];
+    __shared__ float stages[GROUPS == ANY ? kWarps : 1][GROUPS == ANY ? 32 * VPL : 1];
     let_next_start();
     wait_for_stream();
     const int64_t t = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-    if (t < a.T) route_token<ELT, VPL, GROUPS>(a, t, threadIdx.x & 31, lists[threadIdx.x / 32]);
+    if (t < a.T) route_token<ELT, VPL, GROUPS>(a, t, threadIdx.x & 31, lists[threadIdx.x / 32], stages[GROUPS == ANY ? threadIdx.x / 32 : 0]);
 }
 
 // ---- many tokens: four lanes to one
@@ -1072,6 +1091,7 @@ cudaError_t launch(bool grad, RouteArgs a, cudaStream_t s) {
                 a.group_shift = shift;
                 return launch_overlapped(route_kernel<ELT, VPL, LANES>, grid, kWarps * 32, 0, 0, s, a);
             }
+    for (a.group_shift = 0; a.groups << (a.group_shift + 1) <= 32;) ++a.group_shift;
     return launch_overlapped(route_kernel<ELT, VPL, ANY>, grid, kWarps * 32, 0, 0, s, a);
 }
 
