@@ -509,26 +509,26 @@ __device__ __forceinline__ bool alike(const RouteArgs& a, int lane, const float 
     return same;
 }
 
-// Scores of VPL logits: 1 / (1 + exp(-x)), or exp(x - m) for the softmax; 0 for -inf.
-template <int VPL>
-__device__ __forceinline__ void scores(const RouteArgs& a, const float (&x)[VPL], float m, float (&s)[VPL]) {
-    if (a.sigmoid) {
+// Scores of N logits, to be compared: 1 / (1 + exp(-x)), or exp(x - m) for the
+// softmax.  The product with log2(e) is rounded once, which makes the
+// exponential off by |x| units of 2^-24 of itself: times s (1 - s), or its own value,
+// that is less than one.  -inf gives 0.
+constexpr float kLog2e = 1.4426950216293335f;
+template <int N>
+__device__ __forceinline__ void scores(const RouteArgs& a, const float (&x)[N], float m, float (&s)[N]) {
+    const float from = m == -kInf ? 0.0f : m;  // a row of -inf alone
 #pragma unroll
-        for (int i = 0; i < VPL; i += 2) {
-            const int j = VPL > 1 ? i + 1 : i;
-            const float2 e = exp_neg2(make_float2(min_nan(fabsf(x[i]), kExpEnd), min_nan(fabsf(x[j]), kExpEnd)));
-            const float2 inv = make_float2(rcp_approx(fadd(1.0f, e.x)), rcp_approx(fadd(1.0f, e.y))), low = mul2(e, inv);
-            s[i] = x[i] < 0.0f ? low.x : inv.x;
-            s[j] = x[j] < 0.0f ? low.y : inv.y;
-        }
-    } else {
-        const float from = m == -kInf ? 0.0f : m;  // a row of -inf alone
-#pragma unroll
-        for (int i = 0; i < VPL; i += 2) {
-            const int j = VPL > 1 ? i + 1 : i;
-            const float2 e = exp_neg2(make_float2(min_nan(from - x[i], kExpEnd), min_nan(from - x[j], kExpEnd)));
-            s[i] = e.x;
-            s[j] = e.y;
+    for (int i = 0; i < N; i += 2) {
+        const int j = N > 1 ? i + 1 : i;
+        if (a.sigmoid) {
+            const float2 t = mul2(make_float2(x[i], x[j]), both(-kLog2e));
+            const float2 d = fma2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), both(1.0f), both(1.0f));
+            s[i] = rcp_approx(d.x);
+            s[j] = rcp_approx(d.y);
+        } else {
+            const float2 t = mul2(make_float2(x[i] - from, x[j] - from), both(kLog2e));
+            s[i] = ex2_approx(t.x);
+            s[j] = ex2_approx(t.y);
         }
     }
 }
@@ -655,9 +655,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
             total = lane_sum(total);
         }
         if (scored) {
-            // in units of 2^-24 of the largest score: two of exp_neg and the sum, or the reciprocal, and a sum's VPL + 5 terms
+            // in units of 2^-24 of the largest score.  Sigmoid: 1 of the exponential, 1 of the sum, 2 of the reciprocal.  Softmax: 3
+            // of the exponential; of the sum 3, its VPL + 4 additions and 2.3 ln E of what the exponentials are off by; 2 of the rest
             const float most = a.sigmoid ? 1.0f : fdiv(1.0f, total);
-            err = (a.sigmoid ? 6.0f : VPL + 16.0f) * 5.9604645e-8f * most;
+            err = (a.sigmoid ? 6.0f : VPL + 32.0f) * 5.9604645e-8f * most;
             // all experts alike, as those of a router that has learned nothing: ties, which need no second look
             if (!a.bias && __all_sync(kAll, alike<VPL>(a, lane, c, __shfl_sync(kAll, c[0], 0)))) err = -1.0f;
             float b[VPL];
@@ -764,6 +765,11 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
     wait_for_stream();
     const int lane = threadIdx.x & 31, l = lane & 3;
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + threadIdx.x / 32) * 8;
+    bool strange = false;  // a bias of NaN, or of infinity: tokens are left to the whole warp
+    if (a.bias) {
+        for (int e = threadIdx.x; e < a.E; e += kWarps * 32) strange |= !(__ldg(a.bias + e) < kInf);
+        strange = __syncthreads_or(strange);
+    }
     if (t0 >= a.T) return;
     const bool real = t0 + (lane >> 2) < a.T;
     const int64_t t = real ? t0 + (lane >> 2) : a.T - 1;
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
         c[4 * j] = v.x, c[4 * j + 1] = v.y, c[4 * j + 2] = v.z, c[4 * j + 3] = v.w;
     }
     float m = max_nan<4 * J>(c);
-    bool left = m != m;  // to the whole warp
+    bool left = strange || m != m;  // to the whole warp
     if (!a.sigmoid) {
 #pragma unroll
         for (int d = 1; d < 4; d *= 2) m = max(m, __shfl_xor_sync(kAll, m, d));
@@ -785,39 +791,34 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
     float total = 0.0f, err = -1.0f;
     if (scored || !(a.sigmoid || a.renorm)) {
         float most = 1.0f;
-        if (!a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < 4 * J; i += 2) {
-                const float2 e = exp_neg2(make_float2(min_nan(m - c[i], kExpEnd), min_nan(m - c[i + 1], kExpEnd)));
-                total = fadd(total, fadd(e.x, e.y));
-                if (scored) c[i] = c[i] > -kInf ? e.x : -kInf, c[i + 1] = c[i + 1] > -kInf ? e.y : -kInf;
-            }
+        for (int j = 0; j < J; ++j) {  // in place: there are no registers for the logits and the scores
+            float(&x)[4] = reinterpret_cast<float(&)[4]>(c[4 * j]);
+            float z[4];
+            scores<4>(a, x, m, z);
+            total = fadd(total, fadd(fadd(z[0], z[1]), fadd(z[2], z[3])));
+            if (scored)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = x[q] > -kInf ? z[q] : -kInf;
+        }
+        if (!a.sigmoid) {
 #pragma unroll
             for (int d = 1; d < 4; d *= 2) total = fadd(total, __shfl_xor_sync(kAll, total, d));
             most = fdiv(1.0f, total);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4 * J; i += 2) {
-                const float2 e = exp_neg2(make_float2(min_nan(fabsf(c[i]), kExpEnd), min_nan(fabsf(c[i + 1]), kExpEnd)));
-                const float2 inv = make_float2(rcp_approx(fadd(1.0f, e.x)), rcp_approx(fadd(1.0f, e.y))), low = mul2(e, inv);
-                c[i] = c[i] < 0.0f ? c[i] > -kInf ? low.x : -kInf : inv.x;
-                c[i + 1] = c[i + 1] < 0.0f ? c[i + 1] > -kInf ? low.y : -kInf : inv.y;
-            }
         }
         if (scored) {
-            // in units of 2^-24 of the largest score: two of exp_neg and the sum, or the reciprocal, and a sum's 2 J + 2 terms
-            err = (a.sigmoid ? 6.0f : 2 * J + 16.0f) * 5.9604645e-8f * most;
+            // as in route_token, with the J + 4 additions of a quad's sum and ln 256
+            err = (a.sigmoid ? 6.0f : J + 28.0f) * 5.9604645e-8f * most;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (a.bias && (l + 4 * j) * 4 < a.E) b = __ldg(reinterpret_cast<const float4*>(a.bias) + l + 4 * j);
-                const float bs[4] = {b.x, b.y, b.z, b.w};
-                left |= !(max_nan<4>(bs) < kInf);  // NaN, or a score of infinity
                 c[4 * j] = ffma(c[4 * j], most, b.x), c[4 * j + 1] = ffma(c[4 * j + 1], most, b.y);
                 c[4 * j + 2] = ffma(c[4 * j + 2], most, b.z), c[4 * j + 3] = ffma(c[4 * j + 3], most, b.w);
             }
         }
     }
+    bool out[JG ? J / JG : 1] = {};  // a group that is not kept
     if constexpr (JG > 0) {
         constexpr int G = J / JG;
         float score[G];
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
         }
         if (err >= 0.0f && next > -kInf && least - next <= 2 * a.group_top * err + 2 * kRound<float> * size) left = true;
 #pragma unroll
-        for (int i = 0; i < 4 * J; ++i) c[i] = kept[i / (4 * JG)] ? c[i] : -kInf;
+        for (int g = 0; g < G; ++g) out[g] = !kept[g];
     }
     // the lane's chunks' maxima in descending order, the largest kQuadKept of them
     float from;
@@ -855,6 +856,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             float v = max(max(c[4 * j], c[4 * j + 1]), max(c[4 * j + 2], c[4 * j + 3]));
+            if (JG && out[JG ? j / JG : 0]) v = -kInf;
 #pragma unroll
             for (int i = 0; i < kQuadKept && i <= j; ++i) order(top[i], v);
         }
@@ -879,7 +881,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
     float2* mine = reinterpret_cast<float2*>(list) + l * kSlots;
 #pragma unroll
     for (int i = 0; i < 4 * J; ++i)
-        if (c[i] >= from && at < kSlots) mine[at++] = make_float2(c[i], __uint_as_float(((l + 4 * (i / 4)) * 4 + i % 4)));
+        if (c[i] >= (JG && out[JG ? i / (4 * JG) : 0] ? __uint_as_float(0x7FC00000u) : from) && at < kSlots) mine[at++] = make_float2(c[i], __uint_as_float(((l + 4 * (i / 4)) * 4 + i % 4)));
     left |= at == kSlots;
     at = min(at, kSlots - 1);
     // the four lists one behind the other, as keys: by value, then the lower index first
