@@ -1049,8 +1049,8 @@ class Library:
 
     # -- between the products -------------------------------------------
 
-    def _norm_args(self, x, weight, residual, eps, h, y, data, scales, rstd, new=False):
-        """``new``: y, data, scales and rstd were made for this call."""
+    def _norm_args(self, x, weight, residual, eps, h, y, data, scales, rstd, new=False, new_h=False):
+        """``new``: y, data, scales and rstd were made for this call; ``new_h``: h was."""
         dev = _cuda_index(x)
         rows, K, ldx = _matrix(x, "x")
         if weight.get_device() != dev or weight.dim() != 1 or weight.shape[0] != K or not weight.is_contiguous():
@@ -1063,7 +1063,7 @@ class Library:
         if h is not None:
             if residual is None:
                 raise ValueError("h is written only with a residual")
-            ldh, ph = _like_rows(h, x, rows, K, "h", dev), h.data_ptr()
+            ldh, ph = K if new_h else _like_rows(h, x, rows, K, "h", dev), h.data_ptr()
         if (data is None) != (scales is None):
             raise ValueError("data and scales go together")
         if y is not None:
@@ -1109,9 +1109,10 @@ class Library:
             scales = torch.empty((shape[0], per_row) if len(shape) == 2 else shape[:-1] + (per_row,), dtype=torch.uint8, device=device)
         y = torch.empty(shape, dtype=x.dtype, device=device) if normed else None
         rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device) if stats else None
-        if h is None and residual is not None:
+        new_h = h is None and residual is not None
+        if new_h:
             h = torch.empty(shape, dtype=x.dtype, device=device)
-        args = self._norm_args(x, weight, residual, eps, h, y, data, scales, rstd, True)
+        args = self._norm_args(x, weight, residual, eps, h, y, data, scales, rstd, True, new_h)
         self._call(self.L.mxq_rmsnorm, args, "mxq_rmsnorm", x.get_device())
         return Normed(data, scales, y, x if residual is None else h, rstd)
 
