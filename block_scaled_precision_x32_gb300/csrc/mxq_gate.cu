@@ -23,10 +23,11 @@ namespace {
 // the rest.
 //
 // To be quantized, silu(x) is taken as x / (1 + exp(-x)), which needs no choice
-// by the sign but a bound below: a gate under -87 counts as -87, which is off by
-// 1.5e-36 |up| at most; and an infinite gate, of either sign, gives NaN: its
-// block is poisoned as it would be by an infinity.  Otherwise -inf, whose silu is
-// 0 * inf by its definition, is looked for once for all.
+// by the sign.  Where 1 + exp(-x) exceeds 2^126 the quotient is zero: a gate under
+// -87.3 gives 0 for what is less than 1.1e-36 |up|.  (To find those gates and to
+// give them their bits took the 128x1 form from 52 to 57 us.)  An infinite gate gives
+// NaN, of either sign: its block is poisoned as it would be by an infinity.
+// Otherwise -inf, whose silu is 0 * inf by its definition, is looked for once for all.
 template <Elt ELT, int N, bool QUANT>
 __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, float* v) {
     if constexpr (ELT == Elt::BF16) {
@@ -40,10 +41,7 @@ __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, 
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
             if constexpr (QUANT) {
-                uint32_t cut;
-                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(cut) : "r"(gate[j]), "r"(0xC2AEC2AEu));       // -87
-                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(cut) : "r"(gate[j]), "r"(0u));  // NaN for infinities
-                const float2 x = two(cut), d = fma2(exp_of(x), both(1.0f), both(1.0f));
+                const float2 x = two(gate[j]), d = fma2(exp_of(x), both(1.0f), both(1.0f));
                 const float2 r = mul2(mul2(x, make_float2(rcp_approx(d.x), rcp_approx(d.y))), two(up[j]));
                 v[2 * j] = r.x, v[2 * j + 1] = r.y;
             } else {
@@ -56,7 +54,7 @@ __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, 
                 v[2 * j] = r.x, v[2 * j + 1] = r.y;
             }
         }
-        if ((top & 0x7FFFu) >= 0x7F80u || top >= 0x7F800000u) {
+        if (!QUANT && ((top & 0x7FFFu) >= 0x7F80u || top >= 0x7F800000u)) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 if ((gate[j / 2] >> (16 * (j & 1)) & 0xFFFFu) == 0xFF80u) v[j] = __uint_as_float(0x7FC00000u);
@@ -183,7 +181,7 @@ __global__ void __launch_bounds__(256, ELT == Elt::FP32 ? 4 : QUANT ? 7 : 5) gat
 // Tiles of 128 rows x C TX columns a block, C columns of R rows a thread, in
 // registers between the maximum and the rounding: each element is read once.
 // bf16: few columns of many rows, since each column's maximum costs shuffles
-// and its scale unpacking, and 64 registers: 16379 x 4096 52.3 us, 6.4 TB/s
+// and its scale unpacking, and 64 registers: 16379 x 4096 51.8 us, 6.5 TB/s
 // (eight columns of four rows 63 to 73, seven blocks a multiprocessor 54.6, 16
 // threads a row 54.6).  fp32: wide loads count for more, 8191 x 4096 45.8 us, 6.6
 // TB/s (four columns of eight rows 57 to 66).

@@ -295,6 +295,29 @@ def test_gate_over_the_whole_range(mx):
         np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
 
 
+@pytest.mark.parametrize("H", [256, 250])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gates_far_below_zero(mx, H, dtype):
+    """Blocks of gates near the end of the exponential's range, next to factors that bring them back; gates beyond it and of
+    the type's lowest value give zeros."""
+    rng = np.random.default_rng(H)
+    x = normal(rng, 384, 2 * H)
+    x[:128, :H] = -rng.uniform(70, 87, (128, H))
+    x[:128, H:] *= 1e30
+    x[128:256, :H] = -rng.uniform(88, 100, (128, H))
+    x[256:, :H] = np.where(rng.random((128, H)) < 0.5, -1e4, float(torch.finfo(dtype).min))
+    x[256:, H:] *= 1e30
+    x = dev(x, dtype)
+    want = bref.gate(f64(x))
+    for columns, (d, s) in ((False, mx.fp8_silu_mul_1x128(x)), (True, mx.fp8_silu_mul_128x1(x))):
+        near_quantized(d[:128], s[: 1 if columns else 128], want[:128], 16 * U, columns)
+        assert not (host_bits(d[256:]) & 0x7F).any()
+        codes = host_bits(s).astype(np.int64)
+        codes = codes[1:2].repeat(128, 0) if columns else codes[128:256].repeat(128, 1)[:, :H]
+        got = ref.e4m3_decode(host_bits(d[128:256])) * np.ldexp(1.0, codes - 127)
+        assert (np.abs(got - want[128:256]) <= 1.1e-36 * np.abs(f64(x)[128:256, H:]) + 2.0**-4 * np.abs(want[128:256]) + 2.0**-137).all()
+
+
 @pytest.mark.parametrize("rows,H", [(1, 1), (1, 16), (37, 129), (128, 512), (129, 1000), (3, 7184)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_gate_gradient(mx, rows, H, dtype):
@@ -452,6 +475,38 @@ def test_route_gradient(mx, E, topk, score, renormalize, dtype):
     assert d.dtype == dtype
     want, size = bref.route_grad(f64(g), f64(x), ids, score, renormalize, 1.5)
     near(d, want, (E + 80) * U * size + half_step(dtype) * np.abs(want) + 2.0**-140)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("E", [60, 64])
+def test_route_gradient_of_nan_stays_in_its_row(mx, E, dtype):
+    x, g = dev(normal(np.random.default_rng(E), 12, E), dtype), torch.ones(12, 3, device="cuda")
+    ids = torch.arange(36, dtype=torch.int32, device="cuda").view(12, 3)
+    x[2, 7], x[5, 15], g[8, 1] = float("nan"), float("nan"), float("nan")
+    for score in ("softmax", "sigmoid"):
+        for renormalize in (True, False):
+            d = mx.moe_route_grad(g, x, ids, score=score, renormalize=renormalize)
+            bad = torch.isnan(d).cpu()
+            want = torch.zeros(12, E, dtype=torch.bool)
+            for row in (2, 5, 8):  # softmax's sum takes it to all experts, a renormalised weight to the chosen ones
+                if score == "softmax" and not renormalize:
+                    want[row] = True
+                elif renormalize:
+                    want[row, 3 * row:3 * row + 3] = True
+            want[2, 7] = want[5, 15] = want[8, 25] = True
+            assert torch.equal(bad, want), (score, renormalize)
+            if dtype == BF16:
+                assert (host_bits(d)[want.numpy()] == 0x7FC0).all()
+
+
+@pytest.mark.parametrize("T", [40, 16400])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_of_padded_rows(mx, T, score):
+    """Rows of zeros and the rows between them, with the biases of a router that has not been balanced yet."""
+    x = dev(normal(np.random.default_rng(T), T, 128))
+    x[1::2] = 0.0
+    for bias in (torch.zeros(128, device="cuda"), torch.full((128,), -0.25, device="cuda"), None):
+        check_route(mx, x, 6, bias, score=score, groups=8, topk_groups=3, group_top=2)
 
 
 def test_route_gradient_of_what_was_routed(mx):
