@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(U == 1 ? 512 : 1024, U == 1 && ELT == Elt::BF1
     }
 }
 
-constexpr int kAnyThreads = 256, kAnyWarps = kAnyThreads / 32, kHeld = 8;
+constexpr int kAnyThreads = 256, kAnyWarps = kAnyThreads / 32, kHeld = 8, kAhead = 2;
 
 template <Elt ELT>
 __device__ __forceinline__ float value_at(const void* p, int64_t k) {
@@ -145,7 +145,13 @@ __device__ __forceinline__ float value_at(const void* p, int64_t k) {
 // Any alignment and any K: one row to a block, 1x128 blocks to its warps in
 // turn, neighbours to neighbouring lanes: an element at a time, so that
 // instructions bound it.  The first kHeld blocks of a warp (rows of 8192) stay
-// in registers, what is behind them is read again.
+// in registers, what is behind them is read again.  Only the row's last block,
+// where it is not a whole one, looks at each element's place.  Four blocks to a
+// multiprocessor hide each other's barrier: 4095 x 7183 fp32 take 35.9 us, 8191 x
+// 7183 bf16 with residual and y 108, with two thirds of the issue slots taken
+// (three or five blocks, or blocks of 512 threads, 38 to 42 and 119 to 152;
+// persistent blocks with their next rows on the way into shared memory 45 and 150:
+// two of them have room, and wait at their barriers together).
 template <Elt ELT, Elt WELT, bool RES>
 __global__ void __launch_bounds__(kAnyThreads, 4) norm_any_kernel(NormArgs a, int nb) {
     __shared__ __align__(16) float part[kAnyWarps];
@@ -158,15 +164,19 @@ __global__ void __launch_bounds__(kAnyThreads, 4) norm_any_kernel(NormArgs a, in
     void* hp = RES && a.h ? at_row<ELT>(a.h, row, a.ldh) : nullptr;
     void* yp = a.y ? at_row<ELT>(a.y, row, a.K) : nullptr;
     uint8_t* data = a.data ? a.data + row * a.K : nullptr;
-    // the lane's four elements of block b, zeros behind the row
-    const auto read = [&](int b, float (&v)[4]) {
+    constexpr std::true_type kWhole{};
+    constexpr std::false_type kPart{};
+    const int whole_blocks = K / 128;
+    // the lane's four elements of block b; zeros where it is not `there`, and behind the row
+    const auto read = [&](auto whole, int b, bool there, float (&v)[4]) {
         const int k = b * 128 + lane;
+        const auto at = [&](int q) { return there && (decltype(whole)::value || k + 32 * q < K); };
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = k + 32 * q < K ? value_at<ELT>(x, k + 32 * q) : 0.0f;
+        for (int q = 0; q < 4; ++q) v[q] = at(q) ? value_at<ELT>(x, k + 32 * q) : 0.0f;
         if constexpr (RES) {
             float r[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) r[q] = k + 32 * q < K ? value_at<ELT>(res, k + 32 * q) : 0.0f;
+            for (int q = 0; q < 4; ++q) r[q] = at(q) ? value_at<ELT>(res, k + 32 * q) : 0.0f;
 #pragma unroll
             for (int q = 0; q < 4; q += 2) {
                 v[q] = fadd(v[q], r[q]), v[q + 1] = fadd(v[q + 1], r[q + 1]);
@@ -177,54 +187,66 @@ __global__ void __launch_bounds__(kAnyThreads, 4) norm_any_kernel(NormArgs a, in
             }
         }
     };
-    const auto keep = [&](int b, const float (&v)[4], float sum) {
+    const auto keep = [&](auto whole, int b, const float (&v)[4], float sum) {
         const int k = b * 128 + lane;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (hp && k + 32 * q < K) store_f32<ELT>(hp, k + 32 * q, v[q]);
+            if (hp && (decltype(whole)::value || k + 32 * q < K)) store_f32<ELT>(hp, k + 32 * q, v[q]);
             sum = ffma(v[q], v[q], sum);
         }
         return sum;
     };
-    float held[kHeld][4], sum = 0.0f;
+    const bool tail = whole_blocks < nb && whole_blocks % kAnyWarps == warp;  // of this warp
+    float held[kHeld][4], end[4], sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) read(i * kAnyWarps + warp, held[i]);
+    for (int i = 0; i < kHeld; ++i) read(kWhole, i * kAnyWarps + warp, i * kAnyWarps + warp < whole_blocks, held[i]);
+    read(kPart, whole_blocks, tail, end);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-        if (i * kAnyWarps + warp < nb) sum = keep(i * kAnyWarps + warp, held[i], sum);
-    for (int b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps) {
+        if (i * kAnyWarps + warp < whole_blocks) sum = keep(kWhole, i * kAnyWarps + warp, held[i], sum);
+    for (int b = kHeld * kAnyWarps + warp; b < whole_blocks; b += kAnyWarps) {
         float v[4];
-        read(b, v);
-        sum = keep(b, v, sum);
+        read(kWhole, b, true, v);
+        sum = keep(kWhole, b, v, sum);
     }
-    const float rstd = rstd_of(row_sum(sum, part, 0, kAnyWarps), a.K, a.eps);
-    if (a.rstd && threadIdx.x == 0) store_f32<Elt::FP32>(a.rstd, row, rstd);
-    // weights of the lane's four elements of block b; any value behind the row
-    const auto weights = [&](int b, float (&w)[4]) {
+    if (tail) sum = keep(kPart, whole_blocks, end, sum);
+    // weights of the lane's four elements of block b, if it is `there`; zeros behind the row
+    const auto weights = [&](auto whole, int b, bool there, float (&w)[4]) {
         const int k = b * 128 + lane;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int i = k + 32 * q < K ? k + 32 * q : 0;
-            if constexpr (WELT == Elt::BF16) w[q] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.weight) + i) << 16);
-            else w[q] = __ldg(static_cast<const float*>(a.weight) + i);
+            w[q] = 0.0f;
+            if (there && (decltype(whole)::value || k + 32 * q < K)) {
+                if constexpr (WELT == Elt::BF16) w[q] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.weight) + k + 32 * q) << 16);
+                else w[q] = __ldg(static_cast<const float*>(a.weight) + k + 32 * q);
+            }
         }
     };
-    const auto finish = [&](int b, const float (&v)[4], const float (&w)[4]) {
+    // the weights of kAhead blocks are on their way at once, the first ones while the row is summed
+    float w[kAhead][4];
+    const auto ahead = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) weights(kWhole, (i0 + i) * kAnyWarps + warp, (i0 + i) * kAnyWarps + warp < whole_blocks, w[i]);
+    };
+    ahead(0);
+    const float rstd = rstd_of(row_sum(sum, part, 0, kAnyWarps), a.K, a.eps);
+    if (a.rstd && threadIdx.x == 0) store_f32<Elt::FP32>(a.rstd, row, rstd);
+    const auto finish = [&](auto whole, int b, const float (&v)[4], const float (&w)[4]) {
         const int k = b * 128 + lane;
-        const bool there[4] = {k < K, k + 32 < K, k + 64 < K, k + 96 < K};
+        const auto at = [&](int q) { return decltype(whole)::value || k + 32 * q < K; };
         float2 y[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) y[q] = mul2(mul2(make_float2(v[2 * q], v[2 * q + 1]), both(rstd)), make_float2(w[2 * q], w[2 * q + 1]));
-        if (!there[3]) y[1].y = 0.0f;
-        if (!there[2]) y[1].x = 0.0f;
-        if (!there[1]) y[0].y = 0.0f;
-        if (!there[0]) y[0].x = 0.0f;
+        for (int q = 0; q < 2; ++q) {
+            y[q] = mul2(mul2(make_float2(v[2 * q], v[2 * q + 1]), both(rstd)), make_float2(w[2 * q], w[2 * q + 1]));
+            if (!at(2 * q)) y[q].x = 0.0f;
+            if (!at(2 * q + 1)) y[q].y = 0.0f;
+        }
         const float top = absmax3(absmax3(0.0f, y[0].x, y[0].y), y[1].x, y[1].y);
         if (yp)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float f = q & 1 ? y[q / 2].y : y[q / 2].x;
-                if (there[q]) store_f32<ELT>(yp, k + 32 * q, f);
+                if (at(q)) store_f32<ELT>(yp, k + 32 * q, f);
             }
         if (!data) return;
         const uint32_t code = scale_code128(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top) & 0x7FFFFFFFu));
@@ -234,31 +256,33 @@ __global__ void __launch_bounds__(kAnyThreads, 4) norm_any_kernel(NormArgs a, in
         for (int q = 0; q < 2; ++q) {
             const float2 p = mul2(y[q], inv);
             const uint32_t two = code == 255u ? 0x7F7Fu : e4m3x2_from_f32(__float_as_uint(p.y), __float_as_uint(p.x));
-            if (there[2 * q]) data[k + 64 * q] = (uint8_t)two;
-            if (there[2 * q + 1]) data[k + 64 * q + 32] = (uint8_t)(two >> 8);
+            if (at(2 * q)) data[k + 64 * q] = (uint8_t)two;
+            if (at(2 * q + 1)) data[k + 64 * q + 32] = (uint8_t)(two >> 8);
         }
     };
-    // the weights of four blocks are on their way at once
 #pragma unroll
-    for (int i0 = 0; i0 < kHeld; i0 += 4) {
-        float w[4][4];
+    for (int i0 = 0; i0 < kHeld; i0 += kAhead) {
+        if (i0) ahead(i0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) weights((i0 + i) * kAnyWarps + warp, w[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if ((i0 + i) * kAnyWarps + warp < nb) finish((i0 + i) * kAnyWarps + warp, held[i0 + i], w[i]);
+        for (int i = 0; i < kAhead; ++i)
+            if ((i0 + i) * kAnyWarps + warp < whole_blocks) finish(kWhole, (i0 + i) * kAnyWarps + warp, held[i0 + i], w[i]);
     }
-    for (int b = kHeld * kAnyWarps + warp; b < nb; b += kAnyWarps) {
+    for (int b = kHeld * kAnyWarps + warp; b < whole_blocks; b += kAnyWarps) {
         float v[4], w[4];
-        weights(b, w);
+        weights(kWhole, b, true, w);
         // h may lie over x or the residual: what this thread wrote there is read back
         if (hp) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = b * 128 + lane + 32 * q < K ? value_at<ELT>(hp, b * 128 + lane + 32 * q) : 0.0f;
+            for (int q = 0; q < 4; ++q) v[q] = value_at<ELT>(hp, b * 128 + lane + 32 * q);
         } else {
-            read(b, v);
+            read(kWhole, b, true, v);
         }
-        finish(b, v, w);
+        finish(kWhole, b, v, w);
+    }
+    if (tail) {
+        float w[4];
+        weights(kPart, whole_blocks, true, w);
+        finish(kPart, whole_blocks, end, w);
     }
 }
 

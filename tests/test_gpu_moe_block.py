@@ -154,6 +154,38 @@ def test_norm_of_strided_rows_in_place(mx, dtype, K, ld, shift):
             assert torch.equal(t, want)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("K,ld,shift,rows", [(257, 257, 0, 1300), (383, 385, 3, 1220), (1000, 1000, 1, 1000), (1001, 1004, 5, 901), (4096, 4097, 0, 650), (7183, 7183, 0, 640),
+                                             (8190, 8190, 1, 611), (8191, 8191, 7, 610), (8192, 8193, 1, 609)])
+def test_norm_of_many_ragged_rows(mx, K, ld, shift, rows, dtype, residual):
+    """Rows at every place of 16 bytes, as many as take turns on the device: what few of them give, bit for bit, and nothing beside it."""
+    gen = torch.Generator("cuda").manual_seed(K)
+    base = torch.full((2, shift + rows * ld), float("nan"), dtype=dtype, device="cuda")
+    x, res = (b[shift:shift + rows * ld].view(rows, ld)[:, :K] for b in base)
+    x.copy_(torch.randn(rows, K, device="cuda", generator=gen))
+    res.copy_(torch.randn(rows, K, device="cuda", generator=gen))
+    res = res if residual else None
+    w = torch.randn(K, device="cuda", generator=gen).to(dtype if K % 2 else F32)
+    nb = -(-K // 128)
+    out = [Guarded((rows, K), torch.uint8), Guarded((rows, nb), torch.uint8), Guarded((rows, K), dtype), Guarded((rows,), F32)] + ([Guarded((rows, K), dtype)] if residual else [])
+    names = ("data", "scales", "y", "rstd", "h")
+    mx.plan_rmsnorm(x, w, res, 1e-5, **{n: o.t for n, o in zip(names, out)})()
+    assert all(o.intact() for o in out)
+    for a in range(0, rows, 200):
+        part = slice(a, min(a + 200, rows))
+        few = mx.rmsnorm(x[part], w, None if res is None else res[part], 1e-5, normed=True, stats=True)
+        for n, o in zip(names, out):
+            np.testing.assert_array_equal(host_bits(o.t[part]), host_bits(getattr(few, n)))
+    check_norm(few, x[part], None if res is None else res[part], w, 1e-5, dtype)
+    if residual:  # in place
+        for over in (x, res):
+            keep = over.clone()
+            got = mx.rmsnorm(x, w, res, 1e-5, h=over)
+            assert torch.equal(got.data, out[0].t) and torch.equal(got.scales, out[1].t) and torch.equal(over, out[4].t)
+            over.copy_(keep)
+
+
 def test_norm_in_place_over_x_and_over_the_residual(mx):
     rng = np.random.default_rng(5)
     for K in (1040, 1041, 9001):
