@@ -731,11 +731,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 //   - a group is JG chunks of each lane; every lane knows all groups' scores;
 //   - the ninth largest of the chunks' maxima bounds the candidates: each lane
 //     sorts its own, and two exchanges merge the four lists;
-//   - each lane appends its candidates to a list of eight, the lists are put
-//     together, and a candidate's rank is the number of those ahead of it.
-// A token with anything unusual (groups that cannot be told apart, NaN, more
-// than seven candidates in a lane) is left to the whole warp, which then takes
-// it by itself.  For topk up to 8.
+//   - each lane appends its candidates to a list, the lists are put together,
+//     and a candidate's rank is the number of those ahead of it.
+// A token with anything unusual (groups that cannot be told apart, NaN, kSlots
+// candidates in a lane or more than kRanked) is left to the whole warp, which then
+// takes it by itself: code that is seldom run and has to be fetched, 10 us for
+// the first such token.  kSlots 8, which three of a thousand random tokens meet,
+// took 53 us for 43.  For topk up to 8.
 //
 // 65536 x 256 fp32 with sigmoid, a bias and groups take 53 us, where their 71 MB
 // would take 11 (a warp to each took 68); bf16 softmax without groups 24.  Bound
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 // half the rate they could start at: all of it is unrolled, so that the scores
 // stay in registers.  96 registers, five blocks a multiprocessor: 128 and 80
 // registers took 5% longer.
-constexpr int kQuadTopk = 8, kQuadKept = kQuadTopk + 1, kSlots = 8;
+constexpr int kQuadTopk = 8, kQuadKept = kQuadTopk + 1, kSlots = 12, kRanked = 28;
 constexpr int64_t kQuadTokens = 16384;  // from here on it is the faster one
 
 __device__ __forceinline__ void order(float& a, float& b) {  // the larger one first
@@ -914,16 +916,19 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
         n += other;
     }
     before -= at;
+    left |= n > kRanked;
+    n = min(n, kRanked);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kSlots - 1; ++i)
         if (i < at) list[before + i] = key[i];
-    if (l == 0) list[n] = 0;  // n <= 28; the ranks are counted two at a time
+    __syncwarp();  // with more than kRanked this lies over one of them
+    if (l == 0) list[n] = 0;  // the ranks are counted two at a time
     __syncwarp();
-    uint64_t own[kSlots - 1];
-    int rank[kSlots - 1];
+    uint64_t own[kRanked / 4];
+    int rank[kRanked / 4];
 #pragma unroll
-    for (int r = 0; r < kSlots - 1; ++r) {
+    for (int r = 0; r < kRanked / 4; ++r) {
         own[r] = 0, rank[r] = 0;
         if (__any_sync(kAll, l + 4 * r < n)) {
             own[r] = l + 4 * r < n ? list[l + 4 * r] : 0;
@@ -935,7 +940,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
     }
     __syncwarp();
 #pragma unroll
-    for (int r = 0; r < kSlots - 1; ++r)
+    for (int r = 0; r < kRanked / 4; ++r)
         if (l + 4 * r < n) list[rank[r]] = own[r];
     __syncwarp();
     left = __ballot_sync(kAll, left) >> (lane & 28) & 15;  // of one of the four, of all
