@@ -232,11 +232,36 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int l
 // How the experts' groups lie: none, a power of two of whole lanes each, or otherwise.
 enum Groups { NONE, LANES, ANY };
 
+// Is the lane's group, of 1 << shift lanes, among the best?  mine: its score,
+// size: the magnitudes in it; a choice within the error of the scores sets `unsure`.
+template <typename Real>
+__device__ __forceinline__ bool kept_group(const RouteArgs& a, int lane, const Real& mine, float size, int group, int shift, float err, bool& unsure) {
+    int ahead = 0;
+    // a group's lanes share the comparisons with the others
+#pragma unroll 1
+    for (int g0 = 0; g0 < a.groups; g0 += 1 << shift) {
+        const int g = g0 + (lane & ((1 << shift) - 1));
+        const Real other = lane_at(mine, (g << shift) & 31);
+        const bool less = more(mine, other);
+        ahead += g < a.groups && !less && (g < group || more(other, mine)) ? 1 : 0;
+    }
+    for (int d = 1; d < 1 << shift; d *= 2) ahead += __shfl_xor_sync(kAll, ahead, d);
+    const bool real = group < a.groups;
+    if (err >= 0.0f && a.topk_groups < a.groups) {
+        // the last group that is kept against the best that is not
+        const unsigned last = __ballot_sync(kAll, real && ahead == a.topk_groups - 1), next = __ballot_sync(kAll, real && ahead == a.topk_groups);
+        const Real least = lane_at(mine, __ffs(last) - 1), best = lane_at(mine, __ffs(next) - 1);
+        const float tol = 2 * a.group_top * err + 2 * kRound<Real> * warp_max(size);
+        unsure |= !none(best) && gap(least, best) <= tol;
+    }
+    return real && ahead < a.topk_groups;
+}
+
 // Takes the experts of all but the best groups out (c = -inf).
 template <int VPL, Groups GROUPS, typename Real>
 __device__ __forceinline__ void best_groups(const RouteArgs& a, int lane, Real (&c)[VPL], float err, bool& unsure, float* stage = nullptr) {
     Top2<Real> top;
-    int group = lane, shift = 0, ahead = 0;
+    int group = lane, shift = 0;
     if constexpr (GROUPS == ANY && std::is_same<Real, float>::value) {
         // through shared memory, as many lanes to a group as there are for each
         shift = a.group_shift;
@@ -267,24 +292,7 @@ __device__ __forceinline__ void best_groups(const RouteArgs& a, int lane, Real (
             if (lane == g) top = of;
         }
     }
-    const Real mine = top.score(a.group_top);
-    // a group's lanes share the comparisons with the others
-#pragma unroll 1
-    for (int g0 = 0; g0 < a.groups; g0 += 1 << shift) {
-        const int g = g0 + (lane & ((1 << shift) - 1));
-        const Real other = lane_at(mine, (g << shift) & 31);
-        const bool less = more(mine, other);
-        ahead += g < a.groups && !less && (g < group || more(other, mine)) ? 1 : 0;
-    }
-    for (int d = 1; d < 1 << shift; d *= 2) ahead += __shfl_xor_sync(kAll, ahead, d);
-    const bool real = group < a.groups, kept = real && ahead < a.topk_groups;
-    if (err >= 0.0f && a.topk_groups < a.groups) {
-        // the last group that is kept against the best that is not
-        const unsigned last = __ballot_sync(kAll, real && ahead == a.topk_groups - 1), next = __ballot_sync(kAll, real && ahead == a.topk_groups);
-        const Real least = lane_at(mine, __ffs(last) - 1), best = lane_at(mine, __ffs(next) - 1);
-        const float tol = 2 * a.group_top * err + 2 * kRound<Real> * warp_max(top.size());
-        unsure |= !none(best) && gap(least, best) <= tol;
-    }
+    const bool kept = kept_group<Real>(a, lane, top.score(a.group_top), top.size(), group, shift, err, unsure);
     if constexpr (GROUPS == LANES) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) c[i] = kept ? c[i] : of<Real>(-kInf);
@@ -733,20 +741,24 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 //     sorts its own, and two exchanges merge the four lists;
 //   - each lane appends its candidates to a list, the lists are put together,
 //     and a candidate's rank is the number of those ahead of it.
-// A token with anything unusual (groups that cannot be told apart, NaN, kSlots
-// candidates in a lane or more than kRanked) is left to the whole warp, which then
-// takes it by itself: code that is seldom run and has to be fetched, 10 us for
-// the first such token.  kSlots 8, which three of a thousand random tokens meet,
-// took 53 us for 43.  For topk up to 8.
+// Groups and candidates that 24 bits cannot put in order are looked at again by
+// the whole warp, and the token goes on.  One with anything else unusual (NaN,
+// groups that 48 bits cannot tell apart either, kSlots candidates in a lane or more
+// than kRanked) is left to the whole warp, which then takes it by itself.  Each of
+// these holds the warp up for 5 to 10 us: without any of them the largest case
+// below would take 41 us.  kSlots 8, which three of a thousand random tokens meet,
+// took it from 50 to 52.  For topk up to 8.
 //
-// 65536 x 256 fp32 with sigmoid, a bias and groups take 53 us, where their 71 MB
-// would take 11 (a warp to each took 68); bf16 softmax without groups 24.  Bound
+// 65536 x 256 fp32 with sigmoid, a bias and groups take 48 us, where their 71 MB
+// would take 11 (a warp to each took 68); bf16 softmax without groups 22.  Bound
 // by instructions, about 410 a token, which the instruction cache delivers at
 // half the rate they could start at: all of it is unrolled, so that the scores
-// stay in registers.  96 registers, five blocks a multiprocessor: 128 and 80
-// registers took 5% longer.
+// stay in registers.  96 registers, 20 warps a multiprocessor in blocks of one
+// (16: 49 us; 18, 21 and more, whose registers spill: 54 to 63; blocks of two or
+// four warps: 50).
 constexpr int kQuadTopk = 8, kQuadKept = kQuadTopk + 1, kSlots = 12, kRanked = 28;
 constexpr int64_t kQuadTokens = 16384;  // from here on it is the faster one
+constexpr int kQuadWarps = 1;  // a warp that looks twice at a token keeps no others from making room
 
 __device__ __forceinline__ void order(float& a, float& b) {  // the larger one first
     const float t = max(a, b);
@@ -764,6 +776,74 @@ __device__ __forceinline__ float4 load_chunk(const RouteArgs& a, int64_t t, int 
     }
 }
 
+// A second look, with 48 bits, at the groups of a token: a bit for each that is
+// kept, -1 where 48 bits do not tell either.  Only what can be among the largest of
+// its group gets one.
+template <Elt ELT, int VPL>
+__device__ __noinline__ int groups48(const RouteArgs& a, int64_t t, int lane) {
+    float c[VPL], b[VPL];
+    load_logits<ELT, VPL>(a, t, lane, c);
+    float m = max_nan<VPL>(c), most = 1.0f;
+    Wide sum = wide(0.0f);
+    const bool same = __all_sync(kAll, alike<VPL>(a, lane, c, __shfl_sync(kAll, c[0], 0)));
+    if (same) return -1;  // most likely ties
+    if (!a.sigmoid) {
+        m = warp_max(m);
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) {
+            const float x = logit<ELT>(a, t, e);
+            sum = add(sum, exp_neg_wide(x == -kInf ? wide(kExpEnd) : sum_of(m, -x)));
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int d = 16; d; d /= 2) sum = add(sum, lane_xor(sum, d));
+        sum = reciprocal(sum);
+        most = sum.h;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) b[i] = 0.0f;
+    if (a.bias) load_bias<VPL>(a, lane, b);
+    {
+        float s[VPL];
+        scores<VPL>(a, c, m, s);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = c[i] > -kInf ? ffma(s[i], most, b[i]) : -kInf;
+    }
+    Top2<float> top = top2_of<VPL>(c);
+    const int shift = a.group_shift, group = lane >> shift;
+#pragma unroll 1
+    for (int d = 1; d < 1 << shift; d *= 2) top.merge(d);
+    const float last = a.group_top == 1 ? top.a : top.b, err = (a.sigmoid ? 6.0f : VPL + 32.0f) * 5.9604645e-8f * most,
+                from = last - (2 * err + kRound<float> * fabsf(last));
+    unsigned may = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) may |= c[i] >= from && c[i] > -kInf ? 1u << i : 0u;
+    Top2<Wide> best;
+#pragma unroll 1
+    while (__any_sync(kAll, may != 0)) {
+        const int e = may ? lane * VPL + __ffs(may) - 1 : 0;
+        const float x = logit<ELT>(a, t, e), bias = a.bias ? a.bias[e] : 0.0f;
+        Wide v = exp_neg_wide(a.sigmoid ? wide(fabsf(x)) : x == -kInf ? wide(kExpEnd) : sum_of(m, -x));
+        if (a.sigmoid) {
+            const Wide inv = reciprocal(add(wide(1.0f), v));
+            v = x < 0.0f ? mul(v, inv) : inv;
+        } else {
+            v = mul(v, sum);
+        }
+        if (a.bias) v = add(v, wide(bias));
+        if (may) best.add(v);
+        may &= may - 1;
+    }
+#pragma unroll 1
+    for (int d = 1; d < 1 << shift; d *= 2) best.merge(d);
+    bool unsure = false;
+    const bool kept = kept_group<Wide>(a, lane, best.score(a.group_top), best.size(), group, shift, most * (1.0f / (1ull << 41)), unsure);  // as in resolve
+    const unsigned lanes = __ballot_sync(kAll, kept);
+    int bits = 0;
+    for (int g = 0; g < a.groups; ++g) bits |= (int)(lanes >> (g << shift) & 1) << g;
+    return __any_sync(kAll, unsure) ? -1 : bits;
+}
+
 template <Elt ELT, int J, int JG>
 __device__ __noinline__ void route_left(const RouteArgs& a, unsigned left, int64_t t, int lane, uint64_t* list) {
     for (; left; left &= left - 1) {
@@ -773,15 +853,15 @@ __device__ __noinline__ void route_left(const RouteArgs& a, unsigned left, int64
 }
 
 template <Elt ELT, int J, int JG>
-__global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid_constant__ RouteArgs a) {
-    __shared__ __align__(16) uint64_t lists[kWarps][8][4 * kSlots];
+__global__ void __launch_bounds__(kQuadWarps * 32, 20 / kQuadWarps) route_quad_kernel(const __grid_constant__ RouteArgs a) {
+    __shared__ __align__(16) uint64_t lists[kQuadWarps][8][4 * kSlots];
     let_next_start();
     wait_for_stream();
     const int lane = threadIdx.x & 31, l = lane & 3;
-    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + threadIdx.x / 32) * 8;
+    const int64_t t0 = ((int64_t)blockIdx.x * kQuadWarps + threadIdx.x / 32) * 8;
     bool strange = false;  // a bias of NaN, or of infinity: tokens are left to the whole warp
     if (a.bias) {
-        for (int e = threadIdx.x; e < a.E; e += kWarps * 32) strange |= !(__ldg(a.bias + e) < kInf);
+        for (int e = threadIdx.x; e < a.E; e += kQuadWarps * 32) strange |= !(__ldg(a.bias + e) < kInf);
         strange = __syncthreads_or(strange);
     }
     if (t0 >= a.T) return;
@@ -857,9 +937,20 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
             least = kept[g] ? min(least, score[g]) : least;
             next = kept[g] ? next : max(next, score[g]);
         }
-        if (err >= 0.0f && next > -kInf && least - next <= 2 * a.group_top * err + 2 * kRound<float> * size) left = true;
 #pragma unroll
         for (int g = 0; g < G; ++g) out[g] = !kept[g];
+        if (scored) {  // the same for every lane, as err is not: a row that cannot be scored has NaN there
+            unsigned nears = __ballot_sync(kAll, next > -kInf && least - next <= 2 * a.group_top * err + 2 * kRound<float> * size && !left);
+            while (nears) {  // one token after the other, by the whole warp
+                const int quad = (__ffs(nears) - 1) >> 2, bits = groups48<ELT, J / 2>(a, __shfl_sync(kAll, t, 4 * quad), lane);
+                if (lane >> 2 == quad) {
+                    left |= bits < 0;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) out[g] = !(bits >> g & 1);
+                }
+                nears &= ~(15u << (4 * quad));
+            }
+        }
     }
     // the lane's chunks' maxima in descending order, the largest kQuadKept of them
     float from;
@@ -944,7 +1035,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) route_quad_kernel(const __grid
         if (l + 4 * r < n) list[rank[r]] = own[r];
     __syncwarp();
     left = __ballot_sync(kAll, left) >> (lane & 28) & 15;  // of one of the four, of all
-    if (scored) {  // the same for every lane, as err is not: a row that cannot be scored has NaN there
+    if (scored) {
         bool near = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -1099,11 +1190,11 @@ cudaError_t launch(bool grad, RouteArgs a, cudaStream_t s) {
         const bool chunks = a.E % 4 == 0 && on_bytes(a.logits, 16) && (a.T <= 1 || a.ld % 4 == 0) && on_bytes(a.bias, 16);
         if (chunks && a.topk <= kQuadTopk && a.T >= kQuadTokens) {
             constexpr int J = 2 * VPL;
-            const dim3 grid((unsigned)ceil_div(a.T, kWarps * 8));
-            if (a.groups == 1) return launch_overlapped(route_quad_kernel<ELT, J, 0>, grid, kWarps * 32, 0, 0, s, a);
+            const dim3 grid((unsigned)ceil_div(a.T, kQuadWarps * 8));
+            if (a.groups == 1) return launch_overlapped(route_quad_kernel<ELT, J, 0>, grid, kQuadWarps * 32, 0, 0, s, a);
             for (a.group_shift = 0; VPL << a.group_shift < a.group_size;) ++a.group_shift;
-            if (a.group_size == 16) return launch_overlapped(route_quad_kernel<ELT, J, 1>, grid, kWarps * 32, 0, 0, s, a);
-            if (a.group_size == 32) return launch_overlapped(route_quad_kernel<ELT, J, 2>, grid, kWarps * 32, 0, 0, s, a);
+            if (a.group_size == 16) return launch_overlapped(route_quad_kernel<ELT, J, 1>, grid, kQuadWarps * 32, 0, 0, s, a);
+            if (a.group_size == 32) return launch_overlapped(route_quad_kernel<ELT, J, 2>, grid, kQuadWarps * 32, 0, 0, s, a);
         }
     }
     if (a.groups == 1) return launch_overlapped(route_kernel<ELT, VPL, NONE>, grid, kWarps * 32, 0, 0, s, a);

@@ -694,6 +694,32 @@ def test_route_of_many_tokens(mx, case, dtype):
         check_route(mx, near_ties, topk, dev((0.7 - s).astype(np.float32)), **kw)
 
 
+@pytest.mark.parametrize("E,groups,topk_groups", [(256, 8, 4), (256, 16, 3), (128, 4, 2), (128, 8, 7), (160, 5, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [40, 16389])
+def test_route_of_groups_that_32_bits_cannot_tell_apart(mx, E, groups, topk_groups, score, T):
+    """The last group that is kept and the first that is not differ by a few units of 2^-26 of a score, or less."""
+    rng = np.random.default_rng(E + groups)
+    x = (1.5 * normal(rng, T, E)).astype(np.float64)
+    bias = 0.05 * normal(rng, E).astype(np.float64) if score == "sigmoid" else np.zeros(E)
+    act = bref.sigmoid if score == "sigmoid" else np.exp
+    c = (act(x) + bias).reshape(T, groups, -1)
+    order = np.argsort(c, 2)
+    two = np.take_along_axis(c, order[:, :, -2:], 2)
+    rank = np.argsort(-two.sum(2), 1)
+    rows = np.arange(0, T, 7)
+    kept, out = rank[rows, topk_groups - 1], rank[rows, topk_groups]
+    # the second largest of the group that is out makes its sum that of the other
+    e = out * (E // groups) + order[rows, out, -2]
+    s = two[rows, kept].sum(1) - two[rows, out, 1] - bias[e] + 2.0**-26 * rng.standard_normal(len(rows)) * (1 if score == "sigmoid" else 8)
+    fine = (s > 0) & (s + bias[e] < two[rows, out, 1]) & ((s < 1) | (score == "softmax"))
+    rows, e, s = rows[fine], e[fine], s[fine]
+    x[rows, e] = np.log(s / (1 - s)) if score == "sigmoid" else np.log(s)
+    assert len(rows) > 0
+    kw = dict(score=score, groups=groups, topk_groups=topk_groups, group_top=2)
+    check_route(mx, dev(x), 6, dev(bias) if score == "sigmoid" else None, **kw)
+
+
 def test_route_of_many_tokens_gives_what_few_do(mx):
     """A token's choice does not depend on how many there are with it."""
     x = torch.randn(20000, 256, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
