@@ -68,7 +68,8 @@ __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, 
             asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(relu.x) : "f"(g.x));
             asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(relu.y) : "f"(g.y));
             top = absmax3(top, g.x, g.y);
-            const float2 h = make_float2(min_nan(fabsf(g.x), kExpEnd), min_nan(fabsf(g.y), kExpEnd));
+            const auto size = [](float v) { return __uint_as_float(__float_as_uint(v) & 0x7FFFFFFFu); };  // of subnormal ones too
+            const float2 h = make_float2(min_nan(size(g.x), kExpEnd), min_nan(size(g.y), kExpEnd));
             const float2 r = mul2(silu2(h, exp_neg2(h), relu), make_float2(__uint_as_float(up[2 * j]), __uint_as_float(up[2 * j + 1])));
             v[2 * j] = r.x, v[2 * j + 1] = r.y;
         }

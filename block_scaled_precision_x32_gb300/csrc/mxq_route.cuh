@@ -851,15 +851,17 @@ template <Elt ELT>
 __device__ __noinline__ bool alike_row(const RouteArgs& a, int64_t t) {
     const int lane = threadIdx.x & 31;
     const float x = logit<ELT>(a, t, 0), b = a.bias ? a.bias[0] : 0.0f;
-    bool same = fabsf(x) < kInf && fabsf(b) < kInf && logit<ELT>(a, t, 1 + (lane & 3)) == x;
+    // as patterns: subnormal numbers are not zeros
+    const auto is = [](float v, float w) { return __float_as_uint(v) == __float_as_uint(w); };
+    bool same = fabsf(x) < kInf && fabsf(b) < kInf && is(logit<ELT>(a, t, 1 + (lane & 3)), x);
     if (!__any_sync(kAll, same)) return false;  // most often
 #pragma unroll 4
     for (int chunk = lane & 3; chunk * 4 < a.E; chunk += 4) {
         const float4 v = load_chunk<ELT>(a, t, chunk);
-        same &= v.x == x && v.y == x && v.z == x && v.w == x;
+        same &= is(v.x, x) && is(v.y, x) && is(v.z, x) && is(v.w, x);
         if (a.bias) {
             const float4 c = __ldg(reinterpret_cast<const float4*>(a.bias) + chunk);
-            same &= c.x == b && c.y == b && c.z == b && c.w == b;
+            same &= is(c.x, b) && is(c.y, b) && is(c.z, b) && is(c.w, b);
         }
     }
     __syncwarp();

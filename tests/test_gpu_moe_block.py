@@ -647,6 +647,31 @@ def test_the_fast_math_build_gives_the_same(mx):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("size", [1.0, 1e-38, 1e-41])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_the_fast_math_build_gives_the_same_near_the_ends(mx, size, dtype):
+    """Subnormal numbers too, by every kernel: many tokens and few, whole units and ragged rows."""
+    fast = mxq.Library(fastmath=True)
+    gen = torch.Generator("cuda").manual_seed(11)
+    new = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+
+    def same(f):
+        for a, b in zip(f(fast), f(mx)):
+            np.testing.assert_array_equal(a.cpu() if a.dtype == torch.int32 else host_bits(a), b.cpu() if b.dtype == torch.int32 else host_bits(b))
+
+    for T in (300, 16400):
+        for E, bias, kw in ((256, True, dict(score="sigmoid", groups=8, topk_groups=4, group_top=2)), (256, False, {}), (64, False, dict(score="sigmoid")),
+                            (160, True, dict(groups=8, topk_groups=2, renormalize=False)), (128, True, dict(score="sigmoid"))):
+            x, b = (size * new(T, E)).to(dtype), 0.05 * size * new(E) if bias else None
+            same(lambda m: m.moe_route(x, 8, bias=b, **kw))
+    for K in (512, 511):
+        x, w = (size * new(400, K)).to(dtype), new(K)
+        x2 = torch.cat([size * new(400, K), 1e30 * new(400, K)], 1).to(dtype)
+        r = mx.rmsnorm(x, w, x, stats=True)
+        same(lambda m: [t for t in m.rmsnorm(x, w, x, normed=True, stats=True)] + list(m.rmsnorm_grad(x, r.h, w, r.rstd, g_h=x)))
+        same(lambda m: [m.silu_mul(x2), *m.fp8_silu_mul_1x128(x2), *m.fp8_silu_mul_128x1(x2), m.silu_mul_grad(x, x2)])
+
+
 # ------------------------------------------------- routers of many tokens
 
 MANY = [
