@@ -138,9 +138,15 @@ __device__ __forceinline__ Wide larger(Wide a, Wide b) { return more(a, b) ? a :
 template <typename Real>
 __device__ __forceinline__ Real smaller(Real a, Real b) { return min(a, b); }
 __device__ __forceinline__ Wide smaller(Wide a, Wide b) { return more(a, b) ? b : a; }
-template <typename Real>
-__device__ __forceinline__ Real plus(Real a, Real b) { return a + b; }
-__device__ __forceinline__ Wide plus(Wide a, Wide b) { return add(a, b); }
+// (a + b) / 2 for a >= b > -inf, whose halves come first: two of the type's
+// largest or lowest numbers do not overflow.  An infinite a is the result itself,
+// which the steps of a Wide sum would make a NaN.
+__device__ __forceinline__ float half(float a) { return fmul(a, 0.5f); }
+__device__ __forceinline__ double half(double a) { return a * 0.5; }
+__device__ __forceinline__ Wide half(Wide a) { return {fmul(a.h, 0.5f), fmul(a.l, 0.5f)}; }
+__device__ __forceinline__ float half_sum(float a, float b) { return ffma(a, 0.5f, half(b)); }
+__device__ __forceinline__ double half_sum(double a, double b) { return half(a) + half(b); }
+__device__ __forceinline__ Wide half_sum(Wide a, Wide b) { return a.h == kInf ? a : add(half(a), half(b)); }
 template <typename Real>
 __device__ __forceinline__ Real lane_xor(Real v, int d) { return __shfl_xor_sync(kAll, v, d); }
 __device__ __forceinline__ Wide lane_xor(Wide v, int d) { return {__shfl_xor_sync(kAll, v.h, d), __shfl_xor_sync(kAll, v.l, d)}; }
@@ -182,9 +188,11 @@ struct Top2 {
         o.b = lane_xor(b, d);
         add(o);
     }
-    // The group's score; -inf where no expert of it can be chosen.
-    __device__ __forceinline__ Real score(int top) const { return top == 1 || none(b) ? a : plus(a, b); }
-    __device__ __forceinline__ float size() const { return (none(a) ? 0.0f : size_of(a)) + (none(b) ? 0.0f : size_of(b)); }
+    // The group's score, half of it where it is a sum; -inf where no expert of it can be chosen.
+    __device__ __forceinline__ Real score(int top) const { return top == 1 ? a : none(b) ? half(a) : half_sum(a, b); }
+    // Magnitudes that are rounded in it; what is infinite is exact.
+    __device__ __forceinline__ float size() const { return finite_size(size_of(a)) + finite_size(size_of(b)); }
+    __device__ __forceinline__ static float finite_size(float v) { return v < kInf ? half(v) : 0.0f; }
 };
 template <int N, typename Real>
 __device__ __forceinline__ Top2<Real> top2_of(const Real* c) {
@@ -251,8 +259,8 @@ __device__ __forceinline__ bool kept_group(const RouteArgs& a, int lane, const R
         // the last group that is kept against the best that is not
         const unsigned last = __ballot_sync(kAll, real && ahead == a.topk_groups - 1), next = __ballot_sync(kAll, real && ahead == a.topk_groups);
         const Real least = lane_at(mine, __ffs(last) - 1), best = lane_at(mine, __ffs(next) - 1);
-        const float tol = 2 * a.group_top * err + 2 * kRound<Real> * warp_max(size);
-        unsure |= !none(best) && gap(least, best) <= tol;
+        const float tol = 2 * err + 3 * kRound<Real> * warp_max(size);
+        unsure |= size_of(least) < kInf && !none(best) && !(gap(least, best) > tol);  // infinite ones are ties, or far ahead
     }
     return real && ahead < a.topk_groups;
 }
@@ -309,10 +317,11 @@ __device__ __forceinline__ void best_groups(const RouteArgs& a, int lane, Real (
 }
 
 // Can two neighbours of the order, last in front of e, not be told apart?
-// Equal logits with equal biases are ties, which the index decides.
+// Equal logits with equal biases are ties, which the index decides, and so are
+// infinite c; one of them is far ahead of what is finite.
 template <Elt ELT, typename Real>
 __device__ __forceinline__ bool too_near(const RouteArgs& a, int64_t t, float err, Real last_c, int last, Real c, int e) {
-    return gap(last_c, c) <= 2 * err + kRound<Real> * max(size_of(last_c), size_of(c)) &&
+    return size_of(last_c) < kInf && gap(last_c, c) <= 2 * err + kRound<Real> * max(size_of(last_c), size_of(c)) &&
            !(logit<ELT>(a, t, last) == logit<ELT>(a, t, e) && (!a.bias || a.bias[last] == a.bias[e]));
 }
 
@@ -415,7 +424,7 @@ __device__ __noinline__ bool resolve(const RouteArgs& a, int64_t t, int n, uint6
         const Wide o = lane_at(c, j);
         const float ox = __shfl_sync(kAll, x, j), ob = __shfl_sync(kAll, b, j);
         if (__shfl_sync(kAll, rank, j) == rank + 1 && rank < a.topk && lane < n && !(ox == x && ob == b))
-            unsure |= gap(c, o) <= 2 * err + kRound<Wide> * max(size_of(c), size_of(o));
+            unsure |= size_of(c) < kInf && gap(c, o) <= 2 * err + kRound<Wide> * max(size_of(c), size_of(o));
     }
     __syncwarp();
     if (lane < n) list[rank] = (uint64_t)key_of(c.h) << 32 | (uint32_t)~id;
@@ -964,7 +973,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 20 / kQuadWarps) route_quad_k
 #pragma unroll
         for (int g = 0; g < G; ++g) out[g] = !kept[g];
         if (scored) {  // the same for every lane, as err is not: a row that cannot be scored has NaN there
-            unsigned nears = __ballot_sync(kAll, next > -kInf && least - next <= 2 * a.group_top * err + 2 * kRound<float> * size && !left);
+            unsigned nears = __ballot_sync(kAll, next > -kInf && least - next <= 2 * err + 3 * kRound<float> * size && !left);
             if (nears) {
                 left |= alike_row<ELT>(a, t);
                 nears &= __ballot_sync(kAll, !left);

@@ -1,0 +1,68 @@
+"""The router on the GPU near the ends of its biases' range.  Tolerances as in
+test_gpu_moe_block, but where a test derives its own."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_x32_gb300 as mxq
+from tests.test_gpu_moe_block import F32, check_route, dev, normal
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = float(torch.finfo(F32).min)
+
+
+@pytest.fixture(scope="module")
+def mx():
+    return mxq.library()
+
+
+# ------------------------------------------------------------------ router
+
+
+def grouped_logits(rng, T, E, groups):
+    """Ordinary rows, and among them rows of two groups that are alike, whose order only the index decides, and rows of groups a
+    few units in the last place apart."""
+    x = 1.5 * normal(rng, T, E)
+    size = E // groups
+    for i in range(groups):
+        a, b = (slice(g * size, (g + 1) * size) for g in (i, (i + 3) % groups))
+        x[i::29, b] = x[i::29, a]
+        x[i + 11::29, b] = x[i + 11::29, a] * (1 + np.float32(2e-7))
+    return x
+
+
+@pytest.mark.parametrize("T", [70, 16389])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [np.inf, LOWEST, -1e38, 3e38])
+@pytest.mark.parametrize("topk_groups", [1, 4])
+def test_route_of_groups_with_biases_at_the_ends(mx, T, score, value, topk_groups):
+    """One expert, or all of a group, always or never to be chosen by its bias, in each group in turn."""
+    E, groups = 128, 8
+    rng = np.random.default_rng(topk_groups)
+    x = dev(grouped_logits(rng, T, E, groups))
+    for ordinary, places in ((0.0, range(groups)), (0.05, range(groups))) if T < 1000 else ((0.0, (0, 3, 7)), (0.05, (4,))):
+        for g in places:
+            for experts in (slice(16 * g + 5, 16 * g + 6), slice(16 * g, 16 * g + 16)):
+                b = (ordinary * normal(rng, E)).astype(np.float32)
+                b[experts] = value
+                check_route(mx, x, 8, dev(b), score=score, groups=groups, topk_groups=topk_groups, group_top=2)
+
+
+@pytest.mark.parametrize("T", [70, 16389])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_route_of_several_groups_with_biases_at_the_ends(mx, T, group_top):
+    """More groups that are always, or never, to be chosen than there are places, or than there are others; a group of the
+    type's lowest value is ahead of one without any expert."""
+    E, groups = 128, 8
+    rng = np.random.default_rng(group_top)
+    x = grouped_logits(rng, T, E, groups)
+    x[3::17, 64:80] = -np.inf
+    for values in ((np.inf, np.inf, np.inf, np.inf, np.inf), (LOWEST, LOWEST, LOWEST, LOWEST, LOWEST), (3e38, 3.2e38, 3e38, np.inf, 3.4e38),
+                   (LOWEST, -np.inf, LOWEST, np.inf, LOWEST), (np.inf, LOWEST, -3e38, -3.2e38, 2e38)):
+        b = np.zeros(E, np.float32)
+        for g, v in zip((1, 2, 4, 6, 7), values):
+            b[16 * g: 16 * g + 16] = v
+        for score in ("softmax", "sigmoid"):
+            check_route(mx, dev(x), 4, dev(b), score=score, groups=groups, topk_groups=4, group_top=group_top)
