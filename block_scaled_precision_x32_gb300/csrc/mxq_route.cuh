@@ -242,6 +242,9 @@ enum Groups { NONE, LANES, ANY };
 
 // Is the lane's group, of 1 << shift lanes, among the best?  mine: its score,
 // size: the magnitudes in it; a choice within the error of the scores sets `unsure`.
+// The choice is certain if no group's own error takes it across the middle
+// between the last group that is kept and the best that is not: a group that a
+// bias of -1e9 keeps out has a large error, and is far from it.
 template <typename Real>
 __device__ __forceinline__ bool kept_group(const RouteArgs& a, int lane, const Real& mine, float size, int group, int shift, float err, bool& unsure) {
     int ahead = 0;
@@ -256,11 +259,10 @@ __device__ __forceinline__ bool kept_group(const RouteArgs& a, int lane, const R
     for (int d = 1; d < 1 << shift; d *= 2) ahead += __shfl_xor_sync(kAll, ahead, d);
     const bool real = group < a.groups;
     if (err >= 0.0f && a.topk_groups < a.groups) {
-        // the last group that is kept against the best that is not
         const unsigned last = __ballot_sync(kAll, real && ahead == a.topk_groups - 1), next = __ballot_sync(kAll, real && ahead == a.topk_groups);
         const Real least = lane_at(mine, __ffs(last) - 1), best = lane_at(mine, __ffs(next) - 1);
-        const float tol = 2 * err + 3 * kRound<Real> * warp_max(size);
-        unsure |= size_of(least) < kInf && !none(best) && !(gap(least, best) > tol);  // infinite ones are ties, or far ahead
+        const float from_middle = half(gap(least, best)) + (ahead < a.topk_groups ? gap(mine, least) : gap(best, mine));
+        unsure |= real && size_of(least) < kInf && !none(best) && !(from_middle > err + 1.5f * kRound<Real> * size);  // infinite ones are ties, or far ahead
     }
     return real && ahead < a.topk_groups;
 }
@@ -787,6 +789,38 @@ __device__ __forceinline__ float4 load_chunk(const RouteArgs& a, int64_t t, int 
     }
 }
 
+// What 24 bits tell of the groups of a token with each one's own error: a bit for
+// each that is kept, -1 where they do not tell.  The four lanes have registers for
+// the largest error alone (with each group's in them the usual call took 50 us
+// instead of 48), which a group that a bias of -1e9 keeps out sets for every token:
+// 65536 x 256 take 99 us then, and 315 if all of them go on to 48 bits.
+template <Elt ELT, int VPL>
+__device__ __noinline__ int groups24(const RouteArgs& a, int64_t t, int lane) {
+    float c[VPL], s[VPL], b[VPL], total = 0.0f, most = 1.0f;
+    load_logits<ELT, VPL>(a, t, lane, c);
+    scores<VPL>(a, c, a.sigmoid ? 0.0f : warp_max(max_nan<VPL>(c)), s);
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) total = fadd(total, s[i]);
+        most = fdiv(1.0f, lane_sum(total));
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) b[i] = 0.0f;
+    if (a.bias) load_bias<VPL>(a, lane, b);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = c[i] > -kInf ? ffma(s[i], most, b[i]) : -kInf;
+    Top2<float> top = top2_of<VPL>(c);
+    const int shift = a.group_shift;
+#pragma unroll 1
+    for (int d = 1; d < 1 << shift; d *= 2) top.merge(d);
+    bool unsure = false;
+    const float err = (a.sigmoid ? 6.0f : VPL + 32.0f) * 5.9604645e-8f * most;  // as in route_token
+    const unsigned lanes = __ballot_sync(kAll, kept_group<float>(a, lane, top.score(a.group_top), top.size(), lane >> shift, shift, err, unsure));
+    int bits = 0;
+    for (int g = 0; g < a.groups; ++g) bits |= (int)(lanes >> (g << shift) & 1) << g;
+    return __any_sync(kAll, unsure) ? -1 : bits;
+}
+
 // A second look, with 48 bits, at the groups of a token: a bit for each that is
 // kept, -1 where 48 bits do not tell either.  Only what can be among the largest of
 // its group gets one.
@@ -979,7 +1013,10 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 20 / kQuadWarps) route_quad_k
                 nears &= __ballot_sync(kAll, !left);
             }
             while (nears) {  // one token after the other, by the whole warp
-                const int quad = (__ffs(nears) - 1) >> 2, bits = groups48<ELT, J / 2>(a, __shfl_sync(kAll, t, 4 * quad), lane);
+                const int quad = (__ffs(nears) - 1) >> 2;
+                const int64_t token = __shfl_sync(kAll, t, 4 * quad);
+                int bits = __shfl_sync(kAll, size, 4 * quad) > 16.0f ? groups24<ELT, J / 2>(a, token, lane) : -1;
+                if (bits < 0) bits = groups48<ELT, J / 2>(a, token, lane);
                 if (lane >> 2 == quad) {
                     left |= bits < 0;
 #pragma unroll

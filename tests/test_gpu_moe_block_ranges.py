@@ -66,3 +66,59 @@ def test_route_of_several_groups_with_biases_at_the_ends(mx, T, group_top):
             b[16 * g: 16 * g + 16] = v
         for score in ("softmax", "sigmoid"):
             check_route(mx, dev(x), 4, dev(b), score=score, groups=groups, topk_groups=4, group_top=group_top)
+
+
+def device_us(f, n=5):
+    """Device time of f's launches, the least of n replays of a captured call."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        f()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            f()
+        times = []
+        for _ in range(n):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(1e3 * a.elapsed_time(b))
+    return min(times)
+
+
+@pytest.mark.parametrize("value", [-1e9, -1e30, LOWEST])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_group_masked_by_a_finite_bias_is_no_reason_to_look_twice(mx, value, score):
+    """Three of eight groups are masked: the others' scores are as far apart as they were.  A second look with 48 bits at
+    every token takes six times as long and more; four times is allowed."""
+    T, E = 65536, 256
+    rng = np.random.default_rng(8)
+    x, b = 1.5 * normal(rng, T, E), (0.05 * normal(rng, E)).astype(np.float32)
+    kw = dict(score=score, groups=8, topk_groups=4, group_top=2)
+    logits, plain = dev(x), dev(b)
+    b[32:64] = b[128:160] = b[224:] = value
+    masked = dev(b)
+    check_route(mx, logits[:20001], 8, masked, **kw)
+    check_route(mx, logits[:900], 8, masked, **kw)
+    for n in (T, 4096):
+        few = logits[:n]
+        slow, usual = (device_us(lambda: mx.moe_route(few, 8, bias=v, **kw)) for v in (masked, plain))
+        assert slow < 4 * usual, (n, slow, usual)
+
+
+@pytest.mark.parametrize("T", [70, 16389])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_of_groups_whose_own_error_is_large(mx, T, score):
+    """A dropped group, or a kept one, whose score is a difference of large numbers: it is the one that has to be looked at
+    again, and not the neighbour of the border.  Biases of +-2^k leave a sum of the two best that fp32 gives to 2^(k - 23) only."""
+    E, groups = 128, 8
+    rng = np.random.default_rng(5)
+    x = dev(1.5 * normal(rng, T, E))
+    for k in (12, 18, 21, 22):
+        for g in range(groups):
+            b = (0.05 * normal(rng, E)).astype(np.float32)
+            b[16 * g: 16 * g + 16] = -np.float32(2.0**k)
+            b[16 * g + 3] = np.float32(2.0**k + (0.5 if score == "sigmoid" else 0.0))
+            check_route(mx, x, 8, dev(b), score=score, groups=groups, topk_groups=3, group_top=2)
