@@ -1275,7 +1275,12 @@ cudaError_t launch(bool grad, RouteArgs a, cudaStream_t s) {
     a.group_size = a.E / a.groups;
     if constexpr (VPL == 4 || VPL == 8) {
         const bool chunks = a.E % 4 == 0 && on_bytes(a.logits, 16) && (a.T <= 1 || a.ld % 4 == 0) && on_bytes(a.bias, 16);
-        if (chunks && a.topk <= kQuadTopk && a.T >= kQuadTokens) {
+        // kept experts of so few chunks that no bound is found among the chunks' maxima, and more of them than can be ranked: every token
+        // would be left to the whole warp after all.  32 kept in two groups or one, 65536 x 128: 125 and 121 us, a warp to each 47 and 48;
+        // 65536 x 256: 193 and 167, a warp to each 76 and 68
+        const int kept = a.groups > 1 ? a.topk_groups * a.group_size : a.E;
+        const bool crowded = kept > kRanked && kept < 4 * kQuadKept;
+        if (chunks && !crowded && a.topk <= kQuadTopk && a.T >= kQuadTokens) {
             constexpr int J = 2 * VPL;
             const dim3 grid((unsigned)ceil_div(a.T, kQuadWarps * 8));
             if (a.groups == 1) return launch_overlapped(route_quad_kernel<ELT, J, 0>, grid, kQuadWarps * 32, 0, 0, s, a);

@@ -122,3 +122,16 @@ def test_route_of_groups_whose_own_error_is_large(mx, T, score):
             b[16 * g: 16 * g + 16] = -np.float32(2.0**k)
             b[16 * g + 3] = np.float32(2.0**k + (0.5 if score == "sigmoid" else 0.0))
             check_route(mx, x, 8, dev(b), score=score, groups=groups, topk_groups=3, group_top=2)
+
+
+@pytest.mark.parametrize("groups,topk_groups", [(8, 2), (4, 1)])
+def test_a_router_that_keeps_two_warps_worth_of_experts(mx, groups, topk_groups):
+    """32 kept experts are all candidates: they do not fit the lists of the four-lane kernel, whose tokens would all be taken
+    again one by one (seven times as long).  One group more is the yardstick; three times its time is allowed."""
+    T, E = 65536, 128
+    rng = np.random.default_rng(2)
+    x, b = dev(1.5 * normal(rng, T, E)), dev(0.05 * normal(rng, E))
+    kw = dict(score="sigmoid", groups=groups, group_top=2, bias=b)
+    check_route(mx, x[:16400], 4, b, score="sigmoid", groups=groups, topk_groups=topk_groups, group_top=2)
+    crowded, usual = (device_us(lambda: mx.moe_route(x, 4, topk_groups=n, **kw)) for n in (topk_groups, topk_groups + 1))
+    assert crowded < 3 * usual, (crowded, usual)
