@@ -152,21 +152,14 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // exp(-a) for a >= 0, off by 3e-7 of itself at most.  exp(-a) = 2^t with
 // t = -a log2(e); the product is kept to twice its bits, t + r, so that its
 // rounding does not grow with a, and 2^(t + r) = 2^t (1 + r ln 2) for the
-// small r.  a is cut off at 160, where the result is zero either way: the
-// caller of exp_neg2 does that.  NaN stays NaN.
+// small r.  a is cut off at 160, where the result is zero either way.  NaN stays
+// NaN.
 constexpr float kExpHi = -1.4426950216293335f, kExpLo = -1.9259629911e-8f, kLn2 = 0.6931471805599453f, kExpEnd = 160.0f;
 __device__ __forceinline__ float exp_neg(float a) {
     a = min_nan(a, kExpEnd);
     const float t = fmul(a, kExpHi), r = ffma(a, kExpLo, ffma(a, kExpHi, -t)), p = ex2_approx(t);
     return ffma(fmul(p, kLn2), r, p);
 }
-__device__ __forceinline__ float2 exp_neg2(float2 a) {
-    const float2 t = mul2(a, both(-kExpHi));  // -t
-    const float2 r = fma2(a, both(kExpLo), fma2(a, both(kExpHi), t));
-    const float2 p = make_float2(ex2_approx(-t.x), ex2_approx(-t.y));
-    return fma2(mul2(p, both(kLn2)), r, p);
-}
-
 __device__ __forceinline__ float rcp_approx(float v) {
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(v));
     return v;
@@ -183,16 +176,6 @@ struct Sigmoid {
         rest = neg ? inv : low;
     }
 };
-
-// silu(x) = x / (1 + exp(-x)) of two values: with h = |x| and e = exp(-h),
-// 1 / (1 + exp(-x)) is 1 - e / (1 + e) for x >= 0 and e / (1 + e) below, so
-// that silu(x) = max(x, 0) - h e / (1 + e) for both: no choice to be made.
-// h comes cut off at kExpEnd, relu is max(x, 0).  Off by 11 units of 2^-24 of
-// itself: e / (1 + e) by 10, and it is at most one half.
-__device__ __forceinline__ float2 silu2(float2 h, float2 e, float2 relu) {
-    const float2 d = fma2(e, both(-1.0f), both(-1.0f));
-    return fma2(h, mul2(e, make_float2(rcp_approx(d.x), rcp_approx(d.y))), relu);
-}
 
 // Largest magnitude of `m` and two more values; NaN if one of them is.
 __device__ __forceinline__ float absmax3(float m, float a, float b) {

@@ -13,71 +13,80 @@
 namespace mxq {
 namespace {
 
+// exp(-x) passes the end of fp32's range for a gate x of -87.3, but what it
+// leaves of a large other factor may be any number.  Gates below kFar take it as
+// exp(-x) 2^-116, and the other factor times 2^-116 as well, both exact: their
+// results keep all their bits down to -167.7.  Below that they are 0, for what is
+// less than 167.8 2^-242 = 2.4e-71 of the other factor.  (What the
+// scaled factor loses where it is subnormal does not count: below kFar
+// 2^116 x / (1 + exp(-x)), which it is multiplied with, is at most 1.)
+constexpr float kFar = -85.0f, kShift = 116.0f, kScale = 0x1p-116f;
+struct Scaled {
+    float2 shift, scale;
+    __device__ __forceinline__ explicit Scaled(float2 x) {
+        const bool a = x.x < kFar, b = x.y < kFar;
+        shift = make_float2(a ? kShift : 0.0f, b ? kShift : 0.0f);
+        scale = make_float2(a ? kScale : 1.0f, b ? kScale : 1.0f);
+    }
+};
+
+// 1 is added to it, or 2^-116 to what is larger: nothing is lost by taking
+// subnormal results as zeros, which saves three instructions.
+__device__ __forceinline__ float ex2_ftz(float t) {
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return p;
+}
+__device__ __forceinline__ float2 ex2_neg(float2 t) { return make_float2(ex2_ftz(-t.x), ex2_ftz(-t.y)); }
+
+// exp(-x) scale of two fp32 gates, off by 4 units of 2^-24 of itself: as exp_neg,
+// for numbers of either sign.  Below -168, where it is out of range, it is that of
+// -168, and above 160 0.
+__device__ __forceinline__ float2 exp_scaled(float2 x, const Scaled& c) {
+    const auto cut = [](float v) {
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-168.0f));
+        return min_nan(v, kExpEnd);
+    };
+    x = make_float2(cut(x.x), cut(x.y));
+    const float2 t = mul2(x, both(-kExpHi)), r = fma2(x, both(kExpLo), fma2(x, both(kExpHi), t)), p = ex2_neg(fma2(t, both(1.0f), c.shift));
+    return fma2(mul2(p, both(kLn2)), r, p);
+}
+
 // N = 2, 4, ... values of a: gate and up as Unit's words hold them.  Bound by
 // instructions as much as by memory, so two values go through each.
 //
-// The exponential of a bf16 gate takes fewer of them than exp_neg2: log2(e) is
-// cut into K1 of 16 bits, whose product with the gate's 8 is exact, and the
-// rest K2 = 7.1e-6: exp(-h) = 2^(-h K1) (1 - h K2 ln 2), off by (h K2)^2 / 4 <
-// 1.5 units of 2^-24 for the second order left out, up to h = 88, and 5 with
-// the rest.
+// silu(x) is taken as x / (1 + exp(-x)), which needs no choice by the sign; -inf
+// gives the NaN that it has by its definition, 0 * inf.
 //
-// To be quantized, silu(x) is taken as x / (1 + exp(-x)), which needs no choice
-// by the sign.  Where 1 + exp(-x) exceeds 2^126 the quotient is zero: a gate under
-// -87.3 gives 0 for what is less than 1.1e-36 |up|.  (To find those gates and to
-// give them their bits took the 128x1 form from 52 to 57 us.)  An infinite gate gives
-// NaN, of either sign: its block is poisoned as it would be by an infinity.
-// Otherwise -inf, whose silu is 0 * inf by its definition, is looked for once for all.
+// The exponential of a bf16 gate takes fewer instructions than that of others:
+// log2(e) is cut into K1 of 16 bits, whose product with the gate's 8 is exact, and
+// the rest K2 = 7.1e-6: exp(-x) = 2^(-x K1) (1 - x K2 ln 2), off by (x K2 ln 2)^2 / 2
+// for the second order left out: 1.5 units of 2^-24 at 88 and 6 at 168; 4 more for
+// the rest.  In the FP8 forms an infinite bf16 gate gives NaN, of either sign: its
+// block is poisoned as it would be by an infinity.
 template <Elt ELT, int N, bool QUANT>
 __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, float* v) {
-    if constexpr (ELT == Elt::BF16) {
-        constexpr float K1 = 47274.0f / 32768.0f, K2 = 7.0526077e-6f * kLn2;
-        const auto two = [](uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
-        const auto exp_of = [&](float2 h) {  // exp(-h)
-            const float2 t = mul2(h, both(K1));
-            return mul2(make_float2(ex2_approx(-t.x), ex2_approx(-t.y)), fma2(h, both(-K2), both(1.0f)));
-        };
-        uint32_t top = 0;
+    constexpr float K1 = 47274.0f / 32768.0f, K2 = 7.0526077e-6f * kLn2;
+    const auto two = [](const uint32_t* w, int j) {
+        if constexpr (ELT == Elt::BF16) return make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+        else return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+    };
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-            if constexpr (QUANT) {
-                const float2 x = two(gate[j]), d = fma2(exp_of(x), both(1.0f), both(1.0f));
-                const float2 r = mul2(mul2(x, make_float2(rcp_approx(d.x), rcp_approx(d.y))), two(up[j]));
-                v[2 * j] = r.x, v[2 * j + 1] = r.y;
-            } else {
-                const uint32_t mag = gate[j] & 0x7FFF7FFFu;
-                uint32_t cut, relu;
-                asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(cut) : "r"(mag), "r"(0x43204320u));  // kExpEnd
-                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(relu) : "r"(gate[j]), "r"(0u));
-                top = u16x2_max(top, mag);
-                const float2 r = mul2(silu2(two(cut), exp_of(two(cut)), two(relu)), two(up[j]));
-                v[2 * j] = r.x, v[2 * j + 1] = r.y;
-            }
+    for (int j = 0; j < N / 2; ++j) {
+        const float2 x = two(gate, j);
+        const Scaled c(x);
+        float2 e;
+        if constexpr (ELT == Elt::BF16) {
+            uint32_t cut = gate[j];
+            if constexpr (!QUANT) asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(cut) : "r"(0x43204320u));  // kExpEnd
+            const float2 y = two(&cut, 0);
+            e = mul2(ex2_neg(fma2(y, both(K1), c.shift)), fma2(y, both(-K2), both(1.0f)));
+        } else {
+            e = exp_scaled(x, c);
         }
-        if (!QUANT && ((top & 0x7FFFu) >= 0x7F80u || top >= 0x7F800000u)) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if ((gate[j / 2] >> (16 * (j & 1)) & 0xFFFFu) == 0xFF80u) v[j] = __uint_as_float(0x7FC00000u);
-        }
-    } else {
-        float top = 0.0f;
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-            const float2 g = make_float2(__uint_as_float(gate[2 * j]), __uint_as_float(gate[2 * j + 1]));
-            float2 relu;
-            asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(relu.x) : "f"(g.x));
-            asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(relu.y) : "f"(g.y));
-            top = absmax3(top, g.x, g.y);
-            const auto size = [](float v) { return __uint_as_float(__float_as_uint(v) & 0x7FFFFFFFu); };  // of subnormal ones too
-            const float2 h = make_float2(min_nan(size(g.x), kExpEnd), min_nan(size(g.y), kExpEnd));
-            const float2 r = mul2(silu2(h, exp_neg2(h), relu), make_float2(__uint_as_float(up[2 * j]), __uint_as_float(up[2 * j + 1])));
-            v[2 * j] = r.x, v[2 * j + 1] = r.y;
-        }
-        if (__float_as_uint(top) >= 0x7F800000u) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (gate[j] == 0xFF800000u) v[j] = __uint_as_float(0x7FC00000u);
-        }
+        const float2 d = fma2(e, both(1.0f), c.scale);
+        const float2 r = mul2(mul2(x, make_float2(rcp_approx(d.x), rcp_approx(d.y))), mul2(two(up, j), c.scale));
+        v[2 * j] = r.x, v[2 * j + 1] = r.y;
     }
 }
 
@@ -122,10 +131,10 @@ __device__ __forceinline__ uint32_t amax_of(const float* v) {
 }
 
 // Rows of units of 16 elements, eight lanes to a 1x128 block.  Bound by HBM:
-// 16384 x 4096 bf16 to FP8 53.5 us, 6.3 TB/s (units of 8 elements 67 to 86), to
-// bf16 68, 5.9 TB/s.
+// 16384 x 4096 bf16 to FP8 54.0 us, 6.2 TB/s (units of 8 elements 67 to 86; six or
+// seven blocks a multiprocessor, whose registers spill, 59), to bf16 57.4, 7.0 TB/s.
 template <Elt ELT, bool QUANT>
-__global__ void __launch_bounds__(256, ELT == Elt::FP32 ? 4 : QUANT ? 7 : 5) gate_rows_kernel(GateArgs a, int64_t nb) {
+__global__ void __launch_bounds__(256, ELT == Elt::FP32 ? 4 : QUANT ? 5 : 6) gate_rows_kernel(GateArgs a, int64_t nb) {
     let_next_start();
     wait_for_stream();
     constexpr int N = 16, LANES = 128 / N, W = N * elt_bytes<ELT>() / 4;
@@ -184,14 +193,15 @@ __global__ void __launch_bounds__(256, ELT == Elt::FP32 ? 4 : QUANT ? 7 : 5) gat
 // Tiles of 128 rows x C TX columns a block, C columns of R rows a thread, in
 // registers between the maximum and the rounding: each element is read once.
 // bf16: few columns of many rows, since each column's maximum costs shuffles
-// and its scale unpacking, and 64 registers: 16379 x 4096 51.8 us, 6.5 TB/s
+// and its scale unpacking, and 64 registers: 16379 x 4096 51.9 us, 6.5 TB/s
 // (eight columns of four rows 63 to 73, seven blocks a multiprocessor 54.6, 16
-// threads a row 54.6).  fp32: wide loads count for more, 8191 x 4096 45.8 us, 6.6
-// TB/s (four columns of eight rows 57 to 66).
+// threads a row 54.6).  fp32: wide loads count for more, 8191 x 4096 48.8 us, 6.2
+// TB/s (four columns of eight rows 57 to 66; five or seven blocks a multiprocessor 56.6
+// and 51.2).
 template <Elt ELT>
 struct GateTile {
     static constexpr bool kBf16 = ELT == Elt::BF16;
-    static constexpr int kC = kBf16 ? 4 : 8, kX = kBf16 ? 8 : 4, kRows = kBf16 ? 8 : 4, kBlocks = kBf16 ? 8 : 7;
+    static constexpr int kC = kBf16 ? 4 : 8, kX = kBf16 ? 8 : 4, kRows = kBf16 ? 8 : 4, kBlocks = kBf16 ? 8 : 6;
     static constexpr int kThreads = kX * 128 / kRows;
 };
 template <Elt ELT>
@@ -282,7 +292,7 @@ struct GateGrad {
 // Any alignment and any H, every form but COLUMNS: one row to blockIdx.x, its
 // 1x128 blocks to the warps of blockIdx.y in turn, an element at a time,
 // neighbours to neighbouring lanes.  Bound by instructions: 8191 x 4095 bf16 to FP8
-// 43.5 us, its gradient 66, 3.9 and 5.1 TB/s.
+// 44.1 us, its gradient 66, 3.8 and 5.1 TB/s.
 template <Elt ELT, GateForm FORM>
 __global__ void __launch_bounds__(256) gate_any_kernel(GateArgs a, int nb) {
     let_next_start();

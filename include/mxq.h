@@ -560,9 +560,9 @@ MXQ_API mxq_status mxq_moe_route_grad(const float* g, const mxq_route* p, const 
  * the fp32 a, as mxq_fp8_quant_1x128 does for the second product and
  * mxq_fp8_quant_128x1 for its weight's gradient: data [rows, H]; scales [rows,
  * ceil(H/128)] or [ceil(rows/128), H].
- * silu(-inf) is NaN (0 * inf); an infinite bf16 gate of either sign poisons its
- * block, as an infinity does.  The fp8 forms of a bf16 gate below -87.3 give 0 for
- * what is less than 1.1e-36 |up|.
+ * silu(-inf) is NaN (0 * inf); an infinite gate of either sign poisons its block in
+ * the fp8 forms, as an infinity does.  Gates below -167.7 give 0 for what is less
+ * than 2.4e-71 |up|.
  * Errors: INVALID_ARG, UNSUPPORTED_DTYPE. */
 MXQ_API mxq_status mxq_silu_mul(const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldx, void* out,
                                 cudaStream_t stream);
