@@ -39,34 +39,40 @@ __device__ __forceinline__ float ex2_ftz(float t) {
 }
 __device__ __forceinline__ float2 ex2_neg(float2 t) { return make_float2(ex2_ftz(-t.x), ex2_ftz(-t.y)); }
 
-// exp(-x) scale of two fp32 gates, off by 4 units of 2^-24 of itself: as exp_neg,
-// for numbers of either sign.  Below -168, where it is out of range, it is that of
-// -168, and above 160 0.
+// exp(-x) scale of two gates, off by 4 units of 2^-24 of itself: as exp_neg, for
+// numbers of either sign.  CUT: that of -168, where 1 / (1 + exp(-x)) is 0, below it,
+// and 0 above 160.  Else it passes into infinity, and is NaN for +inf.
+//
+// That of a bf16 gate takes fewer instructions: log2(e) is cut into K1 of 16 bits,
+// whose product with the gate's 8 is exact, and the rest K2 = 7.1e-6: exp(-x) =
+// 2^(-x K1) (1 - x K2 ln 2), off by (x K2 ln 2)^2 / 2 more for the second order left out,
+// 1.5 units at 88 and 6 at 168.
+template <Elt ELT, bool CUT>
 __device__ __forceinline__ float2 exp_scaled(float2 x, const Scaled& c) {
     const auto cut = [](float v) {
         asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-168.0f));
         return min_nan(v, kExpEnd);
     };
-    x = make_float2(cut(x.x), cut(x.y));
-    const float2 t = mul2(x, both(-kExpHi)), r = fma2(x, both(kExpLo), fma2(x, both(kExpHi), t)), p = ex2_neg(fma2(t, both(1.0f), c.shift));
-    return fma2(mul2(p, both(kLn2)), r, p);
+    if constexpr (CUT) x = make_float2(cut(x.x), cut(x.y));
+    if constexpr (ELT == Elt::BF16) {
+        constexpr float K1 = 47274.0f / 32768.0f, K2 = 7.0526077e-6f * kLn2;
+        return mul2(ex2_neg(fma2(x, both(K1), c.shift)), fma2(x, both(-K2), both(1.0f)));
+    } else {
+        static_assert(CUT);  // the largest numbers' product with log2(e) is infinite
+        const float2 t = mul2(x, both(-kExpHi)), r = fma2(x, both(kExpLo), fma2(x, both(kExpHi), t)), p = ex2_neg(fma2(t, both(1.0f), c.shift));
+        return fma2(mul2(p, both(kLn2)), r, p);
+    }
 }
 
 // N = 2, 4, ... values of a: gate and up as Unit's words hold them.  Bound by
 // instructions as much as by memory, so two values go through each.
 //
 // silu(x) is taken as x / (1 + exp(-x)), which needs no choice by the sign; -inf
-// gives the NaN that it has by its definition, 0 * inf.
-//
-// The exponential of a bf16 gate takes fewer instructions than that of others:
-// log2(e) is cut into K1 of 16 bits, whose product with the gate's 8 is exact, and
-// the rest K2 = 7.1e-6: exp(-x) = 2^(-x K1) (1 - x K2 ln 2), off by (x K2 ln 2)^2 / 2
-// for the second order left out: 1.5 units of 2^-24 at 88 and 6 at 168; 4 more for
-// the rest.  In the FP8 forms an infinite bf16 gate gives NaN, of either sign: its
-// block is poisoned as it would be by an infinity.
+// gives the NaN that it has by its definition, 0 * inf.  In the FP8 forms an infinite
+// bf16 gate gives NaN, of either sign: its block is poisoned as it would be by an
+// infinity.
 template <Elt ELT, int N, bool QUANT>
 __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, float* v) {
-    constexpr float K1 = 47274.0f / 32768.0f, K2 = 7.0526077e-6f * kLn2;
     const auto two = [](const uint32_t* w, int j) {
         if constexpr (ELT == Elt::BF16) return make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
         else return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
@@ -75,16 +81,7 @@ __device__ __forceinline__ void gated(const uint32_t* gate, const uint32_t* up, 
     for (int j = 0; j < N / 2; ++j) {
         const float2 x = two(gate, j);
         const Scaled c(x);
-        float2 e;
-        if constexpr (ELT == Elt::BF16) {
-            uint32_t cut = gate[j];
-            if constexpr (!QUANT) asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(cut) : "r"(0x43204320u));  // kExpEnd
-            const float2 y = two(&cut, 0);
-            e = mul2(ex2_neg(fma2(y, both(K1), c.shift)), fma2(y, both(-K2), both(1.0f)));
-        } else {
-            e = exp_scaled(x, c);
-        }
-        const float2 d = fma2(e, both(1.0f), c.scale);
+        const float2 d = fma2(exp_scaled<ELT, !QUANT || ELT == Elt::FP32>(x, c), both(1.0f), c.scale);
         const float2 r = mul2(mul2(x, make_float2(rcp_approx(d.x), rcp_approx(d.y))), mul2(two(up, j), c.scale));
         v[2 * j] = r.x, v[2 * j + 1] = r.y;
     }
@@ -132,7 +129,7 @@ __device__ __forceinline__ uint32_t amax_of(const float* v) {
 
 // Rows of units of 16 elements, eight lanes to a 1x128 block.  Bound by HBM:
 // 16384 x 4096 bf16 to FP8 54.0 us, 6.2 TB/s (units of 8 elements 67 to 86; six or
-// seven blocks a multiprocessor, whose registers spill, 59), to bf16 57.4, 7.0 TB/s.
+// seven blocks a multiprocessor, whose registers spill, 59), to bf16 58.1, 6.9 TB/s.
 template <Elt ELT, bool QUANT>
 __global__ void __launch_bounds__(256, ELT == Elt::FP32 ? 4 : QUANT ? 5 : 6) gate_rows_kernel(GateArgs a, int64_t nb) {
     let_next_start();
@@ -278,23 +275,36 @@ __global__ void __launch_bounds__(GateTile<ELT>::kThreads, GateTile<ELT>::kBlock
     }
 }
 
+// Gradients of two gates and their other factors, for the gradients g of a:
+// d_up = g silu(x), d_gate = g up silu'(x), silu'(x) = s (1 + x (1 - s)) with s = 1 / (1
+// + exp(-x)).  All of s and silu' is there without the scale, which goes into the
+// products last.  g up may be out of range where d_gate is not: silu' goes with the
+// larger of the two, and of the scale and the smaller one that comes first which
+// takes the product towards 1.
+template <Elt ELT>
 struct GateGrad {
-    float gate, up;
-    // d_up = g silu(gate);  d_gate = g up (s + silu(gate) (1 - s))
-    __device__ __forceinline__ GateGrad(float g, float x, float u) {
-        const Sigmoid s(x);
-        const float silu = fmul(x, s.s);
-        up = fmul(g, silu);
-        gate = fmul(fmul(g, u), ffma(silu, s.rest, s.s));
+    float2 gate, up;
+    __device__ __forceinline__ GateGrad(float2 g, float2 x, float2 u) {
+        const Scaled c(x);
+        const float2 e = exp_scaled<ELT, true>(x, c), d = fma2(e, both(1.0f), c.scale), inv = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 slope = mul2(inv, fma2(x, mul2(e, inv), both(1.0f)));
+        up = mul2(mul2(g, mul2(x, inv)), c.scale);
+        gate = make_float2(product(g.x, u.x, slope.x, c.scale.x), product(g.y, u.y, slope.y, c.scale.y));
+    }
+    __device__ __forceinline__ static float product(float g, float u, float slope, float scale) {
+        const bool first = fabsf(g) > fabsf(u);
+        const float least = first ? u : g, most = fmul(first ? g : u, slope);
+        const bool high = fabsf(most) >= 1.0f;
+        return fmul(fmul(most, high ? scale : least), high ? least : scale);
     }
 };
 
 // Any alignment and any H, every form but COLUMNS: one row to blockIdx.x, its
 // 1x128 blocks to the warps of blockIdx.y in turn, an element at a time,
 // neighbours to neighbouring lanes.  Bound by instructions: 8191 x 4095 bf16 to FP8
-// 44.1 us, its gradient 66, 3.8 and 5.1 TB/s.
+// 44.1 us, its gradient 67.4 (four or six blocks a multiprocessor 73 and 68), 3.8 and 5.0 TB/s.
 template <Elt ELT, GateForm FORM>
-__global__ void __launch_bounds__(256) gate_any_kernel(GateArgs a, int nb) {
+__global__ void __launch_bounds__(256, FORM == GateForm::GRAD ? 5 : 0) gate_any_kernel(GateArgs a, int nb) {
     let_next_start();
     wait_for_stream();
     const int lane = threadIdx.x & 31, H = (int)a.H;
@@ -315,11 +325,16 @@ __global__ void __launch_bounds__(256) gate_any_kernel(GateArgs a, int nb) {
             if constexpr (FORM == GateForm::GRAD) {
                 char* to = static_cast<char*>(a.out) + row * 2 * a.H * elt_bytes<ELT>();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const GateGrad d(__uint_as_float(of[q]), __uint_as_float(gate[q]), __uint_as_float(up[q]));
+                for (int q = 0; q < 4; q += 2) {
+                    const auto two = [q](const uint32_t(&w)[4]) { return make_float2(__uint_as_float(w[q]), __uint_as_float(w[q + 1])); };
+                    const GateGrad<ELT> d(two(of), two(gate), two(up));
                     if (k + 32 * q < H) {
-                        store_f32<ELT>(to, k + 32 * q, d.gate);
-                        store_f32<ELT>(to, H + (int64_t)k + 32 * q, d.up);
+                        store_f32<ELT>(to, k + 32 * q, d.gate.x);
+                        store_f32<ELT>(to, H + (int64_t)k + 32 * q, d.up.x);
+                    }
+                    if (k + 32 * q + 32 < H) {
+                        store_f32<ELT>(to, k + 32 * q + 32, d.gate.y);
+                        store_f32<ELT>(to, H + (int64_t)k + 32 * q + 32, d.up.y);
                     }
                 }
             } else {
@@ -383,9 +398,9 @@ __global__ void __launch_bounds__(512) gate_columns_kernel(GateArgs a) {
 }
 
 // A unit of 16 elements of both halves a thread.  Bound by HBM: 8191 x 7184 bf16
-// 84 us, 7.0 TB/s.
+// 85.3 us, 6.9 TB/s (four or six blocks a multiprocessor 87 and 103).
 template <Elt ELT>
-__global__ void __launch_bounds__(256) gate_grad_kernel(GateArgs a, int64_t nu) {
+__global__ void __launch_bounds__(256, ELT == Elt::BF16 ? 5 : 4) gate_grad_kernel(GateArgs a, int64_t nu) {
     let_next_start();
     wait_for_stream();
     int64_t row, u;
@@ -399,11 +414,11 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(GateArgs a, int64_t nu) 
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const GateGrad p(g.f(2 * j), gate.f(2 * j), up.f(2 * j)), q(g.f(2 * j + 1), gate.f(2 * j + 1), up.f(2 * j + 1));
-        gate.set2(j, p.gate, q.gate);
-        up.set2(j, p.up, q.up);
-        top = max(max(top, __float_as_uint(p.gate) & 0x7FFFFFFFu), __float_as_uint(q.gate) & 0x7FFFFFFFu);
-        top = max(max(top, __float_as_uint(p.up) & 0x7FFFFFFFu), __float_as_uint(q.up) & 0x7FFFFFFFu);
+        const GateGrad<ELT> d(g.f2(j), gate.f2(j), up.f2(j));
+        gate.set2(j, d.gate.x, d.gate.y);
+        up.set2(j, d.up.x, d.up.y);
+        top = max(max(top, __float_as_uint(d.gate.x) & 0x7FFFFFFFu), __float_as_uint(d.gate.y) & 0x7FFFFFFFu);
+        top = max(max(top, __float_as_uint(d.up.x) & 0x7FFFFFFFu), __float_as_uint(d.up.y) & 0x7FFFFFFFu);
     }
     if (top > 0x7F800000u) gate.canonical(), up.canonical();
     gate.store(a.out, row * 2 * a.H + k);

@@ -572,7 +572,8 @@ MXQ_API mxq_status mxq_fp8_silu_mul_128x1(const void* x, mxq_dtype dt, int64_t r
                                           uint8_t* data, uint8_t* scales, cudaStream_t stream);
 /* Gradient of x for the gradient g [rows, ldg] of a: with s = 1 / (1 +
  * exp(-gate)), d_gate = g up s (1 + gate (1 - s)) and d_up = g gate s; d_x [rows, 2H]
- * contiguous, all dt.  Errors as above. */
+ * contiguous, all dt.  g up may be out of range where d_gate is not.  Gates below
+ * -167.7 give 0, for what is less than 2.4e-71 |g up| and |g|.  Errors as above. */
 MXQ_API mxq_status mxq_silu_mul_grad(const void* g, const void* x, mxq_dtype dt, int64_t rows, int64_t H, int64_t ldg,
                                      int64_t ldx, void* d_x, cudaStream_t stream);
 

@@ -86,3 +86,51 @@ def test_infinite_and_lowest_gates_in_every_form(mx, H, dtype):
     assert (f64(mx.silu_mul(x))[3] == 0.5 * float(torch.finfo(dtype).max)).all()
     codes = f64(mx.fp8_silu_mul_1x128(x)[1])
     assert (codes[:2] == 255).all() and (codes[2] == 0).all() and (codes[3] < 255).all()
+
+
+def check_gate_gradient(mx, x, g, rel=FAR):
+    """With gates down to -167 the bounds are those of the forms above: what is added to 1, up to 168 of it, is off by 4 U, and
+    so are the sums that test_gpu_moe_block counts; results may be subnormal."""
+    want, size = bref.gate_grad(f64(g), f64(x))
+    top = float(torch.finfo(x.dtype).max)
+    assert np.isfinite(size).all() and (np.abs(want) < top).all()
+    near(mx.silu_mul_grad(g, x), want, rel * size + half_step(x.dtype) * np.abs(want) + (2.0**-133 if x.dtype == BF16 else 2.0**-148))
+
+
+@pytest.mark.parametrize("H", [64, 61])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gate_gradient_of_factors_whose_product_overflows(mx, H, dtype):
+    """The derivative of silu brings the product back: gates far below zero, and the place where the derivative is zero."""
+    rng = np.random.default_rng(H)
+    for lo, hi, size in ((86, 100, 66), (100, 130, 72), (130, 166, 90), (60, 86, 100), (10, 60, 62)):
+        x, g = normal(rng, 40, 2 * H), normal(rng, 40, H)
+        x[:, :H] = -rng.uniform(lo, hi, (40, H))
+        x[:, H:] = np.sign(x[:, H:]) * np.exp2(rng.uniform(size - 3, size, (40, H)))
+        g = np.sign(g) * np.exp2(rng.uniform(size - 3, size, (40, H)))
+        check_gate_gradient(mx, dev(x, dtype), dev(g, dtype))
+        # one of the factors large, the other small: their order does not matter
+        x[:, H:] *= 2.0**20
+        check_gate_gradient(mx, dev(x, dtype), dev(g * 2.0**-24, dtype))
+        check_gate_gradient(mx, dev(np.concatenate([x[:, :H], g * 2.0**-24], 1), dtype), dev(x[:, H:], dtype))
+
+
+@pytest.mark.parametrize("H", [64, 61])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gate_gradient_of_gates_that_give_zero(mx, H, dtype):
+    """A derivative of zero is zero times any number: not NaN because the other factors' product overflows first."""
+    x, g = torch.full((6, 2 * H), 1e30, device="cuda", dtype=dtype), torch.full((6, H), 1e30, device="cuda", dtype=dtype)
+    for row, gate in enumerate((-250.0, -1e3, -1e30, torch.finfo(dtype).min, -250.0, -1e4)):
+        x[row, :H] = gate
+    x[4, H:], g[4] = 1e38, 1e9
+    assert not mx.silu_mul_grad(g, x).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gate_gradient_over_the_whole_range(mx, dtype):
+    """Every finite bf16 gate beside large, ordinary and small factors."""
+    gate = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(BF16)
+    gate = gate[torch.isfinite(gate.float()) & (gate > -167)]
+    for u, s in ((1.5, 0.75), (2.0**20, 2.0**-30), (-(2.0**-60), 2.0**40), (1e-38, 1.25)):
+        keep = gate[gate.double().abs() * max(abs(u), 1.0) * s < 1e38]
+        x = torch.stack([keep, torch.full_like(keep, u)], 1).to(dtype).contiguous()
+        check_gate_gradient(mx, x, torch.full((len(x), 1), s, device="cuda", dtype=dtype))
