@@ -38,7 +38,7 @@ class Norm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g, g_h, *_):
         h, weight, rstd = ctx.saved_tensors
-        d_h, d_weight = mxq.mxq_rmsnorm_grad(g.contiguous(), h, weight, rstd, g_h=g_h)
+        d_h, d_weight = mxq.mxq_rmsnorm_grad(g.contiguous(), h, weight, rstd, g_h=g_h.contiguous())
         return d_h, d_h, d_weight.to(weight.dtype)
 
 
