@@ -433,7 +433,7 @@ static mxq_status gate(mxq::GateForm form, const void* x, mxq_dtype dt, int64_t 
     const mxq_status st = check_dtype(dt);
     if (st != MXQ_OK) return st;
     const bool grad = form == mxq::GateForm::GRAD, quant = form == mxq::GateForm::ROWS || form == mxq::GateForm::COLUMNS;
-    if (!valid_dim(rows) || !valid_width(2 * H) || !valid_ld(2 * H, ldx) || (grad && !valid_ld(H, ldg))) return MXQ_ERR_INVALID_ARG;
+    if (!valid_dim(rows) || !valid_width(H) || !valid_width(2 * H) || !valid_ld(2 * H, ldx) || (grad && !valid_ld(H, ldg))) return MXQ_ERR_INVALID_ARG;
     if (rows == 0 || H == 0) return MXQ_OK;
     const size_t es = elt_size(dt);
     if (!x || !aligned(x, es) || (grad && (!g || !aligned(g, es)))) return MXQ_ERR_INVALID_ARG;
