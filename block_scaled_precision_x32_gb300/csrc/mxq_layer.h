@@ -87,7 +87,9 @@ struct NormArgs {
 };
 
 // Sums over rows that the blocks of the norm's gradient leave for its second
-// kernel, at most: two blocks to each of a GB300's 152 multiprocessors.
+// kernel, at most: one of each block where they are persistent, one to a
+// multiprocessor (152 on a GB300), and twice as many where rows are longer than
+// those take.
 constexpr int64_t kNormParts = 304;
 
 struct NormGradArgs {
