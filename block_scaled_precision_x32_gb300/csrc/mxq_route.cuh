@@ -318,13 +318,25 @@ __device__ __forceinline__ void best_groups(const RouteArgs& a, int lane, Real (
     }
 }
 
-// Can two neighbours of the order, last in front of e, not be told apart?
-// Equal logits with equal biases are ties, which the index decides, and so are
-// infinite c; one of them is far ahead of what is finite.
+// Equal logits with equal biases are ties, which the index decides.
+template <Elt ELT>
+__device__ __forceinline__ bool are_ties(const RouteArgs& a, int64_t t, int e, int f) {
+    return key_of(logit<ELT>(a, t, e)) == key_of(logit<ELT>(a, t, f)) && (!a.bias || key_of(a.bias[e]) == key_of(a.bias[f]));
+}
+
+// Is c, behind last_c in the order, within the error of the two?  Infinite ones are
+// ties, or far ahead of what is finite.
+template <typename Real>
+__device__ __forceinline__ bool is_near(float err, Real last_c, Real c) {
+    return size_of(last_c) < kInf && gap(last_c, c) <= 2 * err + kRound<Real> * max(size_of(last_c), size_of(c));
+}
+
+// Can two of the order, last in front of e, not be told apart?  To be asked of
+// neighbours among the chosen, and of the last chosen with each that is not: next to
+// it may be its ties alone, and behind them what belongs in its place.
 template <Elt ELT, typename Real>
 __device__ __forceinline__ bool too_near(const RouteArgs& a, int64_t t, float err, Real last_c, int last, Real c, int e) {
-    return size_of(last_c) < kInf && gap(last_c, c) <= 2 * err + kRound<Real> * max(size_of(last_c), size_of(c)) &&
-           !(logit<ELT>(a, t, last) == logit<ELT>(a, t, e) && (!a.bias || a.bias[last] == a.bias[e]));
+    return is_near(err, last_c, c) && !are_ties<ELT>(a, t, last, e);
 }
 
 // The topk largest of c, one after the other: lane j's result is the j-th, -1
@@ -342,11 +354,10 @@ __device__ __forceinline__ int choose_in_turn(const RouteArgs& a, int64_t t, int
     }
     int id = -1, last = -1;
     Real last_c = of<Real>(0.0f);
-    const int rounds = a.topk + (err >= 0.0f ? 1 : 0);
 #pragma unroll 1
-    for (int j = 0; j < rounds; ++j) {
+    for (int j = 0; j < a.topk; ++j) {
         const Key best = warp_max(top);
-        if (best == 0) break;
+        if (best == 0) return id;
         const int src = __ffs(__ballot_sync(kAll, top == best)) - 1;
         int e = 0;
         if (lane == src) {
@@ -363,7 +374,7 @@ __device__ __forceinline__ int choose_in_turn(const RouteArgs& a, int64_t t, int
             }
         }
         e = __shfl_sync(kAll, e, src);
-        if (j < a.topk && lane == j) id = e;
+        if (lane == j) id = e;
         if (err >= 0.0f) {
             Real now;
             from_key(best, now);
@@ -371,6 +382,17 @@ __device__ __forceinline__ int choose_in_turn(const RouteArgs& a, int64_t t, int
             last = e;
             last_c = now;
         }
+    }
+    if (err >= 0.0f) {
+        unsigned near = 0;  // of the lane's others, to the last chosen
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            Real other;
+            from_key(key[i], other);
+            near |= key[i] != 0 && is_near(err, last_c, other) ? 1u << i : 0u;
+        }
+#pragma unroll 1
+        for (; near; near &= near - 1) unsure |= !are_ties<ELT>(a, t, last, lane * VPL + __ffs(near) - 1);
     }
     return id;
 }
@@ -419,18 +441,18 @@ __device__ __noinline__ bool resolve(const RouteArgs& a, int64_t t, int n, uint6
         const int other = __shfl_sync(kAll, id, j);
         rank += more(o, c) || (!more(c, o) && other < id) ? 1 : 0;
     }
-    bool unsure = false;
+    // each place's number, then each place's expert: those of neighbours are compared as too_near has to be asked
     const float err = most * (1.0f / (1ull << 41));  // 2^-45 of the exponential, the sum, the quotient and the product
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-        const Wide o = lane_at(c, j);
-        const float ox = __shfl_sync(kAll, x, j), ob = __shfl_sync(kAll, b, j);
-        if (__shfl_sync(kAll, rank, j) == rank + 1 && rank < a.topk && lane < n && !(ox == x && ob == b))
-            unsure |= size_of(c) < kInf && gap(c, o) <= 2 * err + kRound<Wide> * max(size_of(c), size_of(o));
-    }
+    __syncwarp();
+    if (lane < n) list[rank] = (uint64_t)__float_as_uint(c.h) << 32 | __float_as_uint(c.l);
+    __syncwarp();
+    const auto at = [&](int place) { return wide(__uint_as_float((uint32_t)(list[place] >> 32)), __uint_as_float((uint32_t)list[place])); };
+    const int front = min(lane, a.topk) - 1;
+    bool unsure = lane && lane < n && is_near(err, at(front), at(lane));
     __syncwarp();
     if (lane < n) list[rank] = (uint64_t)key_of(c.h) << 32 | (uint32_t)~id;
     __syncwarp();
+    if (unsure) unsure = !are_ties<ELT>(a, t, (int)~(uint32_t)list[front], (int)~(uint32_t)list[lane]);
     return !__any_sync(kAll, unsure);
 }
 
@@ -486,8 +508,8 @@ __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, int lane,
     __syncwarp();
     if (err >= 0.0f) {
         bool near = false;
-        if (lane < a.topk && lane + 1 < n) {
-            const uint64_t k = list[lane], l = list[lane + 1];
+        if (lane && lane < n) {
+            const uint64_t k = list[min(lane, a.topk) - 1], l = list[lane];
             near = too_near<ELT>(a, t, err, of_key((uint32_t)(k >> 32)), (int)~(uint32_t)k, of_key((uint32_t)(l >> 32)), (int)~(uint32_t)l);
         }
         if (__any_sync(kAll, near)) unsure |= !resolve<ELT>(a, t, n, list);
@@ -736,7 +758,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
 }
 
 template <Elt ELT, int VPL, Groups GROUPS>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 9 : 0) route_kernel(const __grid_constant__ RouteArgs a) {
     __shared__ __align__(16) uint64_t lists[kWarps][32];
     __shared__ float stages[GROUPS == ANY ? kWarps : 1][GROUPS == ANY ? 32 * VPL : 1];
     let_next_start();
@@ -1114,16 +1136,28 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 20 / kQuadWarps) route_quad_k
     __syncwarp();
     left = __ballot_sync(kAll, left) >> (lane & 28) & 15;  // of one of the four, of all
     if (scored) {
-        bool near = false;
+        bool near = false, edge = false;  // edge: the first that is not chosen is near to the last that is
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int place = l + 4 * r;
             if (place < a.topk && place + 1 < n) {
                 const uint64_t k = list[place], o = list[place + 1];
-                near |= too_near<ELT>(a, t, err, of_key((uint32_t)(k >> 32)), (int)~(uint32_t)k, of_key((uint32_t)(o >> 32)), (int)~(uint32_t)o);
+                if (is_near(err, of_key((uint32_t)(k >> 32)), of_key((uint32_t)(o >> 32)))) {
+                    if (place + 1 == a.topk) edge = true;
+                    else near |= !are_ties<ELT>(a, t, (int)~(uint32_t)k, (int)~(uint32_t)o);
+                }
             }
         }
-        unsigned nears = __ballot_sync(kAll, near && !left);
+        unsigned nears = __ballot_sync(kAll, (near || edge) && !left);
+        if (nears) {
+            if (__ballot_sync(kAll, edge) >> (lane & 28) & 15)
+                for (int place = a.topk + l; place < n; place += 4) {
+                    const uint64_t k = list[a.topk - 1], o = list[place];
+                    near |= too_near<ELT>(a, t, err, of_key((uint32_t)(k >> 32)), (int)~(uint32_t)k, of_key((uint32_t)(o >> 32)), (int)~(uint32_t)o);
+                }
+            __syncwarp();
+            nears = __ballot_sync(kAll, near && !left);
+        }
         while (nears) {  // one token after the other, by the whole warp
             const int quad = (__ffs(nears) - 1) >> 2;
             const bool ok = resolve<ELT>(a, __shfl_sync(kAll, t, 4 * quad), __shfl_sync(kAll, n, 4 * quad), lists[threadIdx.x / 32][quad]);

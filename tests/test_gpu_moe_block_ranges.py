@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_scaled_precision_x32_gb300 as mxq
-from tests.test_gpu_moe_block import F32, check_route, dev, normal
+from tests.test_gpu_moe_block import BF16, F32, check_route, dev, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,33 @@ def test_a_router_that_keeps_two_warps_worth_of_experts(mx, groups, topk_groups)
     check_route(mx, x[:16400], 4, b, score="sigmoid", groups=groups, topk_groups=topk_groups, group_top=2)
     crowded, usual = (device_us(lambda: mx.moe_route(x, 4, topk_groups=n, **kw)) for n in (topk_groups, topk_groups + 1))
     assert crowded < 3 * usual, (crowded, usual)
+
+
+@pytest.mark.parametrize("T", [70, 16389])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,topk,more", [(60, 4, {}), (128, 8, {}), (256, 6, dict(groups=8, topk_groups=8, group_top=2)), (512, 1, {}), (128, 32, {})])
+@pytest.mark.parametrize("level", [0.0, 1024.5])
+def test_route_of_ties_at_the_last_place(mx, E, topk, more, score, level, T):
+    """The last place is contested by experts that are alike, and by one with a higher index that is ahead of them by less than
+    24 bits tell, beside the bias: the tie among the others does not settle the place."""
+    rng = np.random.default_rng(E + topk)
+    x = (-4.0 + 0.1 * normal(rng, T, E)).astype(np.float32)
+    for t in range(T):
+        ties = 2 + t % 5 if t % 7 else 40  # more than the candidates' lists hold
+        at = np.sort(rng.permutation(E)[: min(topk - 1 + ties + 1, E)])
+        x[t, at[: topk - 1]] = 3.0 + np.arange(topk - 1) / 16.0
+        x[t, at[topk - 1:]] = 1.0
+        x[t, at[-1]] = 1.0 + 2.0**-23 if level == 0.0 else 1.0 + 2.0**-14
+    bias = np.full(E, level, np.float32)
+    check_route(mx, dev(x), topk, dev(bias), score=score, **more)
+
+
+@pytest.mark.parametrize("T", [70, 16389])
+def test_route_of_ties_among_large_biases(mx, T):
+    """Few different logits beside few different biases, whose fp32 sums with a score are often equal or one step apart."""
+    rng = np.random.default_rng(4)
+    for E, more in ((96, {}), (256, dict(groups=8, topk_groups=3, group_top=2))):
+        x = dev(np.round(4 * normal(rng, T, E)) / 4, BF16)
+        bias = dev(512.0 + rng.integers(0, 3, E) / 16384.0)
+        for score in ("softmax", "sigmoid"):
+            check_route(mx, x, 8, bias, score=score, **more)
