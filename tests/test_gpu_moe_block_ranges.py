@@ -165,3 +165,31 @@ def test_route_of_ties_among_large_biases(mx, T):
         bias = dev(512.0 + rng.integers(0, 3, E) / 16384.0)
         for score in ("softmax", "sigmoid"):
             check_route(mx, x, 8, bias, score=score, **more)
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_route_of_forms_drawn_at_random(mx, seed):
+    """Any number of experts, groups and choices; ties, experts out of service, and biases of every size."""
+    rng = np.random.default_rng(seed)
+    for turn in range(24):
+        E = int(rng.choice([32, 60, 96, 128, 160, 192, 256, 512])) if turn % 2 else int(rng.integers(1, 1025))
+        groups = int(rng.choice([g for g in range(1, 33) if E % g == 0]))
+        size = E // groups
+        kept, top = int(rng.integers(1, groups + 1)), int(rng.integers(1, min(2, size) + 1))
+        topk = int(rng.integers(1, min(9 if turn % 4 else 33, kept * size + 1)))
+        T = 16384 + turn if turn in (5, 17) else int(rng.integers(1, 400))
+        x = (rng.choice([1e-3, 0.1, 1.5, 4.0]) * normal(rng, T, E)).astype(np.float32)
+        if turn % 3 == 0:
+            x[rng.random((T, E)) < 0.3] = -np.inf
+        if turn % 5 == 0:
+            x = np.round(2 * x) / 2
+        if turn % 7 == 0:
+            x += np.float32(20.0)
+        x[rng.random(T) < 0.1] = 0
+        b = (rng.choice([0.0, 0.05, 0.5]) * normal(rng, E)).astype(np.float32)
+        for _ in range(int(rng.integers(0, 4))):
+            v = rng.choice([np.inf, -np.inf, LOWEST, -LOWEST, 0.6 * LOWEST, 1e30, -1e30, 1e9, -1e9, 1e4, -1e4, 65536.5])
+            g = int(rng.integers(groups))
+            b[slice(g * size, (g + 1) * size) if rng.random() < 0.5 else rng.random(E) < 0.1] = v
+        check_route(mx, dev(x, BF16 if turn % 4 == 1 else F32), topk, dev(b) if turn % 6 else None, score=("softmax", "sigmoid")[turn // 2 % 2],
+                    groups=groups, topk_groups=kept, group_top=top, renormalize=bool(turn // 4 % 2))
