@@ -13,7 +13,7 @@
 //
 // A warp to a token, VPL consecutive experts to a lane, in registers.  Bound by
 // instructions and, for few tokens, by the latency of their chain: 48 x 32 with
-// topk 2 take 1.7 us, 65536 x 160 with eight groups 53 us.  From kQuadTokens on
+// topk 2 take 1.7 us, 65536 x 160 with eight groups 54 us.  From kQuadTokens on
 // four lanes take a token where its sizes allow.
 #pragma once
 
